@@ -495,6 +495,142 @@ dust_status dust_estimate_gW_host_sites(const dust_host_site* sites, int64_t n_s
                                         void* stream);
 
 /*
+ * Layer norm, forward and backward (the norm before a linear layer, and the
+ * one before the head, whose gradients are exact: nothing random lies between
+ * them and the loss). Per row of d values, with n = (x - mean) rstd:
+ *   mean = sum x / d    rstd = 1 / sqrt(sum (x - mean)^2 / d + eps)
+ *   y    = n weight + bias
+ *   gx   = rstd (gn - mean(gn) - n mean(gn n)),   gn = gy weight
+ *   gweight = sum over rows of gy n,   gbias = sum over rows of gy
+ * Statistics and sums are fp32 (the variance from deviations, not from a
+ * difference of squares); y and gx are rounded once to `dtype`. Deterministic.
+ *
+ * dust_layer_norm
+ *   x, y     device, T rows of d values, DUST_F32 or DUST_BF16, row strides
+ *            ld_x, ld_y >= d (elements). y may be x itself (same stride); no
+ *            other overlap.
+ *   weight, bias  device f32 [d], either may be NULL (1 and 0).
+ *   eps      finite, >= 0.
+ *   mean, rstd    device f32 [T], written; either may be NULL.
+ * dust_layer_norm_grad
+ *   gy, x    device, as x above (row strides ld_gy, ld_x); mean, rstd device
+ *            f32 [T] of the forward; weight f32 [d] or NULL (1).
+ *   gx       device, `dtype`, row stride ld_gx, or NULL; may be gy itself
+ *            (same stride), no other overlap.
+ *   gweight, gbias  device f32 [d], either may be NULL; overwritten, or added
+ *            to with DUST_ACCUMULATE (the only flag; gx is always
+ *            overwritten). With T = 0 they are zeroed (or left, accumulating).
+ *   workspace  device, >= dust_layer_norm_grad_workspace(T, d) bytes,
+ *            256-byte aligned (partial sums of gweight and gbias); may be
+ *            NULL when both are NULL.
+ * T and d up to 2^31 - 1, T * d up to 2^40 (else DUST_ERR_RANGE). Empty sizes
+ * launch nothing else.
+ */
+dust_status dust_layer_norm(const void* x, dust_dtype dtype, int64_t ld_x, int64_t T, int64_t d,
+                            const float* weight, const float* bias, float eps, void* y,
+                            int64_t ld_y, float* mean, float* rstd, void* stream);
+dust_status dust_layer_norm_grad_workspace(size_t* bytes, int64_t T, int64_t d);
+dust_status dust_layer_norm_grad(const void* gy, int64_t ld_gy, const void* x, int64_t ld_x,
+                                 dust_dtype dtype, int64_t T, int64_t d, const float* weight,
+                                 const float* mean, const float* rstd, uint32_t flags, void* gx,
+                                 int64_t ld_gx, float* gweight, float* gbias, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/*
+ * The head's per-token loss over a vocabulary of V rows, without keeping the
+ * logits: what turns jittered forwards into the estimator's loss changes
+ * ("Dust: every token is a member of the population", "What the released code
+ * actually does", step 2: the reward is the clean loss minus the perturbed
+ * one), and the head's own exact gradients. H [S][T][d] holds S slices of the
+ * same T tokens (dust_forward_jitter's output: the clean slice first, then
+ * one per draw); slice s, token t is row r = s T + t.
+ *   x[r][v]  = scale <H[r], E[v]>              lse[r] = log sum_v exp x[r][v]
+ *   loss[r]  = lse[r] - x[r][targets[t]]       (0 where token t has no target)
+ *   delta[k][t] = loss[k + 1][t] - loss[0][t]  the estimator's loss changes
+ * and with the loss's gradient gloss[r]
+ *   G[r][v]  = gloss[r] (exp(x[r][v] - lse[r]) - [v = targets[t]])
+ *   gH[r]    = scale sum_v G[r][v] E[v]        gE[v] = scale sum_r G[r][v] H[r]
+ *
+ *   H        device, `dtype` (DUST_F32 or DUST_BF16), S*T rows with row stride
+ *            ld_h >= d; E device, `dtype`, V rows, row stride ld_e >= d.
+ *   targets  device i32 [T]. A negative id means no target: loss 0, no
+ *            gradient. Ids >= V are treated alike and make dust_last_error
+ *            report DUST_ERR_INVALID_ARG.
+ *   scale    finite.
+ *   loss, lse  device f32 [S*T], written; loss may be NULL. delta device f32
+ *            [S - 1][T], written, or NULL.
+ *   gloss    device f32 [S*T]. Rows without a target and rows with gloss 0
+ *            take no part in either gradient, whatever H holds there (NaN
+ *            included); their gH is 0.
+ *   gH       device, `dtype`, S*T rows with row stride ld_gh >= d, or NULL.
+ *   gE       device [V][d], gE_dtype DUST_F32, or DUST_BF16 with bf16 inputs;
+ *            or NULL. Overwritten, or added to with DUST_ACCUMULATE (the only
+ *            flag; needs DUST_F32).
+ *   workspace  device, >= the size that the matching query gives, 256-byte
+ *            aligned; contents on entry are ignored.
+ * bf16 inputs: products of the exact bf16 values summed in fp32; in the
+ * gradients G is rounded to bf16 (it is a tensor-core operand), divided by
+ * the largest |gloss| first so that equal weights round as 1 does. fp32
+ * inputs: every product and sum to fp32 accuracy. All sums run in an order
+ * fixed by the sizes and by which rows take part: deterministic.
+ * d >= 1, V >= 1, S >= 1; S*T, d and V up to 2^31 - 1, S*T*d and V*d up to
+ * 2^40 (DUST_ERR_RANGE). T = 0 writes zeros to gE (or leaves it,
+ * accumulating) and nothing else.
+ */
+dust_status dust_head_loss_workspace(size_t* bytes, int64_t S, int64_t T, int64_t d, int64_t V,
+                                     dust_dtype dtype);
+dust_status dust_head_loss(const void* H, int64_t ld_h, const void* E, int64_t ld_e,
+                           dust_dtype dtype, int64_t S, int64_t T, int64_t d, int64_t V,
+                           const int32_t* targets, float scale, float* loss, float* lse,
+                           float* delta, void* workspace, size_t ws_bytes, void* stream);
+dust_status dust_head_loss_grad_workspace(size_t* bytes, int64_t S, int64_t T, int64_t d,
+                                          int64_t V, dust_dtype dtype);
+dust_status dust_head_loss_grad(const void* H, int64_t ld_h, const void* E, int64_t ld_e,
+                                dust_dtype dtype, int64_t S, int64_t T, int64_t d, int64_t V,
+                                const int32_t* targets, float scale, const float* lse,
+                                const float* gloss, uint32_t flags, void* gH, int64_t ld_gh,
+                                void* gE, dust_dtype gE_dtype, void* workspace, size_t ws_bytes,
+                                void* stream);
+
+/*
+ * Distillation through the same head from a teacher's K largest logits a
+ * token. With q[t] = softmax(scale teacher[t]) over the entries present (the
+ * teacher's probabilities renormalised over what was stored), x and lse as
+ * above (`scale` is an inverse temperature, applied to both sides):
+ *   loss[r]  = sum_j q[t][j] (log q[t][j] - (x[r][ids[t][j]] - lse[r]))
+ *   G[r][v]  = gloss[r] (exp(x[r][v] - lse[r]) - sum over j with ids[t][j] = v
+ *              of q[t][j])
+ * and gH, gE from G as above.
+ *   ids      device i32 [T][K]; a negative id marks an absent entry, in any
+ *            place. Ids >= V are absent too and reported as above. An id may
+ *            come twice (its probabilities add). A token with no entry has
+ *            loss 0 and no gradient.
+ *   teacher  device f32 [T][K]; -infinity is a probability of 0. Absent
+ *            entries' values are not used.
+ *   K        1 .. DUST_MAX_TEACHER (else DUST_ERR_RANGE).
+ *   student  device f32 [S*T][K]: x[r][ids[t][j]], 0 for absent entries;
+ *            written by the loss, read by the gradient.
+ * Everything else as for dust_head_loss and dust_head_loss_grad.
+ */
+#define DUST_MAX_TEACHER 1024
+dust_status dust_distill_loss_workspace(size_t* bytes, int64_t S, int64_t T, int64_t d,
+                                        int64_t V, int64_t K, dust_dtype dtype);
+dust_status dust_distill_loss(const void* H, int64_t ld_h, const void* E, int64_t ld_e,
+                              dust_dtype dtype, int64_t S, int64_t T, int64_t d, int64_t V,
+                              const int32_t* ids, const float* teacher, int64_t K, float scale,
+                              float* loss, float* lse, float* student, float* delta,
+                              void* workspace, size_t ws_bytes, void* stream);
+dust_status dust_distill_loss_grad_workspace(size_t* bytes, int64_t S, int64_t T, int64_t d,
+                                             int64_t V, int64_t K, dust_dtype dtype);
+dust_status dust_distill_loss_grad(const void* H, int64_t ld_h, const void* E, int64_t ld_e,
+                                   dust_dtype dtype, int64_t S, int64_t T, int64_t d, int64_t V,
+                                   const int32_t* ids, const float* teacher, int64_t K,
+                                   float scale, const float* lse, const float* student,
+                                   const float* gloss, uint32_t flags, void* gH, int64_t ld_gh,
+                                   void* gE, dust_dtype gE_dtype, void* workspace,
+                                   size_t ws_bytes, void* stream);
+
+/*
  * Per-kernel timing for benchmarks (no counterpart on the pages: this is
  * measurement plumbing). While enabled, every kernel the library launches is
  * bracketed by two CUDA events recorded on its stream; dust_profile_read
@@ -569,7 +705,8 @@ dust_status dust_debug_inject_timeout(int32_t on);
  * dust_last_error — synchronise `stream`, then return and clear the device
  * status word (DUST_OK; DUST_ERR_TIMEOUT when a kernel's bounded wait ran out
  * since the last call; DUST_ERR_INVALID_ARG when dust_scatter_gE or
- * dust_estimate_gE met a token id outside [0, V)). DUST_ERR_CUDA if the
+ * dust_estimate_gE met a token id outside [0, V), or a head loss, a
+ * distillation or one of their gradients an id >= V). DUST_ERR_CUDA if the
  * synchronisation failed.
  */
 dust_status dust_last_error(void* stream);

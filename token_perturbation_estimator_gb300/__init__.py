@@ -9,11 +9,14 @@ the import of a function raises.
 Functions keep the C names: ``dust_noise``, ``dust_jitter_apply``,
 ``dust_forward_jitter``,
 ``dust_credit_scan``, ``dust_error_estimate``, ``dust_estimate_gW``,
-``dust_estimate_gW_host``, ``dust_last_error`` (plus the workspace queries).
+``dust_estimate_gW_host``, ``dust_last_error`` (plus the workspace queries);
+and, beside the estimator, ``dust_layer_norm``, ``dust_head_loss`` and
+``dust_distill_loss``, each with its ``_grad``.
 """
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import re
 
@@ -32,6 +35,7 @@ CENTER, ANTITHETIC, ACCUMULATE = 1, 2, 4
 FORCE_UNFUSED, FORCE_FUSED, WORD_STREAM1, FORCE_SIMT = 8, 16, 32, 64
 # dust_path
 PATH_FUSED_TC, PATH_UNFUSED_TC, PATH_SIMT = 1, 2, 3
+MAX_TEACHER = 1024  # DUST_MAX_TEACHER
 
 
 class DustError(RuntimeError):
@@ -76,6 +80,22 @@ def _signatures():
         "dust_estimate_gE_workspace": (i32, [PSZ, i64, i64, i64, i64]),
         "dust_estimate_gE": (i32, [P, i64, i64, P, i64, i64, P, i64, u64, i32, i64, f32, f32,
                                    f32, u32, P, P, SZ, P]),
+        "dust_layer_norm": (i32, [P, i32, i64, i64, i64, P, P, f32, P, i64, P, P, P]),
+        "dust_layer_norm_grad_workspace": (i32, [PSZ, i64, i64]),
+        "dust_layer_norm_grad": (i32, [P, i64, P, i64, i32, i64, i64, P, P, P, u32, P, i64, P, P,
+                                       P, SZ, P]),
+        "dust_head_loss_workspace": (i32, [PSZ, i64, i64, i64, i64, i32]),
+        "dust_head_loss": (i32, [P, i64, P, i64, i32, i64, i64, i64, i64, P, f32, P, P, P, P, SZ,
+                                 P]),
+        "dust_head_loss_grad_workspace": (i32, [PSZ, i64, i64, i64, i64, i32]),
+        "dust_head_loss_grad": (i32, [P, i64, P, i64, i32, i64, i64, i64, i64, P, f32, P, P, u32,
+                                      P, i64, P, i32, P, SZ, P]),
+        "dust_distill_loss_workspace": (i32, [PSZ, i64, i64, i64, i64, i64, i32]),
+        "dust_distill_loss": (i32, [P, i64, P, i64, i32, i64, i64, i64, i64, P, P, i64, f32, P, P,
+                                    P, P, P, SZ, P]),
+        "dust_distill_loss_grad_workspace": (i32, [PSZ, i64, i64, i64, i64, i64, i32]),
+        "dust_distill_loss_grad": (i32, [P, i64, P, i64, i32, i64, i64, i64, i64, P, P, i64, f32,
+                                         P, P, P, u32, P, i64, P, i32, P, SZ, P]),
         "dust_debug_inject_timeout": (i32, [i32]),
         "dust_pipe_probe": (i32, [i32, i64, C.POINTER(C.c_double), P, P]),
         "dust_pipe_probe_threads": (i32, []),
@@ -400,6 +420,293 @@ def dust_estimate_gW_host(X_host, X_dev, delta_host, delta_dev, seq_host, seq_de
         float(sigma), float(gamma), float(scale), flags, _ptr(gW_host), _ptr(gW_dev),
         _ptr(workspace), workspace.numel(), _stream(stream)), "dust_estimate_gW_host")
     return gW_host
+
+
+# ---------------------------------------------- layer norm, head, distillation --
+
+def _rows(t, name, dtypes, shape=None):
+    """Raise ValueError unless t is a CUDA [T, d] tensor of one of `dtypes`
+    with unit column stride and rows that do not overlap; returns its row
+    stride in elements."""
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    _expect(t, name, dtypes, shape=shape, dim=2)
+    T, d = t.shape
+    if (d > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) < d):
+        raise ValueError("%s must have unit column stride and rows that do not overlap" % name)
+    return max(t.stride(0), d) if T > 1 else d
+
+
+def _vector(t, name, dtype, shape):
+    """Raise ValueError unless t (None passes) is a contiguous CUDA tensor of
+    this dtype and shape."""
+    if t is not None:
+        _need_cuda(t)
+        _expect(t, name, (dtype,), shape=shape)
+
+
+def _same_device(ref, *ts):
+    for t in ts:
+        if t is not None and t.device != ref.device:
+            raise ValueError("every tensor must be on %s" % ref.device)
+
+
+def _in_stream(fn):
+    """Gives fn a keyword `stream`: it then runs with that stream current, so
+    that what it allocates (outputs not passed in, workspace) belongs to the
+    stream that uses it and is not handed out again while the call runs."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _query(name, *args):
+    n = C.c_size_t(0)
+    _check(getattr(lib(), name)(C.byref(n), *args), name)
+    return n.value
+
+
+def _space(workspace, name, device, *args):
+    """The caller's workspace, or a new one of the size that query `name` gives."""
+    if workspace is None:
+        return _workspace(_query(name, *args), device)
+    _need_cuda(workspace)
+    _expect(workspace, "workspace", (_types().u8,), dim=1)
+    return workspace
+
+
+class _Types:
+    def __init__(self):
+        import torch
+        self.f32, self.bf16 = torch.float32, torch.bfloat16
+        self.i32, self.u8 = torch.int32, torch.uint8
+        self.values = (self.f32, self.bf16)
+
+
+_types_cache = None
+
+
+def _types():
+    global _types_cache
+    if _types_cache is None:
+        _types_cache = _Types()
+    return _types_cache
+
+
+@_in_stream
+def dust_layer_norm(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=None):
+    """x: CUDA [T, d] (f32 or bf16, rows may be strided); weight, bias: f32 [d]
+    or None; returns (y of x's dtype [T, d], mean f32 [T], rstd f32 [T])."""
+    import torch
+    ty = _types()
+    ld_x = _rows(x, "x", ty.values)
+    T, d = x.shape
+    if y is None:
+        y = torch.empty((T, d), dtype=x.dtype, device=x.device)
+    if mean is None:
+        mean = torch.empty(T, dtype=ty.f32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(T, dtype=ty.f32, device=x.device)
+    ld_y = _rows(y, "y", (x.dtype,), (T, d))
+    for t, name, n in ((weight, "weight", d), (bias, "bias", d), (mean, "mean", T),
+                       (rstd, "rstd", T)):
+        _vector(t, name, ty.f32, (n,))
+    _same_device(x, weight, bias, y, mean, rstd)
+    _check(lib().dust_layer_norm(_ptr(x), _dtype_code(x), ld_x, T, d, _ptr(weight), _ptr(bias),
+                                 float(eps), _ptr(y), ld_y, _ptr(mean), _ptr(rstd),
+                                 _stream(None)), "dust_layer_norm")
+    return y, mean, rstd
+
+
+@_in_stream
+def dust_layer_norm_grad(gy, x, mean, rstd, weight=None, flags=0, gx=None, gweight=None,
+                         gbias=None, workspace=None):
+    """gy, x: CUDA [T, d] (f32 or bf16, one dtype, rows may be strided); mean,
+    rstd: f32 [T] of the forward; weight: f32 [d] or None. Returns (gx of x's
+    dtype [T, d], gweight f32 [d], gbias f32 [d]); ACCUMULATE adds to the
+    gweight and gbias that are passed in."""
+    import torch
+    ty = _types()
+    ld_x = _rows(x, "x", ty.values)
+    T, d = x.shape
+    ld_gy = _rows(gy, "gy", (x.dtype,), (T, d))
+    if flags & ACCUMULATE and (gweight is None or gbias is None):
+        raise ValueError("ACCUMULATE needs the gweight and gbias to add to")
+    if gx is None:
+        gx = torch.empty((T, d), dtype=x.dtype, device=x.device)
+    if gweight is None:
+        gweight = torch.empty(d, dtype=ty.f32, device=x.device)
+    if gbias is None:
+        gbias = torch.empty(d, dtype=ty.f32, device=x.device)
+    ld_gx = _rows(gx, "gx", (x.dtype,), (T, d))
+    for t, name, n in ((weight, "weight", d), (mean, "mean", T), (rstd, "rstd", T),
+                       (gweight, "gweight", d), (gbias, "gbias", d)):
+        _vector(t, name, ty.f32, (n,))
+    workspace = _space(workspace, "dust_layer_norm_grad_workspace", x.device, T, d)
+    _same_device(x, gy, mean, rstd, weight, gx, gweight, gbias, workspace)
+    _check(lib().dust_layer_norm_grad(_ptr(gy), ld_gy, _ptr(x), ld_x, _dtype_code(x), T, d,
+                                      _ptr(weight), _ptr(mean), _ptr(rstd), flags, _ptr(gx),
+                                      ld_gx, _ptr(gweight), _ptr(gbias), _ptr(workspace),
+                                      workspace.numel(), _stream(None)),
+           "dust_layer_norm_grad")
+    return gx, gweight, gbias
+
+
+def _head_inputs(H, E):
+    """Sizes and row strides of H [T, d] or [S, T, d] and E [V, d]."""
+    ty = _types()
+    if H.dim() not in (2, 3):
+        raise ValueError("H must be [T, d] or [S, T, d], got shape %s" % (tuple(H.shape),))
+    if H.dim() == 3:
+        S, T, d = H.shape
+        if S > 1 and T > 0 and H.stride(0) != T * H.stride(1):
+            raise ValueError("the slices of H must follow one another")
+        rows = H[0] if S == 1 else H.as_strided((S * T, d), (H.stride(1), H.stride(2)))
+    else:
+        S, (T, d), rows = 1, H.shape, H
+    ld_h = _rows(rows, "H", ty.values)
+    ld_e = _rows(E, "E", (H.dtype,))
+    if E.shape[1] != d:
+        raise ValueError("E must be [V, d] matching H, got %s" % (tuple(E.shape),))
+    return S, T, d, E.shape[0], ld_h, ld_e
+
+
+def _loss_outputs(H, S, T, loss, lse, delta, changes):
+    import torch
+    ty = _types()
+    shape = tuple(H.shape[:-1])
+    if loss is None:
+        loss = torch.empty(shape, dtype=ty.f32, device=H.device)
+    if lse is None:
+        lse = torch.empty(shape, dtype=ty.f32, device=H.device)
+    if delta is None and changes:
+        delta = torch.empty((S - 1, T), dtype=ty.f32, device=H.device)
+    _vector(loss, "loss", ty.f32, shape)
+    _vector(lse, "lse", ty.f32, shape)
+    _vector(delta, "delta", ty.f32, (S - 1, T))
+    return loss, lse, delta
+
+
+def _grad_outputs(H, E, lse, gloss, flags, gH, gE, gE_dtype):
+    import torch
+    ty = _types()
+    shape = tuple(H.shape[:-1])
+    _vector(lse, "lse", ty.f32, shape)
+    _vector(gloss, "gloss", ty.f32, shape)
+    if flags & ACCUMULATE and gE is None:
+        raise ValueError("ACCUMULATE needs the gE to add to")
+    if gH is None:
+        gH = torch.empty(tuple(H.shape), dtype=H.dtype, device=H.device)
+    if gE is None:
+        gE = torch.empty(tuple(E.shape), dtype=gE_dtype or ty.f32, device=E.device)
+    _expect(gH, "gH", (H.dtype,), shape=H.shape)
+    _need_cuda(gH)
+    _vector(gE, "gE", gE.dtype if gE.dtype in ty.values else ty.f32, tuple(E.shape))
+    return gH, gE
+
+
+@_in_stream
+def dust_head_loss(H, E, targets, scale=1.0, changes=False, loss=None, lse=None, delta=None,
+                   workspace=None):
+    """H: CUDA [T, d] or [S, T, d] (f32 or bf16); E: [V, d] of H's dtype;
+    targets: i32 [T], negative where a token has none. Returns (loss, lse), f32
+    of H's leading shape, and with changes=True also delta f32 [S - 1, T], each
+    later slice's loss minus the first one's. No logits are kept."""
+    S, T, d, V, ld_h, ld_e = _head_inputs(H, E)
+    ty = _types()
+    _vector(targets, "targets", ty.i32, (T,))
+    loss, lse, delta = _loss_outputs(H, S, T, loss, lse, delta, changes)
+    dt = _dtype_code(H)
+    workspace = _space(workspace, "dust_head_loss_workspace", H.device, S, T, d, V, dt)
+    _same_device(H, E, targets, loss, lse, delta, workspace)
+    _check(lib().dust_head_loss(_ptr(H), ld_h, _ptr(E), ld_e, dt, S, T, d, V, _ptr(targets),
+                                float(scale), _ptr(loss), _ptr(lse), _ptr(delta),
+                                _ptr(workspace), workspace.numel(), _stream(None)),
+           "dust_head_loss")
+    return (loss, lse) if delta is None else (loss, lse, delta)
+
+
+@_in_stream
+def dust_head_loss_grad(H, E, targets, lse, gloss, scale=1.0, flags=0, gH=None, gE=None,
+                        gE_dtype=None, workspace=None):
+    """The gradients of dust_head_loss for gloss (f32, the losses' gradient, H's
+    leading shape) and the forward's lse: returns (gH of H's shape and dtype,
+    gE [V, d], f32 unless gE_dtype is bf16); ACCUMULATE adds to the f32 gE that
+    is passed in."""
+    S, T, d, V, ld_h, ld_e = _head_inputs(H, E)
+    ty = _types()
+    _vector(targets, "targets", ty.i32, (T,))
+    gH, gE = _grad_outputs(H, E, lse, gloss, flags, gH, gE, gE_dtype)
+    dt = _dtype_code(H)
+    workspace = _space(workspace, "dust_head_loss_grad_workspace", H.device, S, T, d, V, dt)
+    _same_device(H, E, targets, lse, gloss, gH, gE, workspace)
+    _check(lib().dust_head_loss_grad(_ptr(H), ld_h, _ptr(E), ld_e, dt, S, T, d, V, _ptr(targets),
+                                     float(scale), _ptr(lse), _ptr(gloss), flags, _ptr(gH), d,
+                                     _ptr(gE), _dtype_code(gE), _ptr(workspace),
+                                     workspace.numel(), _stream(None)), "dust_head_loss_grad")
+    return gH, gE
+
+
+def _teacher_inputs(ids, teacher, T):
+    ty = _types()
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, K], got shape %s" % (tuple(ids.shape),))
+    K = ids.shape[1]
+    _vector(ids, "ids", ty.i32, (T, K))
+    _vector(teacher, "teacher", ty.f32, (T, K))
+    return K
+
+
+@_in_stream
+def dust_distill_loss(H, E, ids, teacher, scale=1.0, changes=False, loss=None, lse=None,
+                      student=None, delta=None, workspace=None):
+    """Distillation from a teacher's K stored logits a token. H, E as for
+    dust_head_loss; ids: i32 [T, K], negative where an entry is absent; teacher:
+    f32 [T, K]. Returns (loss, lse, student), student f32 [..., K] the scaled
+    logits at ids, and with changes=True also delta f32 [S - 1, T]."""
+    import torch
+    S, T, d, V, ld_h, ld_e = _head_inputs(H, E)
+    K = _teacher_inputs(ids, teacher, T)
+    loss, lse, delta = _loss_outputs(H, S, T, loss, lse, delta, changes)
+    shape = tuple(H.shape[:-1]) + (K,)
+    if student is None:
+        student = torch.empty(shape, dtype=_types().f32, device=H.device)
+    _vector(student, "student", _types().f32, shape)
+    dt = _dtype_code(H)
+    workspace = _space(workspace, "dust_distill_loss_workspace", H.device, S, T, d, V, K, dt)
+    _same_device(H, E, ids, teacher, loss, lse, student, delta, workspace)
+    _check(lib().dust_distill_loss(_ptr(H), ld_h, _ptr(E), ld_e, dt, S, T, d, V, _ptr(ids),
+                                   _ptr(teacher), K, float(scale), _ptr(loss), _ptr(lse),
+                                   _ptr(student), _ptr(delta), _ptr(workspace),
+                                   workspace.numel(), _stream(None)), "dust_distill_loss")
+    return (loss, lse, student) if delta is None else (loss, lse, student, delta)
+
+
+@_in_stream
+def dust_distill_loss_grad(H, E, ids, teacher, lse, student, gloss, scale=1.0, flags=0, gH=None,
+                           gE=None, gE_dtype=None, workspace=None):
+    """The gradients of dust_distill_loss for gloss and the forward's lse and
+    student; returns (gH, gE) as dust_head_loss_grad does."""
+    S, T, d, V, ld_h, ld_e = _head_inputs(H, E)
+    K = _teacher_inputs(ids, teacher, T)
+    _vector(student, "student", _types().f32, tuple(H.shape[:-1]) + (K,))
+    gH, gE = _grad_outputs(H, E, lse, gloss, flags, gH, gE, gE_dtype)
+    dt = _dtype_code(H)
+    workspace = _space(workspace, "dust_distill_loss_grad_workspace", H.device, S, T, d, V, K, dt)
+    _same_device(H, E, ids, teacher, lse, student, gloss, gH, gE, workspace)
+    _check(lib().dust_distill_loss_grad(_ptr(H), ld_h, _ptr(E), ld_e, dt, S, T, d, V, _ptr(ids),
+                                        _ptr(teacher), K, float(scale), _ptr(lse), _ptr(student),
+                                        _ptr(gloss), flags, _ptr(gH), d, _ptr(gE),
+                                        _dtype_code(gE), _ptr(workspace), workspace.numel(),
+                                        _stream(None)), "dust_distill_loss_grad")
+    return gH, gE
 
 
 PIPE_XU, PIPE_ALU, PIPE_FMA, PIPE_ISSUE = 0, 1, 2, 3

@@ -31,7 +31,7 @@ cudaError_t ensure_shared_carveout(const void* kernel);
 enum Stage {
     kStageScanLocal, kStageScanCarry, kStageScanFixup, kStageWeight, kStageGemmSimt,
     kStageReduce, kStageGemmTc, kStageFused, kStageNoise, kStageJitter, kStageZero, kStageScore,
-    kStageScatter, kStageForward, kStageCount
+    kStageScatter, kStageForward, kStageNorm, kStageHead, kStageCount
 };
 
 // Brackets the launches issued during its lifetime with profiling events
@@ -215,6 +215,18 @@ size_t scatter_workspace_bytes(int64_t T, int64_t V, int64_t d);
 cudaError_t launch_scatter_gE(const void* g, int g_bf16, const int32_t* ids, int64_t T,
                               int64_t d, int64_t V, float scale, bool accumulate, float* gE,
                               void* workspace, cudaStream_t s);
+
+// Layer norm and its gradients (k_norm.cu): rows of d values with row strides
+// in elements; weight, bias, mean, rstd, gx, gweight and gbias may be null.
+cudaError_t launch_layer_norm(const void* x, int bf16, int64_t ld_x, int64_t T, int64_t d,
+                              const float* weight, const float* bias, float eps, void* y,
+                              int64_t ld_y, float* mean, float* rstd, cudaStream_t s);
+size_t layer_norm_grad_workspace_bytes(int64_t T, int64_t d);
+cudaError_t launch_layer_norm_grad(const void* gy, int64_t ld_gy, const void* x, int64_t ld_x,
+                                   int bf16, int64_t T, int64_t d, const float* weight,
+                                   const float* mean, const float* rstd, bool accumulate, void* gx,
+                                   int64_t ld_gx, float* gweight, float* gbias, float* part,
+                                   cudaStream_t s);
 
 // Fill gW with zeros (T == 0) unless accumulating.
 cudaError_t launch_zero(float* p, int64_t n, cudaStream_t s);
