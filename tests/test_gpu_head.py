@@ -519,3 +519,21 @@ def test_binding_refuses_what_it_would_misread():
     with pytest.raises(dust.DustError):
         big = torch.zeros((20, dust.MAX_TEACHER + 1), device=dev)
         dust.dust_distill_loss(H, E, big.to(torch.int32), big)
+
+
+def test_bounded_wait_that_runs_out_is_reported():
+    """The test hook makes the product's issuing thread wait on a barrier that
+    nothing signals; the kernel gives up after its limit, reports it, and the
+    next call is right."""
+    import torch
+    dev = cuda()
+    H, E, y, gl = _inputs(1, 300, 64, 700, "bf16", dev, seed=20)
+    want = dust.dust_head_loss(H, E, y)
+    assert dust.dust_last_error() == dust.OK
+    dust.lib().dust_debug_inject_timeout(1)
+    dust.dust_head_loss(H, E, y)
+    assert dust.dust_last_error() == dust.ERR_TIMEOUT
+    again = dust.dust_head_loss(H, E, y)
+    assert dust.dust_last_error() == dust.OK
+    for p, q in zip(want, again):
+        assert torch.equal(p, q)

@@ -1,5 +1,8 @@
-// Launch interface of the head's losses and gradients (k_head.cu).
+// Launch interfaces of the head's losses and gradients: k_head.cu (rows,
+// reductions, the order of the steps) and k_head_tc.cu (tensor-core products).
 #pragma once
+#include <cuda.h>
+
 #include "internal.cuh"
 
 namespace dust {
@@ -22,13 +25,85 @@ struct HeadProblem {
     float scale;
 };
 
-size_t head_loss_workspace_bytes(int64_t R, int64_t d, int64_t V, bool distill, bool bf16);
-size_t head_grad_workspace_bytes(int64_t R, int64_t d, int64_t V, bool bf16);
+size_t head_loss_workspace_bytes(const HeadProblem& p);
+size_t head_grad_workspace_bytes(const HeadProblem& p);
 // student: the picked logits [S * T][K] (distillation only).
 cudaError_t launch_head_loss(const HeadProblem& p, float* loss, float* lse, float* student,
                              float* delta, void* ws, cudaStream_t s);
 cudaError_t launch_head_grad(const HeadProblem& p, const float* lse, const float* student,
                              const float* gloss, bool accumulate, void* gH, int64_t ld_gh,
                              void* gE, bool gE_bf16, void* ws, cudaStream_t s);
+
+// ---- tensor-core products (k_head_tc.cu) ----
+
+// A bf16 matrix in 1 plane, or an fp32 one as 3 bf16 planes whose sum it is.
+struct Planes {
+    const void* base;
+    int64_t rows, cols, ld;  // ld in elements, a multiple of 8; base 16-byte aligned
+    int planes;              // planes follow one another, rows * ld elements apart
+};
+
+// One row that takes part in a gradient.
+struct alignas(16) HeadRow {
+    float lse_hi, lse_lo;  // lse log2(e), as a sum of two
+    float weight;          // gloss over the largest |gloss|
+    int32_t target;        // -1 for distillation
+};
+
+struct HeadCounts {      // written on the device by the row pass
+    int32_t rows;        // rows that take part
+    float gmax;          // the largest |gloss| among them (1 if that is 0 or not finite)
+};
+
+constexpr int kHeadTile = 256;  // rows of a CTA pair's tile; its columns too, or half
+constexpr int kHeadBox = 64;    // rows and columns of a TMA box
+
+// Partial softmax sums of one row over half a tile's columns: the largest
+// logit rounded up to a whole number in units of log 2, and the sum of
+// 2^(logit - that).
+struct alignas(8) HeadPart { float m, s; };
+
+struct HeadLogits {
+    Planes H, E;         // [rows][d], [V][d]
+    Planes Hc;           // the rows that take part (gradient), or base null
+    int64_t v0, n;       // columns [v0, v0 + n) of the vocabulary
+    float scale;
+    // forward
+    const int32_t* targets;  // [T], or null
+    int64_t T;
+    HeadPart* part;      // [2 * tiles][ld_part]
+    int64_t ld_part;
+    float* picked;       // [rows] scaled logits of the targets
+    // gradient
+    const HeadCounts* counts;
+    const HeadRow* rows;
+    Planes G;            // [rows rounded up to a tile][n rounded up to a tile]
+};
+
+// Columns of the tiles that the forward takes for these sizes, and so the
+// number of partial sums per row.
+int head_loss_columns(int64_t rows, int64_t V);
+
+cudaError_t launch_head_lse(const HeadLogits& a, cudaStream_t s);
+cudaError_t launch_head_factor(const HeadLogits& a, cudaStream_t s);
+
+// gH += alpha G E_piece and gE_piece = alpha G^T H, one launch.
+struct HeadProducts {
+    Planes G, E, H, Hc;
+    int64_t v0, n;       // vocabulary rows of the piece
+    int64_t d;
+    float scale;
+    const HeadCounts* counts;
+    const int32_t* row_of;  // original row of each row that takes part
+    void* gH;            // or null
+    int64_t ld_gh;
+    bool gh_bf16;
+    float* gh_acc;       // running sums across pieces (null when there is one)
+    bool first, last;    // piece
+    void* gE;            // the piece's rows, or null
+    bool ge_bf16, accumulate;
+};
+size_t head_acc_bytes(int64_t rows, int64_t d);
+cudaError_t launch_head_products(const HeadProducts& a, cudaStream_t s);
 
 }  // namespace dust

@@ -47,6 +47,11 @@ dust_status check_teacher_sizes(int64_t S, int64_t T, int64_t K) {
     return DUST_OK;
 }
 
+// A problem's sizes alone, for the workspace queries.
+HeadProblem sizes(int64_t S, int64_t T, int64_t d, int64_t V, dust_dtype dtype) {
+    return {nullptr, nullptr, d, d, dtype == DUST_BF16, S, T, d, V, {nullptr, nullptr, 1}, 1.0f};
+}
+
 // The checks shared by the four head calls, in one place: sizes, scale,
 // strides, and (for T > 0) the inputs' pointers.
 dust_status check_head(const void* H, int64_t ld_h, const void* E, int64_t ld_e, dust_dtype dtype,
@@ -169,7 +174,7 @@ dust_status dust_head_loss_workspace(size_t* bytes, int64_t S, int64_t T, int64_
     if (!bytes) return DUST_ERR_INVALID_ARG;
     const dust_status st = check_head_sizes(S, T, d, V, dtype);
     if (st != DUST_OK) return st;
-    *bytes = head_loss_workspace_bytes(S * T, d, V, false, dtype == DUST_BF16);
+    *bytes = head_loss_workspace_bytes(sizes(S, T, d, V, dtype));
     return DUST_OK;
 }
 
@@ -182,7 +187,7 @@ dust_status dust_head_loss(const void* H, int64_t ld_h, const void* E, int64_t l
     const HeadProblem p = {H, E, ld_h, ld_e, dtype == DUST_BF16, S, T, d, V,
                            {targets, nullptr, 1}, scale};
     return run_loss(p, loss, lse, nullptr, delta,
-                    head_loss_workspace_bytes(S * T, d, V, false, p.bf16), workspace, ws_bytes,
+                    head_loss_workspace_bytes(p), workspace, ws_bytes,
                     stream);
 }
 
@@ -191,7 +196,7 @@ dust_status dust_head_loss_grad_workspace(size_t* bytes, int64_t S, int64_t T, i
     if (!bytes) return DUST_ERR_INVALID_ARG;
     const dust_status st = check_head_sizes(S, T, d, V, dtype);
     if (st != DUST_OK) return st;
-    *bytes = head_grad_workspace_bytes(S * T, d, V, dtype == DUST_BF16);
+    *bytes = head_grad_workspace_bytes(sizes(S, T, d, V, dtype));
     return DUST_OK;
 }
 
@@ -208,7 +213,7 @@ dust_status dust_head_loss_grad(const void* H, int64_t ld_h, const void* E, int6
     const HeadProblem p = {H, E, ld_h, ld_e, dtype == DUST_BF16, S, T, d, V,
                            {targets, nullptr, 1}, scale};
     return run_grad(p, lse, nullptr, gloss, flags, gH, ld_gh, gE, gE_dtype,
-                    head_grad_workspace_bytes(S * T, d, V, p.bf16), workspace, ws_bytes, stream);
+                    head_grad_workspace_bytes(p), workspace, ws_bytes, stream);
 }
 
 dust_status dust_distill_loss_workspace(size_t* bytes, int64_t S, int64_t T, int64_t d,
@@ -217,7 +222,7 @@ dust_status dust_distill_loss_workspace(size_t* bytes, int64_t S, int64_t T, int
     dust_status st = check_head_sizes(S, T, d, V, dtype);
     if (st == DUST_OK) st = check_teacher_sizes(S, T, K);
     if (st != DUST_OK) return st;
-    *bytes = head_loss_workspace_bytes(S * T, d, V, true, dtype == DUST_BF16);
+    *bytes = head_loss_workspace_bytes(sizes(S, T, d, V, dtype));
     return DUST_OK;
 }
 
@@ -233,7 +238,7 @@ dust_status dust_distill_loss(const void* H, int64_t ld_h, const void* E, int64_
     const HeadProblem p = {H, E, ld_h, ld_e, dtype == DUST_BF16, S, T, d, V,
                            {ids, teacher, K}, scale};
     return run_loss(p, loss, lse, student, delta,
-                    head_loss_workspace_bytes(S * T, d, V, true, p.bf16), workspace, ws_bytes,
+                    head_loss_workspace_bytes(p), workspace, ws_bytes,
                     stream);
 }
 
@@ -243,7 +248,7 @@ dust_status dust_distill_loss_grad_workspace(size_t* bytes, int64_t S, int64_t T
     dust_status st = check_head_sizes(S, T, d, V, dtype);
     if (st == DUST_OK) st = check_teacher_sizes(S, T, K);
     if (st != DUST_OK) return st;
-    *bytes = head_grad_workspace_bytes(S * T, d, V, dtype == DUST_BF16);
+    *bytes = head_grad_workspace_bytes(sizes(S, T, d, V, dtype));
     return DUST_OK;
 }
 
@@ -263,7 +268,7 @@ dust_status dust_distill_loss_grad(const void* H, int64_t ld_h, const void* E, i
     const HeadProblem p = {H, E, ld_h, ld_e, dtype == DUST_BF16, S, T, d, V,
                            {ids, teacher, K}, scale};
     return run_grad(p, lse, student, gloss, flags, gH, ld_gh, gE, gE_dtype,
-                    head_grad_workspace_bytes(S * T, d, V, p.bf16), workspace, ws_bytes, stream);
+                    head_grad_workspace_bytes(p), workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -1,14 +1,22 @@
 // The head's per-token losses and their gradients, over the vocabulary in
 // pieces and without keeping the logits (include/dust.h gives the formulas):
 // softmax cross entropy against a target id, and distillation from a
-// teacher's largest logits.
+// teacher's largest logits. The products are k_head_tc.cu's.
 //
-// One piece of the vocabulary at a time, the logits x = scale H E^T of all
-// rows are formed in the workspace. The forward keeps a running maximum and
-// sum per row (rescaled when the maximum grows) and picks the logits of the
-// target or of the teacher's entries; the backward turns the piece into
-// G = gloss (exp(x - lse) - wanted) in place and adds its part of gH = G E,
-// and its rows of gE = G^T H. The products run on the CUDA cores in fp32.
+// Loss: one launch forms the logits tile by tile and leaves per row a partial
+// maximum and sum for every half tile, and the target's logit; a second one
+// joins them. Distillation picks the K logits of each row by products of its
+// H row with the K rows of E.
+//
+// Gradient, per piece of the vocabulary (a piece's G stays below 2^27
+// values): the logits again as G = weight (exp(x - lse) - wanted) in bf16,
+// then gH += G E and gE = G^T H in one launch. Rows that take no part (no
+// target, no weight) are left out of all products: the others' H rows are
+// moved together first if there are such rows.
+//
+// fp32 inputs, and bf16 ones whose rows do not start on 16 bytes, are first
+// copied into the workspace, as three bf16 planes or padded rows.
+#include <algorithm>
 #include <cmath>
 
 #include "head.cuh"
@@ -19,177 +27,172 @@ namespace {
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-constexpr int64_t kPiece = 4096;  // vocabulary rows a piece
-
-constexpr int kTile = 64, kDepth = 16;
-
-// C[m][n] = scale sum_k A(m, k) B(n, k) (+ C when `add`), operands by strides.
-// A zero in A hides whatever B holds (rows that take no part).
-template <typename TA, typename TB, typename TC>
-__global__ void __launch_bounds__(256)
-    k_head_mm(const TA* __restrict__ A, int64_t am, int64_t ak, const TB* __restrict__ B,
-              int64_t bn, int64_t bk, int64_t M, int64_t N, int64_t K, float scale, TC* C,
-              int64_t ldc, int add) {
-    pdl_wait();
-    pdl_trigger();
-    __shared__ float sa[kDepth][kTile + 1], sb[kDepth][kTile + 1];
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int64_t n0 = static_cast<int64_t>(blockIdx.y) * kTile; n0 < N;
-         n0 += static_cast<int64_t>(gridDim.y) * kTile) {
-        float acc[4][4] = {};
-        for (int64_t k0 = 0; k0 < K; k0 += kDepth) {
-            for (int i = threadIdx.x; i < kTile * kDepth; i += 256) {
-                // The faster index runs along whichever stride is 1.
-                const int ma = ak == 1 ? i / kDepth : i % kTile;
-                const int ka = ak == 1 ? i % kDepth : i / kTile;
-                sa[ka][ma] = m0 + ma < M && k0 + ka < K
-                                 ? to_f(A[(m0 + ma) * am + (k0 + ka) * ak]) : 0.0f;
-                const int nb = bk == 1 ? i / kDepth : i % kTile;
-                const int kb = bk == 1 ? i % kDepth : i / kTile;
-                sb[kb][nb] = n0 + nb < N && k0 + kb < K
-                                 ? to_f(B[(n0 + nb) * bn + (k0 + kb) * bk]) : 0.0f;
-            }
-            __syncthreads();
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-            for (int k = 0; k < kDepth; ++k) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = sa[k][ty * 4 + i];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (a != 0.0f) acc[i][j] = fmaf(a, sb[k][tx * 4 + j], acc[i][j]);
-                }
-            }
-            __syncthreads();
-        }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-                if (m >= M || n >= N) continue;
-                TC* c = C + m * ldc + n;
-                put(c, scale * acc[i][j] + (add ? to_f(*c) : 0.0f));
-            }
-    }
-}
-
-template <typename TA, typename TB, typename TC>
-cudaError_t mm(const TA* A, int64_t am, int64_t ak, const TB* B, int64_t bn, int64_t bk, int64_t M,
-               int64_t N, int64_t K, float scale, TC* C, int64_t ldc, bool add, cudaStream_t s) {
-    const int64_t gx = (M + kTile - 1) / kTile, gy = (N + kTile - 1) / kTile;
-    return launch_pdl(k_head_mm<TA, TB, TC>,
-                      dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy < 65535 ? gy : 65535)),
-                      dim3(256), 0, s, A, am, ak, B, bn, bk, M, N, K, scale, C, ldc, add ? 1 : 0);
-}
-
-__device__ __forceinline__ float block_reduce(float v, bool is_max, float* sh) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const float o = __shfl_xor_sync(0xffffffffu, v, off);
-        v = is_max ? fmaxf(v, o) : v + o;
-    }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = sh[0];
-    for (int i = 1; i < static_cast<int>(blockDim.x >> 5); ++i)
-        v = is_max ? fmaxf(v, sh[i]) : v + sh[i];
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
 }
 
-// One row of a piece: the running maximum and sum, and the picked logits.
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
+__device__ __forceinline__ void report_id(unsigned int* status) {
+    atomicExch(status, 1u /* DUST_ERR_INVALID_ARG */);
+}
+
+// ------------------------------------------------------------------ loss
+
+constexpr int kJoinLanes = 8;  // threads that share a row's partial sums
+
+// A row's partial sums joined, and its cross entropy. Eight threads per row
+// each take every eighth partial; the eight are joined in order.
+__global__ void __launch_bounds__(32 * kJoinLanes)
+    k_head_join(const HeadPart* __restrict__ part, int64_t ld, int n_part, int64_t R, int64_t T,
+                const int32_t* __restrict__ targets, int64_t V,
+                const float* __restrict__ picked, float* loss, float* lse, unsigned int* status) {
+    pdl_wait();
+    pdl_trigger();
+    __shared__ HeadPart sh[kJoinLanes][32];
+    const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    float m = -INFINITY, s = 0.0f;
+    const auto join = [&](const HeadPart& p) {
+        const float nm = fmaxf(m, p.m);
+        // An empty partial has m = -inf and s = 0. NaN sums pass through.
+        const float base = nm == -INFINITY ? 0.0f : nm;
+        s = s * exp2f(m - base) + p.s * exp2f(p.m - base);
+        m = nm;
+    };
+    if (r < R)
+        for (int i = k; i < n_part; i += kJoinLanes) join(part[i * ld + r]);
+    sh[k][lane] = {m, s};
+    __syncthreads();
+    if (k != 0 || r >= R) return;
+    for (int i = 1; i < kJoinLanes; ++i) join(sh[i][lane]);
+    // m is a whole number of powers of two; one rounding for each result.
+    const double l = static_cast<double>(m) * 0.69314718055994530942 +
+                     static_cast<double>(logf(s));
+    lse[r] = static_cast<float>(l);
+    if (!targets) return;
+    const int64_t id = targets[r % T];
+    const bool has = id >= 0 && id < V;
+    if (id >= V) report_id(status);
+    if (loss) loss[r] = has ? static_cast<float>(l - static_cast<double>(picked[r])) : 0.0f;
+}
+
+// student[r][j] = scale <H[r], E[ids[t][j]]>, 0 where the entry is absent.
+// A warp per (row, kPick entries).
+constexpr int kPick = 4;
+
+template <typename TX>
 __global__ void __launch_bounds__(256)
-    k_head_rows(const float* __restrict__ x, int64_t v0, int64_t n, int64_t T, HeadTargets tg,
-                int64_t V, int first, float* __restrict__ run_max, float* __restrict__ run_sum,
-                float* __restrict__ picked, unsigned int* status) {
+    k_head_pick(const TX* __restrict__ H, int64_t ld_h, const TX* __restrict__ E, int64_t ld_e,
+                int64_t R, int64_t T, int64_t d, int64_t V, const int32_t* __restrict__ ids,
+                int64_t K, float scale, int vec, float* __restrict__ student,
+                unsigned int* status) {
     pdl_wait();
     pdl_trigger();
-    __shared__ float sh[8];
-    const int64_t r = blockIdx.x, t = r % T;
-    const float* xr = x + r * n;
+    constexpr int kVec = 16 / sizeof(TX);
+    const int lane = threadIdx.x & 31;
+    const int64_t groups = (K + kPick - 1) / kPick;
+    const int64_t n_warps = static_cast<int64_t>(gridDim.x) * 8;
+    for (int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); w < R * groups;
+         w += n_warps) {
+        const int64_t r = w / groups, j0 = (w - r * groups) * kPick, t = r % T;
+        int32_t id[kPick];
+        float acc[kPick];
+#pragma unroll
+        for (int u = 0; u < kPick; ++u) {
+            id[u] = j0 + u < K ? ids[t * K + j0 + u] : -1;
+            if (id[u] >= V) {
+                if (lane == 0) report_id(status);
+                id[u] = -1;
+            }
+            acc[u] = 0.0f;
+        }
+        const TX* h = H + r * ld_h;
+        if (vec) {
+            for (int64_t c = lane * kVec; c < d; c += 32 * kVec) {
+                const uint4 hv = *reinterpret_cast<const uint4*>(h + c);
+                const TX* hx = reinterpret_cast<const TX*>(&hv);
+#pragma unroll
+                for (int u = 0; u < kPick; ++u) {
+                    if (id[u] < 0) continue;
+                    const uint4 ev = *reinterpret_cast<const uint4*>(E + id[u] * ld_e + c);
+                    const TX* ex = reinterpret_cast<const TX*>(&ev);
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) acc[u] = fmaf(to_f(hx[i]), to_f(ex[i]), acc[u]);
+                }
+            }
+        } else {
+            for (int64_t c = lane; c < d; c += 32) {
+                const float hv = to_f(h[c]);
+#pragma unroll
+                for (int u = 0; u < kPick; ++u)
+                    if (id[u] >= 0) acc[u] = fmaf(hv, to_f(E[id[u] * ld_e + c]), acc[u]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kPick; ++u) {
+            const float x = warp_sum(acc[u]);
+            if (lane == 0 && j0 + u < K) student[r * K + j0 + u] = id[u] >= 0 ? scale * x : 0.0f;
+        }
+    }
+}
+
+// The teacher of a token over its entries present: the largest scaled logit
+// and the logarithm of the sum of exponentials over it; largest -inf where no
+// entry has any probability. Whole warp.
+__device__ __forceinline__ float2 teacher_stats(const int32_t* ids, const float* z, int64_t K,
+                                                int64_t V, float scale, unsigned int* status) {
+    const int lane = threadIdx.x & 31;
     float m = -INFINITY;
-    for (int64_t i = threadIdx.x; i < n; i += blockDim.x) m = fmaxf(m, xr[i]);
-    m = block_reduce(m, true, sh);
-    const float old_m = first ? -INFINITY : run_max[r];
-    const float nm = fmaxf(m, old_m);
-    const float base = nm == -INFINITY ? 0.0f : nm;
+    bool bad = false;
+    for (int64_t j = lane; j < K; j += 32) {
+        const int32_t id = ids[j];
+        bad |= id >= V;
+        if (id >= 0 && id < V) m = fmaxf(m, scale * z[j]);
+    }
+    if (bad && status) report_id(status);
+    m = warp_max(m);
     float q = 0.0f;
-    for (int64_t i = threadIdx.x; i < n; i += blockDim.x) q += expf(xr[i] - base);
-    q = block_reduce(q, false, sh);
-    if (threadIdx.x == 0) {
-        run_max[r] = nm;
-        run_sum[r] = (first ? 0.0f : run_sum[r] * expf(old_m - base)) + q;
+    for (int64_t j = lane; j < K; j += 32) {
+        const int32_t id = ids[j];
+        if (m != -INFINITY && id >= 0 && id < V) q += expf(scale * z[j] - m);
     }
-    for (int64_t j = threadIdx.x; j < tg.K; j += blockDim.x) {
-        const int64_t id = tg.ids[t * tg.K + j];
-        if (id >= V) {
-            if (first) atomicExch(status, 1u /* DUST_ERR_INVALID_ARG */);
-        }
-        if (first && (id < 0 || id >= V)) picked[r * tg.K + j] = 0.0f;
-        if (id >= v0 && id < v0 + n) picked[r * tg.K + j] = xr[id - v0];
-    }
+    q = warp_sum(q);
+    return make_float2(m, logf(q));
 }
 
-// The teacher's largest scaled logit and the sum of exponentials over the
-// entries present; `any` tells whether there is one. Whole block.
-__device__ __forceinline__ void teacher_stats(const HeadTargets& tg, int64_t t, int64_t V,
-                                              float scale, float* sh, float& m, float& sum,
-                                              bool& any) {
-    float a = -INFINITY, have = 0.0f;
-    for (int64_t j = threadIdx.x; j < tg.K; j += blockDim.x) {
-        const int64_t id = tg.ids[t * tg.K + j];
-        if (id < 0 || id >= V) continue;
-        have = 1.0f;
-        a = fmaxf(a, scale * tg.teacher[t * tg.K + j]);
-    }
-    any = block_reduce(have, true, sh) > 0.0f;
-    m = block_reduce(a, true, sh);
-    if (m == -INFINITY) {  // no entry has any probability
-        any = false;
-        m = 0.0f;
-    }
-    float q = 0.0f;
-    for (int64_t j = threadIdx.x; j < tg.K; j += blockDim.x) {
-        const int64_t id = tg.ids[t * tg.K + j];
-        if (id >= 0 && id < V) q += expf(scale * tg.teacher[t * tg.K + j] - m);
-    }
-    sum = block_reduce(q, false, sh);
-}
-
-__global__ void __launch_bounds__(128)
-    k_head_finish(int64_t T, HeadTargets tg, int64_t V, float scale,
-                  const float* __restrict__ run_max, const float* __restrict__ run_sum,
-                  const float* __restrict__ picked, float* loss, float* lse) {
+__global__ void __launch_bounds__(256)
+    k_head_distill(int64_t R, int64_t T, HeadTargets tg, int64_t V, float scale,
+                   const float* __restrict__ lse, const float* __restrict__ student,
+                   float* __restrict__ loss) {
     pdl_wait();
     pdl_trigger();
-    __shared__ float sh[8];
-    const int64_t r = blockIdx.x, t = r % T;
-    const float l = run_max[r] + logf(run_sum[r]);
-    float out = 0.0f;
-    if (!tg.teacher) {
-        const int64_t id = tg.ids[t];
-        if (id >= 0 && id < V) out = l - picked[r];
-    } else {
-        float m, sum;
-        bool any;
-        teacher_stats(tg, t, V, scale, sh, m, sum, any);
-        float a = 0.0f;
-        for (int64_t j = threadIdx.x; any && j < tg.K; j += blockDim.x) {
-            const int64_t id = tg.ids[t * tg.K + j];
-            if (id < 0 || id >= V) continue;
-            const float lq = scale * tg.teacher[t * tg.K + j] - m - logf(sum);
-            const float q = expf(lq);
-            if (q > 0.0f) a += q * (lq - (picked[r * tg.K + j] - l));
-        }
-        out = block_reduce(a, false, sh);
+    const int lane = threadIdx.x & 31;
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (r >= R) return;
+    const int64_t t = r % T;
+    const int32_t* ids = tg.ids + t * tg.K;
+    const float* z = tg.teacher + t * tg.K;
+    const float2 st = teacher_stats(ids, z, tg.K, V, scale, nullptr);
+    const float l = lse[r];
+    float a = 0.0f;
+    for (int64_t j = lane; j < tg.K; j += 32) {
+        const int32_t id = ids[j];
+        if (st.x == -INFINITY || id < 0 || id >= V) continue;
+        const float lq = scale * z[j] - st.x - st.y;
+        const float q = expf(lq);
+        // q = 0 adds nothing, whatever its logarithm.
+        if (q != 0.0f) a = fmaf(q, lq - (student[r * tg.K + j] - l), a);
     }
-    if (threadIdx.x == 0) {
-        lse[r] = l;
-        if (loss) loss[r] = out;
-    }
+    a = warp_sum(a);
+    if (lane == 0) loss[r] = a;
 }
 
 __global__ void __launch_bounds__(256)
@@ -200,156 +203,448 @@ __global__ void __launch_bounds__(256)
     if (i < n) delta[i] = loss[T + i] - loss[i % T];
 }
 
-// A piece of logits into G, in place (block per row).
+// -------------------------------------------------------------- gradients
+
 __global__ void __launch_bounds__(256)
-    k_head_factor(float* x, int64_t v0, int64_t n, int64_t T, HeadTargets tg, int64_t V,
-                  float scale, const float* __restrict__ lse, const float* __restrict__ gloss,
-                  unsigned int* status) {
+    k_head_teacher(int64_t T, HeadTargets tg, int64_t V, float scale, float2* __restrict__ stats,
+                   unsigned int* status) {
     pdl_wait();
     pdl_trigger();
-    __shared__ float sh[8];
-    const int64_t r = blockIdx.x, t = r % T;
-    float* xr = x + r * n;
-    const float g = gloss[r];
-    bool any;
-    float m = 0.0f, sum = 1.0f;
-    if (tg.teacher) {
-        teacher_stats(tg, t, V, scale, sh, m, sum, any);
-    } else {
-        const int64_t id = tg.ids[t];
-        any = id >= 0 && id < V;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (t >= T) return;
+    const float2 st = teacher_stats(tg.ids + t * tg.K, tg.teacher + t * tg.K, tg.K, V, scale,
+                                    status);
+    if ((threadIdx.x & 31) == 0) stats[t] = st;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eRest = static_cast<float>(1.4426950408889634074 - 1.4426950408889634f);
+
+// The rows that take part, in order: which they are, their place (or -1), and
+// what the factor needs of each; and the largest |gloss|. One CTA: warp w
+// takes the w-th part of the rows, 32 at a time, twice (count, then write).
+__global__ void __launch_bounds__(1024)
+    k_head_live(int64_t R, int64_t T, const int32_t* __restrict__ targets,
+                const float2* __restrict__ teacher, int64_t V, const float* __restrict__ lse,
+                const float* __restrict__ gloss, HeadCounts* counts, HeadRow* __restrict__ rows,
+                int32_t* __restrict__ row_of, int32_t* __restrict__ place, unsigned int* status) {
+    pdl_wait();
+    pdl_trigger();
+    __shared__ int s_n[32];
+    __shared__ float s_g[32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t per = (R + 1023) / 1024 * 32;
+    const int64_t r0 = w * per, r1 = r0 + per < R ? r0 + per : R;
+    const auto wanted = [&](int64_t r, int32_t& id) {
+        if (r >= r1) return false;
+        const int64_t t = r % T;
+        if (teacher) {
+            id = -1;
+            return teacher[t].x != -INFINITY;
+        }
+        id = targets[t];
+        return id >= 0 && id < V;
+    };
+    int n = 0;
+    float g = 0.0f;
+    bool bad = false;
+#pragma unroll 4
+    for (int64_t b = r0; b < r1; b += 32) {
+        int32_t id = -1;
+        const bool has = wanted(b + lane, id);
+        bad |= id >= V;
+        const float gl = b + lane < r1 ? gloss[b + lane] : 0.0f;
+        const bool live = has && gl != 0.0f;
+        if (live) g = fmaxf(g, fabsf(gl));
+        n += __popc(__ballot_sync(0xffffffffu, live));
     }
-    if (v0 == 0)
-        for (int64_t j = threadIdx.x; j < tg.K; j += blockDim.x)
-            if (tg.ids[t * tg.K + j] >= V) atomicExch(status, 1u /* DUST_ERR_INVALID_ARG */);
-    const bool live = any && g != 0.0f;
-    for (int64_t i = threadIdx.x; i < n; i += blockDim.x)
-        xr[i] = live ? g * expf(xr[i] - lse[r]) : 0.0f;
+    if (bad) report_id(status);
+    g = warp_max(g);
+    if (lane == 0) {
+        s_n[w] = n;
+        s_g[w] = g;
+    }
     __syncthreads();
-    if (!live || threadIdx.x != 0) return;
-    for (int64_t j = 0; j < tg.K; ++j) {
-        const int64_t id = tg.ids[t * tg.K + j];
-        if (id < v0 || id >= v0 + n) continue;
-        const float q = tg.teacher ? expf(scale * tg.teacher[t * tg.K + j] - m - logf(sum)) : 1.0f;
-        xr[id - v0] -= g * q;
+    int at = 0, all = 0;
+    g = 0.0f;
+    for (int i = 0; i < 32; ++i) {
+        if (i < w) at += s_n[i];
+        all += s_n[i];
+        g = fmaxf(g, s_g[i]);
+    }
+    if (!(g > 0.0f) || g == INFINITY) g = 1.0f;
+    if (threadIdx.x == 0) {
+        counts->rows = all;
+        counts->gmax = g;
+    }
+#pragma unroll 4
+    for (int64_t b = r0; b < r1; b += 32) {
+        const int64_t r = b + lane;
+        int32_t id = -1;
+        const bool has = wanted(r, id);
+        const float gl = r < r1 ? gloss[r] : 0.0f;
+        const bool live = has && gl != 0.0f;
+        const unsigned int mask = __ballot_sync(0xffffffffu, live);
+        const int i = at + __popc(mask & ((1u << lane) - 1u));
+        if (live) {
+            const float l = lse[r];
+            HeadRow h;
+            h.lse_hi = l * kLog2e;
+            h.lse_lo = fmaf(l, kLog2e, -h.lse_hi) + l * kLog2eRest;
+            h.weight = gl / g;
+            h.target = id;
+            rows[i] = h;
+            row_of[i] = static_cast<int32_t>(r);
+        }
+        if (r < r1) place[r] = live ? i : -1;
+        at += __popc(mask);
     }
 }
 
-template <typename TX>
+// Rows into the workspace as bf16 (one plane) or as three bf16 planes, zero
+// from column d to dp. With counts, row i is the i-th that takes part, rows
+// up to the next multiple of 64 are zeroed, and rows of `zero` (gH) that take
+// no part are cleared; if all take part and `only_if_some` is set there is
+// nothing to do.
+template <typename TX, int PLANES>
 __global__ void __launch_bounds__(256)
-    k_head_cast(const float* __restrict__ src, int64_t R, int64_t d, TX* dst, int64_t ld) {
+    k_head_pack(const TX* __restrict__ src, int64_t ld, int64_t n, int64_t d, int64_t dp, int vec,
+                __nv_bfloat16* __restrict__ dst, const HeadCounts* counts,
+                const int32_t* __restrict__ row_of, int only_if_some,
+                const int32_t* __restrict__ place, TX* zero, int64_t ld_zero) {
     pdl_wait();
     pdl_trigger();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i < R * d) put(dst + (i / d) * ld + i % d, src[i]);
+    const int64_t live = counts ? counts->rows : n;
+    if (only_if_some && live == n) return;
+    int64_t end = n;
+    if (counts) {
+        end = (live + 63) / 64 * 64;
+        if (end > n) end = n;
+    }
+    const int lane = threadIdx.x & 31;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < n;
+         i += static_cast<int64_t>(gridDim.x) * 8) {
+        if (zero && place[i] < 0)
+            for (int64_t c = lane; c < d; c += 32) zero[i * ld_zero + c] = TX(0.0f);
+        if (i >= end || !dst) continue;
+        const TX* s = i < live ? src + (row_of ? row_of[i] : i) * ld : nullptr;
+        __nv_bfloat16* o = dst + i * dp;
+        for (int64_t c = lane * 8; c < dp; c += 256) {
+            float v[8];
+            if (s && vec && c + 8 <= d) {
+#pragma unroll
+                for (int u = 0; u < static_cast<int>(sizeof(TX)) / 2; ++u) {
+                    const uint4 x = reinterpret_cast<const uint4*>(s + c)[u];
+                    const TX* xs = reinterpret_cast<const TX*>(&x);
+                    constexpr int per = 16 / sizeof(TX);
+#pragma unroll
+                    for (int k = 0; k < per; ++k) v[u * per + k] = to_f(xs[k]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = s && c + k < d ? to_f(s[c + k]) : 0.0f;
+            }
+#pragma unroll
+            for (int p = 0; p < PLANES; ++p) {
+                __nv_bfloat16 b[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    b[k] = __float2bfloat16_rn(v[k]);
+                    // What this plane leaves (nothing of an infinity).
+                    v[k] = __builtin_isinf(v[k]) ? 0.0f : v[k] - __bfloat162float(b[k]);
+                }
+                *reinterpret_cast<uint4*>(o + p * n * dp + c) = *reinterpret_cast<const uint4*>(b);
+            }
+        }
+    }
 }
+
+// Distillation: G at the teacher's entries of a piece, weight (exp(x - lse) -
+// q), with q summed over the entries of the same id. A warp per row; the
+// row's ids and probabilities in shared memory.
+template <int PLANES>
+__global__ void __launch_bounds__(256)
+    k_head_patch(const HeadCounts* __restrict__ counts, const HeadRow* __restrict__ rows,
+                 const int32_t* __restrict__ row_of, int64_t T, HeadTargets tg, float scale,
+                 const float2* __restrict__ teacher, const float* __restrict__ student, int64_t v0,
+                 int64_t n, __nv_bfloat16* __restrict__ G, int64_t ld_g, int64_t plane) {
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ unsigned char patch_smem[];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int K = static_cast<int>(tg.K);
+    int32_t* s_id = reinterpret_cast<int32_t*>(patch_smem) + w * 2 * K;
+    float* s_q = reinterpret_cast<float*>(s_id + K);
+    const int live = counts->rows;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * warps + w; i < live;
+         i += static_cast<int64_t>(gridDim.x) * warps) {
+        const int64_t r = row_of[i], t = r % T;
+        const float2 st = teacher[t];
+        const HeadRow h = rows[i];
+        __syncwarp();
+        for (int j = lane; j < K; j += 32) {
+            const int64_t id = tg.ids[t * K + j];
+            const bool in = id >= v0 && id < v0 + n;
+            s_id[j] = in ? static_cast<int32_t>(id - v0) : -1;
+            s_q[j] = in ? expf(scale * tg.teacher[t * K + j] - st.x - st.y) : 0.0f;
+        }
+        __syncwarp();
+        for (int j = lane; j < K; j += 32) {
+            const int32_t id = s_id[j];
+            if (id < 0) continue;
+            float q = 0.0f;
+            bool first = true;
+            for (int u = 0; u < K; ++u) {
+                if (s_id[u] != id) continue;
+                first = first && u >= j;
+                q += s_q[u];
+            }
+            if (!first) continue;
+            const float x = student[r * K + j];
+            const float p = exp2f(fmaf(x, kLog2e, -h.lse_hi) - h.lse_lo + x * kLog2eRest);
+            float g = h.weight * (p - q);
+            __nv_bfloat16* o = G + i * ld_g + id;
+#pragma unroll
+            for (int u = 0; u < PLANES; ++u) {
+                const __nv_bfloat16 b = __float2bfloat16_rn(g);
+                o[u * plane] = b;
+                g -= __bfloat162float(b);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host
 
 size_t a256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+int64_t up(int64_t x, int64_t by) { return (x + by - 1) / by * by; }
 
-struct Space {
-    float *x, *run_max, *run_sum, *picked, *loss, *gh;
+// Whether TMA can read the rows where they lie.
+bool direct(const void* p, int64_t ld, bool bf16) {
+    return bf16 && ld % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+}
+
+// Vocabulary rows of a piece: whole tiles, G at most 2^27 values over its
+// planes (256 MB), so that a large vocabulary's G is never whole.
+int64_t piece_of(int64_t R, int64_t V, int planes) {
+    const int64_t cap = (int64_t(1) << 27) / (up(R, kHeadTile) * planes);
+    const int64_t whole = up(V, kHeadTile);
+    int64_t n = std::min(whole, std::max<int64_t>(cap / kHeadTile * kHeadTile, 4 * kHeadTile));
+    // Pieces of about one size.
+    const int64_t pieces = (whole + n - 1) / n;
+    return up((whole + pieces - 1) / pieces, kHeadTile);
+}
+
+struct Carver {
+    unsigned char* base;
+    size_t at = 0;
+    template <typename T> T* take(int64_t n) {
+        T* p = base ? reinterpret_cast<T*>(base + at) : nullptr;
+        at += a256(sizeof(T) * static_cast<size_t>(n));
+        return p;
+    }
+};
+
+struct LossSpace {
+    __nv_bfloat16 *h, *e;
+    HeadPart* part;
+    float *picked, *loss;
     size_t total;
 };
 
-Space carve(void* ws, int64_t R, int64_t d, int64_t V, int64_t K, bool grad) {
-    Space w = {};
-    unsigned char* p = static_cast<unsigned char*>(ws);
-    size_t at = 0;
-    auto take = [&](int64_t n) {
-        float* q = ws ? reinterpret_cast<float*>(p + at) : nullptr;
-        at += a256(sizeof(float) * static_cast<size_t>(n));
-        return q;
-    };
-    w.x = take(R * (V < kPiece ? V : kPiece));
-    if (grad) {
-        w.gh = take(R * d);
-    } else {
-        w.run_max = take(R);
-        w.run_sum = take(R);
-        w.picked = take(K);  // cross entropy: R logits
-        w.loss = take(R);
-    }
-    w.total = at;
+// H and E are sized as if copied, wherever they lie: the size must not
+// depend on addresses. Only what a call needs is touched.
+LossSpace carve_loss(void* ws, const HeadProblem& p) {
+    const int64_t R = p.S * p.T, dp = up(p.d, 8), planes = p.bf16 ? 1 : 3;
+    Carver c{static_cast<unsigned char*>(ws)};
+    LossSpace w;
+    const int64_t slots = 2 * ((p.V + 127) / 128);
+    w.part = c.take<HeadPart>(slots * up(R, 32));
+    w.picked = c.take<float>(R);
+    w.loss = c.take<float>(R);
+    w.h = c.take<__nv_bfloat16>(planes * R * dp);
+    w.e = c.take<__nv_bfloat16>(planes * p.V * dp);
+    w.total = c.at;
     return w;
 }
+
+struct GradSpace {
+    HeadCounts* counts;
+    HeadRow* rows;
+    int32_t *row_of, *place;
+    float2* teacher;
+    __nv_bfloat16 *h, *e, *g;
+    float* acc;
+    int64_t piece;
+    size_t total;
+};
+
+GradSpace carve_grad(void* ws, const HeadProblem& p) {
+    const int64_t R = p.S * p.T, dp = up(p.d, 8), planes = p.bf16 ? 1 : 3;
+    Carver c{static_cast<unsigned char*>(ws)};
+    GradSpace w;
+    w.piece = piece_of(R, p.V, static_cast<int>(planes));
+    w.counts = c.take<HeadCounts>(1);
+    w.rows = c.take<HeadRow>(R);
+    w.row_of = c.take<int32_t>(R);
+    w.place = c.take<int32_t>(R);
+    w.teacher = c.take<float2>(p.T);
+    w.acc = reinterpret_cast<float*>(
+        c.take<unsigned char>(w.piece < p.V ? static_cast<int64_t>(head_acc_bytes(R, p.d)) : 0));
+    w.g = c.take<__nv_bfloat16>(planes * up(R, kHeadTile) * w.piece);
+    w.h = c.take<__nv_bfloat16>(planes * R * dp);
+    w.e = c.take<__nv_bfloat16>(planes * p.V * dp);
+    w.total = c.at;
+    return w;
+}
+
+template <typename TX>
+cudaError_t pack(const void* src, int64_t ld, int64_t n, int64_t d, __nv_bfloat16* dst,
+                 const HeadCounts* counts, const int32_t* row_of, bool only_if_some,
+                 const int32_t* place, void* zero, int64_t ld_zero, cudaStream_t s) {
+    constexpr int P = sizeof(TX) == 2 ? 1 : 3;
+    const int vec = ld * sizeof(TX) % 16 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0;
+    const int64_t blocks = std::min<int64_t>((n + 7) / 8, 152 * 8);
+    return launch_pdl(k_head_pack<TX, P>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s,
+                      static_cast<const TX*>(src), ld, n, d, up(d, 8), vec, dst, counts, row_of,
+                      only_if_some ? 1 : 0, place, static_cast<TX*>(zero), ld_zero);
+}
+
+// The matrix as an operand: where it lies, or copied.
+template <typename TX>
+cudaError_t operand(const void* src, int64_t ld, int64_t n, int64_t d, __nv_bfloat16* copy,
+                    Planes* out, cudaStream_t s) {
+    constexpr bool bf16 = sizeof(TX) == 2;
+    if (direct(src, ld, bf16)) {
+        *out = {src, n, d, ld, 1};
+        return cudaSuccess;
+    }
+    *out = {copy, n, up(d, 8), up(d, 8), bf16 ? 1 : 3};
+    return pack<TX>(src, ld, n, d, copy, nullptr, nullptr, false, nullptr, nullptr, 0, s);
+}
+
+unsigned grid_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); }
+
+#define DUST_TRY(x)                             \
+    do {                                        \
+        const cudaError_t e_ = (x);             \
+        if (e_ != cudaSuccess) return e_;       \
+    } while (0)
 
 template <typename TX>
 cudaError_t loss_typed(const HeadProblem& p, float* loss, float* lse, float* student, float* delta,
                        void* ws, cudaStream_t s) {
     const int64_t R = p.S * p.T;
     const bool distill = p.tg.teacher != nullptr;
-    Space w = carve(ws, R, p.d, p.V, distill ? 0 : R, false);
-    float* picked = distill ? student : w.picked;
+    const LossSpace w = carve_loss(ws, p);
     if (!loss && delta) loss = w.loss;
     unsigned int* st = status_word();
     if (!st) return cudaErrorUnknown;
-    cudaError_t e;
-    for (int64_t v0 = 0; v0 < p.V; v0 += kPiece) {
-        const int64_t n = p.V - v0 < kPiece ? p.V - v0 : kPiece;
-        e = mm(static_cast<const TX*>(p.H), p.ld_h, int64_t(1),
-               static_cast<const TX*>(p.E) + v0 * p.ld_e, p.ld_e, int64_t(1), R, n, p.d, p.scale,
-               w.x, n, false, s);
-        if (e != cudaSuccess) return e;
-        e = launch_pdl(k_head_rows, dim3(static_cast<unsigned>(R)), dim3(256), 0, s, w.x, v0, n,
-                       p.T, p.tg, p.V, v0 == 0 ? 1 : 0, w.run_max, w.run_sum, picked, st);
-        if (e != cudaSuccess) return e;
+    HeadLogits a = {};
+    DUST_TRY(operand<TX>(p.H, p.ld_h, R, p.d, w.h, &a.H, s));
+    DUST_TRY(operand<TX>(p.E, p.ld_e, p.V, p.d, w.e, &a.E, s));
+    a.n = p.V;
+    a.scale = p.scale;
+    a.targets = distill ? nullptr : p.tg.ids;
+    a.T = p.T;
+    a.part = w.part;
+    a.ld_part = up(R, 32);
+    a.picked = w.picked;
+    DUST_TRY(launch_head_lse(a, s));
+    const int bn = head_loss_columns(R, p.V);
+    DUST_TRY(launch_pdl(k_head_join, dim3(grid_of(R, 32)), dim3(32 * kJoinLanes), 0, s, w.part,
+                        a.ld_part, static_cast<int>(2 * ((p.V + bn - 1) / bn)), R, p.T, a.targets,
+                        p.V, w.picked, loss, lse, st));
+    if (distill) {
+        const int vec = p.d % (16 / sizeof(TX)) == 0 && p.ld_h * sizeof(TX) % 16 == 0 &&
+                        p.ld_e * sizeof(TX) % 16 == 0 &&
+                        (reinterpret_cast<uintptr_t>(p.H) | reinterpret_cast<uintptr_t>(p.E)) % 16 == 0;
+        const int64_t work = R * ((p.tg.K + kPick - 1) / kPick);
+        DUST_TRY(launch_pdl(k_head_pick<TX>,
+                            dim3(static_cast<unsigned>(std::min<int64_t>((work + 7) / 8, 152 * 64))),
+                            dim3(256), 0, s, static_cast<const TX*>(p.H), p.ld_h,
+                            static_cast<const TX*>(p.E), p.ld_e, R, p.T, p.d, p.V, p.tg.ids,
+                            p.tg.K, p.scale, vec, student, st));
+        if (loss)
+            DUST_TRY(launch_pdl(k_head_distill, dim3(grid_of(R, 8)), dim3(256), 0, s, R, p.T, p.tg,
+                                p.V, p.scale, lse, student, loss));
     }
-    e = launch_pdl(k_head_finish, dim3(static_cast<unsigned>(R)), dim3(128), 0, s, p.T, p.tg, p.V,
-                   p.scale, w.run_max, w.run_sum, picked, loss, lse);
-    if (e != cudaSuccess || !delta || p.S < 2) return e;
-    const int64_t n = R - p.T;
-    return launch_pdl(k_head_changes, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0,
-                      s, loss, p.T, n, delta);
+    if (!delta || p.S < 2) return cudaSuccess;
+    return launch_pdl(k_head_changes, dim3(grid_of(R - p.T, 256)), dim3(256), 0, s, loss, p.T,
+                      R - p.T, delta);
 }
 
 template <typename TX>
-cudaError_t grad_typed(const HeadProblem& p, const float* lse, const float* gloss, bool accumulate,
-                       void* gH, int64_t ld_gh, void* gE, bool gE_bf16, void* ws,
-                       cudaStream_t s) {
-    const int64_t R = p.S * p.T;
-    Space w = carve(ws, R, p.d, p.V, 0, true);
-    const TX* H = static_cast<const TX*>(p.H);
+cudaError_t grad_typed(const HeadProblem& p, const float* lse, const float* student,
+                       const float* gloss, bool accumulate, void* gH, int64_t ld_gh, void* gE,
+                       bool gE_bf16, void* ws, cudaStream_t s) {
+    constexpr bool bf16 = sizeof(TX) == 2;
+    const int64_t R = p.S * p.T, planes = bf16 ? 1 : 3;
+    const bool distill = p.tg.teacher != nullptr;
+    const GradSpace w = carve_grad(ws, p);
     unsigned int* st = status_word();
     if (!st) return cudaErrorUnknown;
-    cudaError_t e = cudaSuccess;
-    for (int64_t v0 = 0; v0 < p.V; v0 += kPiece) {
-        const int64_t n = p.V - v0 < kPiece ? p.V - v0 : kPiece;
-        const TX* E = static_cast<const TX*>(p.E) + v0 * p.ld_e;
-        e = mm(H, p.ld_h, int64_t(1), E, p.ld_e, int64_t(1), R, n, p.d, p.scale, w.x, n, false, s);
-        if (e != cudaSuccess) return e;
-        e = launch_pdl(k_head_factor, dim3(static_cast<unsigned>(R)), dim3(256), 0, s, w.x, v0, n,
-                       p.T, p.tg, p.V, p.scale, lse, gloss, st);
-        if (e != cudaSuccess) return e;
-        if (gH) {
-            e = mm(w.x, n, int64_t(1), E, int64_t(1), p.ld_e, R, p.d, n, p.scale, w.gh, p.d,
-                   v0 > 0, s);
-            if (e != cudaSuccess) return e;
+    if (distill)
+        DUST_TRY(launch_pdl(k_head_teacher, dim3(grid_of(p.T, 8)), dim3(256), 0, s, p.T, p.tg, p.V,
+                            p.scale, w.teacher, st));
+    DUST_TRY(launch_pdl(k_head_live, dim3(1), dim3(1024), 0, s, R, p.T,
+                        distill ? nullptr : p.tg.ids, distill ? w.teacher : nullptr, p.V, lse,
+                        gloss, w.counts, w.rows, w.row_of, w.place, st));
+    HeadLogits a = {};
+    const bool in_place = direct(p.H, p.ld_h, bf16);
+    const Planes copy = {w.h, R, up(p.d, 8), up(p.d, 8), static_cast<int>(planes)};
+    a.H = in_place ? Planes{p.H, R, p.d, p.ld_h, 1} : copy;
+    if (in_place) a.Hc = copy;
+    DUST_TRY(pack<TX>(p.H, p.ld_h, R, p.d, w.h, w.counts, w.row_of, in_place, w.place, gH, ld_gh,
+                      s));
+    DUST_TRY(operand<TX>(p.E, p.ld_e, p.V, p.d, w.e, &a.E, s));
+    a.scale = p.scale;
+    a.counts = w.counts;
+    a.rows = w.rows;
+    const int64_t g_rows = up(R, kHeadTile);
+    a.G = {w.g, g_rows, w.piece, w.piece, static_cast<int>(planes)};
+    for (int64_t v0 = 0; v0 < p.V; v0 += w.piece) {
+        const int64_t n = std::min(w.piece, p.V - v0);
+        a.v0 = v0;
+        a.n = n;
+        DUST_TRY(launch_head_factor(a, s));
+        if (distill) {
+            const int warps = p.tg.K <= 512 ? 8 : 4;
+            const size_t smem = static_cast<size_t>(warps) * 8 * static_cast<size_t>(p.tg.K);
+            const unsigned blocks = std::min(grid_of(R, warps), 152u * 8u);
+            DUST_TRY(launch_pdl(k_head_patch<bf16 ? 1 : 3>, dim3(blocks), dim3(32 * warps), smem, s,
+                                w.counts, w.rows, w.row_of, p.T, p.tg, p.scale, w.teacher, student,
+                                v0, n, w.g, w.piece, g_rows * w.piece));
         }
-        if (!gE) continue;
-        if (gE_bf16)
-            e = mm(w.x, int64_t(1), n, H, int64_t(1), p.ld_h, n, p.d, R, p.scale,
-                   static_cast<__nv_bfloat16*>(gE) + v0 * p.d, p.d, false, s);
-        else
-            e = mm(w.x, int64_t(1), n, H, int64_t(1), p.ld_h, n, p.d, R, p.scale,
-                   static_cast<float*>(gE) + v0 * p.d, p.d, accumulate, s);
-        if (e != cudaSuccess) return e;
+        HeadProducts m = {};
+        m.G = a.G;
+        m.E = a.E;
+        m.H = a.H;
+        m.Hc = a.Hc;
+        m.v0 = v0;
+        m.n = n;
+        m.d = p.d;
+        m.scale = p.scale;
+        m.counts = w.counts;
+        m.row_of = w.row_of;
+        m.gH = gH;
+        m.ld_gh = ld_gh;
+        m.gh_bf16 = bf16;
+        m.gh_acc = w.piece < p.V ? w.acc : nullptr;
+        m.first = v0 == 0;
+        m.last = v0 + n == p.V;
+        m.gE = gE ? static_cast<unsigned char*>(gE) + v0 * p.d * (gE_bf16 ? 2 : 4) : nullptr;
+        m.ge_bf16 = gE_bf16;
+        m.accumulate = accumulate;
+        DUST_TRY(launch_head_products(m, s));
     }
-    if (!gH) return e;
-    return launch_pdl(k_head_cast<TX>, dim3(static_cast<unsigned>((R * p.d + 255) / 256)),
-                      dim3(256), 0, s, w.gh, R, p.d, static_cast<TX*>(gH), ld_gh);
+    return cudaSuccess;
 }
 
 }  // namespace
 
-size_t head_loss_workspace_bytes(int64_t R, int64_t d, int64_t V, bool distill, bool bf16) {
-    (void)bf16;
-    return carve(nullptr, R, d, V, distill ? 0 : R, false).total;
-}
-
-size_t head_grad_workspace_bytes(int64_t R, int64_t d, int64_t V, bool bf16) {
-    (void)bf16;
-    return carve(nullptr, R, d, V, 0, true).total;
-}
+size_t head_loss_workspace_bytes(const HeadProblem& p) { return carve_loss(nullptr, p).total; }
+size_t head_grad_workspace_bytes(const HeadProblem& p) { return carve_grad(nullptr, p).total; }
 
 cudaError_t launch_head_loss(const HeadProblem& p, float* loss, float* lse, float* student,
                              float* delta, void* ws, cudaStream_t s) {
@@ -361,11 +656,11 @@ cudaError_t launch_head_loss(const HeadProblem& p, float* loss, float* lse, floa
 cudaError_t launch_head_grad(const HeadProblem& p, const float* lse, const float* student,
                              const float* gloss, bool accumulate, void* gH, int64_t ld_gh,
                              void* gE, bool gE_bf16, void* ws, cudaStream_t s) {
-    (void)student;
     ProfScope ps(kStageHead, s);
-    return p.bf16 ? grad_typed<__nv_bfloat16>(p, lse, gloss, accumulate, gH, ld_gh, gE, gE_bf16,
-                                              ws, s)
-                  : grad_typed<float>(p, lse, gloss, accumulate, gH, ld_gh, gE, gE_bf16, ws, s);
+    return p.bf16 ? grad_typed<__nv_bfloat16>(p, lse, student, gloss, accumulate, gH, ld_gh, gE,
+                                              gE_bf16, ws, s)
+                  : grad_typed<float>(p, lse, student, gloss, accumulate, gH, ld_gh, gE, gE_bf16,
+                                      ws, s);
 }
 
 }  // namespace dust
