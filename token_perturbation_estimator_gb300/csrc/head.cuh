@@ -71,7 +71,7 @@ struct HeadLogits {
     // forward
     const int32_t* targets;  // [T], or null
     int64_t T;
-    HeadPart* part;      // [2 * tiles][ld_part]
+    HeadPart* part;      // [2 * column tiles][ld_part]
     int64_t ld_part;
     float* picked;       // [rows] scaled logits of the targets
     // gradient
@@ -80,14 +80,18 @@ struct HeadLogits {
     Planes G;            // [rows rounded up to a tile][n rounded up to a tile]
 };
 
-// Columns of the tiles that the forward takes for these sizes, and so the
-// number of partial sums per row.
+// Columns of the tiles that the forward takes for these sizes.
 int head_loss_columns(int64_t rows, int64_t V);
 
 cudaError_t launch_head_lse(const HeadLogits& a, cudaStream_t s);
 cudaError_t launch_head_factor(const HeadLogits& a, cudaStream_t s);
 
-// gH += alpha G E_piece and gE_piece = alpha G^T H, one launch.
+// Slices of the summed dimension of each product, for the sizes of one piece.
+struct HeadCuts { int gh, ge; };
+HeadCuts head_cuts(int64_t rows, int64_t n, int64_t d, int planes, bool gh, bool ge);
+
+// gH += alpha G E_piece and gE_piece = alpha G^T H, one launch; slices' sums
+// are added up by one more.
 struct HeadProducts {
     Planes G, E, H, Hc;
     int64_t v0, n;       // vocabulary rows of the piece
@@ -98,12 +102,15 @@ struct HeadProducts {
     void* gH;            // or null
     int64_t ld_gh;
     bool gh_bf16;
-    float* gh_acc;       // running sums across pieces (null when there is one)
+    float* gh_acc;       // partial sums: across pieces, and of slices (else null)
+    float* ge_acc;       // of slices (else null)
+    HeadCuts cuts;
     bool first, last;    // piece
     void* gE;            // the piece's rows, or null
     bool ge_bf16, accumulate;
 };
-size_t head_acc_bytes(int64_t rows, int64_t d);
+// Partial sums of a product of m rows and d columns.
+int64_t head_acc_floats(int64_t m, int64_t d, int cut);
 cudaError_t launch_head_products(const HeadProducts& a, cudaStream_t s);
 
 }  // namespace dust

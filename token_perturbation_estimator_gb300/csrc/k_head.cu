@@ -40,6 +40,22 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The same shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ int2 read_at_rank(const int2* p, int rank) {
+    uint32_t at;
+    int2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(at)
+                 : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void report_id(unsigned int* status) {
     atomicExch(status, 1u /* DUST_ERR_INVALID_ARG */);
 }
@@ -220,42 +236,57 @@ __global__ void __launch_bounds__(256)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eRest = static_cast<float>(1.4426950408889634074 - 1.4426950408889634f);
 
-// The rows that take part, in order: which they are, their place (or -1), and
-// what the factor needs of each; and the largest |gloss|. One CTA: warp w
-// takes the w-th part of the rows, 32 at a time, twice (count, then write).
-__global__ void __launch_bounds__(1024)
-    k_head_live(int64_t R, int64_t T, const int32_t* __restrict__ targets,
-                const float2* __restrict__ teacher, int64_t V, const float* __restrict__ lse,
-                const float* __restrict__ gloss, HeadCounts* counts, HeadRow* __restrict__ rows,
-                int32_t* __restrict__ row_of, int32_t* __restrict__ place, unsigned int* status) {
-    pdl_wait();
-    pdl_trigger();
+// The rows that take part, in order: k_head_live writes which they are, their
+// places (or -1), and what the factor needs of each; and the largest |gloss|.
+// One cluster of eight CTAs: CTA c takes the c-th part of the rows, 1024 at a
+// time, twice: counting, then, with the counts of the CTAs before it (read
+// through the cluster's shared memory), writing.
+constexpr int kLiveCtas = 8, kLiveThreads = 1024;
+
+struct LiveRows {
+    int32_t R, T;              // rows, tokens
+    int64_t V;
+    const int32_t* targets;    // or null
+    const float2* teacher;
+    const float* gloss;
+
+    // Whether row r takes part; its target and weight.
+    __device__ __forceinline__ bool wanted(int64_t r, int32_t& id, float& g) const {
+        id = -1;
+        g = 0.0f;
+        if (r >= R) return false;
+        const uint32_t t = R == T ? static_cast<uint32_t>(r)
+                                  : static_cast<uint32_t>(r) % static_cast<uint32_t>(T);
+        g = gloss[r];
+        if (!targets) return teacher[t].x != -INFINITY && g != 0.0f;
+        id = targets[t];
+        return id >= 0 && id < V && g != 0.0f;
+    }
+};
+
+__global__ void __cluster_dims__(kLiveCtas, 1, 1) __launch_bounds__(kLiveThreads, 1)
+    k_head_live(LiveRows a, const float* __restrict__ lse, HeadCounts* counts,
+                HeadRow* __restrict__ rows, int32_t* __restrict__ row_of,
+                int32_t* __restrict__ place, unsigned int* status) {
     __shared__ int s_n[32];
     __shared__ float s_g[32];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t per = (R + 1023) / 1024 * 32;
-    const int64_t r0 = w * per, r1 = r0 + per < R ? r0 + per : R;
-    const auto wanted = [&](int64_t r, int32_t& id) {
-        if (r >= r1) return false;
-        const int64_t t = r % T;
-        if (teacher) {
-            id = -1;
-            return teacher[t].x != -INFINITY;
-        }
-        id = targets[t];
-        return id >= 0 && id < V;
-    };
+    __shared__ int2 s_cta;  // this CTA's rows that take part; bits of its largest |gloss|
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, cta = blockIdx.x;
+    // Parts of whole thousands of rows, each warp's rows in one run of it.
+    const int32_t per = (a.R + kLiveCtas * kLiveThreads - 1) / (kLiveCtas * kLiveThreads);
+    const int64_t r0 = (static_cast<int64_t>(cta) * kLiveThreads + w * 32) * per;
     int n = 0;
     float g = 0.0f;
     bool bad = false;
 #pragma unroll 4
-    for (int64_t b = r0; b < r1; b += 32) {
-        int32_t id = -1;
-        const bool has = wanted(b + lane, id);
-        bad |= id >= V;
-        const float gl = b + lane < r1 ? gloss[b + lane] : 0.0f;
-        const bool live = has && gl != 0.0f;
-        if (live) g = fmaxf(g, fabsf(gl));
+    for (int32_t i = 0; i < per; ++i) {
+        int32_t id;
+        float gl;
+        const bool live = a.wanted(r0 + i * 32 + lane, id, gl);
+        bad |= id >= a.V;
+        if (live) g = fmaxf(g, fabsf(gl));  // NaN is passed over
         n += __popc(__ballot_sync(0xffffffffu, live));
     }
     if (bad) report_id(status);
@@ -265,39 +296,45 @@ __global__ void __launch_bounds__(1024)
         s_g[w] = g;
     }
     __syncthreads();
-    int at = 0, all = 0;
+    int at = __reduce_add_sync(0xffffffffu, lane < w ? s_n[lane] : 0);
+    if (w == 0) {
+        const int all = __reduce_add_sync(0xffffffffu, s_n[lane]);
+        g = warp_max(s_g[lane]);
+        if (lane == 0) s_cta = make_int2(all, __float_as_int(g));
+    }
+    cluster_barrier();
+    int all = 0;
     g = 0.0f;
-    for (int i = 0; i < 32; ++i) {
-        if (i < w) at += s_n[i];
-        all += s_n[i];
-        g = fmaxf(g, s_g[i]);
+#pragma unroll
+    for (int c = 0; c < kLiveCtas; ++c) {
+        const int2 o = read_at_rank(&s_cta, c);
+        if (c < cta) at += o.x;
+        all += o.x;
+        g = fmaxf(g, __int_as_float(o.y));
     }
+    cluster_barrier();  // nobody leaves before its counts are read
     if (!(g > 0.0f) || g == INFINITY) g = 1.0f;
-    if (threadIdx.x == 0) {
-        counts->rows = all;
-        counts->gmax = g;
-    }
+    if (cta == 0 && threadIdx.x == 0) *counts = {all, g};
 #pragma unroll 4
-    for (int64_t b = r0; b < r1; b += 32) {
-        const int64_t r = b + lane;
-        int32_t id = -1;
-        const bool has = wanted(r, id);
-        const float gl = r < r1 ? gloss[r] : 0.0f;
-        const bool live = has && gl != 0.0f;
+    for (int32_t i = 0; i < per; ++i) {
+        const int64_t r = r0 + i * 32 + lane;
+        int32_t id;
+        float gl;
+        const bool live = a.wanted(r, id, gl);
         const unsigned int mask = __ballot_sync(0xffffffffu, live);
-        const int i = at + __popc(mask & ((1u << lane) - 1u));
-        if (live) {
-            const float l = lse[r];
-            HeadRow h;
-            h.lse_hi = l * kLog2e;
-            h.lse_lo = fmaf(l, kLog2e, -h.lse_hi) + l * kLog2eRest;
-            h.weight = gl / g;
-            h.target = id;
-            rows[i] = h;
-            row_of[i] = static_cast<int32_t>(r);
-        }
-        if (r < r1) place[r] = live ? i : -1;
+        const int to = at + __popc(mask & ((1u << lane) - 1u));
         at += __popc(mask);
+        if (r >= a.R) continue;
+        place[r] = live ? to : -1;
+        if (!live) continue;
+        const float l = lse[r];
+        HeadRow h;
+        h.lse_hi = l * kLog2e;
+        h.lse_lo = fmaf(l, kLog2e, -h.lse_hi) + l * kLog2eRest;
+        h.weight = gl / g;
+        h.target = id;
+        rows[to] = h;
+        row_of[to] = static_cast<int32_t>(r);
     }
 }
 
@@ -458,8 +495,8 @@ LossSpace carve_loss(void* ws, const HeadProblem& p) {
     const int64_t R = p.S * p.T, dp = up(p.d, 8), planes = p.bf16 ? 1 : 3;
     Carver c{static_cast<unsigned char*>(ws)};
     LossSpace w;
-    const int64_t slots = 2 * ((p.V + 127) / 128);
-    w.part = c.take<HeadPart>(slots * up(R, 32));
+    const int64_t bn = head_loss_columns(R, p.V);
+    w.part = c.take<HeadPart>(2 * ((p.V + bn - 1) / bn) * up(R, 32));
     w.picked = c.take<float>(R);
     w.loss = c.take<float>(R);
     w.h = c.take<__nv_bfloat16>(planes * R * dp);
@@ -474,7 +511,7 @@ struct GradSpace {
     int32_t *row_of, *place;
     float2* teacher;
     __nv_bfloat16 *h, *e, *g;
-    float* acc;
+    float *gh_acc, *ge_acc;
     int64_t piece;
     size_t total;
 };
@@ -489,8 +526,14 @@ GradSpace carve_grad(void* ws, const HeadProblem& p) {
     w.row_of = c.take<int32_t>(R);
     w.place = c.take<int32_t>(R);
     w.teacher = c.take<float2>(p.T);
-    w.acc = reinterpret_cast<float*>(
-        c.take<unsigned char>(w.piece < p.V ? static_cast<int64_t>(head_acc_bytes(R, p.d)) : 0));
+    // Sized for both gradients, whichever are asked for.
+    const int P = static_cast<int>(planes);
+    const HeadCuts both = head_cuts(R, std::min(w.piece, p.V), p.d, P, true, true);
+    const HeadCuts gh = head_cuts(R, std::min(w.piece, p.V), p.d, P, true, false);
+    const HeadCuts ge = head_cuts(R, std::min(w.piece, p.V), p.d, P, false, true);
+    const int cut0 = std::max(both.gh, gh.gh), cut1 = std::max(both.ge, ge.ge);
+    w.gh_acc = c.take<float>(w.piece < p.V || cut0 > 1 ? head_acc_floats(R, p.d, cut0) : 0);
+    w.ge_acc = c.take<float>(cut1 > 1 ? head_acc_floats(w.piece, p.d, cut1) : 0);
     w.g = c.take<__nv_bfloat16>(planes * up(R, kHeadTile) * w.piece);
     w.h = c.take<__nv_bfloat16>(planes * R * dp);
     w.e = c.take<__nv_bfloat16>(planes * p.V * dp);
@@ -587,9 +630,10 @@ cudaError_t grad_typed(const HeadProblem& p, const float* lse, const float* stud
     if (distill)
         DUST_TRY(launch_pdl(k_head_teacher, dim3(grid_of(p.T, 8)), dim3(256), 0, s, p.T, p.tg, p.V,
                             p.scale, w.teacher, st));
-    DUST_TRY(launch_pdl(k_head_live, dim3(1), dim3(1024), 0, s, R, p.T,
-                        distill ? nullptr : p.tg.ids, distill ? w.teacher : nullptr, p.V, lse,
-                        gloss, w.counts, w.rows, w.row_of, w.place, st));
+    const LiveRows live = {static_cast<int32_t>(R), static_cast<int32_t>(p.T), p.V,
+                           distill ? nullptr : p.tg.ids, w.teacher, gloss};
+    DUST_TRY(launch_pdl(k_head_live, dim3(kLiveCtas), dim3(kLiveThreads), 0, s, live, lse,
+                        w.counts, w.rows, w.row_of, w.place, st));
     HeadLogits a = {};
     const bool in_place = direct(p.H, p.ld_h, bf16);
     const Planes copy = {w.h, R, up(p.d, 8), up(p.d, 8), static_cast<int>(planes)};
@@ -603,6 +647,9 @@ cudaError_t grad_typed(const HeadProblem& p, const float* lse, const float* stud
     a.rows = w.rows;
     const int64_t g_rows = up(R, kHeadTile);
     a.G = {w.g, g_rows, w.piece, w.piece, static_cast<int>(planes)};
+    const HeadCuts cuts =
+        head_cuts(R, std::min(w.piece, p.V), p.d, static_cast<int>(planes), gH != nullptr,
+                  gE != nullptr);
     for (int64_t v0 = 0; v0 < p.V; v0 += w.piece) {
         const int64_t n = std::min(w.piece, p.V - v0);
         a.v0 = v0;
@@ -630,7 +677,10 @@ cudaError_t grad_typed(const HeadProblem& p, const float* lse, const float* stud
         m.gH = gH;
         m.ld_gh = ld_gh;
         m.gh_bf16 = bf16;
-        m.gh_acc = w.piece < p.V ? w.acc : nullptr;
+        // One choice for all pieces: gH's slices run on across them.
+        m.cuts = cuts;
+        m.gh_acc = w.piece < p.V || cuts.gh > 1 ? w.gh_acc : nullptr;
+        m.ge_acc = cuts.ge > 1 ? w.ge_acc : nullptr;
         m.first = v0 == 0;
         m.last = v0 + n == p.V;
         m.gE = gE ? static_cast<unsigned char*>(gE) + v0 * p.d * (gE_bf16 ? 2 : 4) : nullptr;

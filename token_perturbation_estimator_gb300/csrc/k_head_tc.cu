@@ -31,6 +31,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "f32x2.cuh"
 #include "head.cuh"
 #include "tc_common.cuh"
 
@@ -40,19 +41,27 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
 namespace {
 
-constexpr int kStages = 6;
 constexpr int kHalf = 128;                        // rows of A per CTA
 constexpr int kBoxBytes = kHeadBox * kHeadBox * 2;
 constexpr int kStageBytes = 4 * kBoxBytes;        // two boxes of A, two of B
 constexpr int kEpiWarps = 8;
+constexpr int kShare = kEpiWarps / 4;             // warps that share a TMEM lane quarter
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kStageBuf = 32 * 32 * 2;            // 32 rows x 32 columns of G
 constexpr int kStoreBufs = 2;
-constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kStoreBufs * kStageBuf + 1024 + 512;
+constexpr int kStoreBytes = kEpiWarps * kStoreBufs * kStageBuf;
+constexpr int kSlotFloats = kHeadTile * kHeadTile;  // a tile of partial sums
 constexpr uint32_t kTmemCols = 512;               // two accumulators of 256 columns
-static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 
 enum Mode { kLse, kFactor, kMul };
+
+// Steps in flight: what shared memory holds beside the store buffers.
+constexpr int kStages = 6;
+template <int MODE> constexpr int smem_of() {
+    return kStages * kStageBytes + (MODE == kFactor ? kStoreBytes : 0) + 1024;
+}
+static_assert(smem_of<kFactor>() + 512 <= 227 * 1024, "shared memory per CTA, barriers included");
+
 
 struct Ctl {
     uint64_t full[kStages];
@@ -65,12 +74,6 @@ struct Ctl {
     int abort;
     int issued;
     int consumed;
-};
-
-// One product C[m][n] = sum over k A(m, k) B(n, k) of a launch.
-struct Dims {
-    int64_t m, n, k;
-    int mt, nt;  // tiles
 };
 
 struct TcArgs {
@@ -90,9 +93,10 @@ struct TcArgs {
     const int32_t* row_of;     // kMul
     unsigned char* gH;
     int64_t ld_gh;
-    float* gh_acc;
+    float *gh_acc, *ge_acc;    // tiles of partial sums, by unit
     unsigned char* gE;
     int gh_bf16, ge_bf16, gh_vec, ge_vec, first, last, accumulate;
+    int cut0, cut1;            // slices of the summed dimension, gH and gE
     int stall;
     unsigned int* status;
 };
@@ -107,45 +111,75 @@ __device__ __forceinline__ int plane_b(int planes, int p) {
     return planes == 1 ? 0 : b[p];
 }
 
-// Where a tile lies: which product (0: logits or gH, 1: gE), its first row
-// and column, and its steps along the summed dimension per pair of planes.
+// Where a unit of work lies: which product (0: logits or gH, 1: gE), its
+// first row and column, and its steps along the summed dimension (of every
+// pair of planes).
 struct Tile {
     int job;
     int64_t m0, n0;
-    int steps;
-    int index;  // among the product's tiles
+    int k0, steps;
+    int index;  // its column of tiles (logits), or the unit (kMul)
 };
 
 template <int MODE>
 struct Plan {
     int64_t rows;
-    int mt, nt;        // job 0
-    int mt1, nt1;      // job 1 (kMul)
-    int n0_tiles, n1_tiles, total;
-    int steps0, steps1;
-    bool one_first;
+    int mt, nt;              // tiles of job 0
+    int steps0, steps1;      // of a whole tile
+    int units0, units1, total;
+    bool one_first;          // kMul: gE's units are the longer ones
+    int cluster, clusters;
+    int high, rounds;        // see unit()
 
-    __device__ Plan(const TcArgs& a) {
+    __device__ Plan(const TcArgs& a, int c, int n) : cluster(c), clusters(n) {
         rows = a.counts ? a.counts->rows : a.rows;
         const auto up = [](int64_t v, int64_t by) { return static_cast<int>((v + by - 1) / by); };
+        nt = up(MODE == kMul ? a.d : a.n, a.bn);
         if (MODE != kMul) {
             mt = up(rows, kHeadTile);
-            nt = up(a.n, a.bn);
             steps0 = up(a.d, 64);
-            n0_tiles = mt * nt;
-            mt1 = nt1 = n1_tiles = steps1 = 0;
+            steps1 = units1 = 0;
+            units0 = mt * nt;
+            one_first = false;
+            high = rounds = 0;
         } else {
             mt = a.gH ? up(rows, kHeadTile) : 0;
-            nt = up(a.d, a.bn);
             steps0 = up(a.n, 64);
-            n0_tiles = mt * nt;
-            mt1 = a.gE ? up(a.n, kHeadTile) : 0;
-            nt1 = nt;
             steps1 = up(rows, 64);
-            n1_tiles = mt1 * nt1;
+            units0 = mt * nt * a.cut0;
+            units1 = (a.gE ? up(a.n, kHeadTile) : 0) * nt * a.cut1;
+            const int cost0 = max(1, up(steps0, a.cut0)), cost1 = max(1, up(steps1, a.cut1));
+            one_first = cost1 > cost0;
+            const int longs = one_first ? units1 : units0;
+            high = longs % clusters;
+            rounds = high == 0 ? 0 : up(max(cost0, cost1), min(cost0, cost1));
         }
-        total = n0_tiles + n1_tiles;
-        one_first = steps1 > steps0;  // the longer tiles start first
+        total = units0 + units1;
+    }
+
+    // The i-th unit of this cluster, or -1. Long units (of whichever product)
+    // are dealt round robin, then the short ones to whoever is done first: the
+    // clusters from `high` on have one long unit less, and take `rounds` short
+    // ones each while the others finish; from there on everyone in turn. The
+    // units are numbered long ones first.
+    __device__ int unit(const TcArgs& a, int i) const {
+        if (MODE != kMul) {
+            const int64_t t = cluster + static_cast<int64_t>(i) * clusters;
+            return t < total ? static_cast<int>(t) : -1;
+        }
+        const int longs = one_first ? units1 : units0, shorts = total - longs;
+        const int mine = longs / clusters + (cluster < high ? 1 : 0);
+        if (i < mine) return cluster + i * clusters;
+        i -= mine;
+        int64_t t;
+        const int low = clusters - high;
+        if (cluster >= high && i < rounds) {
+            t = static_cast<int64_t>(i) * low + cluster - high;
+        } else {
+            if (cluster >= high) i -= rounds;
+            t = static_cast<int64_t>(rounds) * low + static_cast<int64_t>(i) * clusters + cluster;
+        }
+        return t < shorts ? longs + static_cast<int>(t) : -1;
     }
 
     __device__ Tile at(const TcArgs& a, int t) const {
@@ -160,17 +194,22 @@ struct Plan {
             w.job = 0;
             w.m0 = static_cast<int64_t>(g * a.group + (in - c * gm)) * kHeadTile;
             w.n0 = static_cast<int64_t>(c) * a.bn;
+            w.k0 = 0;
             w.steps = steps0;
             w.index = c;
         } else {
-            const int firsts = one_first ? n1_tiles : n0_tiles;
+            const int firsts = one_first ? units1 : units0;
             const bool job1 = (t < firsts) == one_first;
             const int i = t < firsts ? t : t - firsts;
-            const int r = i / nt;  // columns fastest: a row block of G is read by neighbours
+            const int cut = job1 ? a.cut1 : a.cut0;
+            const int steps = job1 ? steps1 : steps0;
+            const int tile = i / cut, part = i - tile * cut;
+            const int r = tile / nt;  // columns fastest: a row block of G is read by neighbours
             w.job = job1 ? 1 : 0;
             w.m0 = static_cast<int64_t>(r) * kHeadTile;
-            w.n0 = static_cast<int64_t>(i - r * nt) * a.bn;
-            w.steps = job1 ? steps1 : steps0;
+            w.n0 = static_cast<int64_t>(tile - r * nt) * a.bn;
+            w.k0 = static_cast<int>(static_cast<int64_t>(steps) * part / cut);
+            w.steps = static_cast<int>(static_cast<int64_t>(steps) * (part + 1) / cut) - w.k0;
             w.index = i;
         }
         return w;
@@ -181,6 +220,12 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -238,191 +283,227 @@ __device__ __forceinline__ void store_row(unsigned char* row, int64_t col, const
 template <bool FULL>
 __device__ __forceinline__ void softmax_block(const float (&v)[32], int n, float c, float& m,
                                               float& s) {
-    float top = v[0];
-    if (c >= 0.0f) {
+    // The largest c v, whichever sign c has.
+    float top = -INFINITY;
+    if (!FULL || c < 0.0f) {
 #pragma unroll
-        for (int i = 1; i < 32; ++i)
-            if (FULL || i < n) top = fmaxf(top, v[i]);
+        for (int i = 0; i < 32; ++i)
+            if (i < n) top = fmaxf(top, c < 0.0f ? -v[i] : v[i]);
+        if (c < 0.0f) top = -top;
     } else {
+        float t[2] = {v[0], v[1]};
 #pragma unroll
-        for (int i = 1; i < 32; ++i)
-            if (FULL || i < n) top = fminf(top, v[i]);
+        for (int i = 2; i < 30; i += 4) {
+            t[0] = max3(t[0], v[i], v[i + 1]);
+            t[1] = max3(t[1], v[i + 2], v[i + 3]);
+        }
+        top = max3(fmaxf(t[0], t[1]), v[30], v[31]);
     }
     const float nm = fmaxf(m, ceilf(c * top));
     const float base = nm == -INFINITY ? 0.0f : nm;
-    float e0 = 0.0f, e1 = 0.0f;
+    float sum;
+    if (FULL) {
+        float2 e[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+        const float2 cc = {c, c}, bb = {-base, -base};
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-        if (FULL || i < n) e0 += ex2(fmaf(c, v[i], -base));
-        if (FULL || i + 1 < n) e1 += ex2(fmaf(c, v[i + 1], -base));
+        for (int i = 0; i < 32; i += 2) {
+            float2 t = fma2(cc, make_float2(v[i], v[i + 1]), bb);
+            t.x = ex2(t.x);
+            t.y = ex2(t.y);
+            e[(i >> 1) & 1] = add2(e[(i >> 1) & 1], t);
+        }
+        const float2 u = add2(e[0], e[1]);
+        sum = u.x + u.y;
+    } else {
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) sum += ex2(fmaf(c, v[i], -base));
     }
-    s = fmaf(s, ex2(m - base), e0 + e1);
+    s = fmaf(s, ex2(m - base), sum);
     m = nm;
 }
 
-// Epilogue of one tile for one warp: rows 32 q + lane of this CTA's half,
+// What a row needs besides the accumulator; loaded a unit ahead.
+struct RowOf {
+    int64_t row;
+    bool live;
+    HeadRow info;      // kLse: the target alone
+    int64_t out_row;
+};
+
+// Epilogue of one unit for one warp: rows 32 q + lane of this CTA's half,
 // columns [h bn / 2, (h + 1) bn / 2).
 template <int MODE, int PLANES>
 struct Epilogue {
     const TcArgs& a;
     const CUtensorMap* tmG;
     unsigned char* bufs;  // this warp's store buffers
+    uint32_t rank;
+    int q, h, lane;
     uint32_t used = 0;
 
-    __device__ Epilogue(const TcArgs& args, const CUtensorMap* g, unsigned char* b)
-        : a(args), tmG(g), bufs(b) {}
-
-    // What the row needs besides the accumulator; loaded before the wait.
-    int64_t row;
-    bool live;
-    int32_t target;
-    HeadRow info;
-    int64_t out_row;
-
-    __device__ void begin(const Tile& w, const Plan<MODE>& plan, uint32_t rank, int q, int lane) {
-        row = w.m0 + rank * kHalf + 32 * q + lane;
+    __device__ RowOf begin(const Tile& w, const Plan<MODE>& plan) const {
+        RowOf o;
+        o.row = w.m0 + rank * kHalf + 32 * q + lane;
+        o.info.target = -1;
+        o.out_row = o.row;
         if (MODE == kLse) {
-            live = row < plan.rows;
-            target = live && a.targets ? a.targets[row % a.T] : -1;
+            o.live = o.row < plan.rows;
+            if (o.live && a.targets)
+                o.info.target = a.targets[static_cast<uint32_t>(o.row) % static_cast<uint32_t>(a.T)];
         } else if (MODE == kFactor) {
-            live = row < plan.rows;
-            if (live) info = a.info[row];
-            target = live ? info.target : -1;
+            o.live = o.row < plan.rows;
+            if (o.live) o.info = a.info[o.row];
         } else if (w.job == 0) {
-            live = row < plan.rows;
-            out_row = live && a.row_of ? a.row_of[row] : row;
+            o.live = o.row < plan.rows;
+            if (o.live && a.row_of) o.out_row = a.row_of[o.row];
         } else {
-            live = row < a.n;
-            out_row = row;
+            o.live = o.row < a.n;
+        }
+        return o;
+    }
+
+    __device__ void lse(const Tile& w, const RowOf& o, uint32_t taddr) {
+        const int cols = a.bn / kShare;
+        const float c = a.scale * kLog2e;
+        const int32_t first = static_cast<int32_t>(w.n0) + h * cols;
+        float m = -INFINITY, s = 0.0f;
+        // Target relative to the warp's first column, if it has one there.
+        const int32_t tv = o.info.target - static_cast<int32_t>(a.v0) - first;
+        for (int b = 0; b < cols / 32; ++b) {
+            float v[32];
+            tc::tmem_ld_32x32(taddr + h * cols + 32 * b, v);
+            const int left = static_cast<int>(a.n) - (first + 32 * b);  // columns that exist
+            if (left <= 0) break;
+            const int at = tv - 32 * b;
+            if (o.live && at >= 0 && at < 32 && at < left) {
+                float x = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x = (i == at) ? v[i] : x;
+                a.picked[o.row] = a.scale * x;
+            }
+            if (left >= 32)
+                softmax_block<true>(v, 32, c, m, s);
+            else
+                softmax_block<false>(v, left, c, m, s);
+        }
+        if (o.live)
+            a.part[(static_cast<int64_t>(w.index) * kShare + h) * a.ld_part + o.row] = {m, s};
+    }
+
+    __device__ void factor(const Tile& w, const RowOf& o, uint32_t taddr) {
+        const int cols = a.bn / kShare;
+        const float c = a.scale * kLog2e;
+        const uint32_t swz = (lane >> 1) & 3;
+        for (int b = 0; b < cols / 32; ++b) {
+            float v[32];
+            const int64_t col = w.n0 + h * cols + 32 * b;
+            tc::tmem_ld_32x32(taddr + h * cols + 32 * b, v);
+            const int left = static_cast<int>(a.n - col);
+            const float2 cc = {c, c}, hi = {-o.info.lse_hi, -o.info.lse_hi};
+            const float2 ww = {o.info.weight, o.info.weight};
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float2 t = fma2(cc, make_float2(v[i], v[i + 1]), hi);
+                if (PLANES == 3) {
+                    // The logarithm in two parts: its rounding would be the
+                    // same for the whole row.
+                    t.x -= o.info.lse_lo;
+                    t.y -= o.info.lse_lo;
+                }
+                t.x = ex2(t.x);
+                t.y = ex2(t.y);
+                t = mul2(ww, t);
+                v[i] = t.x;
+                v[i + 1] = t.y;
+            }
+            if (!o.live || left < 32) {  // G is zero where there is no row or column
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = o.live && i < left ? v[i] : 0.0f;
+            }
+            const int64_t tv = o.info.target - a.v0 - col;
+            if (tv >= 0 && tv < 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i == tv) v[i] -= o.info.weight;
+            }
+#pragma unroll
+            for (int p = 0; p < PLANES; ++p) {
+                unsigned char* buf = bufs + (used % kStoreBufs) * kStageBuf;
+                if (used >= kStoreBufs) {
+                    if (lane == 0) tc::bulk_wait_read<kStoreBufs - 1>();
+                    __syncwarp();
+                }
+                const uint32_t dst = tc::smem_u32(buf) + lane * 64;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float x0 = v[8 * u + 2 * j], x1 = v[8 * u + 2 * j + 1];
+                        pk[j] = pack2(x0, x1);
+                        if (p + 1 < PLANES) {  // what this plane leaves
+                            v[8 * u + 2 * j] = x0 - __uint_as_float(pk[j] << 16);
+                            v[8 * u + 2 * j + 1] = x1 - __uint_as_float(pk[j] & 0xffff0000u);
+                        }
+                    }
+                    st_shared_16(dst + ((u ^ swz) << 4), pk);
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    // G is padded to whole tiles: every block lies inside.
+                    tc::tma_store_3d(tmG, buf, static_cast<int32_t>(col),
+                                     static_cast<int32_t>(w.m0 + rank * kHalf + 32 * q), p);
+                    tc::bulk_commit();
+                }
+                ++used;
+            }
         }
     }
 
-    __device__ void run(const Tile& w, uint32_t taddr, int h, int lane, uint32_t rank, int q,
-                        float alpha, bool zero) {
-        const int cols = a.bn / 2;
-        if (MODE == kLse) {
-            const float c = a.scale * kLog2e;
-            const int32_t first = static_cast<int32_t>(w.n0) + h * cols;
-            float m = -INFINITY, s = 0.0f;
-            // Target relative to the warp's first column, if it has one there.
-            const int32_t tv = target - static_cast<int32_t>(a.v0) - first;
-            for (int b = 0; b < cols / 32; ++b) {
-                float v[32];
-                tc::tmem_ld_32x32(taddr + h * cols + 32 * b, v);
-                const int left = static_cast<int>(a.n) - (first + 32 * b);  // columns that exist
-                if (left <= 0) break;
-                const int at = tv - 32 * b;
-                if (live && at >= 0 && at < 32 && at < left) {
-                    float x = 0.0f;
+    __device__ void product(const Tile& w, const RowOf& o, uint32_t taddr, float alpha) {
+        const int cols = a.bn / kShare;
+        const bool job1 = w.job == 1, zero = w.steps == 0;
+        float* acc = job1 ? a.ge_acc : a.gh_acc;
+        const bool add = !job1 && !a.first;
+        // The result is whole here unless other slices or pieces add to it.
+        const bool whole = job1 ? a.cut1 == 1 : a.cut0 == 1 && a.last;
+        for (int b = 0; b < cols / 32; ++b) {
+            const int at = h * cols + 32 * b;
+            const int64_t col = w.n0 + at;
+            if (col >= a.d) break;
+            float v[32];
+            tc::tmem_ld_32x32(taddr + at, v);
+            const int n = a.d - col < 32 ? static_cast<int>(a.d - col) : 32;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x = (i == at) ? v[i] : x;
-                    a.picked[row] = a.scale * x;
-                }
-                if (left >= 32)
-                    softmax_block<true>(v, 32, c, m, s);
-                else
-                    softmax_block<false>(v, left, c, m, s);
-            }
-            if (live) {
-                const HeadPart p = {m, s};
-                a.part[(2 * static_cast<int64_t>(w.index) + h) * a.ld_part + row] = p;
-            }
-        } else if (MODE == kFactor) {
-            const float c = a.scale * kLog2e;
-            const uint32_t swz = (lane >> 1) & 3;
-            for (int b = 0; b < cols / 32; ++b) {
-                float v[32];
-                const int64_t col = w.n0 + h * cols + 32 * b;
-                tc::tmem_ld_32x32(taddr + h * cols + 32 * b, v);
-                const int left = static_cast<int>(a.n - col);
+            for (int i = 0; i < 32; ++i) v[i] = zero ? 0.0f : alpha * v[i];
+            if (acc && (add || !whole)) {
+                // Partial sums lie as the accumulator has them: four columns
+                // of all rows together.
+                float4* p = reinterpret_cast<float4*>(acc + static_cast<int64_t>(w.index) * kSlotFloats) +
+                            at / 4 * kHeadTile + static_cast<int>(rank) * kHalf + 32 * q + lane;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    // The logarithm in two parts: its rounding would be the
-                    // same for the whole row.
-                    float t = fmaf(c, v[i], -info.lse_hi);
-                    if (PLANES == 3) t -= info.lse_lo;
-                    const float e = info.weight * ex2(t);
-                    v[i] = live && i < left ? e : 0.0f;
-                }
-                const int64_t tv = target - a.v0 - col;
-                if (tv >= 0 && tv < 32) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i == tv) v[i] -= info.weight;
-                }
-#pragma unroll
-                for (int p = 0; p < PLANES; ++p) {
-                    unsigned char* buf = bufs + (used % kStoreBufs) * kStageBuf;
-                    if (used >= kStoreBufs) {
-                        if (lane == 0) tc::bulk_wait_read<kStoreBufs - 1>();
-                        __syncwarp();
+                for (int i = 0; i < 8; ++i) {
+                    if (add) {
+                        const float4 u = p[i * kHeadTile];
+                        v[4 * i] += u.x;
+                        v[4 * i + 1] += u.y;
+                        v[4 * i + 2] += u.z;
+                        v[4 * i + 3] += u.w;
                     }
-                    const uint32_t dst = tc::smem_u32(buf) + lane * 64;
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint32_t pk[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float x0 = v[8 * u + 2 * j], x1 = v[8 * u + 2 * j + 1];
-                            pk[j] = pack2(x0, x1);
-                            if (p + 1 < PLANES) {  // what this plane leaves
-                                v[8 * u + 2 * j] = x0 - __uint_as_float(pk[j] << 16);
-                                v[8 * u + 2 * j + 1] = x1 - __uint_as_float(pk[j] & 0xffff0000u);
-                            }
-                        }
-                        st_shared_16(dst + ((u ^ swz) << 4), pk);
-                    }
-                    tc::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        // G is padded to whole tiles: every block lies inside.
-                        tc::tma_store_3d(tmG, buf, static_cast<int32_t>(col),
-                                         static_cast<int32_t>(w.m0 + rank * kHalf + 32 * q), p);
-                        tc::bulk_commit();
-                    }
-                    ++used;
+                    if (!whole)
+                        p[i * kHeadTile] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 }
             }
-        } else {
-            for (int b = 0; b < cols / 32; ++b) {
-                float v[32];
-                const int at = h * cols + 32 * b;
-                const int64_t col = w.n0 + at;
-                tc::tmem_ld_32x32(taddr + at, v);
-                if (col >= a.d) break;
-                const int n = a.d - col < 32 ? static_cast<int>(a.d - col) : 32;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = zero ? 0.0f : alpha * v[i];
-                if (w.job == 1) {
-                    if (live)
-                        store_row(a.gE + out_row * a.d * (a.ge_bf16 ? 2 : 4), col, v, n,
-                                  a.ge_bf16, a.ge_vec, a.accumulate);
-                    continue;
-                }
-                if (a.gh_acc) {
-                    // Running sums in the order of the accumulator: four
-                    // columns of all rows together.
-                    const int in_tile = static_cast<int>(rank) * kHalf + 32 * q + lane;
-                    float4* p = reinterpret_cast<float4*>(
-                        a.gh_acc + static_cast<int64_t>(w.index) * kHeadTile * kHeadTile);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float4* e = p + (at / 4 + i) * kHeadTile + in_tile;
-                        if (!a.first) {
-                            const float4 o = *e;
-                            v[4 * i] += o.x;
-                            v[4 * i + 1] += o.y;
-                            v[4 * i + 2] += o.z;
-                            v[4 * i + 3] += o.w;
-                        }
-                        if (!a.last) *e = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    }
-                    if (!a.last) continue;
-                }
-                if (live)
-                    store_row(a.gH + out_row * a.ld_gh * (a.gh_bf16 ? 2 : 4), col, v, n, a.gh_bf16,
-                              a.gh_vec, false);
-            }
+            if (!whole || !o.live) continue;
+            if (job1)
+                store_row(a.gE + o.out_row * a.d * (a.ge_bf16 ? 2 : 4), col, v, n, a.ge_bf16,
+                          a.ge_vec, a.accumulate);
+            else
+                store_row(a.gH + o.out_row * a.ld_gh * (a.gh_bf16 ? 2 : 4), col, v, n, a.gh_bf16,
+                          a.gh_vec, false);
         }
     }
 };
@@ -437,7 +518,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char* store_bufs = smem + kStages * kStageBytes;
-    Ctl* ctl = reinterpret_cast<Ctl*>(store_bufs + kEpiWarps * kStoreBufs * kStageBuf);
+    __shared__ Ctl ctl_s;
+    Ctl* ctl = &ctl_s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank_of_cta();
     const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
@@ -470,7 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_trigger();
 
-    const Plan<MODE> plan(a);
+    const Plan<MODE> plan(a, cluster, n_clusters);
     const int pairs = a.planes == 1 ? 1 : 6;
     const int b_boxes = a.bn / 128;  // per CTA
     // A tile's products take about 0.3 us per step: the waits for a whole
@@ -491,7 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 B0 = &tm2;
             }
             int it = 0;
-            for (int t = cluster; t < plan.total && !*abort_flag; t += n_clusters) {
+            for (int j = 0, t; !*abort_flag && (t = plan.unit(a, j)) >= 0; ++j) {
                 const Tile w = plan.at(a, t);
                 const CUtensorMap* ma = w.job ? A1 : A0;
                 const CUtensorMap* mb = w.job ? B1 : B0;
@@ -508,7 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int pa = plane_a(a.planes, p), pb = plane_b(a.planes, p);
                     for (int k = 0; k < w.steps; ++k, ++it) {
                         const int st = it % kStages;
-                        if (!tc::mbar_wait_cluster(&ctl->empty[st], ((it / kStages) & 1) ^ 1,
+                        if (!tc::mbar_wait_for(&ctl->empty[st], ((it / kStages) & 1) ^ 1,
                                                    tile_ns) || *abort_flag) {
                             *abort_flag = 1;
                             break;
@@ -517,7 +599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const uint32_t bar = tc::at_rank(&ctl->full[st], 0);
                         if (rank == 0)
                             tc::mbar_arrive_expect_tx(&ctl->full[st], 2 * (2 + b_boxes) * kBoxBytes);
-                        const int32_t kk = k * 64;
+                        const int32_t kk = (w.k0 + k) * 64;
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
                             tc::tma_load_3d_pair(base + u * kBoxBytes, ma, a_mn ? am + 64 * u : kk,
@@ -534,11 +616,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             if (a.stall && !tc::mbar_wait(&ctl->never, 0)) *abort_flag = 1;
-            int it = 0, j = 0;
-            for (int t = cluster; t < plan.total && !*abort_flag; t += n_clusters, ++j) {
+            int it = 0;
+            for (int j = 0, t; !*abort_flag && (t = plan.unit(a, j)) >= 0; ++j) {
                 const Tile w = plan.at(a, t);
                 const int acc = j & 1;
-                if (!tc::mbar_wait_cluster(&ctl->tempty[acc], ((j >> 1) & 1) ^ 1, tile_ns)) {
+                if (!tc::mbar_wait_for(&ctl->tempty[acc], ((j >> 1) & 1) ^ 1, tile_ns)) {
                     *abort_flag = 1;
                     break;
                 }
@@ -552,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int n = pairs * w.steps;
                 for (int k = 0; k < n; ++k, ++it) {
                     const int st = it % kStages;
-                    if (!tc::mbar_wait_cluster(&ctl->full[st], (it / kStages) & 1, tc::kWaitNs) ||
+                    if (!tc::mbar_wait_for(&ctl->full[st], (it / kStages) & 1, tc::kWaitNs) ||
                         *abort_flag) {
                         *abort_flag = 1;
                         break;
@@ -574,29 +656,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (*abort_flag) {
                 // Everything issued so far has to be done before TMEM is freed.
                 tc::mma_commit_pair(&ctl->drain);
-                tc::mbar_wait_cluster(&ctl->drain, 0, tc::kWaitNs);
+                tc::mbar_wait_for(&ctl->drain, 0, tc::kWaitNs);
             }
         }
     } else {
         const int ew = warp - 2, q = warp & 3, h = ew >> 2;
-        Epilogue<MODE, PLANES> epi(a, &tm3, store_bufs + ew * kStoreBufs * kStageBuf);
+        Epilogue<MODE, PLANES> epi{a, &tm3, store_bufs + ew * kStoreBufs * kStageBuf, rank, q, h,
+                                   lane};
         const float alpha = MODE == kMul ? a.scale * a.counts->gmax : 0.0f;
-        int j = 0;
-        for (int t = cluster; t < plan.total; t += n_clusters, ++j) {
-            const Tile w = plan.at(a, t);
+        int t = plan.unit(a, 0);
+        Tile w = t >= 0 ? plan.at(a, t) : Tile{};
+        RowOf o = {};
+        if (t >= 0) o = epi.begin(w, plan);
+        for (int j = 0; t >= 0; ++j) {
             const int acc = j & 1;
-            epi.begin(w, plan, rank, q, lane);
-            const bool ok = tc::mbar_wait_cluster(&ctl->tfull[acc], (j >> 1) & 1, tile_ns);
+            const bool ok = tc::mbar_wait_for(&ctl->tfull[acc], (j >> 1) & 1, tile_ns);
             tc::tc_fence_after();
             if (!__all_sync(0xffffffffu, ok) || *abort_flag) {
                 *abort_flag = 1;
                 break;
             }
-            epi.run(w, tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * 256, h, lane, rank, q,
-                    alpha, w.steps == 0);
+            // The next unit's rows are loaded beside this one's arithmetic.
+            t = plan.unit(a, j + 1);
+            const Tile next = t >= 0 ? plan.at(a, t) : w;
+            RowOf next_o = {};
+            if (t >= 0) next_o = epi.begin(next, plan);
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * 256;
+            if constexpr (MODE == kLse)
+                epi.lse(w, o, taddr);
+            else if constexpr (MODE == kFactor)
+                epi.factor(w, o, taddr);
+            else
+                epi.product(w, o, taddr, alpha);
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_at(tc::at_rank(&ctl->tempty[acc], 0));
+            w = next;
+            o = next_o;
         }
         if (MODE == kFactor) {
             if (lane == 0) tc::bulk_wait_all();
@@ -619,6 +715,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::tc_fence_after();
         tc::tmem_dealloc_pair(tmem, kTmemCols);
     }
+}
+
+// The slices' partial sums of one product added in order, into gH or gE: a
+// CTA takes 32 rows and 32 columns of a tile at a time.
+__global__ void __launch_bounds__(256)
+    k_head_sum(const __grid_constant__ TcArgs a, int job, int64_t tiles) {
+    pdl_wait();
+    pdl_trigger();
+    const int nt = static_cast<int>((a.d + a.bn - 1) / a.bn);
+    const int cut = job ? a.cut1 : a.cut0;
+    const int64_t rows = job ? a.n : a.counts->rows;
+    const int lane = threadIdx.x & 31, c4 = threadIdx.x >> 5;
+    const int64_t blocks = tiles * 8 * (a.bn / 32);
+    for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+        const int64_t tile = b / (8 * (a.bn / 32));
+        const int in = static_cast<int>(b - tile * (8 * (a.bn / 32)));
+        const int r = (in & 7) * 32 + lane, c = (in >> 3) * 32 + c4 * 4;
+        const int64_t row = tile / nt * kHeadTile + r, col = tile % nt * a.bn + c;
+        if (row >= rows || col >= a.d) continue;
+        const float4* p = reinterpret_cast<const float4*>((job ? a.ge_acc : a.gh_acc) +
+                                                          tile * cut * kSlotFloats) +
+                          c / 4 * kHeadTile + r;
+        float4 v = *p;
+        for (int k = 1; k < cut; ++k) {
+            const float4 u = p[static_cast<int64_t>(k) * (kSlotFloats / 4)];
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+        }
+        const float x[4] = {v.x, v.y, v.z, v.w};
+        const bool bf16 = job ? a.ge_bf16 : a.gh_bf16;
+        const int64_t at = job ? row * a.d + col
+                               : static_cast<int64_t>(a.row_of ? a.row_of[row] : row) * a.ld_gh + col;
+        for (int i = 0; i < 4 && col + i < a.d; ++i) {
+            if (bf16) {
+                reinterpret_cast<__nv_bfloat16*>(job ? a.gE : a.gH)[at + i] = __float2bfloat16_rn(x[i]);
+            } else {
+                float* o = reinterpret_cast<float*>(job ? a.gE : a.gH) + at + i;
+                *o = job && a.accumulate ? *o + x[i] : x[i];
+            }
+        }
+    }
+}
+
+cudaError_t launch_sum(const TcArgs& a, int job, int64_t tiles, cudaStream_t s) {
+    const int64_t blocks = std::min<int64_t>(tiles * 8 * (a.bn / 32), 152 * 8);
+    return launch_pdl(k_head_sum, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a, job,
+                      tiles);
 }
 
 // [planes][rows][cols] as a 3-D map of box_rows x box_cols boxes.
@@ -653,11 +798,11 @@ int max_clusters() {
     std::lock_guard<std::mutex> lk(mu);
     if (cache[dev] == 0) {
         const void* k = reinterpret_cast<const void*>(k_head_tc<MODE, PLANES>);
-        if (ensure_smem_limit(k, kSmemBytes) != cudaSuccess) return 0;
+        if (ensure_smem_limit(k, smem_of<MODE>()) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmemBytes;
+        cfg.dynamicSmemBytes = smem_of<MODE>();
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
@@ -681,11 +826,18 @@ cudaError_t launch_tc(const CUtensorMap (&m)[4], TcArgs a, int64_t tiles, cudaSt
     if (!a.status) return cudaErrorUnknown;
     a.stall = take_stall_injection() ? 1 : 0;
     const unsigned clusters = static_cast<unsigned>(std::min<int64_t>(tiles, fit));
-    return launch_pdl(k_head_tc<MODE, PLANES>, dim3(2 * clusters), dim3(kThreads), kSmemBytes, s,
+    return launch_pdl(k_head_tc<MODE, PLANES>, dim3(2 * clusters), dim3(kThreads), smem_of<MODE>(), s,
                       m[0], m[1], m[2], m[3], a);
 }
 
 int64_t tiles_of(int64_t n, int64_t by) { return (n + by - 1) / by; }
+
+constexpr int kPairs = 76;     // CTA pairs of a whole GPU, for the choices below
+constexpr int kMinSteps = 16;  // the shortest slice worth its partial sums: 64 x 16 deep, or a
+                               // quarter of that where a step is six products
+constexpr int kMaxCut = 64;
+
+int product_columns(int64_t d) { return d <= 128 ? 128 : 256; }
 
 // Row tiles that run together: half of the pairs that are resident, so that
 // two columns of tiles are in flight.
@@ -694,9 +846,24 @@ constexpr int kGroup = 38;
 }  // namespace
 
 int head_loss_columns(int64_t rows, int64_t V) {
-    (void)rows;
-    (void)V;
-    return 256;
+    // Narrower tiles while the wide ones leave pairs idle.
+    return tiles_of(rows, kHeadTile) * tiles_of(V, 256) < kPairs ? 128 : 256;
+}
+
+// Slices of the summed dimension for the tiles of gH (n of them added over)
+// and gE (rows of them): more than one where a product's few tiles would each
+// take much longer than an even share of the work.
+HeadCuts head_cuts(int64_t rows, int64_t n, int64_t d, int planes, bool gh, bool ge) {
+    const int64_t nt = tiles_of(d, product_columns(d));
+    const int64_t t0 = gh ? tiles_of(rows, kHeadTile) * nt : 0, s0 = tiles_of(n, 64);
+    const int64_t t1 = ge ? tiles_of(n, kHeadTile) * nt : 0, s1 = tiles_of(rows, 64);
+    const int64_t share = std::max<int64_t>((t0 * s0 + t1 * s1) / kPairs,
+                                            planes == 1 ? kMinSteps : kMinSteps / 4);
+    const auto cut = [&](int64_t tiles, int64_t steps) -> int {
+        if (tiles == 0 || 4 * steps <= 5 * share) return 1;
+        return static_cast<int>(std::min<int64_t>(tiles_of(steps, share), kMaxCut));
+    };
+    return {cut(t0, s0), cut(t1, s1)};
 }
 
 cudaError_t launch_head_lse(const HeadLogits& h, cudaStream_t s) {
@@ -744,9 +911,8 @@ cudaError_t launch_head_factor(const HeadLogits& h, cudaStream_t s) {
                          : launch_tc<kFactor, 3>(m, a, tiles, s);
 }
 
-size_t head_acc_bytes(int64_t rows, int64_t d) {
-    return sizeof(float) * kHeadTile * kHeadTile *
-           static_cast<size_t>(tiles_of(rows, kHeadTile) * tiles_of(d, 128));
+int64_t head_acc_floats(int64_t m, int64_t d, int cut) {
+    return tiles_of(m, kHeadTile) * tiles_of(d, product_columns(d)) * cut * kSlotFloats;
 }
 
 cudaError_t launch_head_products(const HeadProducts& h, cudaStream_t s) {
@@ -762,12 +928,15 @@ cudaError_t launch_head_products(const HeadProducts& h, cudaStream_t s) {
     a.v0 = h.v0;
     a.counts = h.counts;
     a.planes = h.G.planes;
-    a.bn = h.d <= 128 ? 128 : 256;
+    a.bn = product_columns(h.d);
     a.scale = h.scale;
     a.row_of = h.row_of;
     a.gH = static_cast<unsigned char*>(h.gH);
     a.ld_gh = h.ld_gh;
     a.gh_acc = h.gh_acc;
+    a.ge_acc = h.ge_acc;
+    a.cut0 = h.cuts.gh;
+    a.cut1 = h.cuts.ge;
     a.gE = static_cast<unsigned char*>(h.gE);
     a.gh_bf16 = h.gh_bf16;
     a.ge_bf16 = h.ge_bf16;
@@ -780,9 +949,12 @@ cudaError_t launch_head_products(const HeadProducts& h, cudaStream_t s) {
     a.last = h.last;
     a.accumulate = h.accumulate;
     const int64_t nt = tiles_of(a.d, a.bn);
-    const int64_t tiles = (h.gH ? tiles_of(a.rows, kHeadTile) * nt : 0) +
-                          (h.gE ? tiles_of(a.n, kHeadTile) * nt : 0);
-    return launch_tc<kMul, 1>(m, a, tiles, s);
+    const int64_t t0 = h.gH ? tiles_of(a.rows, kHeadTile) * nt : 0;
+    const int64_t t1 = h.gE ? tiles_of(a.n, kHeadTile) * nt : 0;
+    cudaError_t e = launch_tc<kMul, 1>(m, a, t0 * a.cut0 + t1 * a.cut1, s);
+    if (e == cudaSuccess && h.gE && a.cut1 > 1) e = launch_sum(a, 1, t1, s);
+    if (e == cudaSuccess && h.gH && a.cut0 > 1 && h.last) e = launch_sum(a, 0, t0, s);
+    return e;
 }
 
 }  // namespace dust

@@ -222,29 +222,17 @@ __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
 }
 
 __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                  : "memory");
 }
 
-// As mbar_wait, with its own limit and acquiring at cluster scope (the
-// arrivals may come from the other CTA of the pair).
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
-                                                  uint64_t limit_ns) {
-    const uint32_t a = smem_u32(bar);
-    uint64_t t0 = 0;
+// As mbar_wait, with its own limit.
+__device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
     while (true) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(a), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        const uint64_t t = globaltimer();
-        if (t0 == 0) t0 = t;
-        if (t - t0 > limit_ns) return false;
+        if (mbar_try_wait(bar, parity)) return true;
+        if (globaltimer() - t0 > limit_ns) return false;
     }
 }
 
