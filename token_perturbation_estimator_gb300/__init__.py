@@ -423,32 +423,28 @@ def dust_estimate_gW_host(X_host, X_dev, delta_host, delta_dev, seq_host, seq_de
 
 
 # ---------------------------------------------- layer norm, head, distillation --
+# These calls are short enough on the GPU for the host's part to show (a norm
+# of one token takes 3 us there), so each argument is checked in one expression
+# and the reason looked for only when that fails.
 
-def _rows(t, name, dtypes, shape=None):
-    """Raise ValueError unless t is a CUDA [T, d] tensor of one of `dtypes`
-    with unit column stride and rows that do not overlap; returns its row
-    stride in elements."""
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    _expect(t, name, dtypes, shape=shape, dim=2)
-    T, d = t.shape
-    if (d > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) < d):
-        raise ValueError("%s must have unit column stride and rows that do not overlap" % name)
-    return max(t.stride(0), d) if T > 1 else d
-
-
-def _vector(t, name, dtype, shape):
-    """Raise ValueError unless t (None passes) is a contiguous CUDA tensor of
-    this dtype and shape."""
-    if t is not None:
-        _need_cuda(t)
-        _expect(t, name, (dtype,), shape=shape)
+class _Types:
+    def __init__(self):
+        import torch
+        self.f32, self.bf16 = torch.float32, torch.bfloat16
+        self.i32, self.u8 = torch.int32, torch.uint8
+        self.code = {torch.float32: F32, torch.bfloat16: BF16}
+        self.empty, self.empty_like = torch.empty, torch.empty_like
+        self.stream_of = torch._C._cuda_getCurrentRawStream
 
 
-def _same_device(ref, *ts):
-    for t in ts:
-        if t is not None and t.device != ref.device:
-            raise ValueError("every tensor must be on %s" % ref.device)
+_types_cache = None
+
+
+def _types():
+    global _types_cache
+    if _types_cache is None:
+        _types_cache = _Types()
+    return _types_cache
 
 
 def _in_stream(fn):
@@ -467,61 +463,82 @@ def _in_stream(fn):
     return call
 
 
+def _dense(t, name, dtype, shape, dev):
+    """The address of t (None: NULL). Raises ValueError unless it is a
+    contiguous tensor of this dtype and shape on CUDA device `dev`."""
+    if t is None:
+        return None
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev):
+        _need_cuda(t)
+        _expect(t, name, (dtype,), shape=shape)
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, dev, t.device))
+    return t.data_ptr()
+
+
+def _rows(t, name, dtype, shape, dev):
+    """The row stride in elements of t, a tensor of this dtype and shape [T, d]
+    on CUDA device `dev` with unit column stride and rows that do not overlap;
+    raises ValueError for any other."""
+    T, d = shape
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev):
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        _expect(t, name, (dtype,), shape=shape)
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, dev, t.device))
+    ld, step = t.stride()
+    if T <= 1:
+        ld = max(ld, d)
+    if (d > 1 and step != 1) or ld < d:
+        raise ValueError("%s must have unit column stride and rows that do not overlap" % name)
+    return ld
+
+
+def _values(t, name, dims):
+    """The dtype code and CUDA device of t, an f32 or bf16 tensor with one of
+    these numbers of dimensions; raises ValueError for any other."""
+    code = _types().code.get(t.dtype)
+    if code is None or not t.is_cuda or t.dim() not in dims:
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        raise ValueError("%s must be f32 or bf16 with %s dimensions, got %s %s"
+                         % (name, " or ".join(map(str, dims)), t.dtype, tuple(t.shape)))
+    return code, t.get_device()
+
+
 def _query(name, *args):
     n = C.c_size_t(0)
     _check(getattr(lib(), name)(C.byref(n), *args), name)
     return n.value
 
 
-def _space(workspace, name, device, *args):
+def _space(workspace, name, ref, dev, *args):
     """The caller's workspace, or a new one of the size that query `name` gives."""
     if workspace is None:
-        return _workspace(_query(name, *args), device)
-    _need_cuda(workspace)
-    _expect(workspace, "workspace", (_types().u8,), dim=1)
+        return _types().empty(max(_query(name, *args), 256), dtype=_types().u8, device=ref.device)
+    _dense(workspace, "workspace", _types().u8, (workspace.numel(),), dev)
     return workspace
-
-
-class _Types:
-    def __init__(self):
-        import torch
-        self.f32, self.bf16 = torch.float32, torch.bfloat16
-        self.i32, self.u8 = torch.int32, torch.uint8
-        self.values = (self.f32, self.bf16)
-
-
-_types_cache = None
-
-
-def _types():
-    global _types_cache
-    if _types_cache is None:
-        _types_cache = _Types()
-    return _types_cache
 
 
 @_in_stream
 def dust_layer_norm(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=None):
     """x: CUDA [T, d] (f32 or bf16, rows may be strided); weight, bias: f32 [d]
     or None; returns (y of x's dtype [T, d], mean f32 [T], rstd f32 [T])."""
-    import torch
     ty = _types()
-    ld_x = _rows(x, "x", ty.values)
-    T, d = x.shape
+    code, dev = _values(x, "x", (2,))
+    T, d = shape = x.shape
     if y is None:
-        y = torch.empty((T, d), dtype=x.dtype, device=x.device)
+        y = ty.empty(shape, dtype=x.dtype, device=x.device)
     if mean is None:
-        mean = torch.empty(T, dtype=ty.f32, device=x.device)
+        mean = ty.empty(T, dtype=ty.f32, device=x.device)
     if rstd is None:
-        rstd = torch.empty(T, dtype=ty.f32, device=x.device)
-    ld_y = _rows(y, "y", (x.dtype,), (T, d))
-    for t, name, n in ((weight, "weight", d), (bias, "bias", d), (mean, "mean", T),
-                       (rstd, "rstd", T)):
-        _vector(t, name, ty.f32, (n,))
-    _same_device(x, weight, bias, y, mean, rstd)
-    _check(lib().dust_layer_norm(_ptr(x), _dtype_code(x), ld_x, T, d, _ptr(weight), _ptr(bias),
-                                 float(eps), _ptr(y), ld_y, _ptr(mean), _ptr(rstd),
-                                 _stream(None)), "dust_layer_norm")
+        rstd = ty.empty_like(mean)
+    st = lib().dust_layer_norm(
+        x.data_ptr(), code, _rows(x, "x", x.dtype, shape, dev), T, d,
+        _dense(weight, "weight", ty.f32, (d,), dev), _dense(bias, "bias", ty.f32, (d,), dev),
+        eps, y.data_ptr(), _rows(y, "y", x.dtype, shape, dev),
+        _dense(mean, "mean", ty.f32, (T,), dev), _dense(rstd, "rstd", ty.f32, (T,), dev),
+        ty.stream_of(dev))
+    _check(st, "dust_layer_norm")
     return y, mean, rstd
 
 
@@ -532,38 +549,34 @@ def dust_layer_norm_grad(gy, x, mean, rstd, weight=None, flags=0, gx=None, gweig
     rstd: f32 [T] of the forward; weight: f32 [d] or None. Returns (gx of x's
     dtype [T, d], gweight f32 [d], gbias f32 [d]); ACCUMULATE adds to the
     gweight and gbias that are passed in."""
-    import torch
     ty = _types()
-    ld_x = _rows(x, "x", ty.values)
-    T, d = x.shape
-    ld_gy = _rows(gy, "gy", (x.dtype,), (T, d))
+    code, dev = _values(x, "x", (2,))
+    T, d = shape = x.shape
     if flags & ACCUMULATE and (gweight is None or gbias is None):
         raise ValueError("ACCUMULATE needs the gweight and gbias to add to")
     if gx is None:
-        gx = torch.empty((T, d), dtype=x.dtype, device=x.device)
+        gx = ty.empty(shape, dtype=x.dtype, device=x.device)
     if gweight is None:
-        gweight = torch.empty(d, dtype=ty.f32, device=x.device)
+        gweight = ty.empty(d, dtype=ty.f32, device=x.device)
     if gbias is None:
-        gbias = torch.empty(d, dtype=ty.f32, device=x.device)
-    ld_gx = _rows(gx, "gx", (x.dtype,), (T, d))
-    for t, name, n in ((weight, "weight", d), (mean, "mean", T), (rstd, "rstd", T),
-                       (gweight, "gweight", d), (gbias, "gbias", d)):
-        _vector(t, name, ty.f32, (n,))
-    workspace = _space(workspace, "dust_layer_norm_grad_workspace", x.device, T, d)
-    _same_device(x, gy, mean, rstd, weight, gx, gweight, gbias, workspace)
-    _check(lib().dust_layer_norm_grad(_ptr(gy), ld_gy, _ptr(x), ld_x, _dtype_code(x), T, d,
-                                      _ptr(weight), _ptr(mean), _ptr(rstd), flags, _ptr(gx),
-                                      ld_gx, _ptr(gweight), _ptr(gbias), _ptr(workspace),
-                                      workspace.numel(), _stream(None)),
-           "dust_layer_norm_grad")
+        gbias = ty.empty_like(gweight)
+    workspace = _space(workspace, "dust_layer_norm_grad_workspace", x, dev, T, d)
+    st = lib().dust_layer_norm_grad(
+        gy.data_ptr(), _rows(gy, "gy", x.dtype, shape, dev), x.data_ptr(),
+        _rows(x, "x", x.dtype, shape, dev), code, T, d,
+        _dense(weight, "weight", ty.f32, (d,), dev), _dense(mean, "mean", ty.f32, (T,), dev),
+        _dense(rstd, "rstd", ty.f32, (T,), dev), flags, gx.data_ptr(),
+        _rows(gx, "gx", x.dtype, shape, dev), _dense(gweight, "gweight", ty.f32, (d,), dev),
+        _dense(gbias, "gbias", ty.f32, (d,), dev), workspace.data_ptr(), workspace.numel(),
+        ty.stream_of(dev))
+    _check(st, "dust_layer_norm_grad")
     return gx, gweight, gbias
 
 
 def _head_inputs(H, E):
-    """Sizes and row strides of H [T, d] or [S, T, d] and E [V, d]."""
-    ty = _types()
-    if H.dim() not in (2, 3):
-        raise ValueError("H must be [T, d] or [S, T, d], got shape %s" % (tuple(H.shape),))
+    """dtype code, device, sizes S, T, d, V and the addresses and row strides
+    of H [T, d] or [S, T, d] and E [V, d], as the C calls take them."""
+    code, dev = _values(H, "H", (2, 3))
     if H.dim() == 3:
         S, T, d = H.shape
         if S > 1 and T > 0 and H.stride(0) != T * H.stride(1):
@@ -571,45 +584,41 @@ def _head_inputs(H, E):
         rows = H[0] if S == 1 else H.as_strided((S * T, d), (H.stride(1), H.stride(2)))
     else:
         S, (T, d), rows = 1, H.shape, H
-    ld_h = _rows(rows, "H", ty.values)
-    ld_e = _rows(E, "E", (H.dtype,))
-    if E.shape[1] != d:
+    ld_h = _rows(rows, "H", H.dtype, (S * T, d), dev)
+    if E.dim() != 2 or E.shape[1] != d:
         raise ValueError("E must be [V, d] matching H, got %s" % (tuple(E.shape),))
-    return S, T, d, E.shape[0], ld_h, ld_e
+    V = E.shape[0]
+    return code, dev, S, T, d, V, (H.data_ptr(), ld_h, E.data_ptr(),
+                                   _rows(E, "E", H.dtype, (V, d), dev), code, S, T, d, V)
 
 
-def _loss_outputs(H, S, T, loss, lse, delta, changes):
-    import torch
+def _loss_outputs(H, S, T, dev, loss, lse, delta, changes):
     ty = _types()
-    shape = tuple(H.shape[:-1])
+    shape = H.shape[:-1]
     if loss is None:
-        loss = torch.empty(shape, dtype=ty.f32, device=H.device)
+        loss = ty.empty(shape, dtype=ty.f32, device=H.device)
     if lse is None:
-        lse = torch.empty(shape, dtype=ty.f32, device=H.device)
+        lse = ty.empty_like(loss)
     if delta is None and changes:
-        delta = torch.empty((S - 1, T), dtype=ty.f32, device=H.device)
-    _vector(loss, "loss", ty.f32, shape)
-    _vector(lse, "lse", ty.f32, shape)
-    _vector(delta, "delta", ty.f32, (S - 1, T))
-    return loss, lse, delta
+        delta = ty.empty((S - 1, T), dtype=ty.f32, device=H.device)
+    return loss, lse, delta, (_dense(loss, "loss", ty.f32, shape, dev),
+                              _dense(lse, "lse", ty.f32, shape, dev)), \
+        _dense(delta, "delta", ty.f32, (S - 1, T), dev)
 
 
-def _grad_outputs(H, E, lse, gloss, flags, gH, gE, gE_dtype):
-    import torch
+def _grad_outputs(H, E, d, dev, flags, gH, gE, gE_dtype):
     ty = _types()
-    shape = tuple(H.shape[:-1])
-    _vector(lse, "lse", ty.f32, shape)
-    _vector(gloss, "gloss", ty.f32, shape)
     if flags & ACCUMULATE and gE is None:
         raise ValueError("ACCUMULATE needs the gE to add to")
     if gH is None:
-        gH = torch.empty(tuple(H.shape), dtype=H.dtype, device=H.device)
+        gH = ty.empty(H.shape, dtype=H.dtype, device=H.device)
     if gE is None:
-        gE = torch.empty(tuple(E.shape), dtype=gE_dtype or ty.f32, device=E.device)
-    _expect(gH, "gH", (H.dtype,), shape=H.shape)
-    _need_cuda(gH)
-    _vector(gE, "gE", gE.dtype if gE.dtype in ty.values else ty.f32, tuple(E.shape))
-    return gH, gE
+        gE = ty.empty(E.shape, dtype=gE_dtype or ty.f32, device=E.device)
+    gcode = ty.code.get(gE.dtype)
+    if gcode is None:
+        raise ValueError("gE must be f32 or bf16, got %s" % gE.dtype)
+    return gH, gE, (flags, _dense(gH, "gH", H.dtype, H.shape, dev), d,
+                    _dense(gE, "gE", gE.dtype, E.shape, dev), gcode)
 
 
 @_in_stream
@@ -619,17 +628,14 @@ def dust_head_loss(H, E, targets, scale=1.0, changes=False, loss=None, lse=None,
     targets: i32 [T], negative where a token has none. Returns (loss, lse), f32
     of H's leading shape, and with changes=True also delta f32 [S - 1, T], each
     later slice's loss minus the first one's. No logits are kept."""
-    S, T, d, V, ld_h, ld_e = _head_inputs(H, E)
     ty = _types()
-    _vector(targets, "targets", ty.i32, (T,))
-    loss, lse, delta = _loss_outputs(H, S, T, loss, lse, delta, changes)
-    dt = _dtype_code(H)
-    workspace = _space(workspace, "dust_head_loss_workspace", H.device, S, T, d, V, dt)
-    _same_device(H, E, targets, loss, lse, delta, workspace)
-    _check(lib().dust_head_loss(_ptr(H), ld_h, _ptr(E), ld_e, dt, S, T, d, V, _ptr(targets),
-                                float(scale), _ptr(loss), _ptr(lse), _ptr(delta),
-                                _ptr(workspace), workspace.numel(), _stream(None)),
-           "dust_head_loss")
+    code, dev, S, T, d, V, operands = _head_inputs(H, E)
+    loss, lse, delta, outs, delta_at = _loss_outputs(H, S, T, dev, loss, lse, delta, changes)
+    workspace = _space(workspace, "dust_head_loss_workspace", H, dev, S, T, d, V, code)
+    st = lib().dust_head_loss(*operands, _dense(targets, "targets", ty.i32, (T,), dev), scale,
+                              *outs, delta_at, workspace.data_ptr(), workspace.numel(),
+                              ty.stream_of(dev))
+    _check(st, "dust_head_loss")
     return (loss, lse) if delta is None else (loss, lse, delta)
 
 
@@ -640,28 +646,26 @@ def dust_head_loss_grad(H, E, targets, lse, gloss, scale=1.0, flags=0, gH=None, 
     leading shape) and the forward's lse: returns (gH of H's shape and dtype,
     gE [V, d], f32 unless gE_dtype is bf16); ACCUMULATE adds to the f32 gE that
     is passed in."""
-    S, T, d, V, ld_h, ld_e = _head_inputs(H, E)
     ty = _types()
-    _vector(targets, "targets", ty.i32, (T,))
-    gH, gE = _grad_outputs(H, E, lse, gloss, flags, gH, gE, gE_dtype)
-    dt = _dtype_code(H)
-    workspace = _space(workspace, "dust_head_loss_grad_workspace", H.device, S, T, d, V, dt)
-    _same_device(H, E, targets, lse, gloss, gH, gE, workspace)
-    _check(lib().dust_head_loss_grad(_ptr(H), ld_h, _ptr(E), ld_e, dt, S, T, d, V, _ptr(targets),
-                                     float(scale), _ptr(lse), _ptr(gloss), flags, _ptr(gH), d,
-                                     _ptr(gE), _dtype_code(gE), _ptr(workspace),
-                                     workspace.numel(), _stream(None)), "dust_head_loss_grad")
+    code, dev, S, T, d, V, operands = _head_inputs(H, E)
+    shape = H.shape[:-1]
+    gH, gE, outs = _grad_outputs(H, E, d, dev, flags, gH, gE, gE_dtype)
+    workspace = _space(workspace, "dust_head_loss_grad_workspace", H, dev, S, T, d, V, code)
+    st = lib().dust_head_loss_grad(*operands, _dense(targets, "targets", ty.i32, (T,), dev),
+                                   scale, _dense(lse, "lse", ty.f32, shape, dev),
+                                   _dense(gloss, "gloss", ty.f32, shape, dev), *outs,
+                                   workspace.data_ptr(), workspace.numel(), ty.stream_of(dev))
+    _check(st, "dust_head_loss_grad")
     return gH, gE
 
 
-def _teacher_inputs(ids, teacher, T):
+def _teacher_inputs(ids, teacher, T, dev):
     ty = _types()
     if ids.dim() != 2:
         raise ValueError("ids must be [T, K], got shape %s" % (tuple(ids.shape),))
     K = ids.shape[1]
-    _vector(ids, "ids", ty.i32, (T, K))
-    _vector(teacher, "teacher", ty.f32, (T, K))
-    return K
+    return K, (_dense(ids, "ids", ty.i32, (T, K), dev),
+               _dense(teacher, "teacher", ty.f32, (T, K), dev), K)
 
 
 @_in_stream
@@ -671,21 +675,18 @@ def dust_distill_loss(H, E, ids, teacher, scale=1.0, changes=False, loss=None, l
     dust_head_loss; ids: i32 [T, K], negative where an entry is absent; teacher:
     f32 [T, K]. Returns (loss, lse, student), student f32 [..., K] the scaled
     logits at ids, and with changes=True also delta f32 [S - 1, T]."""
-    import torch
-    S, T, d, V, ld_h, ld_e = _head_inputs(H, E)
-    K = _teacher_inputs(ids, teacher, T)
-    loss, lse, delta = _loss_outputs(H, S, T, loss, lse, delta, changes)
-    shape = tuple(H.shape[:-1]) + (K,)
+    ty = _types()
+    code, dev, S, T, d, V, operands = _head_inputs(H, E)
+    K, entries = _teacher_inputs(ids, teacher, T, dev)
+    loss, lse, delta, outs, delta_at = _loss_outputs(H, S, T, dev, loss, lse, delta, changes)
+    shape = (*H.shape[:-1], K)
     if student is None:
-        student = torch.empty(shape, dtype=_types().f32, device=H.device)
-    _vector(student, "student", _types().f32, shape)
-    dt = _dtype_code(H)
-    workspace = _space(workspace, "dust_distill_loss_workspace", H.device, S, T, d, V, K, dt)
-    _same_device(H, E, ids, teacher, loss, lse, student, delta, workspace)
-    _check(lib().dust_distill_loss(_ptr(H), ld_h, _ptr(E), ld_e, dt, S, T, d, V, _ptr(ids),
-                                   _ptr(teacher), K, float(scale), _ptr(loss), _ptr(lse),
-                                   _ptr(student), _ptr(delta), _ptr(workspace),
-                                   workspace.numel(), _stream(None)), "dust_distill_loss")
+        student = ty.empty(shape, dtype=ty.f32, device=H.device)
+    workspace = _space(workspace, "dust_distill_loss_workspace", H, dev, S, T, d, V, K, code)
+    st = lib().dust_distill_loss(*operands, *entries, scale, *outs,
+                                 _dense(student, "student", ty.f32, shape, dev), delta_at,
+                                 workspace.data_ptr(), workspace.numel(), ty.stream_of(dev))
+    _check(st, "dust_distill_loss")
     return (loss, lse, student) if delta is None else (loss, lse, student, delta)
 
 
@@ -694,18 +695,19 @@ def dust_distill_loss_grad(H, E, ids, teacher, lse, student, gloss, scale=1.0, f
                            gE=None, gE_dtype=None, workspace=None):
     """The gradients of dust_distill_loss for gloss and the forward's lse and
     student; returns (gH, gE) as dust_head_loss_grad does."""
-    S, T, d, V, ld_h, ld_e = _head_inputs(H, E)
-    K = _teacher_inputs(ids, teacher, T)
-    _vector(student, "student", _types().f32, tuple(H.shape[:-1]) + (K,))
-    gH, gE = _grad_outputs(H, E, lse, gloss, flags, gH, gE, gE_dtype)
-    dt = _dtype_code(H)
-    workspace = _space(workspace, "dust_distill_loss_grad_workspace", H.device, S, T, d, V, K, dt)
-    _same_device(H, E, ids, teacher, lse, student, gloss, gH, gE, workspace)
-    _check(lib().dust_distill_loss_grad(_ptr(H), ld_h, _ptr(E), ld_e, dt, S, T, d, V, _ptr(ids),
-                                        _ptr(teacher), K, float(scale), _ptr(lse), _ptr(student),
-                                        _ptr(gloss), flags, _ptr(gH), d, _ptr(gE),
-                                        _dtype_code(gE), _ptr(workspace), workspace.numel(),
-                                        _stream(None)), "dust_distill_loss_grad")
+    ty = _types()
+    code, dev, S, T, d, V, operands = _head_inputs(H, E)
+    K, entries = _teacher_inputs(ids, teacher, T, dev)
+    shape = H.shape[:-1]
+    gH, gE, outs = _grad_outputs(H, E, d, dev, flags, gH, gE, gE_dtype)
+    workspace = _space(workspace, "dust_distill_loss_grad_workspace", H, dev, S, T, d, V, K, code)
+    st = lib().dust_distill_loss_grad(*operands, *entries, scale,
+                                      _dense(lse, "lse", ty.f32, shape, dev),
+                                      _dense(student, "student", ty.f32, (*shape, K), dev),
+                                      _dense(gloss, "gloss", ty.f32, shape, dev), *outs,
+                                      workspace.data_ptr(), workspace.numel(),
+                                      ty.stream_of(dev))
+    _check(st, "dust_distill_loss_grad")
     return gH, gE
 
 

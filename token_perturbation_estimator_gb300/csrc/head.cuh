@@ -13,6 +13,7 @@ struct HeadTargets {
     const int32_t* ids;     // [T][K]; outside [0, V): absent
     const float* teacher;   // [T][K] teacher logits, or null
     int64_t K;
+    bool many;              // distillation
 };
 
 struct HeadProblem {
@@ -58,6 +59,16 @@ struct HeadCounts {      // written on the device by the row pass
 constexpr int kHeadTile = 256;  // rows of a CTA pair's tile; its columns too, or half
 constexpr int kHeadBox = 64;    // rows and columns of a TMA box
 
+// The teacher's entries of each token in order of their ids (absent ones
+// left out), and where those of each half tile of columns start.
+struct HeadPicks {
+    const int2* entries;    // [T][K]: id, place among the token's entries
+    const uint16_t* starts; // [T][bins + 1]: the first entry of a half tile
+    int bins;               // half tiles
+    int64_t K;
+    float* student;         // [rows][K], written
+};
+
 // Partial softmax sums of one row over half a tile's columns: the largest
 // logit rounded up to a whole number in units of log 2, and the sum of
 // 2^(logit - that).
@@ -74,6 +85,7 @@ struct HeadLogits {
     HeadPart* part;      // [2 * column tiles][ld_part]
     int64_t ld_part;
     float* picked;       // [rows] scaled logits of the targets
+    HeadPicks picks;     // or entries null
     // gradient
     const HeadCounts* counts;
     const HeadRow* rows;

@@ -48,8 +48,10 @@ dust_status check_teacher_sizes(int64_t S, int64_t T, int64_t K) {
 }
 
 // A problem's sizes alone, for the workspace queries.
-HeadProblem sizes(int64_t S, int64_t T, int64_t d, int64_t V, dust_dtype dtype) {
-    return {nullptr, nullptr, d, d, dtype == DUST_BF16, S, T, d, V, {nullptr, nullptr, 1}, 1.0f};
+HeadProblem sizes(int64_t S, int64_t T, int64_t d, int64_t V, int64_t K, bool distill,
+                  dust_dtype dtype) {
+    return {nullptr, nullptr, d, d, dtype == DUST_BF16, S, T, d, V, {nullptr, nullptr, K, distill},
+            1.0f};
 }
 
 // The checks shared by the four head calls, in one place: sizes, scale,
@@ -69,7 +71,7 @@ dust_status check_head(const void* H, int64_t ld_h, const void* E, int64_t ld_e,
 
 dust_status run_loss(const HeadProblem& p, float* loss, float* lse, float* student, float* delta,
                      size_t need, void* ws, size_t ws_bytes, void* stream) {
-    if (!lse || (p.tg.teacher && !student)) return DUST_ERR_INVALID_ARG;
+    if (!lse || (p.tg.many && !student)) return DUST_ERR_INVALID_ARG;
     if (!ws_ok(ws, ws_bytes, need)) return DUST_ERR_WORKSPACE;
     return cuda_status(launch_head_loss(p, loss, lse, student, delta, ws,
                                         static_cast<cudaStream_t>(stream)));
@@ -103,7 +105,7 @@ dust_status empty_grad(int64_t V, int64_t d, uint32_t flags, void* gE, dust_dtyp
 dust_status run_grad(const HeadProblem& p, const float* lse, const float* student,
                      const float* gloss, uint32_t flags, void* gH, int64_t ld_gh, void* gE,
                      dust_dtype gE_dtype, size_t need, void* ws, size_t ws_bytes, void* stream) {
-    if (!lse || !gloss || (p.tg.teacher && !student)) return DUST_ERR_INVALID_ARG;
+    if (!lse || !gloss || (p.tg.many && !student)) return DUST_ERR_INVALID_ARG;
     if (!gH && !gE) return DUST_OK;
     if (!ws_ok(ws, ws_bytes, need)) return DUST_ERR_WORKSPACE;
     return cuda_status(launch_head_grad(p, lse, student, gloss, (flags & DUST_ACCUMULATE) != 0, gH,
@@ -174,7 +176,7 @@ dust_status dust_head_loss_workspace(size_t* bytes, int64_t S, int64_t T, int64_
     if (!bytes) return DUST_ERR_INVALID_ARG;
     const dust_status st = check_head_sizes(S, T, d, V, dtype);
     if (st != DUST_OK) return st;
-    *bytes = head_loss_workspace_bytes(sizes(S, T, d, V, dtype));
+    *bytes = head_loss_workspace_bytes(sizes(S, T, d, V, 1, false, dtype));
     return DUST_OK;
 }
 
@@ -185,7 +187,7 @@ dust_status dust_head_loss(const void* H, int64_t ld_h, const void* E, int64_t l
     const dust_status st = check_head(H, ld_h, E, ld_e, dtype, S, T, d, V, targets, scale);
     if (st != DUST_OK || T == 0) return st;
     const HeadProblem p = {H, E, ld_h, ld_e, dtype == DUST_BF16, S, T, d, V,
-                           {targets, nullptr, 1}, scale};
+                           {targets, nullptr, 1, false}, scale};
     return run_loss(p, loss, lse, nullptr, delta,
                     head_loss_workspace_bytes(p), workspace, ws_bytes,
                     stream);
@@ -196,7 +198,7 @@ dust_status dust_head_loss_grad_workspace(size_t* bytes, int64_t S, int64_t T, i
     if (!bytes) return DUST_ERR_INVALID_ARG;
     const dust_status st = check_head_sizes(S, T, d, V, dtype);
     if (st != DUST_OK) return st;
-    *bytes = head_grad_workspace_bytes(sizes(S, T, d, V, dtype));
+    *bytes = head_grad_workspace_bytes(sizes(S, T, d, V, 1, false, dtype));
     return DUST_OK;
 }
 
@@ -211,7 +213,7 @@ dust_status dust_head_loss_grad(const void* H, int64_t ld_h, const void* E, int6
     if (st != DUST_OK) return st;
     if (T == 0) return empty_grad(V, d, flags, gE, gE_dtype, stream);
     const HeadProblem p = {H, E, ld_h, ld_e, dtype == DUST_BF16, S, T, d, V,
-                           {targets, nullptr, 1}, scale};
+                           {targets, nullptr, 1, false}, scale};
     return run_grad(p, lse, nullptr, gloss, flags, gH, ld_gh, gE, gE_dtype,
                     head_grad_workspace_bytes(p), workspace, ws_bytes, stream);
 }
@@ -222,7 +224,7 @@ dust_status dust_distill_loss_workspace(size_t* bytes, int64_t S, int64_t T, int
     dust_status st = check_head_sizes(S, T, d, V, dtype);
     if (st == DUST_OK) st = check_teacher_sizes(S, T, K);
     if (st != DUST_OK) return st;
-    *bytes = head_loss_workspace_bytes(sizes(S, T, d, V, dtype));
+    *bytes = head_loss_workspace_bytes(sizes(S, T, d, V, K, true, dtype));
     return DUST_OK;
 }
 
@@ -236,7 +238,7 @@ dust_status dust_distill_loss(const void* H, int64_t ld_h, const void* E, int64_
     if (st != DUST_OK || T == 0) return st;
     if (!teacher) return DUST_ERR_INVALID_ARG;
     const HeadProblem p = {H, E, ld_h, ld_e, dtype == DUST_BF16, S, T, d, V,
-                           {ids, teacher, K}, scale};
+                           {ids, teacher, K, true}, scale};
     return run_loss(p, loss, lse, student, delta,
                     head_loss_workspace_bytes(p), workspace, ws_bytes,
                     stream);
@@ -248,7 +250,7 @@ dust_status dust_distill_loss_grad_workspace(size_t* bytes, int64_t S, int64_t T
     dust_status st = check_head_sizes(S, T, d, V, dtype);
     if (st == DUST_OK) st = check_teacher_sizes(S, T, K);
     if (st != DUST_OK) return st;
-    *bytes = head_grad_workspace_bytes(sizes(S, T, d, V, dtype));
+    *bytes = head_grad_workspace_bytes(sizes(S, T, d, V, K, true, dtype));
     return DUST_OK;
 }
 
@@ -266,7 +268,7 @@ dust_status dust_distill_loss_grad(const void* H, int64_t ld_h, const void* E, i
     if (T == 0) return empty_grad(V, d, flags, gE, gE_dtype, stream);
     if (!teacher) return DUST_ERR_INVALID_ARG;
     const HeadProblem p = {H, E, ld_h, ld_e, dtype == DUST_BF16, S, T, d, V,
-                           {ids, teacher, K}, scale};
+                           {ids, teacher, K, true}, scale};
     return run_grad(p, lse, student, gloss, flags, gH, ld_gh, gE, gE_dtype,
                     head_grad_workspace_bytes(p), workspace, ws_bytes, stream);
 }

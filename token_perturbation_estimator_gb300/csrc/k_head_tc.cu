@@ -88,6 +88,7 @@ struct TcArgs {
     HeadPart* part;
     int64_t ld_part;
     float* picked;
+    HeadPicks picks;
     const HeadRow* info;       // kFactor
     int64_t g_cols;
     const int32_t* row_of;     // kMul
@@ -330,6 +331,9 @@ struct RowOf {
     bool live;
     HeadRow info;      // kLse: the target alone
     int64_t out_row;
+    int64_t token;     // kLse with a teacher's entries: the next one here, their end
+    int pick, picks_end;
+    int2 entry;
 };
 
 // Epilogue of one unit for one warp: rows 32 q + lane of this CTA's half,
@@ -350,8 +354,17 @@ struct Epilogue {
         o.out_row = o.row;
         if (MODE == kLse) {
             o.live = o.row < plan.rows;
-            if (o.live && a.targets)
-                o.info.target = a.targets[static_cast<uint32_t>(o.row) % static_cast<uint32_t>(a.T)];
+            o.pick = o.picks_end = 0;
+            if (o.live) {
+                o.token = static_cast<uint32_t>(o.row) % static_cast<uint32_t>(a.T);
+                if (a.targets) o.info.target = a.targets[o.token];
+                if (a.picks.entries) {
+                    const uint16_t* at =
+                        a.picks.starts + o.token * (a.picks.bins + 1) + kShare * w.index + h;
+                    o.pick = at[0];
+                    o.picks_end = at[1];
+                }
+            }
         } else if (MODE == kFactor) {
             o.live = o.row < plan.rows;
             if (o.live) o.info = a.info[o.row];
@@ -364,7 +377,12 @@ struct Epilogue {
         return o;
     }
 
-    __device__ void lse(const Tile& w, const RowOf& o, uint32_t taddr) {
+    // The second step of the loads ahead: an entry needs its place first.
+    __device__ void first_pick(RowOf& o) const {
+        if (o.pick < o.picks_end) o.entry = a.picks.entries[o.token * a.picks.K + o.pick];
+    }
+
+    __device__ void lse(const Tile& w, RowOf o, uint32_t taddr) {
         const int cols = a.bn / kShare;
         const float c = a.scale * kLog2e;
         const int32_t first = static_cast<int32_t>(w.n0) + h * cols;
@@ -387,6 +405,19 @@ struct Epilogue {
                 softmax_block<true>(v, 32, c, m, s);
             else
                 softmax_block<false>(v, left, c, m, s);
+        }
+        // The teacher's entries among these columns: one column at a time for
+        // all rows that want it, until no row wants one.
+        int want = o.pick < o.picks_end ? o.entry.x - first : -1;
+        while (const uint32_t mask = __ballot_sync(0xffffffffu, want >= 0)) {
+            const int col = __shfl_sync(0xffffffffu, want, __ffs(mask) - 1);
+            const float x = tc::tmem_ld_column(taddr + h * cols + col);
+            if (want == col) {
+                a.picks.student[o.row * a.picks.K + o.entry.y] = a.scale * x;
+                ++o.pick;
+                first_pick(o);
+                want = o.pick < o.picks_end ? o.entry.x - first : -1;
+            }
         }
         if (o.live)
             a.part[(static_cast<int64_t>(w.index) * kShare + h) * a.ld_part + o.row] = {m, s};
@@ -668,6 +699,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Tile w = t >= 0 ? plan.at(a, t) : Tile{};
         RowOf o = {};
         if (t >= 0) o = epi.begin(w, plan);
+        if (MODE == kLse) epi.first_pick(o);
         for (int j = 0; t >= 0; ++j) {
             const int acc = j & 1;
             const bool ok = tc::mbar_wait_for(&ctl->tfull[acc], (j >> 1) & 1, tile_ns);
@@ -691,6 +723,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_at(tc::at_rank(&ctl->tempty[acc], 0));
+            if (MODE == kLse) epi.first_pick(next_o);
             w = next;
             o = next_o;
         }
@@ -885,6 +918,7 @@ cudaError_t launch_head_lse(const HeadLogits& h, cudaStream_t s) {
     a.part = h.part;
     a.ld_part = h.ld_part;
     a.picked = h.picked;
+    a.picks = h.picks;
     return launch_tc<kLse, 1>(m, a, tiles_of(a.rows, kHeadTile) * tiles_of(a.n, a.bn), s);
 }
 
