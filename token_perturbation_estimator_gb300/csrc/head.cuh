@@ -100,7 +100,7 @@ cudaError_t launch_head_factor(const HeadLogits& a, cudaStream_t s);
 
 // Slices of the summed dimension of each product, for the sizes of one piece.
 struct HeadCuts { int gh, ge; };
-HeadCuts head_cuts(int64_t rows, int64_t n, int64_t d, int planes, bool gh, bool ge);
+HeadCuts head_cuts(int64_t rows, int64_t n, int64_t d, int planes);
 
 // gH += alpha G E_piece and gE_piece = alpha G^T H, one launch; slices' sums
 // are added up by one more.

@@ -64,10 +64,11 @@ __device__ __forceinline__ void report_id(unsigned int* status) {
 
 // ------------------------------------------------------------------ loss
 
-constexpr int kJoinLanes = 8;  // threads that share a row's partial sums
+constexpr int kJoinLanes = 32;  // threads that share a row's partial sums, at most
 
-// A row's partial sums joined, and its cross entropy. Eight threads per row
-// each take every eighth partial; the eight are joined in order.
+// A row's partial sums joined, and its cross entropy. The threads of a row (8
+// to 32, one per warp) each take every so manieth partial; theirs are joined
+// in order.
 __global__ void __launch_bounds__(32 * kJoinLanes)
     k_head_join(const HeadPart* __restrict__ part, int64_t ld, int n_part, int64_t R, int64_t T,
                 const int32_t* __restrict__ targets, int64_t V,
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(32 * kJoinLanes)
     pdl_wait();
     pdl_trigger();
     __shared__ HeadPart sh[kJoinLanes][32];
-    const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, k = threadIdx.x >> 5, lanes = blockDim.x >> 5;
     const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     float m = -INFINITY, s = 0.0f;
     const auto join = [&](const HeadPart& p) {
@@ -86,11 +87,12 @@ __global__ void __launch_bounds__(32 * kJoinLanes)
         m = nm;
     };
     if (r < R)
-        for (int i = k; i < n_part; i += kJoinLanes) join(part[i * ld + r]);
+#pragma unroll 4
+        for (int i = k; i < n_part; i += lanes) join(part[i * ld + r]);
     sh[k][lane] = {m, s};
     __syncthreads();
     if (k != 0 || r >= R) return;
-    for (int i = 1; i < kJoinLanes; ++i) join(sh[i][lane]);
+    for (int i = 1; i < lanes; ++i) join(sh[i][lane]);
     // m is a whole number of powers of two; one rounding for each result.
     const double l = static_cast<double>(m) * 0.69314718055994530942 +
                      static_cast<double>(logf(s));
@@ -522,6 +524,7 @@ struct GradSpace {
     float2* teacher;
     __nv_bfloat16 *h, *e, *g;
     float *gh_acc, *ge_acc;
+    HeadCuts cuts;
     int64_t piece;
     size_t total;
 };
@@ -536,14 +539,10 @@ GradSpace carve_grad(void* ws, const HeadProblem& p) {
     w.row_of = c.take<int32_t>(R);
     w.place = c.take<int32_t>(R);
     w.teacher = c.take<float2>(p.T);
-    // Sized for both gradients, whichever are asked for.
-    const int P = static_cast<int>(planes);
-    const HeadCuts both = head_cuts(R, std::min(w.piece, p.V), p.d, P, true, true);
-    const HeadCuts gh = head_cuts(R, std::min(w.piece, p.V), p.d, P, true, false);
-    const HeadCuts ge = head_cuts(R, std::min(w.piece, p.V), p.d, P, false, true);
-    const int cut0 = std::max(both.gh, gh.gh), cut1 = std::max(both.ge, ge.ge);
-    w.gh_acc = c.take<float>(w.piece < p.V || cut0 > 1 ? head_acc_floats(R, p.d, cut0) : 0);
-    w.ge_acc = c.take<float>(cut1 > 1 ? head_acc_floats(w.piece, p.d, cut1) : 0);
+    // As for both gradients, whichever are asked for.
+    w.cuts = head_cuts(R, std::min(w.piece, p.V), p.d, static_cast<int>(planes));
+    w.gh_acc = c.take<float>(w.piece < p.V || w.cuts.gh > 1 ? head_acc_floats(R, p.d, w.cuts.gh) : 0);
+    w.ge_acc = c.take<float>(w.cuts.ge > 1 ? head_acc_floats(w.piece, p.d, w.cuts.ge) : 0);
     w.g = c.take<__nv_bfloat16>(planes * up(R, kHeadTile) * w.piece);
     w.h = c.take<__nv_bfloat16>(planes * R * dp);
     w.e = c.take<__nv_bfloat16>(planes * p.V * dp);
@@ -615,7 +614,8 @@ cudaError_t loss_typed(const HeadProblem& p, float* loss, float* lse, float* stu
         a.picks = {w.entries, w.starts, bins, p.tg.K, student};
     }
     DUST_TRY(launch_head_lse(a, s));
-    DUST_TRY(launch_pdl(k_head_join, dim3(grid_of(R, 32)), dim3(32 * kJoinLanes), 0, s, w.part,
+    const int join_lanes = std::min(kJoinLanes, std::max(8, bins / 8));
+    DUST_TRY(launch_pdl(k_head_join, dim3(grid_of(R, 32)), dim3(32 * join_lanes), 0, s, w.part,
                         a.ld_part, bins, R, p.T, a.targets, p.V, w.picked, loss, lse, st));
     if (distill && loss)
         DUST_TRY(launch_pdl(k_head_distill, dim3(grid_of(R, 8)), dim3(256), 0, s, R, p.T, p.tg,
@@ -655,9 +655,6 @@ cudaError_t grad_typed(const HeadProblem& p, const float* lse, const float* stud
     a.rows = w.rows;
     const int64_t g_rows = up(R, kHeadTile);
     a.G = {w.g, g_rows, w.piece, w.piece, static_cast<int>(planes)};
-    const HeadCuts cuts =
-        head_cuts(R, std::min(w.piece, p.V), p.d, static_cast<int>(planes), gH != nullptr,
-                  gE != nullptr);
     for (int64_t v0 = 0; v0 < p.V; v0 += w.piece) {
         const int64_t n = std::min(w.piece, p.V - v0);
         a.v0 = v0;
@@ -686,9 +683,9 @@ cudaError_t grad_typed(const HeadProblem& p, const float* lse, const float* stud
         m.ld_gh = ld_gh;
         m.gh_bf16 = bf16;
         // One choice for all pieces: gH's slices run on across them.
-        m.cuts = cuts;
-        m.gh_acc = w.piece < p.V || cuts.gh > 1 ? w.gh_acc : nullptr;
-        m.ge_acc = cuts.ge > 1 ? w.ge_acc : nullptr;
+        m.cuts = w.cuts;
+        m.gh_acc = w.piece < p.V || w.cuts.gh > 1 ? w.gh_acc : nullptr;
+        m.ge_acc = w.cuts.ge > 1 ? w.ge_acc : nullptr;
         m.first = v0 == 0;
         m.last = v0 + n == p.V;
         m.gE = gE ? static_cast<unsigned char*>(gE) + v0 * p.d * (gE_bf16 ? 2 : 4) : nullptr;

@@ -41,6 +41,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
 namespace {
 
+int64_t tiles_of(int64_t n, int64_t by) { return (n + by - 1) / by; }
+
 constexpr int kHalf = 128;                        // rows of A per CTA
 constexpr int kBoxBytes = kHeadBox * kHeadBox * 2;
 constexpr int kStageBytes = 4 * kBoxBytes;        // two boxes of A, two of B
@@ -863,14 +865,33 @@ cudaError_t launch_tc(const CUtensorMap (&m)[4], TcArgs a, int64_t tiles, cudaSt
                       m[0], m[1], m[2], m[3], a);
 }
 
-int64_t tiles_of(int64_t n, int64_t by) { return (n + by - 1) / by; }
+constexpr int kPairs = 76;  // CTA pairs of a whole GPU, for the choices below
 
-constexpr int kPairs = 76;     // CTA pairs of a whole GPU, for the choices below
-constexpr int kMinSteps = 16;  // the shortest slice worth its partial sums: 64 x 16 deep, or a
-                               // quarter of that where a step is six products
-constexpr int kMaxCut = 64;
+// Columns of the tiles of `rows` x `n` logits: 128 where that ends sooner,
+// counted in rounds of the pairs. A narrow tile takes about four fifths of a
+// wide one's time (it loads three quarters of the operands).
+int logit_columns(int64_t rows, int64_t n) {
+    const int64_t mt = tiles_of(rows, kHeadTile);
+    const int64_t wide = tiles_of(mt * tiles_of(n, 256), kPairs) * 20;
+    const int64_t narrow = tiles_of(mt * tiles_of(n, 128), kPairs) * 16;
+    return narrow < wide ? 128 : 256;
+}
 
-int product_columns(int64_t d) { return d <= 128 ? 128 : 256; }
+// Columns of the tiles of the products: by what is computed past d.
+int product_columns(int64_t d) { return tiles_of(d, 128) * 16 < tiles_of(d, 256) * 20 ? 128 : 256; }
+
+// When the last pair is done, in steps, if n_long units of c_long steps and
+// then n_short of c_short are dealt as Plan::unit() does.
+int64_t makespan(int64_t n_long, int64_t c_long, int64_t n_short, int64_t c_short) {
+    const int64_t q = n_long / kPairs, high = n_long % kPairs, low = kPairs - high;
+    const int64_t lo = q * c_long, hi = lo + (high ? c_long : 0);
+    if (n_short == 0) return hi;
+    const int64_t rounds = high ? tiles_of(c_long, c_short) : 0;
+    if (n_short <= rounds * low) return std::max(hi, lo + tiles_of(n_short, low) * c_short);
+    const int64_t rest = n_short - rounds * low, full = rest / kPairs, left = rest % kPairs;
+    return std::max(high ? hi + (full + (left > 0)) * c_short : 0,
+                    lo + (rounds + full + (left > high)) * c_short);
+}
 
 // Row tiles that run together: half of the pairs that are resident, so that
 // two columns of tiles are in flight.
@@ -878,25 +899,39 @@ constexpr int kGroup = 38;
 
 }  // namespace
 
-int head_loss_columns(int64_t rows, int64_t V) {
-    // Narrower tiles while the wide ones leave pairs idle.
-    return tiles_of(rows, kHeadTile) * tiles_of(V, 256) < kPairs ? 128 : 256;
-}
+int head_loss_columns(int64_t rows, int64_t V) { return logit_columns(rows, V); }
 
-// Slices of the summed dimension for the tiles of gH (n of them added over)
-// and gE (rows of them): more than one where a product's few tiles would each
-// take much longer than an even share of the work.
-HeadCuts head_cuts(int64_t rows, int64_t n, int64_t d, int planes, bool gh, bool ge) {
+// Slices of the summed dimension of each product: 1 where whole tiles share
+// the pairs evenly (within a quarter), else the pair of cuts that ends
+// soonest, an epilogue being worth 4 steps of one product, and a cut product's
+// partial sums and their adding up 12 steps and a third of one per unit.
+HeadCuts head_cuts(int64_t rows, int64_t n, int64_t d, int planes) {
+    const int64_t pairs = planes == 1 ? 1 : 6;
     const int64_t nt = tiles_of(d, product_columns(d));
-    const int64_t t0 = gh ? tiles_of(rows, kHeadTile) * nt : 0, s0 = tiles_of(n, 64);
-    const int64_t t1 = ge ? tiles_of(n, kHeadTile) * nt : 0, s1 = tiles_of(rows, 64);
-    const int64_t share = std::max<int64_t>((t0 * s0 + t1 * s1) / kPairs,
-                                            planes == 1 ? kMinSteps : kMinSteps / 4);
-    const auto cut = [&](int64_t tiles, int64_t steps) -> int {
-        if (tiles == 0 || 4 * steps <= 5 * share) return 1;
-        return static_cast<int>(std::min<int64_t>(tiles_of(steps, share), kMaxCut));
+    const int64_t t[2] = {tiles_of(rows, kHeadTile) * nt, tiles_of(n, kHeadTile) * nt};
+    const int64_t steps[2] = {tiles_of(n, 64), tiles_of(rows, 64)};
+    const auto ends = [&](int64_t a, int64_t b) {
+        const int64_t c0 = tiles_of(steps[0], a) * pairs + 4, c1 = tiles_of(steps[1], b) * pairs + 4;
+        return c1 > c0 ? makespan(t[1] * b, c1, t[0] * a, c0) : makespan(t[0] * a, c0, t[1] * b, c1);
     };
-    return {cut(t0, s0), cut(t1, s1)};
+    HeadCuts best = {1, 1};
+    int64_t least = 3 * ends(1, 1);
+    const int64_t even = (t[0] * steps[0] + t[1] * steps[1]) * pairs / kPairs;
+    if (4 * least <= 3 * 5 * even) return best;
+    constexpr int kCuts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 64};
+    for (const int a : kCuts) {
+        if (a > steps[0] || (a > 1 && t[0] * a > 4 * kPairs)) break;
+        for (const int b : kCuts) {
+            if (b > steps[1] || (b > 1 && t[1] * b > 4 * kPairs)) break;
+            const int64_t e = 3 * ends(a, b) + (a > 1 ? 36 + t[0] * a : 0) +
+                              (b > 1 ? 36 + t[1] * b : 0);
+            if (e < least) {
+                least = e;
+                best = {a, b};
+            }
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_head_lse(const HeadLogits& h, cudaStream_t s) {
@@ -936,7 +971,7 @@ cudaError_t launch_head_factor(const HeadLogits& h, cudaStream_t s) {
     a.v0 = h.v0;
     a.counts = h.counts;
     a.planes = h.H.planes;
-    a.bn = 256;
+    a.bn = logit_columns(a.rows, a.n);
     a.group = kGroup;
     a.scale = h.scale;
     a.info = h.rows;
