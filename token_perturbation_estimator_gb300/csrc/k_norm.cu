@@ -15,9 +15,10 @@
 // instructions were reductions and the forward at 65536 x 2048 bf16 was bound
 // by issue at 118 us; with a warp per row but loads straight into registers,
 // it was bound by latency at the same 118 us.
-// Rows that start on 16 bytes are read and written 16 bytes a lane; others
-// value by value, neighbouring lanes on neighbouring values (bf16 ones, 2
-// bytes, straight into registers: cp.async takes 4 at least).
+// Rows that start on 16 bytes are read and written 16 bytes a lane. Others are
+// copied as they lie, from the 16 bytes that hold their first value on, and
+// taken from shared memory value by value, neighbouring lanes on neighbouring
+// values.
 //
 // The backward adds its rows' gy n and gy per column in registers, the CTA's
 // warps add theirs up in shared memory, and each CTA leaves one partial row;
@@ -49,41 +50,70 @@ constexpr int64_t kMaxWidth = kMaxThreads * 16;
 constexpr int kRing = 2;          // rows on their way per warp
 constexpr int kOwnParams = 16;    // values per lane up to which weight and bias stay in registers
 
-// Where a thread's E values of a row lie, thread l of the g that share it.
-// VEC: 16 bytes at a time, load j being columns [(j g + l) per, + per); else
-// single values, per = 1.
-template <typename TX, bool VEC, int E>
+// A thread's E values of a row: of the segment of G E columns that its warp (or
+// part of a warp) holds, the whole row unless the row takes several warps.
+// VEC: 16 bytes at a time, load j being the segment's columns [(j G + lane)
+// per, + per); else single values, per = 1.
+template <typename TX, bool VEC, int G, int E>
 struct Layout {
-    static constexpr int kPer = VEC ? 16 / static_cast<int>(sizeof(TX)) : 1;
+    static constexpr int kSize = static_cast<int>(sizeof(TX));
+    static constexpr int kPer = VEC ? 16 / kSize : 1;
     static constexpr int kLoads = E / kPer;
-    // A thread's bytes of one row in the ring; 0 where rows come straight.
-    static constexpr bool kAsync = VEC || sizeof(TX) == 4;
-    static constexpr int kPiece = VEC ? 16 : 4;
-    static constexpr int kBytes = kAsync ? kLoads * kPiece : 0;
+    // A segment's bytes in the ring: each thread's own places, or the
+    // segment's image, with room for what shares its first 16 bytes.
+    static constexpr int kBytes = G * E * kSize + (VEC ? 0 : 16);
 
-    static __device__ __forceinline__ int column(int l, int g, int j) { return (j * g + l) * kPer; }
+    static __device__ __forceinline__ int column(int lane, int j) { return (j * G + lane) * kPer; }
 };
 
-// Starts the copy of a row (none if !any: zeros) to this thread's places in a
-// slot of the ring, zeros past column d.
-template <typename TX, bool VEC, int E>
-__device__ __forceinline__ void fetch_row(uint32_t slot, const TX* row, bool any, int l, int g,
-                                          int d) {
-    using L = Layout<TX, VEC, E>;
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+                 : "memory");
+}
+
+// Starts the copy of a segment of n columns (or more: FULL) into its place in
+// the ring. VEC: this thread's own values, zeros past the segment. Else 16
+// bytes at a time from the 16 that hold its first value, as long as these do
+// not start before the tensor (`base`); the few values before the next 16 are
+// then copied one by one.
+template <typename TX, bool VEC, int G, int E>
+__device__ __forceinline__ void fetch_row(uint32_t slot, const TX* seg, const TX* base, int lane,
+                                          int n) {
+    using L = Layout<TX, VEC, G, E>;
+    if constexpr (VEC) {
 #pragma unroll
-    for (int j = 0; j < L::kLoads; ++j) {
-        const int c = L::column(l, g, j);
-        const bool in = any && c < d;
-        const uint32_t to = slot + (j * blockDim.x + threadIdx.x) * L::kPiece;
-        const TX* from = in ? row + c : row;
-        if constexpr (VEC)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
-                         "r"(in ? 16 : 0)
-                         : "memory");
-        else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from),
-                         "r"(in ? 4 : 0)
-                         : "memory");
+        for (int j = 0; j < L::kLoads; ++j) {
+            const int c = L::column(lane, j);
+            const bool in = c < n;
+            copy16(slot + (j * G + lane) * 16, in ? seg + c : base, in ? 16 : 0);
+        }
+    } else {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(seg);
+        const int head = static_cast<int>(at & 15);
+        const uintptr_t from = at - head;
+        const int bytes = head + min(n, G * E) * L::kSize;
+        const bool whole = from >= reinterpret_cast<uintptr_t>(base);
+        constexpr int kTurns = E * L::kSize / 16 + 1;
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            const int c = (i * G + lane) * 16;
+            if (c < bytes && (c > 0 || whole))
+                copy16(slot + c, reinterpret_cast<const void*>(from + c), min(16, bytes - c));
+        }
+        if (!whole && lane == 0) {
+            const int k = min(n, (16 - head) / L::kSize);
+            for (int i = 0; i < k; ++i) {
+                const uint32_t to = slot + head + i * L::kSize;
+                if constexpr (sizeof(TX) == 2)
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(to),
+                                 "h"(*reinterpret_cast<const uint16_t*>(seg + i))
+                                 : "memory");
+                else
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to),
+                                 "r"(*reinterpret_cast<const uint32_t*>(seg + i))
+                                 : "memory");
+            }
+        }
     }
 }
 
@@ -98,16 +128,16 @@ __device__ __forceinline__ float2 unpack(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// A row's values from a slot of the ring, or straight from the row.
-template <typename TX, bool VEC, int E>
-__device__ __forceinline__ void get_row(float2 (&v)[E / 2], const unsigned char* slot,
-                                        const TX* row, int l, int g, int d) {
-    using L = Layout<TX, VEC, E>;
+// A segment's values from its place in the ring (`head`: the low 4 bits of
+// where it lay), zeros past its n columns.
+template <typename TX, bool VEC, int G, int E, bool FULL>
+__device__ __forceinline__ void get_row(float2 (&v)[E / 2], const unsigned char* slot, int head,
+                                        int lane, int n) {
+    using L = Layout<TX, VEC, G, E>;
     if constexpr (VEC) {
 #pragma unroll
         for (int j = 0; j < L::kLoads; ++j) {
-            const uint4 q =
-                *reinterpret_cast<const uint4*>(slot + (j * blockDim.x + threadIdx.x) * 16);
+            const uint4 q = *reinterpret_cast<const uint4*>(slot + (j * G + lane) * 16);
             if constexpr (sizeof(TX) == 2) {
                 v[4 * j] = unpack(q.x);
                 v[4 * j + 1] = unpack(q.y);
@@ -119,27 +149,23 @@ __device__ __forceinline__ void get_row(float2 (&v)[E / 2], const unsigned char*
             }
         }
     } else {
+        const TX* at = reinterpret_cast<const TX*>(slot + head) + lane;
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-            float x;
-            if constexpr (L::kAsync) {
-                x = *reinterpret_cast<const float*>(slot + (j * blockDim.x + threadIdx.x) * 4);
-            } else {
-                const int c = L::column(l, g, j);
-                x = c < d ? to_f(row[c]) : 0.0f;
-            }
+            float x = 0.0f;
+            if (FULL || j * G + lane < n) x = to_f(at[j * G]);
             (j & 1 ? v[j / 2].y : v[j / 2].x) = x;
         }
     }
 }
 
-// Sets the values past column d to 0.
-template <typename TX, bool VEC, int E>
-__device__ __forceinline__ void clear_past(float2 (&v)[E / 2], int l, int g, int d) {
-    using L = Layout<TX, VEC, E>;
+// Sets the values past the segment's n columns to 0.
+template <typename TX, bool VEC, int G, int E>
+__device__ __forceinline__ void clear_past(float2 (&v)[E / 2], int lane, int n) {
+    using L = Layout<TX, VEC, G, E>;
 #pragma unroll
     for (int j = 0; j < L::kLoads; ++j) {
-        if (L::column(l, g, j) < d) continue;
+        if (L::column(lane, j) < n) continue;
         if constexpr (VEC) {
 #pragma unroll
             for (int k = 0; k < L::kPer / 2; ++k) v[j * L::kPer / 2 + k] = make_float2(0.0f, 0.0f);
@@ -149,13 +175,13 @@ __device__ __forceinline__ void clear_past(float2 (&v)[E / 2], int l, int g, int
     }
 }
 
-template <typename TX, bool VEC, int E>
-__device__ __forceinline__ void put_row(TX* row, const float2 (&v)[E / 2], int l, int g, int d) {
-    using L = Layout<TX, VEC, E>;
+template <typename TX, bool VEC, int G, int E, bool FULL>
+__device__ __forceinline__ void put_row(TX* seg, const float2 (&v)[E / 2], int lane, int n) {
+    using L = Layout<TX, VEC, G, E>;
+    TX* to = seg + lane * L::kPer;
 #pragma unroll
     for (int j = 0; j < L::kLoads; ++j) {
-        const int c = L::column(l, g, j);
-        if (c >= d) continue;
+        if (!FULL && L::column(lane, j) >= n) continue;
         if constexpr (VEC && sizeof(TX) == 2) {
             uint32_t q[4];
 #pragma unroll
@@ -163,50 +189,63 @@ __device__ __forceinline__ void put_row(TX* row, const float2 (&v)[E / 2], int l
                 const __nv_bfloat162 h = __floats2bfloat162_rn(v[4 * j + k].x, v[4 * j + k].y);
                 q[k] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            *reinterpret_cast<uint4*>(row + c) = make_uint4(q[0], q[1], q[2], q[3]);
+            *reinterpret_cast<uint4*>(to + j * G * L::kPer) = make_uint4(q[0], q[1], q[2], q[3]);
         } else if constexpr (VEC) {
-            *reinterpret_cast<float4*>(row + c) =
+            *reinterpret_cast<float4*>(to + j * G * L::kPer) =
                 make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
         } else {
-            row[c] = from_f<TX>(j & 1 ? v[j / 2].y : v[j / 2].x);
+            to[j * G] = from_f<TX>(j & 1 ? v[j / 2].y : v[j / 2].x);
         }
     }
 }
 
 // A parameter's values at this thread's columns (`none` where there is no
-// parameter): kept in registers, or (many values a lane) one copy per CTA in
-// shared memory, laid out so that lanes read neighbouring 16 bytes.
-template <typename TX, bool VEC, int E>
-__device__ __forceinline__ void own_param(float2 (&w)[E / 2], const float* p, float none, int l,
-                                          int g, int d) {
-    using L = Layout<TX, VEC, E>;
+// parameter; p: at the segment's first): kept in registers, or (many values a
+// lane) one copy per CTA in shared memory, laid out so that lanes read
+// neighbouring 16 bytes.
+template <typename TX, bool VEC, int G, int E>
+__device__ __forceinline__ void own_param(float2 (&w)[E / 2], const float* p, float none, int lane,
+                                          int n) {
+    using L = Layout<TX, VEC, G, E>;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-        const int c = L::column(l, g, i / L::kPer) + i % L::kPer;
-        (i & 1 ? w[i / 2].y : w[i / 2].x) = p && c < d ? p[c] : none;
+        const int c = L::column(lane, i / L::kPer) + i % L::kPer;
+        (i & 1 ? w[i / 2].y : w[i / 2].x) = p && c < n ? p[c] : none;
     }
 }
-template <typename TX, bool VEC, int E, int G>
+template <typename TX, bool VEC, int G, int E>
 __device__ __forceinline__ void share_param(float* to, const float* p, float none, int d) {
-    using L = Layout<TX, VEC, E>;
+    using L = Layout<TX, VEC, G, E>;
     constexpr int N = L::kPer < 4 ? L::kPer : 4;  // floats that a lane reads at once
     for (int i = threadIdx.x; i < G * E; i += blockDim.x) {
-        // i = (chunk G + l) N + k: the k-th of the chunk-th N values of lane l
-        const int k = i % N, l = i / N % G, chunk = i / N / G;
+        // i = (chunk G + lane) N + k: the k-th of a lane's chunk-th N values
+        const int k = i % N, lane = i / N % G, chunk = i / N / G;
         const int at = chunk * N + k;  // its place among the lane's values
-        const int c = L::column(l, G, at / L::kPer) + at % L::kPer;
+        const int c = L::column(lane, at / L::kPer) + at % L::kPer;
         to[i] = p && c < d ? p[c] : none;
     }
 }
-template <typename TX, bool VEC, int E, int G>
-__device__ __forceinline__ float2 shared_param(const float* at, int l, int pair) {
-    using L = Layout<TX, VEC, E>;
+template <typename TX, bool VEC, int G, int E>
+__device__ __forceinline__ float2 shared_param(const float* at, int lane, int pair) {
+    using L = Layout<TX, VEC, G, E>;
     if constexpr (L::kPer == 1) {
-        return make_float2(at[2 * pair * G + l], at[(2 * pair + 1) * G + l]);
+        return make_float2(at[2 * pair * G + lane], at[(2 * pair + 1) * G + lane]);
     } else {  // pairs 2 i and 2 i + 1 share 16 bytes: one load for both
-        const float4 q = reinterpret_cast<const float4*>(at)[(pair / 2) * G + l];
+        const float4 q = reinterpret_cast<const float4*>(at)[(pair / 2) * G + lane];
         return pair & 1 ? make_float2(q.z, q.w) : make_float2(q.x, q.y);
     }
+}
+
+// The threads that share a row meet: the lanes of a warp, or (MULTI) the
+// row's own warps, so that a CTA's rows do not wait for one another.
+template <int MULTI>
+__device__ __forceinline__ void row_sync(int warps) {
+    if constexpr (MULTI > 0)
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x >> 5) / warps),
+                     "r"(32 * warps)
+                     : "memory");
+    else
+        __syncwarp();
 }
 
 // Sums of N values over the threads that share a row, to all of them. G lanes
@@ -223,7 +262,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*sh)[N * 16], int&
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
             for (int k = 0; k < N; ++k) sh[slot][k * 16 + warp] = v[k];
-        __syncthreads();
+        row_sync<MULTI>(warps);
         const int first = warp / warps * warps;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
@@ -248,65 +287,90 @@ __device__ __forceinline__ float total(const float2 (&v)[E / 2]) {
     return a.x + a.y;
 }
 
+// The launch bounds of the kernels below are what sets their registers: 80 a
+// thread for the forward (two CTAs of 9-warp rows where 128 would leave one:
+// 16384 x 4099 bf16, 148 -> 103 us), 128 for the backward, which spills below.
+
+// Where a thread stands: its row among the CTA's, and its segment of it.
+template <int G, int E, int MULTI>
+struct Stand {
+    int rows, sub, lane, seg, n;  // n: the segment's columns, G E or fewer
+    bool full;
+    __device__ Stand(int warps, int d) {
+        const int warp = threadIdx.x >> 5;
+        rows = MULTI ? (blockDim.x >> 5) / warps : blockDim.x / G;
+        sub = MULTI ? warp / warps : threadIdx.x / G;
+        lane = threadIdx.x % G;
+        seg = MULTI ? (warp - sub * warps) * (G * E) : 0;
+        n = d - seg;
+        full = n >= G * E;
+    }
+};
+
 template <typename TX, bool VEC, int G, int E, int MULTI>
-__global__ void __launch_bounds__(MULTI == 2 ? kMaxThreads : kThreads, MULTI ? 1 : E <= 32 ? 3 : 2)
+__global__ void __launch_bounds__(MULTI == 2 ? 768 : kThreads, MULTI == 2 ? 1 : E > 32 ? 2 : 3)
     k_norm(const TX* x, int64_t ld_x, int64_t T, int d, int warps,
            const float* __restrict__ weight, const float* __restrict__ bias, float eps, TX* y,
            int64_t ld_y, float* mean, float* rstd) {
-    using L = Layout<TX, VEC, E>;
+    using L = Layout<TX, VEC, G, E>;
     constexpr bool kOwn = E <= kOwnParams;
     static_assert(kOwn || MULTI == 0, "shared parameters are laid out for one warp per row");
     __shared__ float sh[2][16];
     extern __shared__ __align__(16) unsigned char ring[];
     int slot = 0;
-    const int g = MULTI ? 32 * warps : G;
-    const int l = threadIdx.x % g, sub = threadIdx.x / g, rows = blockDim.x / g;
+    const Stand<G, E, MULTI> me(warps, d);
     const float inv = 1.0f / static_cast<float>(d);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * rows;
-    const uint32_t slot_bytes = blockDim.x * L::kBytes;
-    const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-    const TX* from = x + (first + sub) * ld_x;  // the next row to fetch
-    int64_t ahead = first + sub;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * me.rows;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * me.rows;
+    // The ring's slots are one after another, a segment's place in each.
+    const int slot_bytes = static_cast<int>(blockDim.x) / G * L::kBytes;
+    const unsigned char* mine = ring + threadIdx.x / G * L::kBytes;
+    const uint32_t mine_at = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+    const TX* cur = x + (first + me.sub) * ld_x + me.seg;  // this row, and the next to fetch
+    const TX* from = cur;
+    int64_t ahead = first + me.sub;
     const auto fetch = [&](int at) {
-        const bool any = ahead < T;
-        fetch_row<TX, VEC, E>(ring_at + at * slot_bytes, any ? from : x, any, l, g, d);
+        if (ahead < T) fetch_row<TX, VEC, G, E>(mine_at + at * slot_bytes, from, x, me.lane, me.n);
         copies_begun();
         from += step * ld_x;
         ahead += step;
     };
     pdl_wait();
     pdl_trigger();
-    if constexpr (L::kAsync) {
-        fetch(0);
-        fetch(1);
-    }
+    fetch(0);
+    fetch(1);
     float2 w[kOwn ? E / 2 : 1], b[kOwn ? E / 2 : 1];
-    float* params = reinterpret_cast<float*>(ring + kRing * slot_bytes);
+    float* params = reinterpret_cast<float*>(ring + kRing * slot_bytes);  // past the ring
     if constexpr (kOwn) {
-        own_param<TX, VEC, E>(w, weight, 1.0f, l, g, d);
-        own_param<TX, VEC, E>(b, bias, 0.0f, l, g, d);
+        own_param<TX, VEC, G, E>(w, weight ? weight + me.seg : nullptr, 1.0f, me.lane, me.n);
+        own_param<TX, VEC, G, E>(b, bias ? bias + me.seg : nullptr, 0.0f, me.lane, me.n);
     } else {
-        share_param<TX, VEC, E, G>(params, weight, 1.0f, d);
-        share_param<TX, VEC, E, G>(params + G * E, bias, 0.0f, d);
+        share_param<TX, VEC, G, E>(params, weight, 1.0f, d);
+        share_param<TX, VEC, G, E>(params + G * E, bias, 0.0f, d);
         __syncthreads();
     }
-    TX* to = y + (first + sub) * ld_y;
+    TX* to = y + (first + me.sub) * ld_y + me.seg;
     int at = 0;
-    for (int64_t t0 = first; t0 < T; t0 += step, at ^= 1, to += step * ld_y) {
-        const int64_t t = t0 + sub;  // every thread of the CTA goes as often
-        const bool in = t < T;
+    for (int64_t t0 = first; t0 < T; t0 += step, at ^= 1, to += step * ld_y, cur += step * ld_x) {
+        const int64_t t = t0 + me.sub;  // every thread of the CTA goes as often
         float2 v[E / 2];
-        if constexpr (L::kAsync) copies_landed<kRing - 1>();
-        get_row<TX, VEC, E>(v, ring + at * slot_bytes, in ? x + t * ld_x : x, l, g, d);
+        copies_landed<kRing - 1>();
+        if constexpr (!VEC) __syncwarp();  // the other lanes' copies too
+        const int head = static_cast<int>(reinterpret_cast<uintptr_t>(cur) & 15);
+        if (me.full)
+            get_row<TX, VEC, G, E, true>(v, mine + at * slot_bytes, head, me.lane, me.n);
+        else
+            get_row<TX, VEC, G, E, false>(v, mine + at * slot_bytes, head, me.lane, me.n);
         float s[1] = {total<E>(v)};
-        // The row has been read (its sum needs it): its slot is free.
-        if constexpr (L::kAsync) fetch(at);
+        // The row has been read (its sum needs it): its place is free, an
+        // image's after every lane's part of the sum.
+        if constexpr (VEC) fetch(at);
         row_sum<G, MULTI, 1>(s, sh, slot, warps);
+        if constexpr (!VEC) fetch(at);
         const float mu = s[0] * inv;
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) v[i] = add2(v[i], both(-mu));
-        clear_past<TX, VEC, E>(v, l, g, d);
+        if (!me.full) clear_past<TX, VEC, G, E>(v, me.lane, me.n);
         float2 q[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) q[i & 1] = fma2(v[i], v[i], q[i & 1]);
@@ -314,7 +378,7 @@ __global__ void __launch_bounds__(MULTI == 2 ? kMaxThreads : kThreads, MULTI ? 1
         s[0] = q[0].x + q[0].y;
         row_sum<G, MULTI, 1>(s, sh, slot, warps);
         const float r = 1.0f / sqrtf(fmaf(s[0], inv, eps));
-        if (!in) continue;
+        if (t >= T) continue;
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
             float2 wi, bi;
@@ -322,13 +386,16 @@ __global__ void __launch_bounds__(MULTI == 2 ? kMaxThreads : kThreads, MULTI ? 1
                 wi = w[i];
                 bi = b[i];
             } else {
-                wi = shared_param<TX, VEC, E, G>(params, l, i);
-                bi = shared_param<TX, VEC, E, G>(params + G * E, l, i);
+                wi = shared_param<TX, VEC, G, E>(params, me.lane, i);
+                bi = shared_param<TX, VEC, G, E>(params + G * E, me.lane, i);
             }
             v[i] = fma2(mul2(v[i], both(r)), wi, bi);
         }
-        put_row<TX, VEC, E>(to, v, l, g, d);
-        if (l == 0) {
+        if (me.full)
+            put_row<TX, VEC, G, E, true>(to, v, me.lane, me.n);
+        else
+            put_row<TX, VEC, G, E, false>(to, v, me.lane, me.n);
+        if (me.lane == 0 && me.seg == 0) {
             if (mean) mean[t] = mu;
             if (rstd) rstd[t] = r;
         }
@@ -336,30 +403,32 @@ __global__ void __launch_bounds__(MULTI == 2 ? kMaxThreads : kThreads, MULTI ? 1
 }
 
 template <typename TX, bool VEC, int G, int E, int MULTI>
-__global__ void __launch_bounds__(MULTI == 2 ? kMaxThreads : kThreads, MULTI ? 1 : 2)
+__global__ void __launch_bounds__(MULTI == 2 ? kMaxThreads : kThreads, MULTI == 2 ? 1 : 2)
     k_norm_grad(const TX* gy, int64_t ld_gy, const TX* __restrict__ x, int64_t ld_x, int64_t T,
                 int d, int warps, const float* __restrict__ weight,
                 const float* __restrict__ mean, const float* __restrict__ rstd, TX* gx,
                 int64_t ld_gx, float* __restrict__ part) {
-    using L = Layout<TX, VEC, E>;
+    using L = Layout<TX, VEC, G, E>;
     __shared__ float sh[2][32];
-    // The ring; then, for one sum at a time, floats [rows of the CTA][g E].
+    // The ring; then, for one sum at a time, floats [rows of the CTA][columns].
     extern __shared__ __align__(16) unsigned char ring[];
     int slot = 0;
-    const int g = MULTI ? 32 * warps : G;
-    const int l = threadIdx.x % g, sub = threadIdx.x / g, rows = blockDim.x / g;
+    const Stand<G, E, MULTI> me(warps, d);
     const float inv = 1.0f / static_cast<float>(d);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * rows;
-    const uint32_t slot_bytes = blockDim.x * L::kBytes;
-    const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-    const TX* from_g = gy + (first + sub) * ld_gy;  // the next rows to fetch
-    const TX* from_x = x + (first + sub) * ld_x;
-    int64_t ahead = first + sub;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * me.rows;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * me.rows;
+    const int slot_bytes = static_cast<int>(blockDim.x) / G * L::kBytes;
+    const unsigned char* mine = ring + threadIdx.x / G * L::kBytes;
+    const uint32_t mine_at = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+    const TX* cur_g = gy + (first + me.sub) * ld_gy + me.seg;  // these rows, and the next to fetch
+    const TX* cur_x = x + (first + me.sub) * ld_x + me.seg;
+    const TX *from_g = cur_g, *from_x = cur_x;
+    int64_t ahead = first + me.sub;
     const auto fetch = [&](int at) {
-        const bool any = ahead < T;
-        fetch_row<TX, VEC, E>(ring_at + 2 * at * slot_bytes, any ? from_g : gy, any, l, g, d);
-        fetch_row<TX, VEC, E>(ring_at + (2 * at + 1) * slot_bytes, any ? from_x : x, any, l, g, d);
+        if (ahead < T) {
+            fetch_row<TX, VEC, G, E>(mine_at + 2 * at * slot_bytes, from_g, gy, me.lane, me.n);
+            fetch_row<TX, VEC, G, E>(mine_at + (2 * at + 1) * slot_bytes, from_x, x, me.lane, me.n);
+        }
         copies_begun();
         from_g += step * ld_gy;
         from_x += step * ld_x;
@@ -367,23 +436,22 @@ __global__ void __launch_bounds__(MULTI == 2 ? kMaxThreads : kThreads, MULTI ? 1
     };
     pdl_wait();
     pdl_trigger();
-    if constexpr (L::kAsync) {
-        fetch(0);
-        fetch(1);
-    }
+    fetch(0);
+    fetch(1);
     float2 w[E / 2], aw[E / 2], ab[E / 2];
-    own_param<TX, VEC, E>(w, weight, 1.0f, l, g, d);
+    own_param<TX, VEC, G, E>(w, weight ? weight + me.seg : nullptr, 1.0f, me.lane, me.n);
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) aw[i] = ab[i] = make_float2(0.0f, 0.0f);
     float next_mu = 0.0f, next_r = 0.0f;
-    if (first + sub < T) {
-        next_mu = mean[first + sub];
-        next_r = rstd[first + sub];
+    if (first + me.sub < T) {
+        next_mu = mean[first + me.sub];
+        next_r = rstd[first + me.sub];
     }
-    TX* to = gx + (first + sub) * ld_gx;
+    TX* to = gx + (first + me.sub) * ld_gx + me.seg;
     int at = 0;
-    for (int64_t t0 = first; t0 < T; t0 += step, at ^= 1, to += step * ld_gx) {
-        const int64_t t = t0 + sub;
+    for (int64_t t0 = first; t0 < T; t0 += step, at ^= 1, to += step * ld_gx,
+                 cur_g += step * ld_gy, cur_x += step * ld_x) {
+        const int64_t t = t0 + me.sub;
         const bool in = t < T;
         const float mu = next_mu, r = next_r;
         if (t + step < T) {
@@ -392,13 +460,22 @@ __global__ void __launch_bounds__(MULTI == 2 ? kMaxThreads : kThreads, MULTI ? 1
         }
         float s[2] = {0.0f, 0.0f};
         float2 gn[E / 2], n[E / 2];
-        if constexpr (L::kAsync) copies_landed<kRing - 1>();
-        get_row<TX, VEC, E>(gn, ring + 2 * at * slot_bytes, in ? gy + t * ld_gy : gy, l, g, d);
-        get_row<TX, VEC, E>(n, ring + (2 * at + 1) * slot_bytes, in ? x + t * ld_x : x, l, g, d);
+        copies_landed<kRing - 1>();
+        if constexpr (!VEC) __syncwarp();
+        const int head_g = static_cast<int>(reinterpret_cast<uintptr_t>(cur_g) & 15);
+        const int head_x = static_cast<int>(reinterpret_cast<uintptr_t>(cur_x) & 15);
+        const unsigned char* at_g = mine + 2 * at * slot_bytes;
+        if (me.full) {
+            get_row<TX, VEC, G, E, true>(gn, at_g, head_g, me.lane, me.n);
+            get_row<TX, VEC, G, E, true>(n, at_g + slot_bytes, head_x, me.lane, me.n);
+        } else {
+            get_row<TX, VEC, G, E, false>(gn, at_g, head_g, me.lane, me.n);
+            get_row<TX, VEC, G, E, false>(n, at_g + slot_bytes, head_x, me.lane, me.n);
+        }
         if (in) {
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) n[i] = mul2(add2(n[i], both(-mu)), both(r));
-            clear_past<TX, VEC, E>(n, l, g, d);  // gy is 0 there
+            if (!me.full) clear_past<TX, VEC, G, E>(n, me.lane, me.n);  // gy is 0 there
             float2 q0 = {0.0f, 0.0f}, q1 = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) {
@@ -411,19 +488,23 @@ __global__ void __launch_bounds__(MULTI == 2 ? kMaxThreads : kThreads, MULTI ? 1
             s[0] = q0.x + q0.y;
             s[1] = q1.x + q1.y;
         }
-        // Both rows have been read (the sums need them): their slots are free.
-        if constexpr (L::kAsync) fetch(at);
+        if constexpr (VEC) fetch(at);
         row_sum<G, MULTI, 2>(s, sh, slot, warps);
+        if constexpr (!VEC) fetch(at);
         if (!in || !gx) continue;
         const float a = s[0] * inv, b = s[1] * inv;
 #pragma unroll
         for (int i = 0; i < E / 2; ++i)
             gn[i] = mul2(fma2(n[i], both(-b), add2(gn[i], both(-a))), both(r));
-        put_row<TX, VEC, E>(to, gn, l, g, d);
+        if (me.full)
+            put_row<TX, VEC, G, E, true>(to, gn, me.lane, me.n);
+        else
+            put_row<TX, VEC, G, E, false>(to, gn, me.lane, me.n);
     }
     if (!part) return;
-    if constexpr (L::kAsync) copies_landed<0>();  // the ring is about to hold the sums
+    copies_landed<0>();  // the ring is about to hold the sums
     float* cols = reinterpret_cast<float*>(ring);
+    const int width = (MULTI ? warps : 1) * G * E;
     float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * d;
 #pragma unroll
     for (int which = 0; which < 2; ++which, out += d) {
@@ -431,12 +512,13 @@ __global__ void __launch_bounds__(MULTI == 2 ? kMaxThreads : kThreads, MULTI ? 1
 #pragma unroll
         for (int i = 0; i < E; ++i) {
             const float2 p = which ? ab[i / 2] : aw[i / 2];
-            cols[sub * g * E + L::column(l, g, i / L::kPer) + i % L::kPer] = i & 1 ? p.y : p.x;
+            cols[me.sub * width + me.seg + L::column(me.lane, i / L::kPer) + i % L::kPer] =
+                i & 1 ? p.y : p.x;
         }
         __syncthreads();
         for (int c = threadIdx.x; c < d; c += blockDim.x) {
             float v = 0.0f;
-            for (int i = 0; i < rows; ++i) v += cols[i * g * E + c];
+            for (int i = 0; i < me.rows; ++i) v += cols[i * width + c];
             out[c] = v;
         }
     }
@@ -587,7 +669,8 @@ __global__ void __launch_bounds__(kWideThreads)
 
 constexpr int kMaxResident = 1024;  // partial rows: no more CTAs than this run the backward
 
-// CTAs that fill the current device; Kernel names the kernel that `kernel` is.
+// CTAs that fill the current device; Kernel names the kernel that `kernel` is,
+// `threads` tells its `smem`.
 template <typename Kernel, typename K>
 int resident(K kernel, int threads, int smem) {
     constexpr int kMaxDev = 64, kShapes = kMaxThreads / 32 + 1;
@@ -630,7 +713,7 @@ struct Forward {
     static cudaError_t run(const NormArgs& a, int warps) {
         const int threads = cta_threads<G, MULTI>(warps);
         const int rows = threads / (MULTI ? 32 * warps : G);
-        const int smem = kRing * threads * Layout<TX, VEC, E>::kBytes +
+        const int smem = kRing * (threads / G) * Layout<TX, VEC, G, E>::kBytes +
                          (E <= kOwnParams ? 0 : 2 * G * E * static_cast<int>(sizeof(float)));
         static const auto kernel = k_norm<TX, VEC, G, E, MULTI>;
         const int fill = resident<Forward>(kernel, threads, smem);
@@ -648,8 +731,8 @@ struct Backward {
     static cudaError_t run(const NormArgs& a, int warps) {
         const int threads = cta_threads<G, MULTI>(warps);
         const int rows = threads / (MULTI ? 32 * warps : G);
-        const int smem = threads * std::max(2 * kRing * Layout<TX, VEC, E>::kBytes,
-                                            E * static_cast<int>(sizeof(float)));
+        const int smem = std::max(2 * kRing * (threads / G) * Layout<TX, VEC, G, E>::kBytes,
+                                  threads * E * static_cast<int>(sizeof(float)));
         static const auto kernel = k_norm_grad<TX, VEC, G, E, MULTI>;
         const int fill = resident<Backward>(kernel, threads, smem);
         if (fill <= 0) return cudaErrorUnknown;
@@ -675,7 +758,7 @@ cudaError_t forward_by_width(const NormArgs& a) {
     if (d <= 512) return Forward<TX, VEC, 32, 16, 0>::run(a, 1);
     if (d <= 768) return Forward<TX, VEC, 32, 24, 0>::run(a, 1);
     if (d <= 1024) return Forward<TX, VEC, 32, 32, 0>::run(a, 1);
-    if constexpr (VEC && sizeof(TX) == 2) {
+    if constexpr (sizeof(TX) == 2) {
         if (d <= 1536) return Forward<TX, VEC, 32, 48, 0>::run(a, 1);
         if (d <= 2048) return Forward<TX, VEC, 32, 64, 0>::run(a, 1);
     }
