@@ -96,6 +96,13 @@ struct HeadLogits {
 int head_loss_columns(int64_t rows, int64_t V);
 
 cudaError_t launch_head_lse(const HeadLogits& a, cudaStream_t s);
+
+// ---- the loss of a few rows (k_head_few.cu) ----
+bool head_few(const HeadProblem& p);        // whether there are few enough
+int head_few_parts(const HeadProblem& p);   // partial sums per row
+cudaError_t launch_head_few(const HeadProblem& p, HeadPart* part, int64_t ld_part, float* picked,
+                            float* student, cudaStream_t s);
+
 cudaError_t launch_head_factor(const HeadLogits& a, cudaStream_t s);
 
 // Slices of the summed dimension of each product, for the sizes of one piece.

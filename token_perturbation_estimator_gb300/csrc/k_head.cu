@@ -3,7 +3,7 @@
 // softmax cross entropy against a target id, and distillation from a
 // teacher's largest logits. The products are k_head_tc.cu's.
 //
-// Loss: one launch forms the logits tile by tile and leaves per row a partial
+// Loss (of more than a few rows, which k_head_few.cu takes): one launch forms the logits tile by tile and leaves per row a partial
 // maximum and sum for every half tile, and the target's logit; a second one
 // joins them. For distillation the pass over the tiles also picks the logits
 // of the teacher's entries, which a first launch has put in order. (Formed
@@ -498,21 +498,29 @@ struct LossSpace {
     size_t total;
 };
 
+// Partial sums per row.
+int loss_parts(const HeadProblem& p) {
+    if (head_few(p)) return head_few_parts(p);
+    const int64_t bn = head_loss_columns(p.S * p.T, p.V);
+    return static_cast<int>(2 * ((p.V + bn - 1) / bn));
+}
+
 // H and E are sized as if copied, wherever they lie: the size must not
 // depend on addresses. Only what a call needs is touched.
 LossSpace carve_loss(void* ws, const HeadProblem& p) {
     const int64_t R = p.S * p.T, dp = up(p.d, 8), planes = p.bf16 ? 1 : 3;
+    const int64_t parts = loss_parts(p);
+    const bool tiles = !head_few(p);
     Carver c{static_cast<unsigned char*>(ws)};
     LossSpace w;
-    const int64_t bn = head_loss_columns(R, p.V);
-    w.part = c.take<HeadPart>(2 * ((p.V + bn - 1) / bn) * up(R, 32));
+    w.part = c.take<HeadPart>(parts * up(R, 32));
     w.picked = c.take<float>(R);
-    const bool distill = p.tg.many;
-    w.entries = c.take<int2>(distill ? p.T * p.tg.K : 0);
-    w.starts = c.take<uint16_t>(distill ? p.T * (2 * ((p.V + bn - 1) / bn) + 1) : 0);
+    const bool picks = p.tg.many && tiles;
+    w.entries = c.take<int2>(picks ? p.T * p.tg.K : 0);
+    w.starts = c.take<uint16_t>(picks ? p.T * (parts + 1) : 0);
     w.loss = c.take<float>(R);
-    w.h = c.take<__nv_bfloat16>(planes * R * dp);
-    w.e = c.take<__nv_bfloat16>(planes * p.V * dp);
+    w.h = c.take<__nv_bfloat16>(tiles ? planes * R * dp : 0);
+    w.e = c.take<__nv_bfloat16>(tiles ? planes * p.V * dp : 0);
     w.total = c.at;
     return w;
 }
@@ -592,31 +600,37 @@ cudaError_t loss_typed(const HeadProblem& p, float* loss, float* lse, float* stu
     if (!loss && delta) loss = w.loss;
     unsigned int* st = status_word();
     if (!st) return cudaErrorUnknown;
-    HeadLogits a = {};
-    DUST_TRY(operand<TX>(p.H, p.ld_h, R, p.d, w.h, &a.H, s));
-    DUST_TRY(operand<TX>(p.E, p.ld_e, p.V, p.d, w.e, &a.E, s));
-    a.n = p.V;
-    a.scale = p.scale;
-    a.targets = distill ? nullptr : p.tg.ids;
-    a.T = p.T;
-    a.part = w.part;
-    a.ld_part = up(R, 32);
-    a.picked = w.picked;
-    const int bn = head_loss_columns(R, p.V);
-    const int bins = static_cast<int>(2 * ((p.V + bn - 1) / bn));
-    if (distill) {
-        const int K = static_cast<int>(p.tg.K), warps = K <= 512 ? 8 : 4;
-        int size = 32;
-        while (size < K) size *= 2;
-        DUST_TRY(launch_pdl(k_head_bins, dim3(grid_of(p.T, warps)), dim3(32 * warps),
-                            static_cast<size_t>(warps) * 8 * size, s, p.S, p.T, p.tg.ids, K, size,
-                            p.V, bn / 2, bins, w.entries, w.starts, student, st));
-        a.picks = {w.entries, w.starts, bins, p.tg.K, student};
+    const int32_t* targets = distill ? nullptr : p.tg.ids;
+    const int64_t ld_part = up(R, 32);
+    int parts = loss_parts(p);
+    if (head_few(p)) {
+        DUST_TRY(launch_head_few(p, w.part, ld_part, w.picked, student, s));
+    } else {
+        HeadLogits a = {};
+        DUST_TRY(operand<TX>(p.H, p.ld_h, R, p.d, w.h, &a.H, s));
+        DUST_TRY(operand<TX>(p.E, p.ld_e, p.V, p.d, w.e, &a.E, s));
+        a.n = p.V;
+        a.scale = p.scale;
+        a.targets = targets;
+        a.T = p.T;
+        a.part = w.part;
+        a.ld_part = ld_part;
+        a.picked = w.picked;
+        if (distill) {
+            const int K = static_cast<int>(p.tg.K), warps = K <= 512 ? 8 : 4;
+            int size = 32;
+            while (size < K) size *= 2;
+            DUST_TRY(launch_pdl(k_head_bins, dim3(grid_of(p.T, warps)), dim3(32 * warps),
+                                static_cast<size_t>(warps) * 8 * size, s, p.S, p.T, p.tg.ids, K,
+                                size, p.V, head_loss_columns(R, p.V) / 2, parts, w.entries,
+                                w.starts, student, st));
+            a.picks = {w.entries, w.starts, parts, p.tg.K, student};
+        }
+        DUST_TRY(launch_head_lse(a, s));
     }
-    DUST_TRY(launch_head_lse(a, s));
-    const int join_lanes = std::min(kJoinLanes, std::max(8, bins / 8));
+    const int join_lanes = std::min(kJoinLanes, std::max(8, parts / 8));
     DUST_TRY(launch_pdl(k_head_join, dim3(grid_of(R, 32)), dim3(32 * join_lanes), 0, s, w.part,
-                        a.ld_part, bins, R, p.T, a.targets, p.V, w.picked, loss, lse, st));
+                        ld_part, parts, R, p.T, targets, p.V, w.picked, loss, lse, st));
     if (distill && loss)
         DUST_TRY(launch_pdl(k_head_distill, dim3(grid_of(R, 8)), dim3(256), 0, s, R, p.T, p.tg,
                             p.V, p.scale, lse, student, loss));
