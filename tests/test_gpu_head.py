@@ -540,3 +540,63 @@ def test_bounded_wait_that_runs_out_is_reported():
     assert dust.dust_last_error() == dust.OK
     for p, q in zip(want, again):
         assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_values_next_to_the_largest(dtype):
+    """fp32 operands are split into three bf16 planes: values next to the
+    largest fp32, which would round up to infinity in bf16, stay finite. The
+    scale makes ordinary logits of their products."""
+    import torch
+    dev = cuda()
+    H, E, y, gl = _inputs(1, 40, 16, 300, dtype, dev, seed=21)
+    H *= 3.39e38 / _np(H).__abs__().max() if dtype == "f32" else 1e37
+    E *= 1e-8
+    assert torch.isfinite(H).all()
+    scale = 1e-30
+    loss, lse = dust.dust_head_loss(H, E, y, scale)
+    x = _x(H, E, scale)
+    assert np.abs(_np(lse) - _lse(x)).max() <= 1e-5 * max(1.0, np.abs(x).max())
+    gH, gE = dust.dust_head_loss_grad(H, E, y, lse, gl, scale)
+    assert torch.isfinite(gH.float()).all() and torch.isfinite(gE).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("R", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("d,V", [(512, 4096), (301, 1003), (2048, 700), (8, 20000)])
+def test_single_tokens(R, d, V, dtype):
+    """Few rows, which take their own way to the loss, against 64 bits, with
+    the neighbouring row counts."""
+    dev = cuda()
+    H, E, y, _ = _inputs(1, R, d, V, dtype, dev, seed=22)
+    loss, lse = dust.dust_head_loss(H, E, y, -0.75)
+    x = _x(H, E, -0.75)
+    wl = _lse(x)
+    yn = y.cpu().numpy()
+    want = np.where(yn >= 0, wl - x[np.arange(R), np.maximum(yn, 0)], 0.0)
+    tol = 1e-5 * max(1.0, np.abs(x).max())
+    assert np.abs(_np(lse) - wl).max() <= tol and np.abs(_np(loss) - want).max() <= 2 * tol
+    ids, z = _teacher(R, V, 7, dev)
+    loss, lse, student = dust.dust_distill_loss(H, E, ids, z, -0.75)
+    idn = ids.cpu().numpy()
+    ws = np.where(idn >= 0, x[np.arange(R)[:, None], np.maximum(idn, 0)], 0.0)
+    assert np.abs(_np(student) - ws).max() <= tol and np.abs(_np(lse) - wl).max() <= tol
+
+
+@pytest.mark.parametrize("scale", [0.0, -1.5])
+def test_scales_of_zero_and_below(scale):
+    dev = cuda()
+    H, E, y, gl = _inputs(1, 150, 40, 600, "bf16", dev, seed=23)
+    loss, lse = dust.dust_head_loss(H, E, y, scale)
+    x = _x(H, E, scale)
+    assert np.abs(_np(lse) - _lse(x)).max() <= 1e-5 * max(1.0, np.abs(x).max())
+    gH, gE = dust.dust_head_loss_grad(H, E, y, lse, gl, scale)
+    yn = y.cpu().numpy()
+    G = np.exp(x - _np(lse)[:, None])
+    G[np.arange(150), np.maximum(yn, 0)] -= 1.0
+    G *= np.where(yn >= 0, _np(gl), 0.0)[:, None]
+    wH, wE = _grads(H, E, G, scale)
+    if scale == 0.0:
+        assert (gH == 0).all() and (gE == 0).all()
+    else:
+        _check_grads(gH, gE, wH, wE, "bf16")

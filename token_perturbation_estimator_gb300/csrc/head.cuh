@@ -48,7 +48,7 @@ struct Planes {
 struct alignas(16) HeadRow {
     float lse_hi, lse_lo;  // lse log2(e), as a sum of two
     float weight;          // gloss over the largest |gloss|
-    int32_t target;        // -1 for distillation
+    int32_t target;        // distillation: the row's number
 };
 
 struct HeadCounts {      // written on the device by the row pass
@@ -59,14 +59,16 @@ struct HeadCounts {      // written on the device by the row pass
 constexpr int kHeadTile = 256;  // rows of a CTA pair's tile; its columns too, or half
 constexpr int kHeadBox = 64;    // rows and columns of a TMA box
 
-// The teacher's entries of each token in order of their ids (absent ones
-// left out), and where those of each half tile of columns start.
+// The teacher's entries in order of their ids (absent ones left out), and
+// where those of each half tile of columns start: for the loss of each token,
+// for the gradient of each row.
 struct HeadPicks {
-    const int2* entries;    // [T][K]: id, place among the token's entries
-    const uint16_t* starts; // [T][bins + 1]: the first entry of a half tile
-    int bins;               // half tiles
+    const int2* entries;    // [..][K]: id, and its place among the token's entries; or id, and
+                            // exp(x - lse) - q as a float, the same for every entry of an id
+    const uint16_t* starts; // [..][bins + 1]: the first entry of a half tile
+    int bins;               // half tiles of the whole vocabulary
     int64_t K;
-    float* student;         // [rows][K], written
+    float* student;         // [rows][K], written (loss)
 };
 
 // Partial softmax sums of one row over half a tile's columns: the largest
@@ -78,22 +80,23 @@ struct HeadLogits {
     Planes H, E;         // [rows][d], [V][d]
     Planes Hc;           // the rows that take part (gradient), or base null
     int64_t v0, n;       // columns [v0, v0 + n) of the vocabulary
+    int bn;              // columns of a tile: head_columns()
     float scale;
+    HeadPicks picks;     // distillation, or entries null
     // forward
     const int32_t* targets;  // [T], or null
     int64_t T;
     HeadPart* part;      // [2 * column tiles][ld_part]
     int64_t ld_part;
     float* picked;       // [rows] scaled logits of the targets
-    HeadPicks picks;     // or entries null
     // gradient
     const HeadCounts* counts;
     const HeadRow* rows;
     Planes G;            // [rows rounded up to a tile][n rounded up to a tile]
 };
 
-// Columns of the tiles that the forward takes for these sizes.
-int head_loss_columns(int64_t rows, int64_t V);
+// Columns of the tiles of logits for these sizes.
+int head_columns(int64_t rows, int64_t n);
 
 cudaError_t launch_head_lse(const HeadLogits& a, cudaStream_t s);
 
@@ -103,7 +106,14 @@ int head_few_parts(const HeadProblem& p);   // partial sums per row
 cudaError_t launch_head_few(const HeadProblem& p, HeadPart* part, int64_t ld_part, float* picked,
                             float* student, cudaStream_t s);
 
-cudaError_t launch_head_factor(const HeadLogits& a, cudaStream_t s);
+
+// The tensor maps of a gradient's operands, made once per call.
+struct HeadMaps {
+    CUtensorMap H, Hc, E, G, G_store;
+};
+bool make_head_maps(HeadMaps* m, const Planes& H, const Planes& Hc, const Planes& E,
+                    const Planes& G);
+cudaError_t launch_head_factor(const HeadLogits& a, const HeadMaps& m, cudaStream_t s);
 
 // Slices of the summed dimension of each product, for the sizes of one piece.
 struct HeadCuts { int gh, ge; };
@@ -112,7 +122,8 @@ HeadCuts head_cuts(int64_t rows, int64_t n, int64_t d, int planes);
 // gH += alpha G E_piece and gE_piece = alpha G^T H, one launch; slices' sums
 // are added up by one more.
 struct HeadProducts {
-    Planes G, E, H, Hc;
+    int64_t rows;        // all rows, whether they take part or not
+    int planes;
     int64_t v0, n;       // vocabulary rows of the piece
     int64_t d;
     float scale;
@@ -130,6 +141,6 @@ struct HeadProducts {
 };
 // Partial sums of a product of m rows and d columns.
 int64_t head_acc_floats(int64_t m, int64_t d, int cut);
-cudaError_t launch_head_products(const HeadProducts& a, cudaStream_t s);
+cudaError_t launch_head_products(const HeadProducts& a, const HeadMaps& m, cudaStream_t s);
 
 }  // namespace dust

@@ -12,7 +12,9 @@
 //
 // Gradient, per piece of the vocabulary (a piece's G stays below 2^27
 // values): the logits again as G = weight (exp(x - lse) - wanted) in bf16,
-// then gH += G E and gE = G^T H in one launch. Rows that take no part (no
+// then gH += G E and gE = G^T H in one launch. For distillation a first launch
+// puts each row's entries in order and forms exp(x - lse) - q at them, which
+// the pass over the columns puts in their places. Rows that take no part (no
 // target, no weight) are left out of all products: the others' H rows are
 // moved together first if there are such rows.
 //
@@ -104,83 +106,17 @@ __global__ void __launch_bounds__(32 * kJoinLanes)
     if (loss) loss[r] = has ? static_cast<float>(l - static_cast<double>(picked[r])) : 0.0f;
 }
 
-// A token's entries in order of their ids, for the loss's pass over the
-// columns to pick their logits on its way: a warp per token sorts them (a
-// bitonic network in shared memory), writes them out, and looks up where each
-// half tile's first one is. Entries that are absent come last and are not
-// counted; their logits are written here, 0.
-__global__ void __launch_bounds__(256)
-    k_head_bins(int64_t S, int64_t T, const int32_t* __restrict__ ids, int K, int size, int64_t V,
-                int columns, int bins, int2* __restrict__ entries, uint16_t* __restrict__ starts,
-                float* __restrict__ student, unsigned int* status) {
-    pdl_wait();
-    pdl_trigger();
-    extern __shared__ uint32_t bins_smem[];
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * warps + (threadIdx.x >> 5);
-    if (t >= T) return;
-    uint32_t* id = bins_smem + (threadIdx.x >> 5) * 2 * size;  // size: K or more, a power of two
-    uint32_t* place = id + size;
-    int n = 0;
-    bool bad = false;
-    for (int j = lane; j < size; j += 32) {
-        const int32_t v = j < K ? ids[t * K + j] : -1;
-        const bool in = v >= 0 && v < V;
-        bad |= v >= V;
-        id[j] = in ? static_cast<uint32_t>(v) : 0xffffffffu;
-        place[j] = static_cast<uint32_t>(j);
-        n += __popc(__ballot_sync(0xffffffffu, in));
-        if (j < K && !in)
-            for (int64_t s = 0; s < S; ++s) student[(s * T + t) * K + j] = 0.0f;
-    }
-    if (bad) report_id(status);
-    __syncwarp();
-    for (int k = 2; k <= size; k <<= 1) {
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            for (int i = lane; i < size / 2; i += 32) {
-                const int p = 2 * i - (i & (j - 1)), q = p + j;  // bit j of p is 0
-                const bool rising = (p & k) == 0;
-                // The place breaks ties: the order is the same every time.
-                const bool over = id[p] > id[q] || (id[p] == id[q] && place[p] > place[q]);
-                if (over == rising) {
-                    const uint32_t u = id[p], v = place[p];
-                    id[p] = id[q];
-                    place[p] = place[q];
-                    id[q] = u;
-                    place[q] = v;
-                }
-            }
-            __syncwarp();
-        }
-    }
-    for (int j = lane; j < n; j += 32)
-        entries[t * K + j] = make_int2(static_cast<int>(id[j]), static_cast<int>(place[j]));
-    for (int b = lane; b <= bins; b += 32) {
-        const uint32_t from = static_cast<uint32_t>(b) * static_cast<uint32_t>(columns);
-        int lo = 0, hi = n;  // the first entry at or past `from`
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (id[mid] < from) lo = mid + 1;
-            else hi = mid;
-        }
-        starts[t * (bins + 1) + b] = static_cast<uint16_t>(lo);
-    }
-}
-
 // The teacher of a token over its entries present: the largest scaled logit
 // and the logarithm of the sum of exponentials over it; largest -inf where no
 // entry has any probability. Whole warp.
 __device__ __forceinline__ float2 teacher_stats(const int32_t* ids, const float* z, int64_t K,
-                                                int64_t V, float scale, unsigned int* status) {
+                                                int64_t V, float scale) {
     const int lane = threadIdx.x & 31;
     float m = -INFINITY;
-    bool bad = false;
     for (int64_t j = lane; j < K; j += 32) {
         const int32_t id = ids[j];
-        bad |= id >= V;
         if (id >= 0 && id < V) m = fmaxf(m, scale * z[j]);
     }
-    if (bad && status) report_id(status);
     m = warp_max(m);
     float q = 0.0f;
     for (int64_t j = lane; j < K; j += 32) {
@@ -189,6 +125,110 @@ __device__ __forceinline__ float2 teacher_stats(const int32_t* ids, const float*
     }
     q = warp_sum(q);
     return make_float2(m, logf(q));
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eRest = static_cast<float>(1.4426950408889634074 - 1.4426950408889634f);
+
+struct BinArgs {
+    int64_t items;           // tokens (loss) or rows (gradient)
+    int64_t S, T, V;
+    HeadTargets tg;
+    int size;                // K or more, a power of two, 32 at least
+    int columns, bins;       // half tiles
+    float scale;
+    int2* entries;
+    uint16_t* starts;
+    float* student;          // loss: 0 written where an entry is absent; gradient: read
+    const float* lse;        // gradient
+    int32_t* alive;          // gradient: whether any entry has a probability
+    unsigned int* status;
+};
+
+// Entries in order of their ids, so that the passes over the columns meet
+// them on their way: a warp per token (loss) or row (gradient) sorts them (a
+// bitonic network in shared memory), writes them out, and looks up where each
+// half tile's first one is. Absent entries come last and are not counted.
+// The loss is to write an entry's logit to its place; the gradient is to put
+// exp(x - lse) - q there, which is formed here, with q the teacher's
+// probability summed over the entries of the same id.
+template <bool GRAD>
+__global__ void __launch_bounds__(256) k_head_bins(const BinArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ uint32_t bins_smem[];
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5, size = a.size;
+    const int K = static_cast<int>(a.tg.K);
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * warps + (threadIdx.x >> 5);
+    if (item >= a.items) return;
+    const int64_t t = GRAD ? item % a.T : item;
+    const int32_t* ids = a.tg.ids + t * K;
+    const float* z = a.tg.teacher + t * K;
+    uint32_t* id = bins_smem + (threadIdx.x >> 5) * 3 * size;
+    uint32_t* place = id + size;
+    float* q = reinterpret_cast<float*>(place + size);
+    int n = 0;
+    bool bad = false;
+    for (int j = lane; j < size; j += 32) {
+        const int32_t v = j < K ? ids[j] : -1;
+        const bool in = v >= 0 && v < a.V;
+        bad |= v >= a.V;
+        id[j] = in ? static_cast<uint32_t>(v) : 0xffffffffu;
+        place[j] = static_cast<uint32_t>(j);
+        n += __popc(__ballot_sync(0xffffffffu, in));
+        if (!GRAD && j < K && !in)
+            for (int64_t s = 0; s < a.S; ++s) a.student[(s * a.T + t) * K + j] = 0.0f;
+    }
+    if (bad) report_id(a.status);
+    __syncwarp();
+    for (int k = 2; k <= size; k <<= 1) {
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            for (int i = lane; i < size / 2; i += 32) {
+                const int p = 2 * i - (i & (j - 1)), u = p + j;  // bit j of p is 0
+                const bool rising = (p & k) == 0;
+                // The place breaks ties: the order is the same every time.
+                const bool over = id[p] > id[u] || (id[p] == id[u] && place[p] > place[u]);
+                if (over == rising) {
+                    const uint32_t x = id[p], y = place[p];
+                    id[p] = id[u];
+                    place[p] = place[u];
+                    id[u] = x;
+                    place[u] = y;
+                }
+            }
+            __syncwarp();
+        }
+    }
+    if constexpr (GRAD) {
+        const float2 st = teacher_stats(ids, z, K, a.V, a.scale);
+        if (lane == 0) a.alive[item] = st.x != -INFINITY;
+        if (st.x == -INFINITY) return;  // the row takes no part
+        for (int j = lane; j < n; j += 32) q[j] = expf(a.scale * z[place[j]] - st.x - st.y);
+        __syncwarp();
+        const float l = a.lse[item];
+        for (int j = lane; j < n; j += 32) {
+            int from = j, to = j + 1;  // the entries of this id
+            while (from > 0 && id[from - 1] == id[j]) --from;
+            while (to < n && id[to] == id[j]) ++to;
+            float sum = 0.0f;
+            for (int i = from; i < to; ++i) sum += q[i];
+            const float p = expf(a.student[item * K + place[j]] - l);
+            a.entries[item * K + j] = make_int2(static_cast<int>(id[j]), __float_as_int(p - sum));
+        }
+    } else {
+        for (int j = lane; j < n; j += 32)
+            a.entries[item * K + j] = make_int2(static_cast<int>(id[j]), static_cast<int>(place[j]));
+    }
+    for (int b = lane; b <= a.bins; b += 32) {
+        const uint32_t from = static_cast<uint32_t>(b) * static_cast<uint32_t>(a.columns);
+        int lo = 0, hi = n;  // the first entry at or past `from`
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (id[mid] < from) lo = mid + 1;
+            else hi = mid;
+        }
+        a.starts[item * (a.bins + 1) + b] = static_cast<uint16_t>(lo);
+    }
 }
 
 __global__ void __launch_bounds__(256)
@@ -203,7 +243,7 @@ __global__ void __launch_bounds__(256)
     const int64_t t = r % T;
     const int32_t* ids = tg.ids + t * tg.K;
     const float* z = tg.teacher + t * tg.K;
-    const float2 st = teacher_stats(ids, z, tg.K, V, scale, nullptr);
+    const float2 st = teacher_stats(ids, z, tg.K, V, scale);
     const float l = lse[r];
     float a = 0.0f;
     for (int64_t j = lane; j < tg.K; j += 32) {
@@ -228,21 +268,6 @@ __global__ void __launch_bounds__(256)
 
 // -------------------------------------------------------------- gradients
 
-__global__ void __launch_bounds__(256)
-    k_head_teacher(int64_t T, HeadTargets tg, int64_t V, float scale, float2* __restrict__ stats,
-                   unsigned int* status) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (t >= T) return;
-    const float2 st = teacher_stats(tg.ids + t * tg.K, tg.teacher + t * tg.K, tg.K, V, scale,
-                                    status);
-    if ((threadIdx.x & 31) == 0) stats[t] = st;
-}
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLog2eRest = static_cast<float>(1.4426950408889634074 - 1.4426950408889634f);
-
 // The rows that take part, in order: k_head_live writes which they are, their
 // places (or -1), and what the factor needs of each; and the largest |gloss|.
 // One cluster of eight CTAs: CTA c takes the c-th part of the rows, 1024 at a
@@ -254,7 +279,7 @@ struct LiveRows {
     int32_t R, T;              // rows, tokens
     int64_t V;
     const int32_t* targets;    // or null
-    const float2* teacher;
+    const int32_t* alive;      // distillation
     const float* gloss;
 
     // Whether row r takes part; its target and weight.
@@ -262,11 +287,10 @@ struct LiveRows {
         id = -1;
         g = 0.0f;
         if (r >= R) return false;
-        const uint32_t t = R == T ? static_cast<uint32_t>(r)
-                                  : static_cast<uint32_t>(r) % static_cast<uint32_t>(T);
         g = gloss[r];
-        if (!targets) return teacher[t].x != -INFINITY && g != 0.0f;
-        id = targets[t];
+        if (!targets) return alive[r] != 0 && g != 0.0f;
+        id = targets[R == T ? static_cast<uint32_t>(r)
+                            : static_cast<uint32_t>(r) % static_cast<uint32_t>(T)];
         return id >= 0 && id < V && g != 0.0f;
     }
 };
@@ -339,43 +363,50 @@ __global__ void __cluster_dims__(kLiveCtas, 1, 1) __launch_bounds__(kLiveThreads
         h.lse_hi = l * kLog2e;
         h.lse_lo = fmaf(l, kLog2e, -h.lse_hi) + l * kLog2eRest;
         h.weight = gl / g;
-        h.target = id;
+        h.target = a.targets ? id : static_cast<int32_t>(r);
         rows[to] = h;
         row_of[to] = static_cast<int32_t>(r);
     }
 }
 
 // Rows into the workspace as bf16 (one plane) or as three bf16 planes, zero
-// from column d to dp. With counts, row i is the i-th that takes part, rows
-// up to the next multiple of 64 are zeroed, and rows of `zero` (gH) that take
-// no part are cleared; if all take part and `only_if_some` is set there is
-// nothing to do.
-template <typename TX, int PLANES>
-__global__ void __launch_bounds__(256)
-    k_head_pack(const TX* __restrict__ src, int64_t ld, int64_t n, int64_t d, int64_t dp, int vec,
-                __nv_bfloat16* __restrict__ dst, const HeadCounts* counts,
-                const int32_t* __restrict__ row_of, int only_if_some,
-                const int32_t* __restrict__ place, TX* zero, int64_t ld_zero) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t live = counts ? counts->rows : n;
-    if (only_if_some && live == n) return;
-    int64_t end = n;
-    if (counts) {
-        end = (live + 63) / 64 * 64;
-        if (end > n) end = n;
-    }
+// from column d to dp.
+template <typename TX>
+struct PackJob {
+    const TX* src;
+    int64_t ld, n, d, dp;
+    int vec;                   // rows can be read 16 bytes at a time
+    __nv_bfloat16* dst;
+    // With counts, row i is the i-th that takes part, rows up to the next
+    // multiple of 64 are zeroed, and the rows of `zero` (gH) that take no part
+    // are cleared; if all take part and only_if_some is set there is nothing
+    // to do.
+    const HeadCounts* counts;
+    const int32_t* row_of;
+    int only_if_some;
+    const int32_t* place;
+    TX* zero;
+    int64_t ld_zero;
+    unsigned blocks;           // CTAs that work on it
+};
+
+template <typename TX>
+__device__ void pack_rows(const PackJob<TX>& a, int64_t block) {
+    constexpr int PLANES = sizeof(TX) == 2 ? 1 : 3;
+    const int64_t live = a.counts ? a.counts->rows : a.n;
+    if (a.only_if_some && live == a.n) return;
+    const int64_t end = a.counts ? min((live + 63) / 64 * 64, a.n) : a.n;
     const int lane = threadIdx.x & 31;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < n;
-         i += static_cast<int64_t>(gridDim.x) * 8) {
-        if (zero && place[i] < 0)
-            for (int64_t c = lane; c < d; c += 32) zero[i * ld_zero + c] = TX(0.0f);
-        if (i >= end || !dst) continue;
-        const TX* s = i < live ? src + (row_of ? row_of[i] : i) * ld : nullptr;
-        __nv_bfloat16* o = dst + i * dp;
-        for (int64_t c = lane * 8; c < dp; c += 256) {
+    for (int64_t i = block * 8 + (threadIdx.x >> 5); i < a.n;
+         i += static_cast<int64_t>(a.blocks) * 8) {
+        if (a.zero && a.place[i] < 0)
+            for (int64_t c = lane; c < a.d; c += 32) a.zero[i * a.ld_zero + c] = TX(0.0f);
+        if (i >= end) continue;
+        const TX* s = i < live ? a.src + (a.row_of ? a.row_of[i] : i) * a.ld : nullptr;
+        __nv_bfloat16* o = a.dst + i * a.dp;
+        for (int64_t c = lane * 8; c < a.dp; c += 256) {
             float v[8];
-            if (s && vec && c + 8 <= d) {
+            if (s && a.vec && c + 8 <= a.d) {
 #pragma unroll
                 for (int u = 0; u < static_cast<int>(sizeof(TX)) / 2; ++u) {
                     const uint4 x = reinterpret_cast<const uint4*>(s + c)[u];
@@ -386,7 +417,7 @@ __global__ void __launch_bounds__(256)
                 }
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = s && c + k < d ? to_f(s[c + k]) : 0.0f;
+                for (int k = 0; k < 8; ++k) v[k] = s && c + k < a.d ? to_f(s[c + k]) : 0.0f;
             }
 #pragma unroll
             for (int p = 0; p < PLANES; ++p) {
@@ -394,68 +425,24 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     b[k] = __float2bfloat16_rn(v[k]);
-                    // What this plane leaves (nothing of an infinity).
-                    v[k] = __builtin_isinf(v[k]) ? 0.0f : v[k] - __bfloat162float(b[k]);
+                    // Not up to infinity; and of an infinity nothing is left.
+                    if (__hisinf(b[k])) b[k] = __float2bfloat16_rz(v[k]);
+                    v[k] = __hisinf(b[k]) ? 0.0f : v[k] - __bfloat162float(b[k]);
                 }
-                *reinterpret_cast<uint4*>(o + p * n * dp + c) = *reinterpret_cast<const uint4*>(b);
+                *reinterpret_cast<uint4*>(o + p * a.n * a.dp + c) = *reinterpret_cast<const uint4*>(b);
             }
         }
     }
 }
 
-// Distillation: G at the teacher's entries of a piece, weight (exp(x - lse) -
-// q), with q summed over the entries of the same id. A warp per row; the
-// row's ids and probabilities in shared memory.
-template <int PLANES>
-__global__ void __launch_bounds__(256)
-    k_head_patch(const HeadCounts* __restrict__ counts, const HeadRow* __restrict__ rows,
-                 const int32_t* __restrict__ row_of, int64_t T, HeadTargets tg, float scale,
-                 const float2* __restrict__ teacher, const float* __restrict__ student, int64_t v0,
-                 int64_t n, __nv_bfloat16* __restrict__ G, int64_t ld_g, int64_t plane) {
+template <typename TX>
+__global__ void __launch_bounds__(256) k_head_pack(const PackJob<TX> a, const PackJob<TX> b) {
     pdl_wait();
     pdl_trigger();
-    extern __shared__ unsigned char patch_smem[];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int K = static_cast<int>(tg.K);
-    int32_t* s_id = reinterpret_cast<int32_t*>(patch_smem) + w * 2 * K;
-    float* s_q = reinterpret_cast<float*>(s_id + K);
-    const int live = counts->rows;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * warps + w; i < live;
-         i += static_cast<int64_t>(gridDim.x) * warps) {
-        const int64_t r = row_of[i], t = r % T;
-        const float2 st = teacher[t];
-        const HeadRow h = rows[i];
-        __syncwarp();
-        for (int j = lane; j < K; j += 32) {
-            const int64_t id = tg.ids[t * K + j];
-            const bool in = id >= v0 && id < v0 + n;
-            s_id[j] = in ? static_cast<int32_t>(id - v0) : -1;
-            s_q[j] = in ? expf(scale * tg.teacher[t * K + j] - st.x - st.y) : 0.0f;
-        }
-        __syncwarp();
-        for (int j = lane; j < K; j += 32) {
-            const int32_t id = s_id[j];
-            if (id < 0) continue;
-            float q = 0.0f;
-            bool first = true;
-            for (int u = 0; u < K; ++u) {
-                if (s_id[u] != id) continue;
-                first = first && u >= j;
-                q += s_q[u];
-            }
-            if (!first) continue;
-            const float x = student[r * K + j];
-            const float p = exp2f(fmaf(x, kLog2e, -h.lse_hi) - h.lse_lo + x * kLog2eRest);
-            float g = h.weight * (p - q);
-            __nv_bfloat16* o = G + i * ld_g + id;
-#pragma unroll
-            for (int u = 0; u < PLANES; ++u) {
-                const __nv_bfloat16 b = __float2bfloat16_rn(g);
-                o[u * plane] = b;
-                g -= __bfloat162float(b);
-            }
-        }
-    }
+    if (blockIdx.x < a.blocks)
+        pack_rows(a, blockIdx.x);
+    else
+        pack_rows(b, blockIdx.x - a.blocks);
 }
 
 // ------------------------------------------------------------------ host
@@ -501,7 +488,7 @@ struct LossSpace {
 // Partial sums per row.
 int loss_parts(const HeadProblem& p) {
     if (head_few(p)) return head_few_parts(p);
-    const int64_t bn = head_loss_columns(p.S * p.T, p.V);
+    const int64_t bn = head_columns(p.S * p.T, p.V);
     return static_cast<int>(2 * ((p.V + bn - 1) / bn));
 }
 
@@ -529,7 +516,9 @@ struct GradSpace {
     HeadCounts* counts;
     HeadRow* rows;
     int32_t *row_of, *place;
-    float2* teacher;
+    int32_t* alive;
+    int2* entries;
+    uint16_t* starts;
     __nv_bfloat16 *h, *e, *g;
     float *gh_acc, *ge_acc;
     HeadCuts cuts;
@@ -546,7 +535,10 @@ GradSpace carve_grad(void* ws, const HeadProblem& p) {
     w.rows = c.take<HeadRow>(R);
     w.row_of = c.take<int32_t>(R);
     w.place = c.take<int32_t>(R);
-    w.teacher = c.take<float2>(p.T);
+    const int64_t bn = head_columns(R, std::min(w.piece, p.V));
+    w.alive = c.take<int32_t>(p.tg.many ? R : 0);
+    w.entries = c.take<int2>(p.tg.many ? R * p.tg.K : 0);
+    w.starts = c.take<uint16_t>(p.tg.many ? R * (2 * ((p.V + bn - 1) / bn) + 1) : 0);
     // As for both gradients, whichever are asked for.
     w.cuts = head_cuts(R, std::min(w.piece, p.V), p.d, static_cast<int>(planes));
     w.gh_acc = c.take<float>(w.piece < p.V || w.cuts.gh > 1 ? head_acc_floats(R, p.d, w.cuts.gh) : 0);
@@ -558,29 +550,42 @@ GradSpace carve_grad(void* ws, const HeadProblem& p) {
     return w;
 }
 
+// The copy of a matrix of n rows.
 template <typename TX>
-cudaError_t pack(const void* src, int64_t ld, int64_t n, int64_t d, __nv_bfloat16* dst,
-                 const HeadCounts* counts, const int32_t* row_of, bool only_if_some,
-                 const int32_t* place, void* zero, int64_t ld_zero, cudaStream_t s) {
-    constexpr int P = sizeof(TX) == 2 ? 1 : 3;
-    const int vec = ld * sizeof(TX) % 16 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0;
-    const int64_t blocks = std::min<int64_t>((n + 7) / 8, 152 * 8);
-    return launch_pdl(k_head_pack<TX, P>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s,
-                      static_cast<const TX*>(src), ld, n, d, up(d, 8), vec, dst, counts, row_of,
-                      only_if_some ? 1 : 0, place, static_cast<TX*>(zero), ld_zero);
+PackJob<TX> pack_job(const void* src, int64_t ld, int64_t n, int64_t d, __nv_bfloat16* dst) {
+    PackJob<TX> j = {};
+    j.src = static_cast<const TX*>(src);
+    j.ld = ld;
+    j.n = n;
+    j.d = d;
+    j.dp = up(d, 8);
+    j.vec = ld * sizeof(TX) % 16 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0;
+    j.dst = dst;
+    j.blocks = static_cast<unsigned>(std::min<int64_t>((n + 7) / 8, 152 * 8));
+    return j;
 }
 
-// The matrix as an operand: where it lies, or copied.
 template <typename TX>
-cudaError_t operand(const void* src, int64_t ld, int64_t n, int64_t d, __nv_bfloat16* copy,
-                    Planes* out, cudaStream_t s) {
+cudaError_t pack(const PackJob<TX>& a, const PackJob<TX>& b, cudaStream_t s) {
+    if (a.blocks + b.blocks == 0) return cudaSuccess;
+    return launch_pdl(k_head_pack<TX>, dim3(a.blocks + b.blocks), dim3(256), 0, s, a, b);
+}
+
+// The matrix as an operand: where it lies, or the copy that *job is to make.
+template <typename TX>
+Planes operand(const void* src, int64_t ld, int64_t n, int64_t d, __nv_bfloat16* copy,
+               PackJob<TX>* job) {
     constexpr bool bf16 = sizeof(TX) == 2;
-    if (direct(src, ld, bf16)) {
-        *out = {src, n, d, ld, 1};
-        return cudaSuccess;
-    }
-    *out = {copy, n, up(d, 8), up(d, 8), bf16 ? 1 : 3};
-    return pack<TX>(src, ld, n, d, copy, nullptr, nullptr, false, nullptr, nullptr, 0, s);
+    *job = {};
+    if (direct(src, ld, bf16)) return {src, n, d, ld, 1};
+    *job = pack_job<TX>(src, ld, n, d, copy);
+    return {copy, n, up(d, 8), up(d, 8), bf16 ? 1 : 3};
+}
+
+int sort_size(int64_t K) {
+    int size = 32;
+    while (size < K) size *= 2;
+    return size;
 }
 
 unsigned grid_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); }
@@ -590,6 +595,20 @@ unsigned grid_of(int64_t n, int64_t per) { return static_cast<unsigned>((n + per
         const cudaError_t e_ = (x);             \
         if (e_ != cudaSuccess) return e_;       \
     } while (0)
+
+template <bool GRAD>
+cudaError_t launch_bins(BinArgs b, const HeadProblem& p, cudaStream_t s) {
+    b.S = p.S;
+    b.T = p.T;
+    b.V = p.V;
+    b.tg = p.tg;
+    b.scale = p.scale;
+    b.size = sort_size(p.tg.K);
+    b.status = status_word();
+    const int warps = b.size <= 256 ? 8 : 4;  // at most 48 KB of shared memory
+    return launch_pdl(k_head_bins<GRAD>, dim3(grid_of(b.items, warps)), dim3(32 * warps),
+                      static_cast<size_t>(warps) * 12 * b.size, s, b);
+}
 
 template <typename TX>
 cudaError_t loss_typed(const HeadProblem& p, float* loss, float* lse, float* student, float* delta,
@@ -607,9 +626,12 @@ cudaError_t loss_typed(const HeadProblem& p, float* loss, float* lse, float* stu
         DUST_TRY(launch_head_few(p, w.part, ld_part, w.picked, student, s));
     } else {
         HeadLogits a = {};
-        DUST_TRY(operand<TX>(p.H, p.ld_h, R, p.d, w.h, &a.H, s));
-        DUST_TRY(operand<TX>(p.E, p.ld_e, p.V, p.d, w.e, &a.E, s));
+        PackJob<TX> jh, je;
+        a.H = operand<TX>(p.H, p.ld_h, R, p.d, w.h, &jh);
+        a.E = operand<TX>(p.E, p.ld_e, p.V, p.d, w.e, &je);
+        DUST_TRY(pack(jh, je, s));
         a.n = p.V;
+        a.bn = head_columns(R, p.V);
         a.scale = p.scale;
         a.targets = targets;
         a.T = p.T;
@@ -617,13 +639,14 @@ cudaError_t loss_typed(const HeadProblem& p, float* loss, float* lse, float* stu
         a.ld_part = ld_part;
         a.picked = w.picked;
         if (distill) {
-            const int K = static_cast<int>(p.tg.K), warps = K <= 512 ? 8 : 4;
-            int size = 32;
-            while (size < K) size *= 2;
-            DUST_TRY(launch_pdl(k_head_bins, dim3(grid_of(p.T, warps)), dim3(32 * warps),
-                                static_cast<size_t>(warps) * 8 * size, s, p.S, p.T, p.tg.ids, K,
-                                size, p.V, head_loss_columns(R, p.V) / 2, parts, w.entries,
-                                w.starts, student, st));
+            BinArgs b = {};
+            b.items = p.T;
+            b.columns = a.bn / 2;
+            b.bins = parts;
+            b.entries = w.entries;
+            b.starts = w.starts;
+            b.student = student;
+            DUST_TRY(launch_bins<false>(b, p, s));
             a.picks = {w.entries, w.starts, parts, p.tg.K, student};
         }
         DUST_TRY(launch_head_lse(a, s));
@@ -649,44 +672,52 @@ cudaError_t grad_typed(const HeadProblem& p, const float* lse, const float* stud
     const GradSpace w = carve_grad(ws, p);
     unsigned int* st = status_word();
     if (!st) return cudaErrorUnknown;
-    if (distill)
-        DUST_TRY(launch_pdl(k_head_teacher, dim3(grid_of(p.T, 8)), dim3(256), 0, s, p.T, p.tg, p.V,
-                            p.scale, w.teacher, st));
+    HeadLogits a = {};
+    a.bn = head_columns(R, std::min(w.piece, p.V));
+    if (distill) {
+        BinArgs b = {};
+        b.items = R;
+        b.columns = a.bn / 2;
+        b.bins = static_cast<int>(2 * ((p.V + a.bn - 1) / a.bn));
+        b.entries = w.entries;
+        b.starts = w.starts;
+        b.student = const_cast<float*>(student);
+        b.lse = lse;
+        b.alive = w.alive;
+        DUST_TRY(launch_bins<true>(b, p, s));
+        a.picks = {w.entries, w.starts, b.bins, p.tg.K, nullptr};
+    }
     const LiveRows live = {static_cast<int32_t>(R), static_cast<int32_t>(p.T), p.V,
-                           distill ? nullptr : p.tg.ids, w.teacher, gloss};
+                           distill ? nullptr : p.tg.ids, w.alive, gloss};
     DUST_TRY(launch_pdl(k_head_live, dim3(kLiveCtas), dim3(kLiveThreads), 0, s, live, lse,
                         w.counts, w.rows, w.row_of, w.place, st));
-    HeadLogits a = {};
     const bool in_place = direct(p.H, p.ld_h, bf16);
     const Planes copy = {w.h, R, up(p.d, 8), up(p.d, 8), static_cast<int>(planes)};
     a.H = in_place ? Planes{p.H, R, p.d, p.ld_h, 1} : copy;
     if (in_place) a.Hc = copy;
-    DUST_TRY(pack<TX>(p.H, p.ld_h, R, p.d, w.h, w.counts, w.row_of, in_place, w.place, gH, ld_gh,
-                      s));
-    DUST_TRY(operand<TX>(p.E, p.ld_e, p.V, p.d, w.e, &a.E, s));
+    PackJob<TX> jh = pack_job<TX>(p.H, p.ld_h, R, p.d, w.h), je;
+    jh.counts = w.counts;
+    jh.row_of = w.row_of;
+    jh.only_if_some = in_place;
+    jh.place = w.place;
+    jh.zero = static_cast<TX*>(gH);
+    jh.ld_zero = ld_gh;
+    a.E = operand<TX>(p.E, p.ld_e, p.V, p.d, w.e, &je);
+    DUST_TRY(pack(jh, je, s));
     a.scale = p.scale;
     a.counts = w.counts;
     a.rows = w.rows;
-    const int64_t g_rows = up(R, kHeadTile);
-    a.G = {w.g, g_rows, w.piece, w.piece, static_cast<int>(planes)};
+    a.G = {w.g, up(R, kHeadTile), w.piece, w.piece, static_cast<int>(planes)};
+    HeadMaps maps;
+    if (!make_head_maps(&maps, a.H, a.Hc, a.E, a.G)) return cudaErrorInvalidValue;
     for (int64_t v0 = 0; v0 < p.V; v0 += w.piece) {
         const int64_t n = std::min(w.piece, p.V - v0);
         a.v0 = v0;
         a.n = n;
-        DUST_TRY(launch_head_factor(a, s));
-        if (distill) {
-            const int warps = p.tg.K <= 512 ? 8 : 4;
-            const size_t smem = static_cast<size_t>(warps) * 8 * static_cast<size_t>(p.tg.K);
-            const unsigned blocks = std::min(grid_of(R, warps), 152u * 8u);
-            DUST_TRY(launch_pdl(k_head_patch<bf16 ? 1 : 3>, dim3(blocks), dim3(32 * warps), smem, s,
-                                w.counts, w.rows, w.row_of, p.T, p.tg, p.scale, w.teacher, student,
-                                v0, n, w.g, w.piece, g_rows * w.piece));
-        }
+        DUST_TRY(launch_head_factor(a, maps, s));
         HeadProducts m = {};
-        m.G = a.G;
-        m.E = a.E;
-        m.H = a.H;
-        m.Hc = a.Hc;
+        m.rows = R;
+        m.planes = static_cast<int>(planes);
         m.v0 = v0;
         m.n = n;
         m.d = p.d;
@@ -705,7 +736,7 @@ cudaError_t grad_typed(const HeadProblem& p, const float* lse, const float* stud
         m.gE = gE ? static_cast<unsigned char*>(gE) + v0 * p.d * (gE_bf16 ? 2 : 4) : nullptr;
         m.ge_bf16 = gE_bf16;
         m.accumulate = accumulate;
-        DUST_TRY(launch_head_products(m, s));
+        DUST_TRY(launch_head_products(m, maps, s));
     }
     return cudaSuccess;
 }

@@ -333,9 +333,9 @@ struct RowOf {
     bool live;
     HeadRow info;      // kLse: the target alone
     int64_t out_row;
-    int64_t token;     // kLse with a teacher's entries: the next one here, their end
-    int pick, picks_end;
-    int2 entry;
+    int64_t list;      // with a teacher's entries: which list,
+    int pick, picks_end;  // the next one here, their end,
+    int2 entry;        // and the next one itself
 };
 
 // Epilogue of one unit for one warp: rows 32 q + lane of this CTA's half,
@@ -354,18 +354,13 @@ struct Epilogue {
         o.row = w.m0 + rank * kHalf + 32 * q + lane;
         o.info.target = -1;
         o.out_row = o.row;
+        o.pick = o.picks_end = 0;
         if (MODE == kLse) {
             o.live = o.row < plan.rows;
-            o.pick = o.picks_end = 0;
             if (o.live) {
-                o.token = static_cast<uint32_t>(o.row) % static_cast<uint32_t>(a.T);
-                if (a.targets) o.info.target = a.targets[o.token];
-                if (a.picks.entries) {
-                    const uint16_t* at =
-                        a.picks.starts + o.token * (a.picks.bins + 1) + kShare * w.index + h;
-                    o.pick = at[0];
-                    o.picks_end = at[1];
-                }
+                o.list = static_cast<uint32_t>(o.row) % static_cast<uint32_t>(a.T);
+                if (a.targets) o.info.target = a.targets[o.list];
+                if (a.picks.entries) find_picks(w, o);
             }
         } else if (MODE == kFactor) {
             o.live = o.row < plan.rows;
@@ -379,9 +374,27 @@ struct Epilogue {
         return o;
     }
 
-    // The second step of the loads ahead: an entry needs its place first.
-    __device__ void first_pick(RowOf& o) const {
-        if (o.pick < o.picks_end) o.entry = a.picks.entries[o.token * a.picks.K + o.pick];
+    // Where the row's entries among its columns start and end.
+    __device__ void find_picks(const Tile& w, RowOf& o) const {
+        const int bin = static_cast<int>((a.v0 + w.n0) / (a.bn / kShare)) + h;
+        const uint16_t* at = a.picks.starts + o.list * (a.picks.bins + 1) + bin;
+        o.pick = at[0];
+        o.picks_end = at[1];
+    }
+    __device__ void next_pick(RowOf& o) const {
+        if (o.pick < o.picks_end) o.entry = a.picks.entries[o.list * a.picks.K + o.pick];
+    }
+    // The further steps of the loads ahead, each after what it needs has come:
+    // an entry its place, and kFactor's places the row's number.
+    __device__ void second(const Tile& w, RowOf& o) const {
+        if (MODE == kLse) next_pick(o);
+        if (MODE == kFactor && a.picks.entries && o.live) {
+            o.list = o.info.target;
+            find_picks(w, o);
+        }
+    }
+    __device__ void third(RowOf& o) const {
+        if (MODE == kFactor) next_pick(o);
     }
 
     __device__ void lse(const Tile& w, RowOf o, uint32_t taddr) {
@@ -417,7 +430,7 @@ struct Epilogue {
             if (want == col) {
                 a.picks.student[o.row * a.picks.K + o.entry.y] = a.scale * x;
                 ++o.pick;
-                first_pick(o);
+                next_pick(o);
                 want = o.pick < o.picks_end ? o.entry.x - first : -1;
             }
         }
@@ -425,7 +438,7 @@ struct Epilogue {
             a.part[(static_cast<int64_t>(w.index) * kShare + h) * a.ld_part + o.row] = {m, s};
     }
 
-    __device__ void factor(const Tile& w, const RowOf& o, uint32_t taddr) {
+    __device__ void factor(const Tile& w, RowOf o, uint32_t taddr) {
         const int cols = a.bn / kShare;
         const float c = a.scale * kLog2e;
         const uint32_t swz = (lane >> 1) & 3;
@@ -455,12 +468,14 @@ struct Epilogue {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = o.live && i < left ? v[i] : 0.0f;
             }
-            const int64_t tv = o.info.target - a.v0 - col;
+            const int64_t tv = a.picks.entries ? -1 : o.info.target - a.v0 - col;
             if (tv >= 0 && tv < 32) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     if (i == tv) v[i] -= o.info.weight;
             }
+            const int32_t past = static_cast<int32_t>(a.v0 + col) + 32;
+            const RowOf here = o;  // the block's entries, once more for every plane
 #pragma unroll
             for (int p = 0; p < PLANES; ++p) {
                 unsigned char* buf = bufs + (used % kStoreBufs) * kStageBuf;
@@ -482,6 +497,21 @@ struct Epilogue {
                         }
                     }
                     st_shared_16(dst + ((u ^ swz) << 4), pk);
+                }
+                // The teacher's entries replace what the softmax gave.
+                if (p > 0) o = here;
+                while (o.pick < o.picks_end && o.entry.x < past) {
+                    float g = o.info.weight * __int_as_float(o.entry.y);
+#pragma unroll
+                    for (int k = 0; k < p; ++k) g -= __bfloat162float(__float2bfloat16_rn(g));
+                    const uint32_t c = static_cast<uint32_t>(o.entry.x - (past - 32));
+                    const __nv_bfloat16 e = __float2bfloat16_rn(g);
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + (((c >> 3) ^ swz) << 4) +
+                                                                 (c & 7) * 2),
+                                 "h"(*reinterpret_cast<const uint16_t*>(&e))
+                                 : "memory");
+                    ++o.pick;
+                    next_pick(o);
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
@@ -701,9 +731,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Tile w = t >= 0 ? plan.at(a, t) : Tile{};
         RowOf o = {};
         if (t >= 0) o = epi.begin(w, plan);
-        if (MODE == kLse) epi.first_pick(o);
+        epi.second(w, o);
         for (int j = 0; t >= 0; ++j) {
             const int acc = j & 1;
+            epi.third(o);
             const bool ok = tc::mbar_wait_for(&ctl->tfull[acc], (j >> 1) & 1, tile_ns);
             tc::tc_fence_after();
             if (!__all_sync(0xffffffffu, ok) || *abort_flag) {
@@ -725,7 +756,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_at(tc::at_rank(&ctl->tempty[acc], 0));
-            if (MODE == kLse) epi.first_pick(next_o);
+            if (t >= 0) epi.second(next, next_o);
             w = next;
             o = next_o;
         }
@@ -752,23 +783,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-// The slices' partial sums of one product added in order, into gH or gE: a
-// CTA takes 32 rows and 32 columns of a tile at a time.
+// The slices' partial sums of the products added in order, into gH (t0 tiles)
+// and gE (t1 tiles): a CTA takes 32 rows and 32 columns of a tile at a time.
 __global__ void __launch_bounds__(256)
-    k_head_sum(const __grid_constant__ TcArgs a, int job, int64_t tiles) {
+    k_head_sum(const __grid_constant__ TcArgs a, int64_t t0, int64_t t1) {
     pdl_wait();
     pdl_trigger();
     const int nt = static_cast<int>((a.d + a.bn - 1) / a.bn);
-    const int cut = job ? a.cut1 : a.cut0;
-    const int64_t rows = job ? a.n : a.counts->rows;
+    const int per = 8 * (a.bn / 32);
     const int lane = threadIdx.x & 31, c4 = threadIdx.x >> 5;
-    const int64_t blocks = tiles * 8 * (a.bn / 32);
-    for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-        const int64_t tile = b / (8 * (a.bn / 32));
-        const int in = static_cast<int>(b - tile * (8 * (a.bn / 32)));
+    for (int64_t b = blockIdx.x; b < (t0 + t1) * per; b += gridDim.x) {
+        const bool job = b >= t0 * per;
+        const int64_t tile = b / per - (job ? t0 : 0);
+        const int in = static_cast<int>(b % per);
         const int r = (in & 7) * 32 + lane, c = (in >> 3) * 32 + c4 * 4;
         const int64_t row = tile / nt * kHeadTile + r, col = tile % nt * a.bn + c;
-        if (row >= rows || col >= a.d) continue;
+        if (row >= (job ? a.n : a.counts->rows) || col >= a.d) continue;
+        const int cut = job ? a.cut1 : a.cut0;
         const float4* p = reinterpret_cast<const float4*>((job ? a.ge_acc : a.gh_acc) +
                                                           tile * cut * kSlotFloats) +
                           c / 4 * kHeadTile + r;
@@ -795,10 +826,9 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-cudaError_t launch_sum(const TcArgs& a, int job, int64_t tiles, cudaStream_t s) {
-    const int64_t blocks = std::min<int64_t>(tiles * 8 * (a.bn / 32), 152 * 8);
-    return launch_pdl(k_head_sum, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a, job,
-                      tiles);
+cudaError_t launch_sum(const TcArgs& a, int64_t t0, int64_t t1, cudaStream_t s) {
+    const int64_t blocks = std::min<int64_t>((t0 + t1) * 8 * (a.bn / 32), 152 * 8);
+    return launch_pdl(k_head_sum, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a, t0, t1);
 }
 
 // [planes][rows][cols] as a 3-D map of box_rows x box_cols boxes.
@@ -899,7 +929,7 @@ constexpr int kGroup = 38;
 
 }  // namespace
 
-int head_loss_columns(int64_t rows, int64_t V) { return logit_columns(rows, V); }
+int head_columns(int64_t rows, int64_t n) { return logit_columns(rows, n); }
 
 // Slices of the summed dimension of each product: 1 where whole tiles share
 // the pairs evenly (within a quarter), else the pair of cuts that ends
@@ -945,7 +975,7 @@ cudaError_t launch_head_lse(const HeadLogits& h, cudaStream_t s) {
     a.n = h.n;
     a.v0 = h.v0;
     a.planes = h.H.planes;
-    a.bn = head_loss_columns(a.rows, a.n);
+    a.bn = h.bn;
     a.group = kGroup;
     a.scale = h.scale;
     a.targets = h.targets;
@@ -957,13 +987,17 @@ cudaError_t launch_head_lse(const HeadLogits& h, cudaStream_t s) {
     return launch_tc<kLse, 1>(m, a, tiles_of(a.rows, kHeadTile) * tiles_of(a.n, a.bn), s);
 }
 
-cudaError_t launch_head_factor(const HeadLogits& h, cudaStream_t s) {
-    CUtensorMap m[4];
-    if (!operand_map(&m[0], h.H) || !operand_map(&m[2], h.E) ||
-        !make_map(&m[3], h.G, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
-        return cudaErrorInvalidValue;
-    m[1] = m[0];
-    if (h.Hc.base && !operand_map(&m[1], h.Hc)) return cudaErrorInvalidValue;
+bool make_head_maps(HeadMaps* m, const Planes& H, const Planes& Hc, const Planes& E,
+                    const Planes& G) {
+    if (!operand_map(&m->H, H) || !operand_map(&m->E, E) || !operand_map(&m->G, G) ||
+        !make_map(&m->G_store, G, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        return false;
+    m->Hc = m->H;
+    return !Hc.base || operand_map(&m->Hc, Hc);
+}
+
+cudaError_t launch_head_factor(const HeadLogits& h, const HeadMaps& maps, cudaStream_t s) {
+    const CUtensorMap m[4] = {maps.H, maps.Hc, maps.E, maps.G_store};
     TcArgs a = {};
     a.rows = h.H.rows;
     a.d = h.H.cols;
@@ -971,9 +1005,10 @@ cudaError_t launch_head_factor(const HeadLogits& h, cudaStream_t s) {
     a.v0 = h.v0;
     a.counts = h.counts;
     a.planes = h.H.planes;
-    a.bn = logit_columns(a.rows, a.n);
+    a.bn = h.bn;
     a.group = kGroup;
     a.scale = h.scale;
+    a.picks = h.picks;
     a.info = h.rows;
     const int64_t tiles = tiles_of(a.rows, kHeadTile) * tiles_of(a.n, a.bn);
     return a.planes == 1 ? launch_tc<kFactor, 1>(m, a, tiles, s)
@@ -984,19 +1019,15 @@ int64_t head_acc_floats(int64_t m, int64_t d, int cut) {
     return tiles_of(m, kHeadTile) * tiles_of(d, product_columns(d)) * cut * kSlotFloats;
 }
 
-cudaError_t launch_head_products(const HeadProducts& h, cudaStream_t s) {
-    CUtensorMap m[4];
-    if (!operand_map(&m[0], h.G) || !operand_map(&m[1], h.E) || !operand_map(&m[2], h.H))
-        return cudaErrorInvalidValue;
-    m[3] = m[2];
-    if (h.Hc.base && !operand_map(&m[3], h.Hc)) return cudaErrorInvalidValue;
+cudaError_t launch_head_products(const HeadProducts& h, const HeadMaps& maps, cudaStream_t s) {
+    const CUtensorMap m[4] = {maps.G, maps.E, maps.H, maps.Hc};
     TcArgs a = {};
-    a.rows = h.H.rows;
+    a.rows = h.rows;
     a.d = h.d;
     a.n = h.n;
     a.v0 = h.v0;
     a.counts = h.counts;
-    a.planes = h.G.planes;
+    a.planes = h.planes;
     a.bn = product_columns(h.d);
     a.scale = h.scale;
     a.row_of = h.row_of;
@@ -1021,8 +1052,8 @@ cudaError_t launch_head_products(const HeadProducts& h, cudaStream_t s) {
     const int64_t t0 = h.gH ? tiles_of(a.rows, kHeadTile) * nt : 0;
     const int64_t t1 = h.gE ? tiles_of(a.n, kHeadTile) * nt : 0;
     cudaError_t e = launch_tc<kMul, 1>(m, a, t0 * a.cut0 + t1 * a.cut1, s);
-    if (e == cudaSuccess && h.gE && a.cut1 > 1) e = launch_sum(a, 1, t1, s);
-    if (e == cudaSuccess && h.gH && a.cut0 > 1 && h.last) e = launch_sum(a, 0, t0, s);
+    const int64_t s0 = a.cut0 > 1 && h.last ? t0 : 0, s1 = a.cut1 > 1 ? t1 : 0;
+    if (e == cudaSuccess && s0 + s1 > 0) e = launch_sum(a, s0, s1, s);
     return e;
 }
 
