@@ -600,3 +600,26 @@ def test_scales_of_zero_and_below(scale):
         assert (gH == 0).all() and (gE == 0).all()
     else:
         _check_grads(gH, gE, wH, wE, "bf16")
+
+
+def test_what_is_not_a_number_shows():
+    """A teacher's NaN at an entry present, or one in a row of H that has a
+    target, gives a loss of NaN in that row alone."""
+    import torch
+    dev = cuda()
+    H, E, y, gl = _inputs(1, 140, 64, 500, "bf16", dev, seed=24)
+    ids, z = _teacher(140, 500, 6, dev)
+    ids[10], z[10] = torch.arange(6, dtype=torch.int32, device=dev), float("nan")
+    ids[11], z[11, 3] = torch.arange(6, dtype=torch.int32, device=dev), float("nan")
+    loss, lse, student = dust.dust_distill_loss(H, E, ids, z)
+    assert torch.isnan(loss[10:12]).all() and torch.isfinite(lse).all()
+    keep = torch.ones(140, dtype=torch.bool, device=dev)
+    keep[10:12] = False
+    assert torch.isfinite(loss[keep]).all()
+    gH, _ = dust.dust_distill_loss_grad(H, E, ids, z, lse, student, gl)
+    assert torch.isnan(gH[10:12].float()).any(1).all() and torch.isfinite(gH[keep].float()).all()
+    H = H.clone()
+    H[7, 5], y[7] = float("nan"), 3
+    loss, lse = dust.dust_head_loss(H, E, y)
+    keep = torch.arange(140, device=dev) != 7
+    assert torch.isnan(loss[7]) and torch.isfinite(loss[keep]).all()

@@ -434,7 +434,9 @@ class _Types:
         self.i32, self.u8 = torch.int32, torch.uint8
         self.code = {torch.float32: F32, torch.bfloat16: BF16}
         self.empty, self.empty_like = torch.empty, torch.empty_like
-        self.stream_of = torch._C._cuda_getCurrentRawStream
+        # The current stream's handle; the public way builds an object first (5 us).
+        self.stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 _types_cache = None

@@ -52,6 +52,7 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kStageBuf = 32 * 32 * 2;            // 32 rows x 32 columns of G
 constexpr int kStoreBufs = 2;
 constexpr int kStoreBytes = kEpiWarps * kStoreBufs * kStageBuf;
+constexpr int kPickBuf = 32 * 32 * 4;             // 32 rows x 32 columns of logits (kLse)
 constexpr int kSlotFloats = kHeadTile * kHeadTile;  // a tile of partial sums
 constexpr uint32_t kTmemCols = 512;               // two accumulators of 256 columns
 
@@ -60,9 +61,11 @@ enum Mode { kLse, kFactor, kMul };
 // Steps in flight: what shared memory holds beside the store buffers.
 constexpr int kStages = 6;
 template <int MODE> constexpr int smem_of() {
-    return kStages * kStageBytes + (MODE == kFactor ? kStoreBytes : 0) + 1024;
+    return kStages * kStageBytes + 1024 +
+           (MODE == kFactor ? kStoreBytes : MODE == kLse ? kEpiWarps * kPickBuf : 0);
 }
-static_assert(smem_of<kFactor>() + 512 <= 227 * 1024, "shared memory per CTA, barriers included");
+static_assert(smem_of<kFactor>() + 512 <= 227 * 1024 && smem_of<kLse>() + 512 <= 227 * 1024,
+              "shared memory per CTA, barriers included");
 
 
 struct Ctl {
@@ -335,7 +338,7 @@ struct RowOf {
     int64_t out_row;
     int64_t list;      // with a teacher's entries: which list,
     int pick, picks_end;  // the next one here, their end,
-    int2 entry;        // and the next one itself
+    int2 entry, after; // the next one itself and the one after it
 };
 
 // Epilogue of one unit for one warp: rows 32 q + lane of this CTA's half,
@@ -344,7 +347,7 @@ template <int MODE, int PLANES>
 struct Epilogue {
     const TcArgs& a;
     const CUtensorMap* tmG;
-    unsigned char* bufs;  // this warp's store buffers
+    unsigned char* bufs;  // this warp's store buffers; kLse: its rows' logits
     uint32_t rank;
     int q, h, lane;
     uint32_t used = 0;
@@ -381,20 +384,36 @@ struct Epilogue {
         o.pick = at[0];
         o.picks_end = at[1];
     }
+    __device__ void first_picks(RowOf& o) const {
+        const int2* at = a.picks.entries + o.list * a.picks.K + o.pick;
+        if (o.pick < o.picks_end) o.entry = at[0];
+        if (o.pick + 1 < o.picks_end) o.after = at[1];
+    }
+    // On to the next entry; the one after it is on its way meanwhile.
     __device__ void next_pick(RowOf& o) const {
-        if (o.pick < o.picks_end) o.entry = a.picks.entries[o.list * a.picks.K + o.pick];
+        ++o.pick;
+        o.entry = o.after;
+        if (o.pick + 1 < o.picks_end) o.after = a.picks.entries[o.list * a.picks.K + o.pick + 1];
     }
     // The further steps of the loads ahead, each after what it needs has come:
     // an entry its place, and kFactor's places the row's number.
     __device__ void second(const Tile& w, RowOf& o) const {
-        if (MODE == kLse) next_pick(o);
+        if (MODE == kLse) first_picks(o);
         if (MODE == kFactor && a.picks.entries && o.live) {
             o.list = o.info.target;
             find_picks(w, o);
         }
     }
     __device__ void third(RowOf& o) const {
-        if (MODE == kFactor) next_pick(o);
+        if (MODE == kFactor) first_picks(o);
+    }
+
+    // Whether any of this warp's 32 rows is wanted: kLse and kMul want those
+    // that exist; of G, kMul sums over rows up to the next multiple of 64.
+    __device__ bool wanted(const Tile& w, const Plan<MODE>& plan) const {
+        const int64_t row = w.m0 + rank * kHalf + 32 * q;
+        if (MODE == kMul) return row < (w.job == 1 ? a.n : plan.rows);
+        return row < (MODE == kFactor ? (plan.rows + 63) / 64 * 64 : plan.rows);
     }
 
     __device__ void lse(const Tile& w, RowOf o, uint32_t taddr) {
@@ -409,30 +428,36 @@ struct Epilogue {
             tc::tmem_ld_32x32(taddr + h * cols + 32 * b, v);
             const int left = static_cast<int>(a.n) - (first + 32 * b);  // columns that exist
             if (left <= 0) break;
+            // Logits that are wanted by themselves, the target's and the
+            // teacher's entries': the row's 32 through shared memory, where a
+            // thread can choose among its own.
             const int at = tv - 32 * b;
-            if (o.live && at >= 0 && at < 32 && at < left) {
-                float x = 0.0f;
+            const int32_t past = first + 32 * b + 32;
+            const bool pick = o.pick < o.picks_end && o.entry.x < past;
+            if (pick || (o.live && at >= 0 && at < 32 && at < left)) {
+                const uint32_t buf = tc::smem_u32(bufs) + lane * 128;
+                const uint32_t swz = lane & 7;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x = (i == at) ? v[i] : x;
-                a.picked[o.row] = a.scale * x;
+                for (int u = 0; u < 8; ++u)
+                    st_shared_16(buf + ((u ^ swz) << 4), reinterpret_cast<const uint32_t*>(v) + 4 * u);
+                const auto logit = [&](int c) {
+                    float x;
+                    asm volatile("ld.shared.f32 %0, [%1];"
+                                 : "=f"(x)
+                                 : "r"(buf + (((c >> 2) ^ swz) << 4) + (c & 3) * 4)
+                                 : "memory");
+                    return a.scale * x;
+                };
+                if (!pick) a.picked[o.row] = logit(at);
+                while (o.pick < o.picks_end && o.entry.x < past) {
+                    a.picks.student[o.row * a.picks.K + o.entry.y] = logit(o.entry.x - (past - 32));
+                    next_pick(o);
+                }
             }
             if (left >= 32)
                 softmax_block<true>(v, 32, c, m, s);
             else
                 softmax_block<false>(v, left, c, m, s);
-        }
-        // The teacher's entries among these columns: one column at a time for
-        // all rows that want it, until no row wants one.
-        int want = o.pick < o.picks_end ? o.entry.x - first : -1;
-        while (const uint32_t mask = __ballot_sync(0xffffffffu, want >= 0)) {
-            const int col = __shfl_sync(0xffffffffu, want, __ffs(mask) - 1);
-            const float x = tc::tmem_ld_column(taddr + h * cols + col);
-            if (want == col) {
-                a.picks.student[o.row * a.picks.K + o.entry.y] = a.scale * x;
-                ++o.pick;
-                next_pick(o);
-                want = o.pick < o.picks_end ? o.entry.x - first : -1;
-            }
         }
         if (o.live)
             a.part[(static_cast<int64_t>(w.index) * kShare + h) * a.ld_part + o.row] = {m, s};
@@ -510,7 +535,6 @@ struct Epilogue {
                                                                  (c & 7) * 2),
                                  "h"(*reinterpret_cast<const uint16_t*>(&e))
                                  : "memory");
-                    ++o.pick;
                     next_pick(o);
                 }
                 tc::fence_proxy_async_smem();
@@ -724,8 +748,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         const int ew = warp - 2, q = warp & 3, h = ew >> 2;
-        Epilogue<MODE, PLANES> epi{a, &tm3, store_bufs + ew * kStoreBufs * kStageBuf, rank, q, h,
-                                   lane};
+        constexpr int kOwn = MODE == kLse ? kPickBuf : kStoreBufs * kStageBuf;
+        Epilogue<MODE, PLANES> epi{a, &tm3, store_bufs + ew * kOwn, rank, q, h, lane};
         const float alpha = MODE == kMul ? a.scale * a.counts->gmax : 0.0f;
         int t = plan.unit(a, 0);
         Tile w = t >= 0 ? plan.at(a, t) : Tile{};
@@ -747,12 +771,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             RowOf next_o = {};
             if (t >= 0) next_o = epi.begin(next, plan);
             const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * 256;
-            if constexpr (MODE == kLse)
-                epi.lse(w, o, taddr);
-            else if constexpr (MODE == kFactor)
-                epi.factor(w, o, taddr);
-            else
-                epi.product(w, o, taddr, alpha);
+            if (epi.wanted(w, plan)) {
+                if constexpr (MODE == kLse)
+                    epi.lse(w, o, taddr);
+                else if constexpr (MODE == kFactor)
+                    epi.factor(w, o, taddr);
+                else
+                    epi.product(w, o, taddr, alpha);
+            }
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_at(tc::at_rank(&ctl->tempty[acc], 0));
@@ -838,8 +864,10 @@ bool make_map(CUtensorMap* map, const Planes& p, uint32_t box_cols, uint32_t box
     if (!fn) return false;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.cols), static_cast<cuuint64_t>(p.rows),
                           static_cast<cuuint64_t>(p.planes)};
+    // (One plane: its distance to the next is not used, but has a limit.)
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.ld) * 2,
-                             static_cast<cuuint64_t>(p.rows) * static_cast<cuuint64_t>(p.ld) * 2};
+                             static_cast<cuuint64_t>(p.planes == 1 ? 1 : p.rows) *
+                                 static_cast<cuuint64_t>(p.ld) * 2};
     cuuint32_t box[3] = {box_cols, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.base), dims, strides,

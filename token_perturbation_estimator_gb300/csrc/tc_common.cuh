@@ -197,14 +197,6 @@ __device__ __forceinline__ void tmem_ld_32xN(uint32_t taddr, float (&v)[N]) {
     for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 32 lanes of one column.
-__device__ __forceinline__ float tmem_ld_column(uint32_t taddr) {
-    uint32_t r;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-    return __uint_as_float(r);
-}
-
 // ---------------------------------------------------------------- CTA pairs
 // Two CTAs of a cluster (ranks 0 and 1) as one tile: cta_group::2. Each loads
 // its half of A's and of B's rows into its own shared memory at the same
