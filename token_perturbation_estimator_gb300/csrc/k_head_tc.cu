@@ -127,6 +127,33 @@ struct Tile {
     int index;  // its column of tiles (logits), or the unit (kMul)
 };
 
+// Division by a number that stays the same: a product and a correction (a
+// division proper takes some forty instructions, and a tile's place takes
+// several; with one step of products per tile that bound the kernel).
+struct Divider {
+    uint32_t d, inverse;
+    __device__ explicit Divider(int n) : d(static_cast<uint32_t>(max(n, 1))) {
+        inverse = d == 1 ? 0xffffffffu : static_cast<uint32_t>((1ull << 32) / d);
+    }
+    // a < 2^31: the product is 0 to 2 short of the quotient.
+    __device__ __forceinline__ void operator()(int a, int& q, int& r) const {
+        uint32_t u = __umulhi(static_cast<uint32_t>(a), inverse);
+        uint32_t left = static_cast<uint32_t>(a) - u * d;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (left >= d) {
+                left -= d;
+                ++u;
+            }
+        q = static_cast<int>(u);
+        r = static_cast<int>(left);
+    }
+};
+
+__device__ __forceinline__ int divide_up(int64_t v, int by) {
+    return static_cast<int>(static_cast<uint32_t>(v + by - 1) / static_cast<uint32_t>(by));
+}
+
 template <int MODE>
 struct Plan {
     int64_t rows;
@@ -135,30 +162,37 @@ struct Plan {
     int units0, units1, total;
     bool one_first;          // kMul: gE's units are the longer ones
     int cluster, clusters;
-    int high, rounds;        // see unit()
+    int longs, mine, high, rounds;  // see unit()
+    Divider by_nt, by_group, by_gm, by_last;
 
-    __device__ Plan(const TcArgs& a, int c, int n) : cluster(c), clusters(n) {
+    __device__ Plan(const TcArgs& a, int c, int n)
+        : cluster(c), clusters(n), by_nt(1), by_group(1), by_gm(1), by_last(1) {
         rows = a.counts ? a.counts->rows : a.rows;
-        const auto up = [](int64_t v, int64_t by) { return static_cast<int>((v + by - 1) / by); };
-        nt = up(MODE == kMul ? a.d : a.n, a.bn);
+        nt = divide_up(MODE == kMul ? a.d : a.n, a.bn);
+        by_nt = Divider(nt);
         if (MODE != kMul) {
-            mt = up(rows, kHeadTile);
-            steps0 = up(a.d, 64);
+            mt = divide_up(rows, kHeadTile);
+            steps0 = divide_up(a.d, 64);
             steps1 = units1 = 0;
             units0 = mt * nt;
             one_first = false;
-            high = rounds = 0;
+            longs = mine = high = rounds = 0;
+            by_group = Divider(a.group * nt);
+            by_gm = Divider(a.group);
+            by_last = Divider(mt % a.group);
         } else {
-            mt = a.gH ? up(rows, kHeadTile) : 0;
-            steps0 = up(a.n, 64);
-            steps1 = up(rows, 64);
+            mt = a.gH ? divide_up(rows, kHeadTile) : 0;
+            steps0 = divide_up(a.n, 64);
+            steps1 = divide_up(rows, 64);
             units0 = mt * nt * a.cut0;
-            units1 = (a.gE ? up(a.n, kHeadTile) : 0) * nt * a.cut1;
-            const int cost0 = max(1, up(steps0, a.cut0)), cost1 = max(1, up(steps1, a.cut1));
+            units1 = (a.gE ? divide_up(a.n, kHeadTile) : 0) * nt * a.cut1;
+            const int cost0 = max(1, divide_up(steps0, a.cut0));
+            const int cost1 = max(1, divide_up(steps1, a.cut1));
             one_first = cost1 > cost0;
-            const int longs = one_first ? units1 : units0;
+            longs = one_first ? units1 : units0;
             high = longs % clusters;
-            rounds = high == 0 ? 0 : up(max(cost0, cost1), min(cost0, cost1));
+            mine = longs / clusters + (cluster < high ? 1 : 0);
+            rounds = high == 0 ? 0 : divide_up(max(cost0, cost1), min(cost0, cost1));
         }
         total = units0 + units1;
     }
@@ -168,13 +202,11 @@ struct Plan {
     // clusters from `high` on have one long unit less, and take `rounds` short
     // ones each while the others finish; from there on everyone in turn. The
     // units are numbered long ones first.
-    __device__ int unit(const TcArgs& a, int i) const {
+    __device__ int unit(int i) const {
         if (MODE != kMul) {
             const int64_t t = cluster + static_cast<int64_t>(i) * clusters;
             return t < total ? static_cast<int>(t) : -1;
         }
-        const int longs = one_first ? units1 : units0, shorts = total - longs;
-        const int mine = longs / clusters + (cluster < high ? 1 : 0);
         if (i < mine) return cluster + i * clusters;
         i -= mine;
         int64_t t;
@@ -185,7 +217,7 @@ struct Plan {
             if (cluster >= high) i -= rounds;
             t = static_cast<int64_t>(rounds) * low + static_cast<int64_t>(i) * clusters + cluster;
         }
-        return t < shorts ? longs + static_cast<int>(t) : -1;
+        return t < total - longs ? longs + static_cast<int>(t) : -1;
     }
 
     __device__ Tile at(const TcArgs& a, int t) const {
@@ -193,29 +225,37 @@ struct Plan {
         if (MODE != kMul) {
             // Groups of row tiles; inside one, rows fastest: the group's H
             // stays in L2 while E streams by once per group.
-            const int per = a.group * nt;
-            const int g = t / per, in = t - g * per;
-            const int gm = min(a.group, mt - g * a.group);
-            const int c = in / gm;
+            int g, in, c, r;
+            by_group(t, g, in);
+            if ((g + 1) * a.group <= mt)
+                by_gm(in, c, r);
+            else
+                by_last(in, c, r);
             w.job = 0;
-            w.m0 = static_cast<int64_t>(g * a.group + (in - c * gm)) * kHeadTile;
+            w.m0 = static_cast<int64_t>(g * a.group + r) * kHeadTile;
             w.n0 = static_cast<int64_t>(c) * a.bn;
             w.k0 = 0;
             w.steps = steps0;
             w.index = c;
         } else {
-            const int firsts = one_first ? units1 : units0;
-            const bool job1 = (t < firsts) == one_first;
-            const int i = t < firsts ? t : t - firsts;
+            const bool job1 = (t < longs) == one_first;
+            const int i = t < longs ? t : t - longs;
             const int cut = job1 ? a.cut1 : a.cut0;
             const int steps = job1 ? steps1 : steps0;
-            const int tile = i / cut, part = i - tile * cut;
-            const int r = tile / nt;  // columns fastest: a row block of G is read by neighbours
+            int tile = i;
+            w.k0 = 0;
+            w.steps = steps;
+            if (cut > 1) {
+                tile = i / cut;
+                const int64_t part = i - tile * cut;
+                w.k0 = static_cast<int>(steps * part / cut);
+                w.steps = static_cast<int>(steps * (part + 1) / cut) - w.k0;
+            }
+            int r, c;  // columns fastest: a row block of G is read by neighbours
+            by_nt(tile, r, c);
             w.job = job1 ? 1 : 0;
             w.m0 = static_cast<int64_t>(r) * kHeadTile;
-            w.n0 = static_cast<int64_t>(tile - r * nt) * a.bn;
-            w.k0 = static_cast<int>(static_cast<int64_t>(steps) * part / cut);
-            w.steps = static_cast<int>(static_cast<int64_t>(steps) * (part + 1) / cut) - w.k0;
+            w.n0 = static_cast<int64_t>(c) * a.bn;
             w.index = i;
         }
         return w;
@@ -660,7 +700,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 B0 = &tm2;
             }
             int it = 0;
-            for (int j = 0, t; !*abort_flag && (t = plan.unit(a, j)) >= 0; ++j) {
+            for (int j = 0, t; !*abort_flag && (t = plan.unit(j)) >= 0; ++j) {
                 const Tile w = plan.at(a, t);
                 const CUtensorMap* ma = w.job ? A1 : A0;
                 const CUtensorMap* mb = w.job ? B1 : B0;
@@ -704,8 +744,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0 && rank == 0) {
             if (a.stall && !tc::mbar_wait(&ctl->never, 0)) *abort_flag = 1;
             int it = 0;
-            for (int j = 0, t; !*abort_flag && (t = plan.unit(a, j)) >= 0; ++j) {
-                const Tile w = plan.at(a, t);
+            int t = plan.unit(0);
+            Tile next = t >= 0 ? plan.at(a, t) : Tile{};
+            for (int j = 0; !*abort_flag && t >= 0; ++j) {
+                const Tile w = next;
+                // The next one's place is worked out before this one's steps.
+                t = plan.unit(j + 1);
+                if (t >= 0) next = plan.at(a, t);
                 const int acc = j & 1;
                 if (!tc::mbar_wait_for(&ctl->tempty[acc], ((j >> 1) & 1) ^ 1, tile_ns)) {
                     *abort_flag = 1;
@@ -751,7 +796,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         constexpr int kOwn = MODE == kLse ? kPickBuf : kStoreBufs * kStageBuf;
         Epilogue<MODE, PLANES> epi{a, &tm3, store_bufs + ew * kOwn, rank, q, h, lane};
         const float alpha = MODE == kMul ? a.scale * a.counts->gmax : 0.0f;
-        int t = plan.unit(a, 0);
+        int t = plan.unit(0);
         Tile w = t >= 0 ? plan.at(a, t) : Tile{};
         RowOf o = {};
         if (t >= 0) o = epi.begin(w, plan);
@@ -766,7 +811,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 break;
             }
             // The next unit's rows are loaded beside this one's arithmetic.
-            t = plan.unit(a, j + 1);
+            t = plan.unit(j + 1);
             const Tile next = t >= 0 ? plan.at(a, t) : w;
             RowOf next_o = {};
             if (t >= 0) next_o = epi.begin(next, plan);
