@@ -115,6 +115,9 @@ bool make_head_maps(HeadMaps* m, const Planes& H, const Planes& Hc, const Planes
                     const Planes& G);
 cudaError_t launch_head_factor(const HeadLogits& a, const HeadMaps& m, cudaStream_t s);
 
+// Vocabulary rows of a piece of the gradients.
+int64_t head_piece(int64_t rows, int64_t V, int64_t d, int planes);
+
 // Slices of the summed dimension of each product, for the sizes of one piece.
 struct HeadCuts { int gh, ge; };
 HeadCuts head_cuts(int64_t rows, int64_t n, int64_t d, int planes);

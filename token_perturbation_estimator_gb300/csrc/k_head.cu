@@ -10,7 +10,7 @@
 // apart, as products of a row of H with K rows of E, they took 74 us beside
 // the 183 us of the logits, 4096 rows, d 1024, V 32768, K 64.)
 //
-// Gradient, per piece of the vocabulary (a piece's G stays below 2^27
+// Gradient, per piece of the vocabulary (a piece's G stays below 2^28
 // values): the logits again as G = weight (exp(x - lse) - wanted) in bf16,
 // then gH += G E and gE = G^T H in one launch. For distillation a first launch
 // puts each row's entries in order and forms exp(x - lse) - q at them, which
@@ -482,17 +482,6 @@ bool direct(const void* p, int64_t ld, bool bf16) {
     return bf16 && ld % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }
 
-// Vocabulary rows of a piece: whole tiles, G at most 2^27 values over its
-// planes (256 MB), so that a large vocabulary's G is never whole.
-int64_t piece_of(int64_t R, int64_t V, int planes) {
-    const int64_t cap = (int64_t(1) << 27) / (up(R, kHeadTile) * planes);
-    const int64_t whole = up(V, kHeadTile);
-    int64_t n = std::min(whole, std::max<int64_t>(cap / kHeadTile * kHeadTile, 4 * kHeadTile));
-    // Pieces of about one size.
-    const int64_t pieces = (whole + n - 1) / n;
-    return up((whole + pieces - 1) / pieces, kHeadTile);
-}
-
 struct Carver {
     unsigned char* base;
     size_t at = 0;
@@ -557,7 +546,7 @@ GradSpace carve_grad(void* ws, const HeadProblem& p) {
     const int64_t R = p.S * p.T, dp = up(p.d, 8), planes = p.bf16 ? 1 : 3;
     Carver c{static_cast<unsigned char*>(ws)};
     GradSpace w;
-    w.piece = piece_of(R, p.V, static_cast<int>(planes));
+    w.piece = head_piece(R, p.V, p.d, static_cast<int>(planes));
     w.counts = c.take<HeadCounts>(1);
     w.rows = c.take<HeadRow>(R);
     w.row_of = c.take<int32_t>(R);

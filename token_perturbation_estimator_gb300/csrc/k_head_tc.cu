@@ -1037,6 +1037,37 @@ HeadCuts head_cuts(int64_t rows, int64_t n, int64_t d, int planes) {
     return best;
 }
 
+// The whole vocabulary if its G has at most 2^28 values over the planes (512
+// MB), else pieces of whole tiles of that or less (four tiles at least): of
+// the sizes down to half of it the one whose tiles leave the pairs idle
+// least, by the steps of all pieces' rounds (16384 rows, d 512, V 32768:
+// pieces of 8192 took 1282 us, of 16384 1208).
+int64_t head_piece(int64_t rows, int64_t V, int64_t d, int planes) {
+    constexpr int64_t kMost = int64_t(1) << 28, kLaunches = 50;  // two launches, in steps
+    const int64_t mt = tiles_of(rows, kHeadTile), whole = tiles_of(V, kHeadTile);
+    const int64_t cap = std::max<int64_t>(kMost / (mt * kHeadTile * planes) / kHeadTile, 4);
+    if (whole <= cap) return whole * kHeadTile;
+    const int64_t pairs = planes == 1 ? 1 : 6, nt = tiles_of(d, product_columns(d));
+    const int64_t logits = tiles_of(d, 64) * pairs + 3, c1 = tiles_of(rows, 64) * pairs + 4;
+    const auto cost = [&](int64_t n) {  // of a piece of n tiles
+        const int64_t c0 = n * (kHeadTile / 64) * pairs + 4, t0 = mt * nt, t1 = n * nt;
+        // A quarter of a step per tile of gH: its running sums, read and written.
+        return tiles_of(mt * n, kPairs) * logits + kLaunches + t0 / 4 +
+               (c1 > c0 ? makespan(t1, c1, t0, c0) : makespan(t0, c0, t1, c1));
+    };
+    int64_t best = cap, least = -1;
+    const int64_t by = std::max<int64_t>(1, cap / 64);
+    for (int64_t n = cap; n >= (cap + 1) / 2; n -= by) {
+        const int64_t full = whole / n, rest = whole % n;
+        const int64_t c = full * cost(n) + (rest ? cost(rest) : 0);
+        if (least < 0 || c < least) {
+            least = c;
+            best = n;
+        }
+    }
+    return best * kHeadTile;
+}
+
 cudaError_t launch_head_lse(const HeadLogits& h, cudaStream_t s) {
     CUtensorMap m[4];
     if (!operand_map(&m[0], h.H) || !operand_map(&m[2], h.E)) return cudaErrorInvalidValue;
