@@ -52,7 +52,7 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kStageBuf = 32 * 32 * 2;            // 32 rows x 32 columns of G
 constexpr int kStoreBufs = 2;
 constexpr int kStoreBytes = kEpiWarps * kStoreBufs * kStageBuf;
-constexpr int kPickBuf = 32 * 32 * 4;             // 32 rows x 32 columns of logits (kLse)
+constexpr int kTurnBuf = 32 * 32 * 4;             // 32 rows x 32 columns of fp32 (kLse, kMul)
 constexpr int kSlotFloats = kHeadTile * kHeadTile;  // a tile of partial sums
 constexpr uint32_t kTmemCols = 512;               // two accumulators of 256 columns
 
@@ -62,7 +62,7 @@ enum Mode { kLse, kFactor, kMul };
 constexpr int kStages = 6;
 template <int MODE> constexpr int smem_of() {
     return kStages * kStageBytes + 1024 +
-           (MODE == kFactor ? kStoreBytes : MODE == kLse ? kEpiWarps * kPickBuf : 0);
+           (MODE == kFactor ? kStoreBytes : kEpiWarps * kTurnBuf);
 }
 static_assert(smem_of<kFactor>() + 512 <= 227 * 1024 && smem_of<kLse>() + 512 <= 227 * 1024,
               "shared memory per CTA, barriers included");
@@ -81,6 +81,14 @@ struct Ctl {
     int consumed;
 };
 
+// An output of the products: rows `pitch` bytes apart, whose starts and ends
+// lie on multiples of `align` bytes (16 at most).
+struct OutRows {
+    unsigned char* base;
+    int64_t pitch;
+    int bf16, align;
+};
+
 struct TcArgs {
     int64_t rows, d, n, v0;    // rows without a device count
     const HeadCounts* counts;
@@ -97,11 +105,9 @@ struct TcArgs {
     const HeadRow* info;       // kFactor
     int64_t g_cols;
     const int32_t* row_of;     // kMul
-    unsigned char* gH;
-    int64_t ld_gh;
+    OutRows out0, out1;        // gH, gE
     float *gh_acc, *ge_acc;    // tiles of partial sums, by unit
-    unsigned char* gE;
-    int gh_bf16, ge_bf16, gh_vec, ge_vec, first, last, accumulate;
+    int first, last, accumulate;
     int cut0, cut1;            // slices of the summed dimension, gH and gE
     int stall;
     unsigned int* status;
@@ -181,11 +187,11 @@ struct Plan {
             by_gm = Divider(a.group);
             by_last = Divider(mt % a.group);
         } else {
-            mt = a.gH ? divide_up(rows, kHeadTile) : 0;
+            mt = a.out0.base ? divide_up(rows, kHeadTile) : 0;
             steps0 = divide_up(a.n, 64);
             steps1 = divide_up(rows, 64);
             units0 = mt * nt * a.cut0;
-            units1 = (a.gE ? divide_up(a.n, kHeadTile) : 0) * nt * a.cut1;
+            units1 = (a.out1.base ? divide_up(a.n, kHeadTile) : 0) * nt * a.cut1;
             const int cost0 = max(1, divide_up(steps0, a.cut0));
             const int cost1 = max(1, divide_up(steps1, a.cut1));
             one_first = cost1 > cost0;
@@ -287,40 +293,91 @@ __device__ __forceinline__ void st_shared_16(uint32_t addr, const uint32_t* v) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Up to 32 consecutive values of a row, of which `n` lie inside the output.
-__device__ __forceinline__ void store_row(unsigned char* row, int64_t col, const float (&v)[32],
-                                          int n, bool bf16, bool vec, bool add) {
-    if (bf16) {
-        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(row) + col;
-        if (vec && n >= 32) {
+__device__ __forceinline__ float4 ld_shared_4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Writes 32 columns from `col` of which `n` lie inside the output: a lane has
+// a row's values v, and row `to` is its place (-1: none). They are turned
+// around in shared memory (4 KB at buf, 16-byte pieces permuted by row), so
+// that neighbouring lanes write neighbouring columns. With a row per lane,
+// each store touched 32 lines: 3 rows, d 898, V 16557, bf16 took 213 us for
+// the products, with 2-byte stores.
+__device__ __forceinline__ void store_block(uint32_t buf, const float (&v)[32], int lane, int32_t to,
+                                            const OutRows& out, int64_t col, int n, bool add) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                reinterpret_cast<uint4*>(p)[i] =
-                    make_uint4(pack2(v[8 * i], v[8 * i + 1]), pack2(v[8 * i + 2], v[8 * i + 3]),
-                               pack2(v[8 * i + 4], v[8 * i + 5]), pack2(v[8 * i + 6], v[8 * i + 7]));
-        } else {
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t u[4] = {__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                               __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
+        st_shared_16(buf + lane * 128 + ((i ^ (lane & 7)) << 4), u);
+    }
+    __syncwarp();
+    unsigned char* first = out.base + col * (out.bf16 ? 2 : 4);
+    if (out.align == 16 && !out.bf16) {
+        const int c = lane & 7;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < n) p[i] = __float2bfloat16_rn(v[i]);
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            const int32_t at = __shfl_sync(0xffffffffu, to, r);
+            if (at < 0 || 4 * c >= n) continue;
+            float4 x = ld_shared_4(buf + r * 128 + ((c ^ (r & 7)) << 4));
+            float4* p = reinterpret_cast<float4*>(first + at * out.pitch) + c;
+            if (add) {
+                const float4 o = *p;
+                x = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+            }
+            *p = x;
+        }
+    } else if (out.align == 16) {
+        const int c = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
+            const int32_t at = __shfl_sync(0xffffffffu, to, r);
+            if (at < 0 || 8 * c >= n) continue;
+            const float4 x = ld_shared_4(buf + r * 128 + (((2 * c) ^ (r & 7)) << 4));
+            const float4 y = ld_shared_4(buf + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4));
+            reinterpret_cast<uint4*>(first + at * out.pitch)[c] =
+                make_uint4(pack2(x.x, x.y), pack2(x.z, x.w), pack2(y.x, y.y), pack2(y.z, y.w));
+        }
+    } else if (out.bf16 && out.align >= 4) {
+        const int c = lane & 15;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+            const int r = 2 * i + (lane >> 4);
+            const int32_t at = __shfl_sync(0xffffffffu, to, r);
+            if (at < 0 || 2 * c >= n) continue;  // rows of an even number of values
+            float x, y;
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                         : "=f"(x), "=f"(y)
+                         : "r"(buf + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8)
+                         : "memory");
+            reinterpret_cast<uint32_t*>(first + at * out.pitch)[c] = pack2(x, y);
         }
     } else {
-        float* p = reinterpret_cast<float*>(row) + col;
-        if (vec && n >= 32) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float4 o = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                if (add) {
-                    const float4 b = reinterpret_cast<const float4*>(p)[i];
-                    o = make_float4(b.x + o.x, b.y + o.y, b.z + o.z, b.w + o.w);
-                }
-                reinterpret_cast<float4*>(p)[i] = o;
+#pragma unroll 4
+        for (int r = 0; r < 32; ++r) {
+            const int32_t at = __shfl_sync(0xffffffffu, to, r);
+            if (at < 0 || lane >= n) continue;
+            float x;
+            asm volatile("ld.shared.f32 %0, [%1];"
+                         : "=f"(x)
+                         : "r"(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4)
+                         : "memory");
+            if (out.bf16) {
+                reinterpret_cast<__nv_bfloat16*>(first + at * out.pitch)[lane] = __float2bfloat16_rn(x);
+            } else {
+                float* p = reinterpret_cast<float*>(first + at * out.pitch) + lane;
+                *p = add ? *p + x : x;
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < n) p[i] = add ? p[i] + v[i] : v[i];
         }
     }
+    __syncwarp();
 }
 
 // Adds a block's columns to a row's running sum s of 2^(c v - m). m stays a
@@ -387,7 +444,7 @@ template <int MODE, int PLANES>
 struct Epilogue {
     const TcArgs& a;
     const CUtensorMap* tmG;
-    unsigned char* bufs;  // this warp's store buffers; kLse: its rows' logits
+    unsigned char* bufs;  // this warp's shared memory: kFactor's store buffers, others' 32 x 32 values
     uint32_t rank;
     int q, h, lane;
     uint32_t used = 0;
@@ -597,6 +654,9 @@ struct Epilogue {
         const bool add = !job1 && !a.first;
         // The result is whole here unless other slices or pieces add to it.
         const bool whole = job1 ? a.cut1 == 1 : a.cut0 == 1 && a.last;
+        const OutRows& out = job1 ? a.out1 : a.out0;
+        const int32_t to = o.live ? static_cast<int32_t>(o.out_row) : -1;
+        const uint32_t buf = tc::smem_u32(bufs);
         for (int b = 0; b < cols / 32; ++b) {
             const int at = h * cols + 32 * b;
             const int64_t col = w.n0 + at;
@@ -624,13 +684,8 @@ struct Epilogue {
                         p[i * kHeadTile] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 }
             }
-            if (!whole || !o.live) continue;
-            if (job1)
-                store_row(a.gE + o.out_row * a.d * (a.ge_bf16 ? 2 : 4), col, v, n, a.ge_bf16,
-                          a.ge_vec, a.accumulate);
-            else
-                store_row(a.gH + o.out_row * a.ld_gh * (a.gh_bf16 ? 2 : 4), col, v, n, a.gh_bf16,
-                          a.gh_vec, false);
+            if (whole)
+                store_block(buf, v, lane, to, out, col, n, job1 && a.accumulate);
         }
     }
 };
@@ -793,7 +848,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         const int ew = warp - 2, q = warp & 3, h = ew >> 2;
-        constexpr int kOwn = MODE == kLse ? kPickBuf : kStoreBufs * kStageBuf;
+        constexpr int kOwn = MODE == kFactor ? kStoreBufs * kStageBuf : kTurnBuf;
         Epilogue<MODE, PLANES> epi{a, &tm3, store_bufs + ew * kOwn, rank, q, h, lane};
         const float alpha = MODE == kMul ? a.scale * a.counts->gmax : 0.0f;
         int t = plan.unit(0);
@@ -883,14 +938,14 @@ __global__ void __launch_bounds__(256)
             v.w += u.w;
         }
         const float x[4] = {v.x, v.y, v.z, v.w};
-        const bool bf16 = job ? a.ge_bf16 : a.gh_bf16;
-        const int64_t at = job ? row * a.d + col
-                               : static_cast<int64_t>(a.row_of ? a.row_of[row] : row) * a.ld_gh + col;
+        const OutRows& out = job ? a.out1 : a.out0;
+        const int64_t to = !job && a.row_of ? a.row_of[row] : row;
+        unsigned char* at = out.base + to * out.pitch;
         for (int i = 0; i < 4 && col + i < a.d; ++i) {
-            if (bf16) {
-                reinterpret_cast<__nv_bfloat16*>(job ? a.gE : a.gH)[at + i] = __float2bfloat16_rn(x[i]);
+            if (out.bf16) {
+                reinterpret_cast<__nv_bfloat16*>(at)[col + i] = __float2bfloat16_rn(x[i]);
             } else {
-                float* o = reinterpret_cast<float*>(job ? a.gE : a.gH) + at + i;
+                float* o = reinterpret_cast<float*>(at) + col + i;
                 *o = job && a.accumulate ? *o + x[i] : x[i];
             }
         }
@@ -1135,20 +1190,21 @@ cudaError_t launch_head_products(const HeadProducts& h, const HeadMaps& maps, cu
     a.bn = product_columns(h.d);
     a.scale = h.scale;
     a.row_of = h.row_of;
-    a.gH = static_cast<unsigned char*>(h.gH);
-    a.ld_gh = h.ld_gh;
     a.gh_acc = h.gh_acc;
     a.ge_acc = h.ge_acc;
     a.cut0 = h.cuts.gh;
     a.cut1 = h.cuts.ge;
-    a.gE = static_cast<unsigned char*>(h.gE);
-    a.gh_bf16 = h.gh_bf16;
-    a.ge_bf16 = h.ge_bf16;
-    const auto vec = [](const void* p, int64_t ld, bool bf16) {
-        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (bf16 ? 2 : 4) % 16 == 0;
+    const auto out = [&](void* p, int64_t ld, bool bf16) {
+        // The rows' length too: what follows it is not written.
+        const int size = bf16 ? 2 : 4;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * size) |
+                             static_cast<uintptr_t>(h.d * size);
+        int align = 16;
+        while (align > size && at % align != 0) align /= 2;
+        return OutRows{static_cast<unsigned char*>(p), ld * size, bf16, align};
     };
-    a.gh_vec = vec(h.gH, h.ld_gh, h.gh_bf16);
-    a.ge_vec = vec(h.gE, h.d, h.ge_bf16);
+    a.out0 = out(h.gH, h.ld_gh, h.gh_bf16);
+    a.out1 = out(h.gE, h.d, h.ge_bf16);
     a.first = h.first;
     a.last = h.last;
     a.accumulate = h.accumulate;
