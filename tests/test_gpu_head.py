@@ -623,3 +623,66 @@ def test_what_is_not_a_number_shows():
     loss, lse = dust.dust_head_loss(H, E, y)
     keep = torch.arange(140, device=dev) != 7
     assert torch.isnan(loss[7]) and torch.isfinite(loss[keep]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("R", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("d,V", [(512, 4096), (301, 1003), (2048, 700), (8, 20000), (898, 129)])
+def test_gradients_of_single_tokens(R, d, V, dtype):
+    """Few rows, which take their own way to the gradients, with the
+    neighbouring row counts; gE also added to what is there."""
+    import torch
+    dev = cuda()
+    scale = 0.75
+    H, E, y, gl = _inputs(1, R, d, V, dtype, dev, seed=25)
+    if R > 2:
+        H[1], y[1] = float("nan"), -1  # takes no part
+    _, lse = dust.dust_head_loss(torch.nan_to_num(H), E, y, scale)
+    out = torch.full((V, d), 0.5, device=dev)
+    gH, gE = dust.dust_head_loss_grad(H, E, y, lse, gl, scale)
+    dust.dust_head_loss_grad(H, E, y, lse, gl, scale, dust.ACCUMULATE, gE=out)
+    Hz = torch.nan_to_num(H)
+    x = _x(Hz, E, scale)
+    p = np.exp(x - _lse(x)[:, None])
+    yn = y.cpu().numpy()
+    w = np.where(yn >= 0, _np(gl), 0.0)[:, None]
+    G = p.copy()
+    G[np.arange(R), np.maximum(yn, 0)] -= 1.0
+    wH, wE = _grads(Hz, E, G * w, scale)
+    if (yn >= 0).any():
+        _check_grads(gH, gE, wH, wE, dtype)
+        # out is 0.5 and more, rounded once: half a step of 2^-24 per value.
+        assert (np.linalg.norm(_np(out) - 0.5 - wE) <=
+                GRAD_TOL[dtype] * np.linalg.norm(wE) + 2.0 ** -24 * (0.5 * (V * d) ** 0.5 + np.linalg.norm(wE)))
+    assert (_np(gH)[yn < 0] == 0).all()
+    ids, z = _teacher(R, V, 7, dev)
+    H = Hz
+    loss, lse, student = dust.dust_distill_loss(H, E, ids, z, scale)
+    gH, gE = dust.dust_distill_loss_grad(H, E, ids, z, lse, student, gl, scale)
+    q = _probs(ids, z, scale)
+    G = p * (q.sum(1) > 0)[:, None]
+    idn = ids.cpu().numpy()
+    for t in range(R):
+        for j in range(7):
+            if idn[t, j] >= 0 and q[t, j] > 0:
+                G[t, idn[t, j]] -= q[t, j]
+    wH, wE = _grads(H, E, G * _np(gl)[:, None], scale)
+    if (q.sum(1) > 0).any():
+        _check_grads(gH, gE, wH, wE, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_few_rows_against_more(dtype):
+    """The gradients of three rows, and of the same rows among nine of which
+    the others take no part: two ways to the same result."""
+    import torch
+    dev = cuda()
+    H, E, y, gl = _inputs(1, 9, 96, 700, dtype, dev, seed=26)
+    y[:] = -1
+    y[[0, 4, 8]] = torch.tensor([5, 699, 64], dtype=torch.int32, device=dev)
+    _, lse = dust.dust_head_loss(H, E, y)
+    gH, gE = dust.dust_head_loss_grad(H, E, y, lse, gl)
+    few = [t[[0, 4, 8]].contiguous() for t in (H, y, lse, gl)]
+    fH, fE = dust.dust_head_loss_grad(few[0], E, *few[1:])
+    assert rel_fro(_np(fH), _np(gH)[[0, 4, 8]]) <= 2 * GRAD_TOL[dtype]
+    assert rel_fro(_np(fE), _np(gE)) <= 2 * GRAD_TOL[dtype]

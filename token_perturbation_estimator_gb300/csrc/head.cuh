@@ -105,7 +105,12 @@ bool head_few(const HeadProblem& p);        // whether there are few enough
 int head_few_parts(const HeadProblem& p);   // partial sums per row
 cudaError_t launch_head_few(const HeadProblem& p, HeadPart* part, int64_t ld_part, float* picked,
                             float* student, cudaStream_t s);
-
+bool head_few_grad(const HeadProblem& p);
+int head_few_grad_rows(const HeadProblem& p);   // rows of E a CTA takes at a time (the picks' bins)
+int head_few_grad_parts(const HeadProblem& p);  // parts of R d values
+cudaError_t launch_head_few_grad(const HeadProblem& p, const HeadPicks& picks, const int32_t* alive,
+                                 const float* lse, const float* gloss, bool accumulate, float* part,
+                                 void* gH, int64_t ld_gh, void* gE, bool gE_bf16, cudaStream_t s);
 
 // The tensor maps of a gradient's operands, made once per call.
 struct HeadMaps {

@@ -535,6 +535,7 @@ struct GradSpace {
     int32_t* alive;
     int2* entries;
     uint16_t* starts;
+    int bins;
     __nv_bfloat16 *h, *e, *g;
     float *gh_acc, *ge_acc;
     HeadCuts cuts;
@@ -545,16 +546,24 @@ struct GradSpace {
 GradSpace carve_grad(void* ws, const HeadProblem& p) {
     const int64_t R = p.S * p.T, dp = up(p.d, 8), planes = p.bf16 ? 1 : 3;
     Carver c{static_cast<unsigned char*>(ws)};
-    GradSpace w;
+    GradSpace w = {};
+    w.alive = c.take<int32_t>(p.tg.many ? R : 0);
+    w.entries = c.take<int2>(p.tg.many ? R * p.tg.K : 0);
+    if (head_few_grad(p)) {
+        w.bins = static_cast<int>((p.V + head_few_grad_rows(p) - 1) / head_few_grad_rows(p));
+        w.starts = c.take<uint16_t>(p.tg.many ? R * (w.bins + 1) : 0);
+        w.gh_acc = c.take<float>(head_few_grad_parts(p) * R * p.d);
+        w.total = c.at;
+        return w;
+    }
     w.piece = head_piece(R, p.V, p.d, static_cast<int>(planes));
     w.counts = c.take<HeadCounts>(1);
     w.rows = c.take<HeadRow>(R);
     w.row_of = c.take<int32_t>(R);
     w.place = c.take<int32_t>(R);
     const int64_t bn = head_columns(R, std::min(w.piece, p.V));
-    w.alive = c.take<int32_t>(p.tg.many ? R : 0);
-    w.entries = c.take<int2>(p.tg.many ? R * p.tg.K : 0);
-    w.starts = c.take<uint16_t>(p.tg.many ? R * (2 * ((p.V + bn - 1) / bn) + 1) : 0);
+    w.bins = static_cast<int>(2 * ((p.V + bn - 1) / bn));
+    w.starts = c.take<uint16_t>(p.tg.many ? R * (w.bins + 1) : 0);
     // As for both gradients, whichever are asked for.
     w.cuts = head_cuts(R, std::min(w.piece, p.V), p.d, static_cast<int>(planes));
     w.gh_acc = c.take<float>(w.piece < p.V || w.cuts.gh > 1 ? head_acc_floats(R, p.d, w.cuts.gh) : 0);
@@ -688,13 +697,14 @@ cudaError_t grad_typed(const HeadProblem& p, const float* lse, const float* stud
     const GradSpace w = carve_grad(ws, p);
     unsigned int* st = status_word();
     if (!st) return cudaErrorUnknown;
+    const bool few = head_few_grad(p);
     HeadLogits a = {};
-    a.bn = head_columns(R, std::min(w.piece, p.V));
+    if (!few) a.bn = head_columns(R, std::min(w.piece, p.V));
     if (distill) {
         BinArgs b = {};
         b.items = R;
-        b.columns = a.bn / 2;
-        b.bins = static_cast<int>(2 * ((p.V + a.bn - 1) / a.bn));
+        b.columns = few ? head_few_grad_rows(p) : a.bn / 2;
+        b.bins = w.bins;
         b.entries = w.entries;
         b.starts = w.starts;
         b.student = const_cast<float*>(student);
@@ -703,6 +713,9 @@ cudaError_t grad_typed(const HeadProblem& p, const float* lse, const float* stud
         DUST_TRY(launch_bins<true>(b, p, s));
         a.picks = {w.entries, w.starts, b.bins, p.tg.K, nullptr};
     }
+    if (few)
+        return launch_head_few_grad(p, a.picks, w.alive, lse, gloss, accumulate, w.gh_acc, gH, ld_gh,
+                                    gE, gE_bf16, s);
     const LiveRows live = {static_cast<int32_t>(R), static_cast<int32_t>(p.T), p.V,
                            distill ? nullptr : p.tg.ids, w.alive, gloss};
     DUST_TRY(launch_pdl(k_head_live, dim3(kLiveCtas), dim3(kLiveThreads), 0, s, live, lse,
