@@ -686,3 +686,40 @@ def test_few_rows_against_more(dtype):
     fH, fE = dust.dust_head_loss_grad(few[0], E, *few[1:])
     assert rel_fro(_np(fH), _np(gH)[[0, 4, 8]]) <= 2 * GRAD_TOL[dtype]
     assert rel_fro(_np(fE), _np(gE)) <= 2 * GRAD_TOL[dtype]
+
+
+@pytest.mark.parametrize("dtype,ge", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("T", [2, 140])
+@pytest.mark.parametrize("d,ld,off", [(33, 40, 0), (36, 40, 0), (64, 72, 8), (100, 101, 0), (64, 64, 1),
+                                      (130, 136, 2), (8, 16, 0)])
+def test_gradients_of_rows_apart(d, ld, off, T, ge, dtype):
+    """gH with room between its rows, gH and gE off 16 bytes: nothing is
+    written beside them, and the values are those of dense outputs (of a few
+    rows: but for the order of the sums, which follows the alignment)."""
+    import ctypes as C
+    import torch
+    dev = cuda()
+    V = 333
+    H, E, y, gl = _inputs(1, T, d, V, dtype, dev, seed=27)
+    _, lse = dust.dust_head_loss(H, E, y)
+    ge_type = torch.float32 if ge == "f32" else torch.bfloat16
+    gH, gE = dust.dust_head_loss_grad(H, E, y, lse, gl, gE_dtype=ge_type)
+    n = C.c_size_t(0)
+    L = dust.lib()
+    code = dust.BF16 if dtype == "bf16" else dust.F32
+    assert L.dust_head_loss_grad_workspace(C.byref(n), 1, T, d, V, code) == dust.OK
+    ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    p = lambda t: C.c_void_p(t.data_ptr())  # noqa: E731
+    flatH = torch.full((T * ld + off + 16,), 9.0, dtype=H.dtype, device=dev)
+    flatE = torch.full((V * d + off + 16,), 9.0, dtype=ge_type, device=dev)
+    st = L.dust_head_loss_grad(p(H), d, p(E), d, code, 1, T, d, V, p(y), 1.0, p(lse), p(gl), 0,
+                               p(flatH[off:]), ld, p(flatE[off:]),
+                               dust.F32 if ge == "f32" else dust.BF16, p(ws), n.value,
+                               C.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == dust.OK
+    rows = flatH[off:off + T * ld].view(T, ld)
+    assert (rows[:, d:] == 9.0).all()
+    for a, b in ((rows[:, :d], gH), (flatE[off:off + V * d].view(V, d), gE)):
+        assert torch.equal(a, b) or T == 2 and rel_fro(_np(a), _np(b)) <= GRAD_TOL[dtype]
+    for flat, end in ((flatH, off + T * ld), (flatE, off + V * d)):
+        assert (flat[:off] == 9.0).all() and (flat[end:] == 9.0).all()

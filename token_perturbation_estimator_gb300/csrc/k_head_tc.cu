@@ -306,8 +306,8 @@ __device__ __forceinline__ float4 ld_shared_4(uint32_t addr) {
 // a row's values v, and row `to` is its place (-1: none). They are turned
 // around in shared memory (4 KB at buf, 16-byte pieces permuted by row), so
 // that neighbouring lanes write neighbouring columns. With a row per lane,
-// each store touched 32 lines: 3 rows, d 898, V 16557, bf16 took 213 us for
-// the products, with 2-byte stores.
+// each store touched 32 lines: the gradients of 3 rows, d 898, V 16557, bf16,
+// took 283 us then and 86 so (both on these tiles).
 __device__ __forceinline__ void store_block(uint32_t buf, const float (&v)[32], int lane, int32_t to,
                                             const OutRows& out, int64_t col, int n, bool add) {
 #pragma unroll
@@ -318,62 +318,118 @@ __device__ __forceinline__ void store_block(uint32_t buf, const float (&v)[32], 
     }
     __syncwarp();
     unsigned char* first = out.base + col * (out.bf16 ? 2 : 4);
+    const auto at_row = [&](int r) -> unsigned char* {
+        const int32_t at = __shfl_sync(0xffffffffu, to, r);
+        return at < 0 ? nullptr : first + at * out.pitch;
+    };
+    // Everything that a few stores need is read before the first of them.
     if (out.align == 16 && !out.bf16) {
         const int c = lane & 7;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + (lane >> 3);
-            const int32_t at = __shfl_sync(0xffffffffu, to, r);
-            if (at < 0 || 4 * c >= n) continue;
-            float4 x = ld_shared_4(buf + r * 128 + ((c ^ (r & 7)) << 4));
-            float4* p = reinterpret_cast<float4*>(first + at * out.pitch) + c;
-            if (add) {
-                const float4 o = *p;
-                x = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+        for (int i = 0; i < 8; i += 4) {
+            float4* p[4];
+            float4 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = 4 * (i + k) + (lane >> 3);
+                p[k] = reinterpret_cast<float4*>(at_row(r));
+                x[k] = ld_shared_4(buf + r * 128 + ((c ^ (r & 7)) << 4));
+                if (4 * c >= n) p[k] = nullptr;
+                if (add && p[k]) {
+                    const float4 o = p[k][c];
+                    x[k] = make_float4(o.x + x[k].x, o.y + x[k].y, o.z + x[k].z, o.w + x[k].w);
+                }
             }
-            *p = x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (p[k]) p[k][c] = x[k];
         }
     } else if (out.align == 16) {
         const int c = lane & 3;
+        uint4* p[4];
+        uint4 x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane >> 2);
-            const int32_t at = __shfl_sync(0xffffffffu, to, r);
-            if (at < 0 || 8 * c >= n) continue;
-            const float4 x = ld_shared_4(buf + r * 128 + (((2 * c) ^ (r & 7)) << 4));
-            const float4 y = ld_shared_4(buf + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4));
-            reinterpret_cast<uint4*>(first + at * out.pitch)[c] =
-                make_uint4(pack2(x.x, x.y), pack2(x.z, x.w), pack2(y.x, y.y), pack2(y.z, y.w));
+        for (int k = 0; k < 4; ++k) {
+            const int r = 8 * k + (lane >> 2);
+            p[k] = reinterpret_cast<uint4*>(at_row(r));
+            const float4 y = ld_shared_4(buf + r * 128 + (((2 * c) ^ (r & 7)) << 4));
+            const float4 z = ld_shared_4(buf + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4));
+            x[k] = make_uint4(pack2(y.x, y.y), pack2(y.z, y.w), pack2(z.x, z.y), pack2(z.z, z.w));
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (p[k] && 8 * c < n) p[k][c] = x[k];
     } else if (out.bf16 && out.align >= 4) {
-        const int c = lane & 15;
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-            const int r = 2 * i + (lane >> 4);
-            const int32_t at = __shfl_sync(0xffffffffu, to, r);
-            if (at < 0 || 2 * c >= n) continue;  // rows of an even number of values
-            float x, y;
-            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                         : "=f"(x), "=f"(y)
-                         : "r"(buf + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8)
-                         : "memory");
-            reinterpret_cast<uint32_t*>(first + at * out.pitch)[c] = pack2(x, y);
+        const int c = lane & 15;  // rows of an even number of values
+#pragma unroll
+        for (int i = 0; i < 16; i += 8) {
+            uint32_t* p[8];
+            uint32_t x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = 2 * (i + k) + (lane >> 4);
+                p[k] = reinterpret_cast<uint32_t*>(at_row(r));
+                float lo, hi;
+                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                             : "=f"(lo), "=f"(hi)
+                             : "r"(buf + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8)
+                             : "memory");
+                x[k] = pack2(lo, hi);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (p[k] && 2 * c < n) p[k][c] = x[k];
+        }
+    } else if (const int32_t row0 = __shfl_sync(0xffffffffu, to, 0);
+               __all_sync(0xffffffffu, to < 0 || to == row0 + lane)) {
+        // Neighbouring rows: the first `live` of them exist. No shuffles, one
+        // running address (65 rows, d 129, V 1003, fp32: 44.8 -> 38.4 us).
+        const int live = __popc(__ballot_sync(0xffffffffu, to >= 0));
+        uint32_t at[8];  // by row mod 8
+#pragma unroll
+        for (int k = 0; k < 8; ++k) at[k] = buf + (((lane >> 2) ^ k) << 4) + (lane & 3) * 4;
+        unsigned char* p = first + row0 * out.pitch + lane * (out.bf16 ? 2 : 4);
+        const int rows = lane < n ? live : 0;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[k]) : "r"(at[k] + (i + k) * 128) : "memory");
+            if (add) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (i + k < rows) x[k] = *reinterpret_cast<const float*>(p + k * out.pitch) + x[k];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (i + k >= rows) continue;
+                if (out.bf16) *reinterpret_cast<__nv_bfloat16*>(p + k * out.pitch) = __float2bfloat16_rn(x[k]);
+                else *reinterpret_cast<float*>(p + k * out.pitch) = x[k];
+            }
+            p += 8 * out.pitch;
         }
     } else {
-#pragma unroll 4
-        for (int r = 0; r < 32; ++r) {
-            const int32_t at = __shfl_sync(0xffffffffu, to, r);
-            if (at < 0 || lane >= n) continue;
-            float x;
-            asm volatile("ld.shared.f32 %0, [%1];"
-                         : "=f"(x)
-                         : "r"(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4)
-                         : "memory");
-            if (out.bf16) {
-                reinterpret_cast<__nv_bfloat16*>(first + at * out.pitch)[lane] = __float2bfloat16_rn(x);
-            } else {
-                float* p = reinterpret_cast<float*>(first + at * out.pitch) + lane;
-                *p = add ? *p + x : x;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            unsigned char* p[8];
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = i + k;
+                p[k] = at_row(r);
+                asm volatile("ld.shared.f32 %0, [%1];"
+                             : "=f"(x[k])
+                             : "r"(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4)
+                             : "memory");
+                if (lane >= n) p[k] = nullptr;
+                if (add && p[k]) x[k] = reinterpret_cast<const float*>(p[k])[lane] + x[k];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (!p[k]) continue;
+                if (out.bf16) reinterpret_cast<__nv_bfloat16*>(p[k])[lane] = __float2bfloat16_rn(x[k]);
+                else reinterpret_cast<float*>(p[k])[lane] = x[k];
             }
         }
     }
