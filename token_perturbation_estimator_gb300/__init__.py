@@ -507,6 +507,7 @@ def _values(t, name, dims):
     return code, t.get_device()
 
 
+@functools.lru_cache(maxsize=256)  # a size follows from the other sizes alone
 def _query(name, *args):
     n = C.c_size_t(0)
     _check(getattr(lib(), name)(C.byref(n), *args), name)
@@ -514,11 +515,30 @@ def _query(name, *args):
 
 
 def _space(workspace, name, ref, dev, *args):
-    """The caller's workspace, or a new one of the size that query `name` gives."""
+    """The caller's workspace, or a new one of the size that query `name` gives:
+    (tensor, address, bytes)."""
     if workspace is None:
-        return _types().empty(max(_query(name, *args), 256), dtype=_types().u8, device=ref.device)
-    _dense(workspace, "workspace", _types().u8, (workspace.numel(),), dev)
-    return workspace
+        n = max(_query(name, *args), 256)
+        workspace = _types().empty(n, dtype=_types().u8, device=ref.device)
+        return workspace, workspace.data_ptr(), n
+    n = workspace.numel()
+    return workspace, _dense(workspace, "workspace", _types().u8, (n,), dev), n
+
+
+def _output(t, name, dtype, shape, ref, dev):
+    """The caller's output, checked, or a new one: (tensor, address)."""
+    if t is None:
+        t = _types().empty(shape, dtype=dtype, device=ref.device)
+        return t, t.data_ptr()
+    return t, _dense(t, name, dtype, shape, dev)
+
+
+def _output_rows(t, name, dtype, shape, ref, dev):
+    """The same for rows that may be strided: (tensor, address, row stride)."""
+    if t is None:
+        t = _types().empty(shape, dtype=dtype, device=ref.device)
+        return t, t.data_ptr(), shape[1]
+    return t, t.data_ptr(), _rows(t, name, dtype, shape, dev)
 
 
 @_in_stream
@@ -528,18 +548,13 @@ def dust_layer_norm(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd
     ty = _types()
     code, dev = _values(x, "x", (2,))
     T, d = shape = x.shape
-    if y is None:
-        y = ty.empty(shape, dtype=x.dtype, device=x.device)
-    if mean is None:
-        mean = ty.empty(T, dtype=ty.f32, device=x.device)
-    if rstd is None:
-        rstd = ty.empty_like(mean)
+    y, y_at, ld_y = _output_rows(y, "y", x.dtype, shape, x, dev)
+    mean, mean_at = _output(mean, "mean", ty.f32, (T,), x, dev)
+    rstd, rstd_at = _output(rstd, "rstd", ty.f32, (T,), x, dev)
     st = lib().dust_layer_norm(
         x.data_ptr(), code, _rows(x, "x", x.dtype, shape, dev), T, d,
         _dense(weight, "weight", ty.f32, (d,), dev), _dense(bias, "bias", ty.f32, (d,), dev),
-        eps, y.data_ptr(), _rows(y, "y", x.dtype, shape, dev),
-        _dense(mean, "mean", ty.f32, (T,), dev), _dense(rstd, "rstd", ty.f32, (T,), dev),
-        ty.stream_of(dev))
+        eps, y_at, ld_y, mean_at, rstd_at, ty.stream_of(dev))
     _check(st, "dust_layer_norm")
     return y, mean, rstd
 
@@ -556,21 +571,16 @@ def dust_layer_norm_grad(gy, x, mean, rstd, weight=None, flags=0, gx=None, gweig
     T, d = shape = x.shape
     if flags & ACCUMULATE and (gweight is None or gbias is None):
         raise ValueError("ACCUMULATE needs the gweight and gbias to add to")
-    if gx is None:
-        gx = ty.empty(shape, dtype=x.dtype, device=x.device)
-    if gweight is None:
-        gweight = ty.empty(d, dtype=ty.f32, device=x.device)
-    if gbias is None:
-        gbias = ty.empty_like(gweight)
-    workspace = _space(workspace, "dust_layer_norm_grad_workspace", x, dev, T, d)
+    gx, gx_at, ld_gx = _output_rows(gx, "gx", x.dtype, shape, x, dev)
+    gweight, gweight_at = _output(gweight, "gweight", ty.f32, (d,), x, dev)
+    gbias, gbias_at = _output(gbias, "gbias", ty.f32, (d,), x, dev)
+    workspace, ws_at, ws_bytes = _space(workspace, "dust_layer_norm_grad_workspace", x, dev, T, d)
     st = lib().dust_layer_norm_grad(
         gy.data_ptr(), _rows(gy, "gy", x.dtype, shape, dev), x.data_ptr(),
         _rows(x, "x", x.dtype, shape, dev), code, T, d,
         _dense(weight, "weight", ty.f32, (d,), dev), _dense(mean, "mean", ty.f32, (T,), dev),
-        _dense(rstd, "rstd", ty.f32, (T,), dev), flags, gx.data_ptr(),
-        _rows(gx, "gx", x.dtype, shape, dev), _dense(gweight, "gweight", ty.f32, (d,), dev),
-        _dense(gbias, "gbias", ty.f32, (d,), dev), workspace.data_ptr(), workspace.numel(),
-        ty.stream_of(dev))
+        _dense(rstd, "rstd", ty.f32, (T,), dev), flags, gx_at, ld_gx, gweight_at, gbias_at,
+        ws_at, ws_bytes, ty.stream_of(dev))
     _check(st, "dust_layer_norm_grad")
     return gx, gweight, gbias
 
@@ -597,30 +607,25 @@ def _head_inputs(H, E):
 def _loss_outputs(H, S, T, dev, loss, lse, delta, changes):
     ty = _types()
     shape = H.shape[:-1]
-    if loss is None:
-        loss = ty.empty(shape, dtype=ty.f32, device=H.device)
-    if lse is None:
-        lse = ty.empty_like(loss)
-    if delta is None and changes:
-        delta = ty.empty((S - 1, T), dtype=ty.f32, device=H.device)
-    return loss, lse, delta, (_dense(loss, "loss", ty.f32, shape, dev),
-                              _dense(lse, "lse", ty.f32, shape, dev)), \
-        _dense(delta, "delta", ty.f32, (S - 1, T), dev)
+    loss, loss_at = _output(loss, "loss", ty.f32, shape, H, dev)
+    lse, lse_at = _output(lse, "lse", ty.f32, shape, H, dev)
+    delta_at = None
+    if delta is not None or changes:
+        delta, delta_at = _output(delta, "delta", ty.f32, (S - 1, T), H, dev)
+    return loss, lse, delta, (loss_at, lse_at), delta_at
 
 
 def _grad_outputs(H, E, d, dev, flags, gH, gE, gE_dtype):
     ty = _types()
     if flags & ACCUMULATE and gE is None:
         raise ValueError("ACCUMULATE needs the gE to add to")
-    if gH is None:
-        gH = ty.empty(H.shape, dtype=H.dtype, device=H.device)
-    if gE is None:
-        gE = ty.empty(E.shape, dtype=gE_dtype or ty.f32, device=E.device)
-    gcode = ty.code.get(gE.dtype)
+    ge_type = (gE_dtype or ty.f32) if gE is None else gE.dtype
+    gcode = ty.code.get(ge_type)
     if gcode is None:
-        raise ValueError("gE must be f32 or bf16, got %s" % gE.dtype)
-    return gH, gE, (flags, _dense(gH, "gH", H.dtype, H.shape, dev), d,
-                    _dense(gE, "gE", gE.dtype, E.shape, dev), gcode)
+        raise ValueError("gE must be f32 or bf16, got %s" % ge_type)
+    gH, gh_at = _output(gH, "gH", H.dtype, H.shape, H, dev)
+    gE, ge_at = _output(gE, "gE", ge_type, E.shape, E, dev)
+    return gH, gE, (flags, gh_at, d, ge_at, gcode)
 
 
 @_in_stream
@@ -633,10 +638,10 @@ def dust_head_loss(H, E, targets, scale=1.0, changes=False, loss=None, lse=None,
     ty = _types()
     code, dev, S, T, d, V, operands = _head_inputs(H, E)
     loss, lse, delta, outs, delta_at = _loss_outputs(H, S, T, dev, loss, lse, delta, changes)
-    workspace = _space(workspace, "dust_head_loss_workspace", H, dev, S, T, d, V, code)
+    workspace, ws_at, ws_bytes = _space(workspace, "dust_head_loss_workspace", H, dev,
+                                        S, T, d, V, code)
     st = lib().dust_head_loss(*operands, _dense(targets, "targets", ty.i32, (T,), dev), scale,
-                              *outs, delta_at, workspace.data_ptr(), workspace.numel(),
-                              ty.stream_of(dev))
+                              *outs, delta_at, ws_at, ws_bytes, ty.stream_of(dev))
     _check(st, "dust_head_loss")
     return (loss, lse) if delta is None else (loss, lse, delta)
 
@@ -652,11 +657,12 @@ def dust_head_loss_grad(H, E, targets, lse, gloss, scale=1.0, flags=0, gH=None, 
     code, dev, S, T, d, V, operands = _head_inputs(H, E)
     shape = H.shape[:-1]
     gH, gE, outs = _grad_outputs(H, E, d, dev, flags, gH, gE, gE_dtype)
-    workspace = _space(workspace, "dust_head_loss_grad_workspace", H, dev, S, T, d, V, code)
+    workspace, ws_at, ws_bytes = _space(workspace, "dust_head_loss_grad_workspace", H, dev,
+                                        S, T, d, V, code)
     st = lib().dust_head_loss_grad(*operands, _dense(targets, "targets", ty.i32, (T,), dev),
                                    scale, _dense(lse, "lse", ty.f32, shape, dev),
                                    _dense(gloss, "gloss", ty.f32, shape, dev), *outs,
-                                   workspace.data_ptr(), workspace.numel(), ty.stream_of(dev))
+                                   ws_at, ws_bytes, ty.stream_of(dev))
     _check(st, "dust_head_loss_grad")
     return gH, gE
 
@@ -682,12 +688,11 @@ def dust_distill_loss(H, E, ids, teacher, scale=1.0, changes=False, loss=None, l
     K, entries = _teacher_inputs(ids, teacher, T, dev)
     loss, lse, delta, outs, delta_at = _loss_outputs(H, S, T, dev, loss, lse, delta, changes)
     shape = (*H.shape[:-1], K)
-    if student is None:
-        student = ty.empty(shape, dtype=ty.f32, device=H.device)
-    workspace = _space(workspace, "dust_distill_loss_workspace", H, dev, S, T, d, V, K, code)
-    st = lib().dust_distill_loss(*operands, *entries, scale, *outs,
-                                 _dense(student, "student", ty.f32, shape, dev), delta_at,
-                                 workspace.data_ptr(), workspace.numel(), ty.stream_of(dev))
+    student, student_at = _output(student, "student", ty.f32, shape, H, dev)
+    workspace, ws_at, ws_bytes = _space(workspace, "dust_distill_loss_workspace", H, dev,
+                                        S, T, d, V, K, code)
+    st = lib().dust_distill_loss(*operands, *entries, scale, *outs, student_at, delta_at,
+                                 ws_at, ws_bytes, ty.stream_of(dev))
     _check(st, "dust_distill_loss")
     return (loss, lse, student) if delta is None else (loss, lse, student, delta)
 
@@ -702,13 +707,13 @@ def dust_distill_loss_grad(H, E, ids, teacher, lse, student, gloss, scale=1.0, f
     K, entries = _teacher_inputs(ids, teacher, T, dev)
     shape = H.shape[:-1]
     gH, gE, outs = _grad_outputs(H, E, d, dev, flags, gH, gE, gE_dtype)
-    workspace = _space(workspace, "dust_distill_loss_grad_workspace", H, dev, S, T, d, V, K, code)
+    workspace, ws_at, ws_bytes = _space(workspace, "dust_distill_loss_grad_workspace", H, dev,
+                                        S, T, d, V, K, code)
     st = lib().dust_distill_loss_grad(*operands, *entries, scale,
                                       _dense(lse, "lse", ty.f32, shape, dev),
                                       _dense(student, "student", ty.f32, (*shape, K), dev),
                                       _dense(gloss, "gloss", ty.f32, shape, dev), *outs,
-                                      workspace.data_ptr(), workspace.numel(),
-                                      ty.stream_of(dev))
+                                      ws_at, ws_bytes, ty.stream_of(dev))
     _check(st, "dust_distill_loss_grad")
     return gH, gE
 
