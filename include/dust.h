@@ -570,10 +570,12 @@ dust_status dust_layer_norm_grad(const void* gy, int64_t ld_gy, const void* x, i
  *            aligned; contents on entry are ignored.
  * bf16 inputs: products of the exact bf16 values summed in fp32; in the
  * gradients G is rounded to bf16 (it is a tensor-core operand), divided by
- * the largest |gloss| first so that equal weights round as 1 does. fp32
+ * the largest |gloss| first so that equal weights round as 1 does (of a few
+ * rows, S*T up to 4, it may stay fp32). fp32
  * inputs: every product and sum to fp32 accuracy (each operand to 24 bits,
- * or to 2^-133 where that is more: operands below 2^-110). All sums run in an order
- * fixed by the sizes and by which rows take part: deterministic.
+ * or to 2^-133 where that is more: operands below 2^-110). All sums run in an
+ * order fixed by the sizes, by which rows take part and by whether rows start
+ * on 16 bytes: deterministic.
  * d >= 1, V >= 1, S >= 1; S*T, d and V up to 2^31 - 1, S*T*d and V*d up to
  * 2^40 (DUST_ERR_RANGE). T = 0 writes zeros to gE (or leaves it,
  * accumulating) and nothing else.

@@ -3,7 +3,9 @@
 // softmax cross entropy against a target id, and distillation from a
 // teacher's largest logits. The products are k_head_tc.cu's.
 //
-// Loss (of more than a few rows, which k_head_few.cu takes): one launch forms the logits tile by tile and leaves per row a partial
+// A few rows go to k_head_few.cu.
+//
+// Loss: one launch forms the logits tile by tile and leaves per row a partial
 // maximum and sum for every half tile, and the target's logit; a second one
 // joins them. For distillation the pass over the tiles also picks the logits
 // of the teacher's entries, which a first launch has put in order. (Formed
@@ -20,6 +22,10 @@
 //
 // fp32 inputs, and bf16 ones whose rows do not start on 16 bytes, are first
 // copied into the workspace, as three bf16 planes or padded rows.
+//
+// What is here is bound by latency but for the copies: 4 to 8 us a launch
+// (16384 rows: which take part 5 us, joining 128 partials of 4096 rows 7 us,
+// ordering 64 entries of 4096 tokens 14 us).
 #include <algorithm>
 #include <cmath>
 
@@ -153,7 +159,8 @@ struct BinArgs {
 // Entries in order of their ids, so that the passes over the columns meet
 // them on their way: a warp per token (loss) or row (gradient) sorts them (by
 // counting, or many of them by a bitonic network, in shared memory), writes
-// them out, and looks up where each half tile's first one is. Absent entries come last and are not counted.
+// them out, and looks up where each half tile's first one is. Absent entries
+// come last and are not counted.
 // The loss is to write an entry's logit to its place; the gradient is to put
 // exp(x - lse) - q there, which is formed here, with q the teacher's
 // probability summed over the entries of the same id.

@@ -1,6 +1,6 @@
 // The head's loss and gradients for a few rows (single tokens being scored).
-// Loss: every row of E is read once, as it lies, and multiplied with all rows of H on the CUDA
-// cores, fp32 throughout. Bound by E's bytes; the tensor-core kernel spends a
+// Loss: every row of E is read once, as it lies, and multiplied with all rows
+// of H on the CUDA cores, fp32 throughout. Bound by E's bytes; the tensor-core kernel spends a
 // 256-row tile on these rows, and first copies an fp32 E into three planes.
 //
 // A warp takes 16 / NR rows of E at a time (NR: the rows of H, rounded up to
