@@ -117,19 +117,16 @@ struct TcArgs {
     float *gh_acc, *ge_acc;    // tiles of partial sums, by unit
     int first, last, accumulate;
     int cut0, cut1;            // slices of the summed dimension, gH and gE
+    int joint;                 // all planes of a step together (see joint_planes)
     int stall;
     unsigned int* status;
 };
 
-// Planes of A and B of the p-th product, the smallest products first.
-__device__ __forceinline__ int plane_a(int planes, int p) {
-    constexpr int a[6] = {2, 0, 1, 1, 0, 0};
-    return planes == 1 ? 0 : a[p];
-}
-__device__ __forceinline__ int plane_b(int planes, int p) {
-    constexpr int b[6] = {0, 2, 1, 0, 1, 0};
-    return planes == 1 ? 0 : b[p];
-}
+// Planes of A and B of the p-th product, the smallest products first: (2, 0),
+// (0, 2), (1, 1), (1, 0), (0, 1), (0, 0). In registers: a table in memory
+// would be read per step.
+__device__ __forceinline__ int plane_a(int p) { return 0x001102 >> (4 * p) & 15; }
+__device__ __forceinline__ int plane_b(int p) { return 0x010120 >> (4 * p) & 15; }
 
 // Where a unit of work lies: which product (0: logits or gH, 1: gE), its
 // first row and column, and its steps along the summed dimension (of every
@@ -727,6 +724,12 @@ struct Epilogue {
             if (col >= a.d) break;
             float v[32];
             tc::tmem_ld_32x32(taddr + at, v);
+            if (a.joint) {
+                float big[32];
+                tc::tmem_ld_32x32(taddr + 128 + at, big);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] += big[i];
+            }
             const int n = a.d - col < 32 ? static_cast<int>(a.d - col) : 32;
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = zero ? 0.0f : alpha * v[i];
@@ -753,6 +756,37 @@ struct Epilogue {
         }
     }
 };
+
+// As mbar_wait_for, and false as soon as anyone in this CTA has given up. The
+// flag is read while there is something to wait for, not on the way.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                              volatile int* abort_flag) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = tc::globaltimer();
+    while (true) {
+        if (tc::mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag || tc::globaltimer() - t0 > limit_ns) return false;
+    }
+}
+
+// An operand in the stages: the descriptor of stage 0, and the bytes from one
+// 16-deep slice of a step to the next.
+struct Operand {
+    uint64_t first;
+    uint32_t slice;
+};
+
+// The products of one step: A of one stage, B of the same or another. (The
+// address is the descriptor's lowest field and stays below its 14 bits.)
+__device__ __forceinline__ void issue_step(uint32_t to, const Operand& A, int stage_a, const Operand& B,
+                                           int stage_b, uint32_t idesc, bool add) {
+    const uint64_t da = A.first + static_cast<uint32_t>(stage_a) * (kStageBytes >> 4);
+    const uint64_t db = B.first + static_cast<uint32_t>(stage_b) * (kStageBytes >> 4);
+#pragma unroll
+    for (uint32_t u = 0; u < 4; ++u)
+        tc::mma_bf16_pair(to, da + (u * A.slice >> 4), db + (u * B.slice >> 4), idesc,
+                          add || u != 0 ? 1u : 0u);
+}
 
 // Maps: kLse H, -, E, -; kFactor H, Hc, E, G; kMul G, E, H, Hc.
 template <int MODE, int PLANES>
@@ -807,58 +841,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::kWaitNs + 2000ull * static_cast<uint64_t>(pairs) * max(plan.steps0, plan.steps1);
 
     if (warp == 0) {
-        if (lane == 0) {
-            // The rows that take part are read where they lie unless some were left out.
-            const bool compact = a.counts && a.rows != plan.rows;
-            const CUtensorMap *A0, *B0, *A1 = nullptr, *B1 = nullptr;
-            if (MODE == kMul) {
-                A0 = &tm0; B0 = &tm1;                      // gH = G E
-                A1 = &tm0; B1 = compact ? &tm3 : &tm2;     // gE = G^T H
-            } else {
-                A0 = compact ? &tm1 : &tm0;
-                B0 = &tm2;
-            }
-            int it = 0;
-            for (int j = 0, t; !*abort_flag && (t = plan.unit(j)) >= 0; ++j) {
-                const Tile w = plan.at(a, t);
-                const CUtensorMap* ma = w.job ? A1 : A0;
-                const CUtensorMap* mb = w.job ? B1 : B0;
-                // Which operand has the summed dimension in rows.
-                const bool a_mn = MODE == kMul && w.job == 1, b_mn = MODE == kMul;
-                const int32_t am = static_cast<int32_t>(w.m0) + static_cast<int32_t>(rank) * kHalf;
-                // E is whole: its rows of the piece start at v0.
-                const int32_t v0 = static_cast<int32_t>(a.v0);
-                const int32_t bn0 = static_cast<int32_t>(w.n0) +
-                                    static_cast<int32_t>(rank) * (a.bn / 2) +
-                                    (MODE == kMul ? 0 : v0);
-                const int32_t b_k0 = MODE == kMul && w.job == 0 ? v0 : 0;
-                for (int p = 0; p < pairs && !*abort_flag; ++p) {
-                    const int pa = plane_a(a.planes, p), pb = plane_b(a.planes, p);
-                    for (int k = 0; k < w.steps; ++k, ++it) {
-                        const int st = it % kStages;
-                        if (!tc::mbar_wait_for(&ctl->empty[st], ((it / kStages) & 1) ^ 1,
-                                                   tile_ns) || *abort_flag) {
-                            *abort_flag = 1;
-                            break;
-                        }
-                        unsigned char* base = smem + st * kStageBytes;
-                        const uint32_t bar = tc::at_rank(&ctl->full[st], 0);
-                        if (rank == 0)
-                            tc::mbar_arrive_expect_tx(&ctl->full[st], 2 * (2 + b_boxes) * kBoxBytes);
-                        const int32_t kk = (w.k0 + k) * 64;
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-                            tc::tma_load_3d_pair(base + u * kBoxBytes, ma, a_mn ? am + 64 * u : kk,
-                                                 a_mn ? kk : am + 64 * u, pa, bar);
-                        for (int u = 0; u < b_boxes; ++u)
-                            tc::tma_load_3d_pair(base + (2 + u) * kBoxBytes, mb,
-                                                 b_mn ? bn0 + 64 * u : kk,
-                                                 b_mn ? b_k0 + kk : bn0 + 64 * u, pb, bar);
+        // The rows that take part are read where they lie unless some were left out.
+        const bool compact = a.counts && a.rows != plan.rows;
+        // A lane for each box of a step: two of A, one or two of B.
+        const bool is_b = lane >= 2;
+        const int box = lane & 1;
+        const bool active = lane < 2 + b_boxes;
+        const CUtensorMap *m0, *m1 = nullptr;
+        if (MODE == kMul) {
+            m0 = is_b ? &tm1 : &tm0;                         // gH = G E
+            m1 = is_b ? (compact ? &tm3 : &tm2) : &tm0;      // gE = G^T H
+        } else {
+            m0 = is_b ? &tm2 : compact ? &tm1 : &tm0;
+        }
+        int it = 0;
+        bool stop = false;  // the same in all lanes
+        for (int j = 0, t; !stop && (t = plan.unit(j)) >= 0; ++j) {
+            const Tile w = plan.at(a, t);
+            const CUtensorMap* map = w.job ? m1 : m0;
+            // Which operand has the summed dimension in rows.
+            const bool mn = is_b ? MODE == kMul : MODE == kMul && w.job == 1;
+            // E is whole: its rows of the piece start at v0.
+            const int32_t v0 = static_cast<int32_t>(a.v0);
+            const int32_t at = (is_b ? static_cast<int32_t>(w.n0) + static_cast<int32_t>(rank) * (a.bn / 2) +
+                                           (MODE == kMul ? 0 : v0)
+                                     : static_cast<int32_t>(w.m0) + static_cast<int32_t>(rank) * kHalf) +
+                               64 * box;
+            const int32_t k_first = w.k0 * 64 + (is_b && MODE == kMul && w.job == 0 ? v0 : 0);
+            // Steps of one pair of planes after another, or the planes of
+            // one step after another, the smallest first.
+            const int outer = a.joint ? w.steps : pairs, inner = a.joint ? 3 : w.steps;
+            for (int p = 0; p < outer && !stop; ++p) {
+                const int own = pairs == 1 ? 0 : is_b ? plane_b(p) : plane_a(p);
+                for (int i = 0; i < inner; ++i, ++it) {
+                    const int32_t kk = k_first + 64 * (a.joint ? p : i);
+                    const int plane = a.joint ? 2 - i : own;
+                    const int st = it % kStages;
+                    stop = !__all_sync(0xffffffffu, wait_or_abort(&ctl->empty[st], ((it / kStages) & 1) ^ 1,
+                                                                  tile_ns, abort_flag));
+                    if (stop) {
+                        *abort_flag = 1;
+                        break;
                     }
+                    if (rank == 0 && lane == 0)
+                        tc::mbar_arrive_expect_tx(&ctl->full[st], 2 * (2 + b_boxes) * kBoxBytes);
+                    __syncwarp();
+                    if (active)
+                        tc::tma_load_3d_pair(smem + st * kStageBytes + lane * kBoxBytes, map,
+                                             mn ? at : kk, mn ? kk : at, plane,
+                                             tc::at_rank(&ctl->full[st], 0));
                 }
             }
-            ctl->issued = it;
         }
+        if (lane == 0) ctl->issued = it;
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             if (a.stall && !tc::mbar_wait(&ctl->never, 0)) *abort_flag = 1;
@@ -871,34 +906,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 t = plan.unit(j + 1);
                 if (t >= 0) next = plan.at(a, t);
                 const int acc = j & 1;
-                if (!tc::mbar_wait_for(&ctl->tempty[acc], ((j >> 1) & 1) ^ 1, tile_ns)) {
+                if (!wait_or_abort(&ctl->tempty[acc], ((j >> 1) & 1) ^ 1, tile_ns, abort_flag)) {
                     *abort_flag = 1;
                     break;
                 }
                 tc::tc_fence_after();
                 const bool a_mn = MODE == kMul && w.job == 1, b_mn = MODE == kMul;
                 const uint32_t idesc = tc::idesc_bf16(kHeadTile, a.bn, a_mn, b_mn);
-                // Bytes from one 16-deep slice of a step to the next.
-                const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
-                const uint32_t a_lbo = a_mn ? kBoxBytes : 16, b_lbo = b_mn ? kBoxBytes : 16;
                 const uint32_t dst = tmem + acc * 256;
-                const int n = pairs * w.steps;
-                for (int k = 0; k < n; ++k, ++it) {
-                    const int st = it % kStages;
-                    if (!tc::mbar_wait_for(&ctl->full[st], (it / kStages) & 1, tc::kWaitNs) ||
-                        *abort_flag) {
+                const Operand A = {tc::sdesc_sw128(tc::smem_u32(smem), a_mn ? kBoxBytes : 16, 1024),
+                                   a_mn ? 2048u : 32u};
+                const Operand B = {tc::sdesc_sw128(tc::smem_u32(smem + 2 * kBoxBytes),
+                                                   b_mn ? kBoxBytes : 16, 1024),
+                                   b_mn ? 2048u : 32u};
+                const int n = a.joint ? w.steps : pairs * w.steps;
+                for (int k = 0; k < n; ++k) {
+                    const int s2 = it % kStages;
+                    bool ok = wait_or_abort(&ctl->full[s2], (it / kStages) & 1, tc::kWaitNs, abort_flag);
+                    if (!a.joint) {
+                        if (!ok) {
+                            *abort_flag = 1;
+                            break;
+                        }
+                        tc::tc_fence_after();
+                        issue_step(dst, A, s2, B, s2, idesc, k != 0);
+                        tc::mma_commit_pair(&ctl->empty[s2]);
+                        ++it;
+                        continue;
+                    }
+                    const int s1 = (it + 1) % kStages, s0 = (it + 2) % kStages;
+                    ok = ok &&
+                         wait_or_abort(&ctl->full[s1], ((it + 1) / kStages) & 1, tc::kWaitNs, abort_flag) &&
+                         wait_or_abort(&ctl->full[s0], ((it + 2) / kStages) & 1, tc::kWaitNs, abort_flag);
+                    if (!ok) {
                         *abort_flag = 1;
                         break;
                     }
                     tc::tc_fence_after();
-                    const uint32_t sa = tc::smem_u32(smem + st * kStageBytes);
-                    const uint32_t sb = sa + 2 * kBoxBytes;
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        tc::mma_bf16_pair(dst, tc::sdesc_sw128(sa + u * a_step, a_lbo, 1024),
-                                          tc::sdesc_sw128(sb + u * b_step, b_lbo, 1024), idesc,
-                                          (k | u) != 0 ? 1u : 0u);
-                    tc::mma_commit_pair(&ctl->empty[st]);
+                    issue_step(dst, A, s2, B, s0, idesc, k != 0);
+                    issue_step(dst, A, s0, B, s2, idesc, true);
+                    tc::mma_commit_pair(&ctl->empty[s2]);
+                    issue_step(dst, A, s1, B, s1, idesc, true);
+                    issue_step(dst, A, s1, B, s0, idesc, true);
+                    issue_step(dst, A, s0, B, s1, idesc, true);
+                    tc::mma_commit_pair(&ctl->empty[s1]);
+                    issue_step(dst + 128, A, s0, B, s0, idesc, k != 0);
+                    tc::mma_commit_pair(&ctl->empty[s0]);
+                    it += 3;
                 }
                 if (*abort_flag) break;
                 tc::mma_commit_pair(&ctl->tfull[acc]);
@@ -923,7 +977,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int j = 0; t >= 0; ++j) {
             const int acc = j & 1;
             epi.third(o);
-            const bool ok = tc::mbar_wait_for(&ctl->tfull[acc], (j >> 1) & 1, tile_ns);
+            const bool ok = wait_or_abort(&ctl->tfull[acc], (j >> 1) & 1, tile_ns, abort_flag);
             tc::tc_fence_after();
             if (!__all_sync(0xffffffffu, ok) || *abort_flag) {
                 *abort_flag = 1;
@@ -1252,6 +1306,7 @@ cudaError_t launch_head_products(const HeadProducts& h, const HeadMaps& maps, cu
     a.counts = h.counts;
     a.planes = h.planes;
     a.bn = product_columns(h.d);
+    a.joint = a.planes == 3 && a.bn == 128;
     a.scale = h.scale;
     a.row_of = h.row_of;
     a.gh_acc = h.gh_acc;
