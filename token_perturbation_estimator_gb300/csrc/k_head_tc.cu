@@ -757,16 +757,65 @@ struct Epilogue {
     }
 };
 
+// try_wait that may suspend the thread for up to hint ns.
+__device__ __forceinline__ bool try_wait_hint(uint64_t* bar, uint32_t parity, uint32_t hint) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity), "r"(hint)
+        : "memory");
+    return ok != 0;
+}
+
 // As mbar_wait_for, and false as soon as anyone in this CTA has given up. The
 // flag is read while there is something to wait for, not on the way.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
                                               volatile int* abort_flag) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
+    if (try_wait_hint(bar, parity, 100000)) return true;
     const uint64_t t0 = tc::globaltimer();
     while (true) {
-        if (tc::mbar_try_wait(bar, parity)) return true;
+        if (try_wait_hint(bar, parity, 100000)) return true;
         if (*abort_flag || tc::globaltimer() - t0 > limit_ns) return false;
     }
+}
+
+// The same for a whole warp, whose lanes all get the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                          volatile int* abort_flag) {
+    if (__all_sync(0xffffffffu, try_wait_hint(bar, parity, 100000))) return true;
+    const uint64_t t0 = tc::globaltimer();
+    while (true) {
+        if (__all_sync(0xffffffffu, try_wait_hint(bar, parity, 100000))) return true;
+        const bool enough = *abort_flag || tc::globaltimer() - t0 > limit_ns;
+        if (__any_sync(0xffffffffu, enough)) return false;
+    }
+}
+
+// Lane 0's value, which the compiler then knows to be the same in all lanes.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+__device__ __forceinline__ Tile uniform(const Tile& t) {
+    Tile w;
+    w.job = uniform(t.job);
+    w.m0 = uniform(static_cast<int>(t.m0));
+    w.n0 = uniform(static_cast<int>(t.n0));
+    w.k0 = uniform(t.k0);
+    w.steps = uniform(t.steps);
+    w.index = t.index;
+    return w;
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
 }
 
 // An operand in the stages: the descriptor of stage 0, and the bytes from one
@@ -800,8 +849,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     unsigned char* store_bufs = smem + kStages * kStageBytes;
     __shared__ Ctl ctl_s;
     Ctl* ctl = &ctl_s;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = tc::cluster_rank_of_cta();
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const uint32_t rank = uniform(tc::cluster_rank_of_cta());
     const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
@@ -840,80 +889,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint64_t tile_ns =
         tc::kWaitNs + 2000ull * static_cast<uint64_t>(pairs) * max(plan.steps0, plan.steps1);
 
+    // The loads and the products are issued by one lane each, but the whole
+    // warp goes through the steps with them: places, addresses and descriptors
+    // are then the same in all lanes for the compiler too, which keeps them in
+    // uniform registers. (In a branch of one lane, every operand of every
+    // instruction was moved there first: 145 cycles a load, 57 a product.)
     if (warp == 0) {
+        const bool one = elect_one();
         // The rows that take part are read where they lie unless some were left out.
-        const bool compact = a.counts && a.rows != plan.rows;
-        // A lane for each box of a step: two of A, one or two of B.
-        const bool is_b = lane >= 2;
-        const int box = lane & 1;
-        const bool active = lane < 2 + b_boxes;
-        const CUtensorMap *m0, *m1 = nullptr;
+        const bool compact = uniform(a.counts && a.rows != plan.rows) != 0;
+        const uint32_t full = tc::at_rank(&ctl->full[0], 0);
+        const uint32_t bytes = 2 * (2 + b_boxes) * kBoxBytes;  // of a step, both CTAs
+        const CUtensorMap *A0, *B0, *A1 = nullptr, *B1 = nullptr;
         if (MODE == kMul) {
-            m0 = is_b ? &tm1 : &tm0;                         // gH = G E
-            m1 = is_b ? (compact ? &tm3 : &tm2) : &tm0;      // gE = G^T H
+            A0 = &tm0; B0 = &tm1;                      // gH = G E
+            A1 = &tm0; B1 = compact ? &tm3 : &tm2;     // gE = G^T H
         } else {
-            m0 = is_b ? &tm2 : compact ? &tm1 : &tm0;
+            A0 = compact ? &tm1 : &tm0;
+            B0 = &tm2;
         }
-        int it = 0;
-        bool stop = false;  // the same in all lanes
-        for (int j = 0, t; !stop && (t = plan.unit(j)) >= 0; ++j) {
-            const Tile w = plan.at(a, t);
-            const CUtensorMap* map = w.job ? m1 : m0;
+        int it = 0, st = 0;
+        uint32_t parity = 1;
+        bool stop = false;
+        for (int j = 0, t; !stop && (t = uniform(plan.unit(j))) >= 0; ++j) {
+            const Tile w = uniform(plan.at(a, t));
+            const CUtensorMap* ma = w.job ? A1 : A0;
+            const CUtensorMap* mb = w.job ? B1 : B0;
             // Which operand has the summed dimension in rows.
-            const bool mn = is_b ? MODE == kMul : MODE == kMul && w.job == 1;
+            const bool a_mn = MODE == kMul && w.job == 1, b_mn = MODE == kMul;
+            const int32_t am = static_cast<int32_t>(w.m0) + static_cast<int32_t>(rank) * kHalf;
             // E is whole: its rows of the piece start at v0.
             const int32_t v0 = static_cast<int32_t>(a.v0);
-            const int32_t at = (is_b ? static_cast<int32_t>(w.n0) + static_cast<int32_t>(rank) * (a.bn / 2) +
-                                           (MODE == kMul ? 0 : v0)
-                                     : static_cast<int32_t>(w.m0) + static_cast<int32_t>(rank) * kHalf) +
-                               64 * box;
-            const int32_t k_first = w.k0 * 64 + (is_b && MODE == kMul && w.job == 0 ? v0 : 0);
+            const int32_t bn0 = static_cast<int32_t>(w.n0) +
+                                static_cast<int32_t>(rank) * (a.bn / 2) + (MODE == kMul ? 0 : v0);
+            const int32_t b_k0 = MODE == kMul && w.job == 0 ? v0 : 0;
             // Steps of one pair of planes after another, or the planes of
             // one step after another, the smallest first.
             const int outer = a.joint ? w.steps : pairs, inner = a.joint ? 3 : w.steps;
             for (int p = 0; p < outer && !stop; ++p) {
-                const int own = pairs == 1 ? 0 : is_b ? plane_b(p) : plane_a(p);
+                const int pa0 = pairs == 1 ? 0 : plane_a(p), pb0 = pairs == 1 ? 0 : plane_b(p);
                 for (int i = 0; i < inner; ++i, ++it) {
-                    const int32_t kk = k_first + 64 * (a.joint ? p : i);
-                    const int plane = a.joint ? 2 - i : own;
-                    const int st = it % kStages;
-                    stop = !__all_sync(0xffffffffu, wait_or_abort(&ctl->empty[st], ((it / kStages) & 1) ^ 1,
-                                                                  tile_ns, abort_flag));
-                    if (stop) {
+                    const int32_t kk = (w.k0 + (a.joint ? p : i)) * 64;
+                    const int pa = a.joint ? 2 - i : pa0, pb = a.joint ? 2 - i : pb0;
+                    if (!warp_wait(&ctl->empty[st], parity, tile_ns, abort_flag)) {
                         *abort_flag = 1;
+                        stop = true;
                         break;
                     }
-                    if (rank == 0 && lane == 0)
-                        tc::mbar_arrive_expect_tx(&ctl->full[st], 2 * (2 + b_boxes) * kBoxBytes);
+                    unsigned char* base = smem + st * kStageBytes;
+                    const uint32_t bar = full + st * 8;
+                    if (one) {
+                        if (rank == 0) tc::mbar_arrive_expect_tx(&ctl->full[st], bytes);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            tc::tma_load_3d_pair(base + u * kBoxBytes, ma, a_mn ? am + 64 * u : kk,
+                                                 a_mn ? kk : am + 64 * u, pa, bar);
+                        tc::tma_load_3d_pair(base + 2 * kBoxBytes, mb, b_mn ? bn0 : kk,
+                                             b_mn ? b_k0 + kk : bn0, pb, bar);
+                        if (b_boxes == 2)
+                            tc::tma_load_3d_pair(base + 3 * kBoxBytes, mb, b_mn ? bn0 + 64 : kk,
+                                                 b_mn ? b_k0 + kk : bn0 + 64, pb, bar);
+                    }
                     __syncwarp();
-                    if (active)
-                        tc::tma_load_3d_pair(smem + st * kStageBytes + lane * kBoxBytes, map,
-                                             mn ? at : kk, mn ? kk : at, plane,
-                                             tc::at_rank(&ctl->full[st], 0));
+                    if (++st == kStages) {
+                        st = 0;
+                        parity ^= 1;
+                    }
                 }
             }
         }
         if (lane == 0) ctl->issued = it;
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            if (a.stall && !tc::mbar_wait(&ctl->never, 0)) *abort_flag = 1;
-            int it = 0;
-            int t = plan.unit(0);
-            Tile next = t >= 0 ? plan.at(a, t) : Tile{};
-            for (int j = 0; !*abort_flag && t >= 0; ++j) {
+        if (rank == 0) {
+            const bool one = elect_one();
+            bool stop = a.stall && !__all_sync(0xffffffffu, tc::mbar_wait(&ctl->never, 0));
+            const uint32_t acc0 = uniform(tmem);
+            int it = 0, st = 0;
+            uint32_t parity = 0;
+            const auto advance = [&] {
+                ++it;
+                if (++st == kStages) {
+                    st = 0;
+                    parity ^= 1;
+                }
+            };
+            const auto loaded = [&] {
+                return warp_wait(&ctl->full[st], parity, tc::kWaitNs, abort_flag);
+            };
+            int t = uniform(plan.unit(0));
+            Tile next = t >= 0 ? uniform(plan.at(a, t)) : Tile{};
+            for (int j = 0; !stop && t >= 0; ++j) {
                 const Tile w = next;
                 // The next one's place is worked out before this one's steps.
-                t = plan.unit(j + 1);
-                if (t >= 0) next = plan.at(a, t);
+                t = uniform(plan.unit(j + 1));
+                if (t >= 0) next = uniform(plan.at(a, t));
                 const int acc = j & 1;
-                if (!wait_or_abort(&ctl->tempty[acc], ((j >> 1) & 1) ^ 1, tile_ns, abort_flag)) {
-                    *abort_flag = 1;
+                if (!warp_wait(&ctl->tempty[acc], ((j >> 1) & 1) ^ 1, tile_ns, abort_flag)) {
+                    stop = true;
                     break;
                 }
                 tc::tc_fence_after();
                 const bool a_mn = MODE == kMul && w.job == 1, b_mn = MODE == kMul;
                 const uint32_t idesc = tc::idesc_bf16(kHeadTile, a.bn, a_mn, b_mn);
-                const uint32_t dst = tmem + acc * 256;
+                const uint32_t dst = acc0 + acc * 256;
                 const Operand A = {tc::sdesc_sw128(tc::smem_u32(smem), a_mn ? kBoxBytes : 16, 1024),
                                    a_mn ? 2048u : 32u};
                 const Operand B = {tc::sdesc_sw128(tc::smem_u32(smem + 2 * kBoxBytes),
@@ -921,48 +999,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                    b_mn ? 2048u : 32u};
                 const int n = a.joint ? w.steps : pairs * w.steps;
                 for (int k = 0; k < n; ++k) {
-                    const int s2 = it % kStages;
-                    bool ok = wait_or_abort(&ctl->full[s2], (it / kStages) & 1, tc::kWaitNs, abort_flag);
+                    const int s2 = st;
+                    stop = !loaded();
+                    if (stop) break;
+                    advance();
                     if (!a.joint) {
-                        if (!ok) {
-                            *abort_flag = 1;
-                            break;
-                        }
                         tc::tc_fence_after();
-                        issue_step(dst, A, s2, B, s2, idesc, k != 0);
-                        tc::mma_commit_pair(&ctl->empty[s2]);
-                        ++it;
+                        if (one) {
+                            issue_step(dst, A, s2, B, s2, idesc, k != 0);
+                            tc::mma_commit_pair(&ctl->empty[s2]);
+                        }
+                        __syncwarp();
                         continue;
                     }
-                    const int s1 = (it + 1) % kStages, s0 = (it + 2) % kStages;
-                    ok = ok &&
-                         wait_or_abort(&ctl->full[s1], ((it + 1) / kStages) & 1, tc::kWaitNs, abort_flag) &&
-                         wait_or_abort(&ctl->full[s0], ((it + 2) / kStages) & 1, tc::kWaitNs, abort_flag);
-                    if (!ok) {
-                        *abort_flag = 1;
-                        break;
-                    }
+                    const int s1 = st;
+                    stop = !loaded();
+                    if (stop) break;
+                    advance();
+                    const int s0 = st;
+                    stop = !loaded();
+                    if (stop) break;
+                    advance();
                     tc::tc_fence_after();
-                    issue_step(dst, A, s2, B, s0, idesc, k != 0);
-                    issue_step(dst, A, s0, B, s2, idesc, true);
-                    tc::mma_commit_pair(&ctl->empty[s2]);
-                    issue_step(dst, A, s1, B, s1, idesc, true);
-                    issue_step(dst, A, s1, B, s0, idesc, true);
-                    issue_step(dst, A, s0, B, s1, idesc, true);
-                    tc::mma_commit_pair(&ctl->empty[s1]);
-                    issue_step(dst + 128, A, s0, B, s0, idesc, k != 0);
-                    tc::mma_commit_pair(&ctl->empty[s0]);
-                    it += 3;
+                    if (one) {
+                        issue_step(dst, A, s2, B, s0, idesc, k != 0);
+                        issue_step(dst, A, s0, B, s2, idesc, true);
+                        tc::mma_commit_pair(&ctl->empty[s2]);
+                        issue_step(dst, A, s1, B, s1, idesc, true);
+                        issue_step(dst, A, s1, B, s0, idesc, true);
+                        issue_step(dst, A, s0, B, s1, idesc, true);
+                        tc::mma_commit_pair(&ctl->empty[s1]);
+                        issue_step(dst + 128, A, s0, B, s0, idesc, k != 0);
+                        tc::mma_commit_pair(&ctl->empty[s0]);
+                    }
+                    __syncwarp();
                 }
-                if (*abort_flag) break;
-                tc::mma_commit_pair(&ctl->tfull[acc]);
+                if (stop) break;
+                if (one) tc::mma_commit_pair(&ctl->tfull[acc]);
+                __syncwarp();
             }
-            ctl->consumed = it;
-            if (*abort_flag) {
-                // Everything issued so far has to be done before TMEM is freed.
-                tc::mma_commit_pair(&ctl->drain);
-                tc::mbar_wait_for(&ctl->drain, 0, tc::kWaitNs);
+            if (one) {
+                if (stop) *abort_flag = 1;
+                ctl->consumed = it;
+                if (stop) {
+                    // Everything issued so far has to be done before TMEM is freed.
+                    tc::mma_commit_pair(&ctl->drain);
+                    tc::mbar_wait_for(&ctl->drain, 0, tc::kWaitNs);
+                }
             }
+            __syncwarp();
         }
     } else {
         const int ew = warp - 2, q = warp & 3, h = ew >> 2;
