@@ -117,7 +117,7 @@ struct TcArgs {
     float *gh_acc, *ge_acc;    // tiles of partial sums, by unit
     int first, last, accumulate;
     int cut0, cut1;            // slices of the summed dimension, gH and gE
-    int joint;                 // all planes of a step together (see joint_planes)
+    int joint;                 // kMul, fp32, narrow tiles: see launch_head_products
     int stall;
     unsigned int* status;
 };
@@ -1229,17 +1229,18 @@ cudaError_t launch_tc(const CUtensorMap (&m)[4], TcArgs a, int64_t tiles, cudaSt
 constexpr int kPairs = 76;  // CTA pairs of a whole GPU, for the choices below
 
 // Columns of the tiles of `rows` x `n` logits: 128 where that ends sooner,
-// counted in rounds of the pairs. A narrow tile takes about four fifths of a
-// wide one's time (it loads three quarters of the operands).
+// counted in rounds of the pairs. A narrow tile takes 0.58 of a wide one's time
+// (16384 rows, d 1024, V 32768: 663 us in narrow tiles, 570 in wide ones), and
+// 0.65 where d is 512 or less.
 int logit_columns(int64_t rows, int64_t n) {
     const int64_t mt = tiles_of(rows, kHeadTile);
     const int64_t wide = tiles_of(mt * tiles_of(n, 256), kPairs) * 20;
-    const int64_t narrow = tiles_of(mt * tiles_of(n, 128), kPairs) * 16;
+    const int64_t narrow = tiles_of(mt * tiles_of(n, 128), kPairs) * 13;
     return narrow < wide ? 128 : 256;
 }
 
 // Columns of the tiles of the products: by what is computed past d.
-int product_columns(int64_t d) { return tiles_of(d, 128) * 16 < tiles_of(d, 256) * 20 ? 128 : 256; }
+int product_columns(int64_t d) { return tiles_of(d, 128) * 13 < tiles_of(d, 256) * 20 ? 128 : 256; }
 
 // When the last pair is done, in steps, if n_long units of c_long steps and
 // then n_short of c_short are dealt as Plan::unit() does.
@@ -1391,6 +1392,11 @@ cudaError_t launch_head_products(const HeadProducts& h, const HeadMaps& maps, cu
     a.counts = h.counts;
     a.planes = h.planes;
     a.bn = product_columns(h.d);
+    // All planes of a step together: three loads of A and B serve its six
+    // products, and G is read once from HBM instead of once per product (16384
+    // rows, d 64, V 32768: 2798 -> 2050 us). The smallest products are no longer
+    // summed first; so the largest has an accumulator of its own, beside which
+    // the others' rounding does not show. There is room for two of 128 columns.
     a.joint = a.planes == 3 && a.bn == 128;
     a.scale = h.scale;
     a.row_of = h.row_of;
