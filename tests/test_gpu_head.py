@@ -723,3 +723,21 @@ def test_gradients_of_rows_apart(d, ld, off, T, ge, dtype):
         assert torch.equal(a, b) or T == 2 and rel_fro(_np(a), _np(b)) <= GRAD_TOL[dtype]
     for flat, end in ((flatH, off + T * ld), (flatE, off + V * d)):
         assert (flat[:off] == 9.0).all() and (flat[end:] == 9.0).all()
+
+
+def test_long_sums_in_fp32():
+    """fp32 gradients whose sums run over 8192 rows and 8192 ids. What the
+    tensor cores add up at a time is 32 additions of 16 products; each cuts off
+    less than 2^-23 of the running sum, half of that on average: together below
+    32 * 2^-24 = 2e-6, to which the exponentials' own 2^-22 come."""
+    dev = cuda()
+    H, E, y, gl = _inputs(1, 8192, 24, 8192, "f32", dev, seed=28)
+    _, lse = dust.dust_head_loss(H, E, y)
+    gH, gE = dust.dust_head_loss_grad(H, E, y, lse, gl)
+    x = _x(H, E, 1.0)
+    yn = y.cpu().numpy()
+    G = np.exp(x - _lse(x)[:, None])
+    G[np.arange(8192), np.maximum(yn, 0)] -= 1.0
+    G *= np.where(yn >= 0, _np(gl), 0.0)[:, None]
+    wH, wE = _grads(H, E, G, 1.0)
+    assert rel_fro(_np(gH), wH) <= 2.5e-6 and rel_fro(_np(gE), wE) <= 2.5e-6

@@ -64,6 +64,14 @@ constexpr int kTurnBuf = 32 * 32 * 4;             // 32 rows x 32 columns of fp3
 constexpr int kSlotFloats = kHeadTile * kHeadTile;  // a tile of partial sums
 constexpr uint32_t kTmemCols = 512;               // two accumulators of 256 columns
 
+// Steps that fp32 products add up in TMEM at a time. The tensor cores cut a
+// sum's last bits off instead of rounding them, so its error grows with the
+// number of additions, not with its root; runs are joined in registers, rounded
+// (4096 rows, d 512, V 16384, normwise error of gH: 1.9e-5 without runs, 1.3e-6
+// with 16 steps, 6.8e-7 with 8, 4.1e-7 with 4, which takes 5 % longer where
+// sums are short).
+constexpr int kRun = 8;
+
 enum Mode { kLse, kFactor, kMul };
 
 // Steps in flight: what shared memory holds beside the store buffers.
@@ -509,6 +517,9 @@ struct Epilogue {
     uint32_t rank;
     int q, h, lane;
     uint32_t used = 0;
+    // kMul, fp32: a unit's sums over its runs of steps.
+    static constexpr int kSums = MODE == kMul && PLANES == 3 ? 256 / kShare : 1;
+    float sum[kSums] = {};
 
     __device__ RowOf begin(const Tile& w, const Plan<MODE>& plan) const {
         RowOf o;
@@ -708,6 +719,26 @@ struct Epilogue {
         }
     }
 
+    // Adds the accumulators of a run of steps to the unit's sums.
+    __device__ void collect(const Tile& w, uint32_t taddr, bool first) {
+        const int cols = a.bn / kShare;
+#pragma unroll
+        for (int b = 0; b < kSums / 16; ++b) {
+            const int at = h * cols + 16 * b;
+            if (b >= cols / 16 || w.n0 + at >= a.d) break;
+            float v[16];
+            tc::tmem_ld_32xN<16>(taddr + at, v);
+            if (a.joint) {
+                float big[16];
+                tc::tmem_ld_32xN<16>(taddr + 128 + at, big);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] += big[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[16 * b + i] = first ? v[i] : sum[16 * b + i] + v[i];
+        }
+    }
+
     __device__ void product(const Tile& w, const RowOf& o, uint32_t taddr, float alpha) {
         const int cols = a.bn / kShare;
         const bool job1 = w.job == 1, zero = w.steps == 0;
@@ -718,17 +749,17 @@ struct Epilogue {
         const OutRows& out = job1 ? a.out1 : a.out0;
         const int32_t to = o.live ? static_cast<int32_t>(o.out_row) : -1;
         const uint32_t buf = tc::smem_u32(bufs);
-        for (int b = 0; b < cols / 32; ++b) {
+#pragma unroll
+        for (int b = 0; b < 256 / kShare / 32; ++b) {
             const int at = h * cols + 32 * b;
             const int64_t col = w.n0 + at;
-            if (col >= a.d) break;
+            if (b >= cols / 32 || col >= a.d) break;
             float v[32];
-            tc::tmem_ld_32x32(taddr + at, v);
-            if (a.joint) {
-                float big[32];
-                tc::tmem_ld_32x32(taddr + 128 + at, big);
+            if constexpr (PLANES == 3) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] += big[i];
+                for (int i = 0; i < 32; ++i) v[i] = sum[32 * b + i];
+            } else {
+                tc::tmem_ld_32x32(taddr + at, v);
             }
             const int n = a.d - col < 32 ? static_cast<int>(a.d - col) : 32;
 #pragma unroll
@@ -884,6 +915,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const Plan<MODE> plan(a, cluster, n_clusters);
     const int pairs = a.planes == 1 ? 1 : 6;
     const int b_boxes = a.bn / 128;  // per CTA
+    const int run = MODE == kMul && PLANES == 3 ? kRun : 1 << 30;
     // A tile's products take about 0.3 us per step: the waits for a whole
     // tile are given 2 us per step on top of the usual limit.
     const uint64_t tile_ns =
@@ -925,35 +957,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int32_t b_k0 = MODE == kMul && w.job == 0 ? v0 : 0;
             // Steps of one pair of planes after another, or the planes of
             // one step after another, the smallest first.
-            const int outer = a.joint ? w.steps : pairs, inner = a.joint ? 3 : w.steps;
-            for (int p = 0; p < outer && !stop; ++p) {
-                const int pa0 = pairs == 1 ? 0 : plane_a(p), pb0 = pairs == 1 ? 0 : plane_b(p);
-                for (int i = 0; i < inner; ++i, ++it) {
-                    const int32_t kk = (w.k0 + (a.joint ? p : i)) * 64;
-                    const int pa = a.joint ? 2 - i : pa0, pb = a.joint ? 2 - i : pb0;
-                    if (!warp_wait(&ctl->empty[st], parity, tile_ns, abort_flag)) {
-                        *abort_flag = 1;
-                        stop = true;
-                        break;
-                    }
-                    unsigned char* base = smem + st * kStageBytes;
-                    const uint32_t bar = full + st * 8;
-                    if (one) {
-                        if (rank == 0) tc::mbar_arrive_expect_tx(&ctl->full[st], bytes);
+            for (int c = 0; c < w.steps && !stop; c += run) {
+                for (int p = 0, n = min(run, w.steps - c); p < (a.joint ? n : pairs) && !stop; ++p) {
+                    const int pa0 = pairs == 1 ? 0 : plane_a(p), pb0 = pairs == 1 ? 0 : plane_b(p);
+                    for (int i = 0; i < (a.joint ? 3 : n); ++i, ++it) {
+                        const int32_t kk = (w.k0 + c + (a.joint ? p : i)) * 64;
+                        const int pa = a.joint ? 2 - i : pa0, pb = a.joint ? 2 - i : pb0;
+                        if (!warp_wait(&ctl->empty[st], parity, tile_ns, abort_flag)) {
+                            *abort_flag = 1;
+                            stop = true;
+                            break;
+                        }
+                        unsigned char* base = smem + st * kStageBytes;
+                        const uint32_t bar = full + st * 8;
+                        if (one) {
+                            if (rank == 0) tc::mbar_arrive_expect_tx(&ctl->full[st], bytes);
 #pragma unroll
-                        for (int u = 0; u < 2; ++u)
-                            tc::tma_load_3d_pair(base + u * kBoxBytes, ma, a_mn ? am + 64 * u : kk,
-                                                 a_mn ? kk : am + 64 * u, pa, bar);
-                        tc::tma_load_3d_pair(base + 2 * kBoxBytes, mb, b_mn ? bn0 : kk,
-                                             b_mn ? b_k0 + kk : bn0, pb, bar);
-                        if (b_boxes == 2)
-                            tc::tma_load_3d_pair(base + 3 * kBoxBytes, mb, b_mn ? bn0 + 64 : kk,
-                                                 b_mn ? b_k0 + kk : bn0 + 64, pb, bar);
-                    }
-                    __syncwarp();
-                    if (++st == kStages) {
-                        st = 0;
-                        parity ^= 1;
+                            for (int u = 0; u < 2; ++u)
+                                tc::tma_load_3d_pair(base + u * kBoxBytes, ma, a_mn ? am + 64 * u : kk,
+                                                     a_mn ? kk : am + 64 * u, pa, bar);
+                            tc::tma_load_3d_pair(base + 2 * kBoxBytes, mb, b_mn ? bn0 : kk,
+                                                 b_mn ? b_k0 + kk : bn0, pb, bar);
+                            if (b_boxes == 2)
+                                tc::tma_load_3d_pair(base + 3 * kBoxBytes, mb, b_mn ? bn0 + 64 : kk,
+                                                     b_mn ? b_k0 + kk : bn0 + 64, pb, bar);
+                        }
+                        __syncwarp();
+                        if (++st == kStages) {
+                            st = 0;
+                            parity ^= 1;
+                        }
                     }
                 }
             }
@@ -978,12 +1011,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             };
             int t = uniform(plan.unit(0));
             Tile next = t >= 0 ? uniform(plan.at(a, t)) : Tile{};
-            for (int j = 0; !stop && t >= 0; ++j) {
-                const Tile w = next;
-                // The next one's place is worked out before this one's steps.
-                t = uniform(plan.unit(j + 1));
-                if (t >= 0) next = uniform(plan.at(a, t));
-                const int acc = j & 1;
+            // Accumulators are filled in turn, one per run of steps of a unit.
+            Tile w = next;
+            for (int j = 0, i = 0, c = 0; !stop && (c > 0 || t >= 0); ++j) {
+                if (c == 0) {
+                    w = next;
+                    // The next one's place is worked out before this one's steps.
+                    t = uniform(plan.unit(++i));
+                    if (t >= 0) next = uniform(plan.at(a, t));
+                }
+                const int acc = j & 1, steps = min(run, w.steps - c);
                 if (!warp_wait(&ctl->tempty[acc], ((j >> 1) & 1) ^ 1, tile_ns, abort_flag)) {
                     stop = true;
                     break;
@@ -997,7 +1034,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const Operand B = {tc::sdesc_sw128(tc::smem_u32(smem + 2 * kBoxBytes),
                                                    b_mn ? kBoxBytes : 16, 1024),
                                    b_mn ? 2048u : 32u};
-                const int n = a.joint ? w.steps : pairs * w.steps;
+                const int n = a.joint ? steps : pairs * steps;
                 for (int k = 0; k < n; ++k) {
                     const int s2 = st;
                     stop = !loaded();
@@ -1037,6 +1074,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (stop) break;
                 if (one) tc::mma_commit_pair(&ctl->tfull[acc]);
                 __syncwarp();
+                c = w.steps - c > run ? c + run : 0;
             }
             if (one) {
                 if (stop) *abort_flag = 1;
@@ -1059,33 +1097,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         RowOf o = {};
         if (t >= 0) o = epi.begin(w, plan);
         epi.second(w, o);
-        for (int j = 0; t >= 0; ++j) {
-            const int acc = j & 1;
+        bool ok = true;
+        for (int i = 1, j = 0; t >= 0 && ok; ++i) {
             epi.third(o);
-            const bool ok = wait_or_abort(&ctl->tfull[acc], (j >> 1) & 1, tile_ns, abort_flag);
-            tc::tc_fence_after();
-            if (!__all_sync(0xffffffffu, ok) || *abort_flag) {
-                *abort_flag = 1;
-                break;
-            }
-            // The next unit's rows are loaded beside this one's arithmetic.
-            t = plan.unit(j + 1);
-            const Tile next = t >= 0 ? plan.at(a, t) : w;
+            Tile next = w;
             RowOf next_o = {};
-            if (t >= 0) next_o = epi.begin(next, plan);
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * 256;
-            if (epi.wanted(w, plan)) {
-                if constexpr (MODE == kLse)
-                    epi.lse(w, o, taddr);
-                else if constexpr (MODE == kFactor)
-                    epi.factor(w, o, taddr);
-                else
-                    epi.product(w, o, taddr, alpha);
+            for (int c = 0; ok && c >= 0; ++j) {  // runs of steps
+                const int acc = j & 1;
+                ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->tfull[acc], (j >> 1) & 1, tile_ns,
+                                                           abort_flag) && !*abort_flag);
+                tc::tc_fence_after();
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                const bool last = w.steps - c <= run;
+                if (last) {
+                    // The next unit's rows are loaded beside this one's arithmetic.
+                    t = plan.unit(i);
+                    if (t >= 0) {
+                        next = plan.at(a, t);
+                        next_o = epi.begin(next, plan);
+                    }
+                }
+                const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * 256;
+                if (epi.wanted(w, plan)) {
+                    if constexpr (MODE == kLse) {
+                        epi.lse(w, o, taddr);
+                    } else if constexpr (MODE == kFactor) {
+                        epi.factor(w, o, taddr);
+                    } else {
+                        if constexpr (PLANES == 3) epi.collect(w, taddr, c == 0);
+                        if (last) epi.product(w, o, taddr, alpha);
+                    }
+                }
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_at(tc::at_rank(&ctl->tempty[acc], 0));
+                c = last ? -1 : c + run;
             }
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_at(tc::at_rank(&ctl->tempty[acc], 0));
-            if (t >= 0) epi.second(next, next_o);
+            if (ok && t >= 0) epi.second(next, next_o);
             w = next;
             o = next_o;
         }
@@ -1421,7 +1472,8 @@ cudaError_t launch_head_products(const HeadProducts& h, const HeadMaps& maps, cu
     const int64_t nt = tiles_of(a.d, a.bn);
     const int64_t t0 = h.gH ? tiles_of(a.rows, kHeadTile) * nt : 0;
     const int64_t t1 = h.gE ? tiles_of(a.n, kHeadTile) * nt : 0;
-    cudaError_t e = launch_tc<kMul, 1>(m, a, t0 * a.cut0 + t1 * a.cut1, s);
+    const int64_t units = t0 * a.cut0 + t1 * a.cut1;
+    cudaError_t e = a.planes == 1 ? launch_tc<kMul, 1>(m, a, units, s) : launch_tc<kMul, 3>(m, a, units, s);
     const int64_t s0 = a.cut0 > 1 && h.last ? t0 : 0, s1 = a.cut1 > 1 ? t1 : 0;
     if (e == cudaSuccess && s0 + s1 > 0) e = launch_sum(a, s0, s1, s);
     return e;
