@@ -10,7 +10,7 @@
 // joins them. For distillation the pass over the tiles also picks the logits
 // of the teacher's entries, which a first launch has put in order. (Formed
 // apart, as products of a row of H with K rows of E, they took 74 us beside
-// the 183 us of the logits, 4096 rows, d 1024, V 32768, K 64.)
+// the logits' then 183 us, 4096 rows, d 1024, V 32768, K 64.)
 //
 // Gradient, per piece of the vocabulary (a piece's G stays below 2^28
 // values): the logits again as G = weight (exp(x - lse) - wanted) in bf16,

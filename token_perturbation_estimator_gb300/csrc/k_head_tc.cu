@@ -26,13 +26,19 @@
 // eight warps drain the accumulators, two per TMEM lane quarter. All waits are
 // bounded and record DUST_ERR_TIMEOUT in the device status word.
 //
-// Bound by the tensor pipe where d is large, at the clock that the power limit
-// leaves: the gradients of 8192 rows (83 % taking part), d 2048, V 50257 take
-// 2.6 to 2.8 ms, 1490 to 1610 TFLOP/s; the logits of 4096 rows, d 1024, V 32768
-// 180 us, 1530 TFLOP/s. Where d is small the epilogue binds (2.4e12
-// exponentials a second, half of what the special-function units can do: two
-// warps per scheduler, each waiting for TMEM and its own chain): below d 256
-// the time hardly falls. 18432 rows, d 512, V 4096: 63 us with the joining.
+// A step's products take 540 clocks of the tensor pipe, and for long the two
+// issuing warps took longer: 560 to load (four boxes of 60 to 145 clocks, the
+// flag of a failed wait read every step), 540 to issue. Going through the
+// steps as whole warps, with operands in uniform registers, brought the logits
+// of 16384 rows, d 512, V 32768 from 366 to 273 us.
+//
+// Bound by the tensor pipe (94 % busy at d 1024): the logits of 4096 rows, d
+// 1024, V 32768 take 139 us, 1980 TFLOP/s; in long runs the power limit
+// lowers the clock, and the gradients of 8192 rows (83 % taking part), d 2048,
+// V 50257 take 2.13 to 2.47 ms, 1970 to 1700 TFLOP/s. Below d 384 the epilogue
+// binds (2.6e12 exponentials a second, half of what the special-function units
+// can do: two warps per scheduler), and fp32 gradients there HBM, by G's three
+// planes.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -1445,7 +1451,7 @@ cudaError_t launch_head_products(const HeadProducts& h, const HeadMaps& maps, cu
     a.bn = product_columns(h.d);
     // All planes of a step together: three loads of A and B serve its six
     // products, and G is read once from HBM instead of once per product (16384
-    // rows, d 64, V 32768: 2798 -> 2050 us). The smallest products are no longer
+    // rows, d 64, V 32768: 2798 -> 2050 us, 1.5 of them G's bytes). The smallest products are no longer
     // summed first; so the largest has an accumulator of its own, beside which
     // the others' rounding does not show. There is room for two of 128 columns.
     a.joint = a.planes == 3 && a.bn == 128;
