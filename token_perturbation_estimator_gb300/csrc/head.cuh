@@ -148,7 +148,7 @@ struct HeadProducts {
     bool ge_bf16, accumulate;
 };
 // Partial sums of a product of m rows and d columns.
-int64_t head_acc_floats(int64_t m, int64_t d, int cut);
+int64_t head_acc_floats(int64_t m, int64_t d, int planes, int cut);
 cudaError_t launch_head_products(const HeadProducts& a, const HeadMaps& m, cudaStream_t s);
 
 }  // namespace dust

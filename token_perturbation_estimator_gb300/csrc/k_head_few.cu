@@ -531,7 +531,7 @@ cudaError_t launch_head_few(const HeadProblem& p, HeadPart* part, int64_t ld_par
 // The gradients' rule, by the same measure, us here / there:
 //   bf16  R 1  9 / 24, 105 / 236   R 2  11 / 24, 120 / 236
 //         R 4  16 / 24, 158 / 236
-//   fp32  R 1  9 / 52, 187 / 967   R 8  25 / 52, 527 / 942
+//   fp32  R 1  9 / 45, 187 / 1160  R 8  25 / 45, 527 / 1156
 // and with d 4096, V 32000, where one CTA fits an SM, bf16 R 4 346 / 287.
 bool head_few_grad(const HeadProblem& p) {
     const int64_t R = p.S * p.T;

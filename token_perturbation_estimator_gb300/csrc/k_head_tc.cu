@@ -524,7 +524,7 @@ struct Epilogue {
     int q, h, lane;
     uint32_t used = 0;
     // kMul, fp32: a unit's sums over its runs of steps.
-    static constexpr int kSums = MODE == kMul && PLANES == 3 ? 256 / kShare : 1;
+    static constexpr int kSums = MODE == kMul && PLANES == 3 ? 128 / kShare : 1;
     float sum[kSums] = {};
 
     __device__ RowOf begin(const Tile& w, const Plan<MODE>& plan) const {
@@ -745,7 +745,8 @@ struct Epilogue {
         }
     }
 
-    __device__ void product(const Tile& w, const RowOf& o, uint32_t taddr, float alpha) {
+    // one_run: the accumulators hold the whole sum (bf16, or few steps).
+    __device__ void product(const Tile& w, const RowOf& o, uint32_t taddr, float alpha, bool one_run) {
         const int cols = a.bn / kShare;
         const bool job1 = w.job == 1, zero = w.steps == 0;
         float* acc = job1 ? a.ge_acc : a.gh_acc;
@@ -755,18 +756,9 @@ struct Epilogue {
         const OutRows& out = job1 ? a.out1 : a.out0;
         const int32_t to = o.live ? static_cast<int32_t>(o.out_row) : -1;
         const uint32_t buf = tc::smem_u32(bufs);
-#pragma unroll
-        for (int b = 0; b < 256 / kShare / 32; ++b) {
-            const int at = h * cols + 32 * b;
+        // Columns [at, at + 32) of the tile, or what exists of them.
+        const auto write = [&](int at, float (&v)[32]) {
             const int64_t col = w.n0 + at;
-            if (b >= cols / 32 || col >= a.d) break;
-            float v[32];
-            if constexpr (PLANES == 3) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = sum[32 * b + i];
-            } else {
-                tc::tmem_ld_32x32(taddr + at, v);
-            }
             const int n = a.d - col < 32 ? static_cast<int>(a.d - col) : 32;
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = zero ? 0.0f : alpha * v[i];
@@ -790,6 +782,32 @@ struct Epilogue {
             }
             if (whole)
                 store_block(buf, v, lane, to, out, col, n, job1 && a.accumulate);
+        };
+        if (one_run) {
+            // (Not unrolled: tiles of a few rows' gradients spend their time
+            // here, and four copies of it do not fit the instruction cache.)
+#pragma unroll 1
+            for (int at = h * cols; at < (h + 1) * cols && w.n0 + at < a.d; at += 32) {
+                float v[32];
+                tc::tmem_ld_32x32(taddr + at, v);
+                if (PLANES == 3 && a.joint) {
+                    float big[32];
+                    tc::tmem_ld_32x32(taddr + 128 + at, big);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] += big[i];
+                }
+                write(at, v);
+            }
+        } else if constexpr (PLANES == 3) {
+#pragma unroll
+            for (int b = 0; b < kSums / 32; ++b) {
+                const int at = h * cols + 32 * b;
+                if (b >= cols / 32 || w.n0 + at >= a.d) break;
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = sum[32 * b + i];
+                write(at, v);
+            }
         }
     }
 };
@@ -1133,8 +1151,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     } else if constexpr (MODE == kFactor) {
                         epi.factor(w, o, taddr);
                     } else {
-                        if constexpr (PLANES == 3) epi.collect(w, taddr, c == 0);
-                        if (last) epi.product(w, o, taddr, alpha);
+                        const bool one_run = c == 0 && last;
+                        if (PLANES == 3 && !one_run) epi.collect(w, taddr, c == 0);
+                        if (last) epi.product(w, o, taddr, alpha, one_run);
                     }
                 }
                 tc::tc_fence_before();
@@ -1296,8 +1315,12 @@ int logit_columns(int64_t rows, int64_t n) {
     return narrow < wide ? 128 : 256;
 }
 
-// Columns of the tiles of the products: by what is computed past d.
-int product_columns(int64_t d) { return tiles_of(d, 128) * 13 < tiles_of(d, 256) * 20 ? 128 : 256; }
+// Columns of the tiles of the products: by what is computed past d; narrow in
+// fp32, where a unit's sums have to fit the epilogue's registers (kRun), and
+// two accumulators TMEM (see launch_head_products).
+int product_columns(int64_t d, int planes) {
+    return planes == 3 || tiles_of(d, 128) * 13 < tiles_of(d, 256) * 20 ? 128 : 256;
+}
 
 // When the last pair is done, in steps, if n_long units of c_long steps and
 // then n_short of c_short are dealt as Plan::unit() does.
@@ -1326,7 +1349,7 @@ int head_columns(int64_t rows, int64_t n) { return logit_columns(rows, n); }
 // partial sums and their adding up 12 steps and a third of one per unit.
 HeadCuts head_cuts(int64_t rows, int64_t n, int64_t d, int planes) {
     const int64_t pairs = planes == 1 ? 1 : 6;
-    const int64_t nt = tiles_of(d, product_columns(d));
+    const int64_t nt = tiles_of(d, product_columns(d, planes));
     const int64_t t[2] = {tiles_of(rows, kHeadTile) * nt, tiles_of(n, kHeadTile) * nt};
     const int64_t steps[2] = {tiles_of(n, 64), tiles_of(rows, 64)};
     const auto ends = [&](int64_t a, int64_t b) {
@@ -1363,7 +1386,7 @@ int64_t head_piece(int64_t rows, int64_t V, int64_t d, int planes) {
     const int64_t mt = tiles_of(rows, kHeadTile), whole = tiles_of(V, kHeadTile);
     const int64_t cap = std::max<int64_t>(kMost / (mt * kHeadTile * planes) / kHeadTile, 4);
     if (whole <= cap) return whole * kHeadTile;
-    const int64_t pairs = planes == 1 ? 1 : 6, nt = tiles_of(d, product_columns(d));
+    const int64_t pairs = planes == 1 ? 1 : 6, nt = tiles_of(d, product_columns(d, planes));
     const int64_t logits = tiles_of(d, 64) * pairs + 3, c1 = tiles_of(rows, 64) * pairs + 4;
     const auto cost = [&](int64_t n) {  // of a piece of n tiles
         const int64_t c0 = n * (kHeadTile / 64) * pairs + 4, t0 = mt * nt, t1 = n * nt;
@@ -1435,8 +1458,8 @@ cudaError_t launch_head_factor(const HeadLogits& h, const HeadMaps& maps, cudaSt
                          : launch_tc<kFactor, 3>(m, a, tiles, s);
 }
 
-int64_t head_acc_floats(int64_t m, int64_t d, int cut) {
-    return tiles_of(m, kHeadTile) * tiles_of(d, product_columns(d)) * cut * kSlotFloats;
+int64_t head_acc_floats(int64_t m, int64_t d, int planes, int cut) {
+    return tiles_of(m, kHeadTile) * tiles_of(d, product_columns(d, planes)) * cut * kSlotFloats;
 }
 
 cudaError_t launch_head_products(const HeadProducts& h, const HeadMaps& maps, cudaStream_t s) {
@@ -1448,13 +1471,14 @@ cudaError_t launch_head_products(const HeadProducts& h, const HeadMaps& maps, cu
     a.v0 = h.v0;
     a.counts = h.counts;
     a.planes = h.planes;
-    a.bn = product_columns(h.d);
+    a.bn = product_columns(h.d, a.planes);
     // All planes of a step together: three loads of A and B serve its six
     // products, and G is read once from HBM instead of once per product (16384
-    // rows, d 64, V 32768: 2798 -> 2050 us, 1.5 of them G's bytes). The smallest products are no longer
+    // rows, V 32768: d 64 2798 -> 2000 us, 1400 of them G's bytes; d 512, where
+    // wide tiles did without, 6280 -> 5920). The smallest products are no longer
     // summed first; so the largest has an accumulator of its own, beside which
     // the others' rounding does not show. There is room for two of 128 columns.
-    a.joint = a.planes == 3 && a.bn == 128;
+    a.joint = a.planes == 3;
     a.scale = h.scale;
     a.row_of = h.row_of;
     a.gh_acc = h.gh_acc;
