@@ -741,3 +741,18 @@ def test_long_sums_in_fp32():
     G *= np.where(yn >= 0, _np(gl), 0.0)[:, None]
     wH, wE = _grads(H, E, G, 1.0)
     assert rel_fro(_np(gH), wH) <= 2.5e-6 and rel_fro(_np(gE), wE) <= 2.5e-6
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [1030, 4100])
+def test_long_sums_of_logits(d, dtype):
+    """Logits over many columns, all products of one sign, where cutting bits
+    off adds up most: as above, below 2e-6 of the logit."""
+    import torch
+    dev = cuda()
+    H, E, _, _ = _inputs(1, 40, d, 700, dtype, dev, seed=29)
+    H, E = H.abs(), (E.abs() / d ** 0.5)
+    ids = torch.arange(40 * 16, dtype=torch.int32, device=dev).view(40, 16)
+    _, _, student = dust.dust_distill_loss(H, E, ids, torch.zeros((40, 16), device=dev))
+    x = np.take_along_axis(_x(H, E, 1.0), ids.cpu().numpy().astype(np.int64), 1)
+    assert (np.abs(_np(student) - x) / x).max() <= 2e-6

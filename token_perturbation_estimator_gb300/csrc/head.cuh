@@ -96,7 +96,7 @@ struct HeadLogits {
 };
 
 // Columns of the tiles of logits for these sizes.
-int head_columns(int64_t rows, int64_t n);
+int head_columns(int64_t rows, int64_t n, int64_t d);
 
 cudaError_t launch_head_lse(const HeadLogits& a, cudaStream_t s);
 

@@ -511,7 +511,7 @@ struct LossSpace {
 // Partial sums per row.
 int loss_parts(const HeadProblem& p) {
     if (head_few(p)) return head_few_parts(p);
-    const int64_t bn = head_columns(p.S * p.T, p.V);
+    const int64_t bn = head_columns(p.S * p.T, p.V, p.d);
     return static_cast<int>(2 * ((p.V + bn - 1) / bn));
 }
 
@@ -550,6 +550,12 @@ struct GradSpace {
     size_t total;
 };
 
+// Columns of the tiles of G. (In bf16, G's rounding hides what the logits' sums
+// cut off, at any d.)
+int grad_columns(const HeadProblem& p, int64_t piece) {
+    return head_columns(p.S * p.T, std::min(piece, p.V), p.bf16 ? 0 : p.d);
+}
+
 GradSpace carve_grad(void* ws, const HeadProblem& p) {
     const int64_t R = p.S * p.T, dp = up(p.d, 8), planes = p.bf16 ? 1 : 3;
     Carver c{static_cast<unsigned char*>(ws)};
@@ -568,7 +574,7 @@ GradSpace carve_grad(void* ws, const HeadProblem& p) {
     w.rows = c.take<HeadRow>(R);
     w.row_of = c.take<int32_t>(R);
     w.place = c.take<int32_t>(R);
-    const int64_t bn = head_columns(R, std::min(w.piece, p.V));
+    const int64_t bn = grad_columns(p, w.piece);
     w.bins = static_cast<int>(2 * ((p.V + bn - 1) / bn));
     w.starts = c.take<uint16_t>(p.tg.many ? R * (w.bins + 1) : 0);
     // As for both gradients, whichever are asked for.
@@ -663,7 +669,7 @@ cudaError_t loss_typed(const HeadProblem& p, float* loss, float* lse, float* stu
         a.E = operand<TX>(p.E, p.ld_e, p.V, p.d, w.e, &je);
         DUST_TRY(pack(jh, je, s));
         a.n = p.V;
-        a.bn = head_columns(R, p.V);
+        a.bn = head_columns(R, p.V, p.d);
         a.scale = p.scale;
         a.targets = targets;
         a.T = p.T;
@@ -706,7 +712,7 @@ cudaError_t grad_typed(const HeadProblem& p, const float* lse, const float* stud
     if (!st) return cudaErrorUnknown;
     const bool few = head_few_grad(p);
     HeadLogits a = {};
-    if (!few) a.bn = head_columns(R, std::min(w.piece, p.V));
+    if (!few) a.bn = grad_columns(p, w.piece);
     if (distill) {
         BinArgs b = {};
         b.items = R;

@@ -515,7 +515,7 @@ struct RowOf {
 
 // Epilogue of one unit for one warp: rows 32 q + lane of this CTA's half,
 // columns [h bn / 2, (h + 1) bn / 2).
-template <int MODE, int PLANES>
+template <int MODE, int PLANES, bool RUNS>
 struct Epilogue {
     const TcArgs& a;
     const CUtensorMap* tmG;
@@ -523,9 +523,11 @@ struct Epilogue {
     uint32_t rank;
     int q, h, lane;
     uint32_t used = 0;
-    // kMul, fp32: a unit's sums over its runs of steps.
-    static constexpr int kSums = MODE == kMul && PLANES == 3 ? 128 / kShare : 1;
+    // A unit's sums over its runs of steps but the last (narrow tiles), and
+    // whether there are such.
+    static constexpr int kSums = RUNS ? 128 / kShare : 1;
     float sum[kSums] = {};
+    bool summed = false;
 
     __device__ RowOf begin(const Tile& w, const Plan<MODE>& plan) const {
         RowOf o;
@@ -600,7 +602,7 @@ struct Epilogue {
         const int32_t tv = o.info.target - static_cast<int32_t>(a.v0) - first;
         for (int b = 0; b < cols / 32; ++b) {
             float v[32];
-            tc::tmem_ld_32x32(taddr + h * cols + 32 * b, v);
+            whole_sum(taddr, h * cols + 32 * b, v);
             const int left = static_cast<int>(a.n) - (first + 32 * b);  // columns that exist
             if (left <= 0) break;
             // Logits that are wanted by themselves, the target's and the
@@ -645,7 +647,7 @@ struct Epilogue {
         for (int b = 0; b < cols / 32; ++b) {
             float v[32];
             const int64_t col = w.n0 + h * cols + 32 * b;
-            tc::tmem_ld_32x32(taddr + h * cols + 32 * b, v);
+            whole_sum(taddr, h * cols + 32 * b, v);
             const int left = static_cast<int>(a.n - col);
             const float2 cc = {c, c}, hi = {-o.info.lse_hi, -o.info.lse_hi};
             const float2 ww = {o.info.weight, o.info.weight};
@@ -725,28 +727,42 @@ struct Epilogue {
         }
     }
 
-    // Adds the accumulators of a run of steps to the unit's sums.
-    __device__ void collect(const Tile& w, uint32_t taddr, bool first) {
-        const int cols = a.bn / kShare;
+    // Columns [at, at + 32) of the accumulators of a run of steps: both of them
+    // for fp32 products.
+    __device__ void accumulators(uint32_t taddr, int at, float (&v)[32]) const {
+        tc::tmem_ld_32x32(taddr + at, v);
+        if (MODE == kMul && PLANES == 3) {
+            float big[32];
+            tc::tmem_ld_32x32(taddr + 128 + at, big);
 #pragma unroll
-        for (int b = 0; b < kSums / 16; ++b) {
-            const int at = h * cols + 16 * b;
-            if (b >= cols / 16 || w.n0 + at >= a.d) break;
-            float v[16];
-            tc::tmem_ld_32xN<16>(taddr + at, v);
-            if (a.joint) {
-                float big[16];
-                tc::tmem_ld_32xN<16>(taddr + 128 + at, big);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] += big[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sum[16 * b + i] = first ? v[i] : sum[16 * b + i] + v[i];
+            for (int i = 0; i < 32; ++i) v[i] += big[i];
         }
     }
 
-    // one_run: the accumulators hold the whole sum (bf16, or few steps).
-    __device__ void product(const Tile& w, const RowOf& o, uint32_t taddr, float alpha, bool one_run) {
+    // Columns [at, at + 32) of the unit's whole sum, after its last run.
+    __device__ void whole_sum(uint32_t taddr, int at, float (&v)[32]) const {
+        accumulators(taddr, at, v);
+        if (RUNS && summed) {
+            const bool second = (at & 32) != 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += second ? sum[(32 + i) % kSums] : sum[i % kSums];
+        }
+    }
+
+    // Adds a run that is not the last to the unit's sums.
+    __device__ void collect(uint32_t taddr, bool first) {
+        const int cols = a.bn / kShare;
+#pragma unroll
+        for (int b = 0; b < kSums / 32; ++b) {
+            float v[32];
+            accumulators(taddr, h * cols + 32 * b, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                sum[(32 * b + i) % kSums] = first ? v[i] : sum[(32 * b + i) % kSums] + v[i];
+        }
+    }
+
+    __device__ void product(const Tile& w, const RowOf& o, uint32_t taddr, float alpha) {
         const int cols = a.bn / kShare;
         const bool job1 = w.job == 1, zero = w.steps == 0;
         float* acc = job1 ? a.ge_acc : a.gh_acc;
@@ -756,9 +772,14 @@ struct Epilogue {
         const OutRows& out = job1 ? a.out1 : a.out0;
         const int32_t to = o.live ? static_cast<int32_t>(o.out_row) : -1;
         const uint32_t buf = tc::smem_u32(bufs);
-        // Columns [at, at + 32) of the tile, or what exists of them.
-        const auto write = [&](int at, float (&v)[32]) {
+        // (Not unrolled: tiles of few rows' gradients spend their time here, and
+        // four copies of it do not fit the instruction cache.)
+#pragma unroll 1
+        for (int at = h * cols; at < (h + 1) * cols; at += 32) {
             const int64_t col = w.n0 + at;
+            if (col >= a.d) break;
+            float v[32];
+            whole_sum(taddr, at, v);
             const int n = a.d - col < 32 ? static_cast<int>(a.d - col) : 32;
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = zero ? 0.0f : alpha * v[i];
@@ -782,32 +803,6 @@ struct Epilogue {
             }
             if (whole)
                 store_block(buf, v, lane, to, out, col, n, job1 && a.accumulate);
-        };
-        if (one_run) {
-            // (Not unrolled: tiles of a few rows' gradients spend their time
-            // here, and four copies of it do not fit the instruction cache.)
-#pragma unroll 1
-            for (int at = h * cols; at < (h + 1) * cols && w.n0 + at < a.d; at += 32) {
-                float v[32];
-                tc::tmem_ld_32x32(taddr + at, v);
-                if (PLANES == 3 && a.joint) {
-                    float big[32];
-                    tc::tmem_ld_32x32(taddr + 128 + at, big);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] += big[i];
-                }
-                write(at, v);
-            }
-        } else if constexpr (PLANES == 3) {
-#pragma unroll
-            for (int b = 0; b < kSums / 32; ++b) {
-                const int at = h * cols + 32 * b;
-                if (b >= cols / 32 || w.n0 + at >= a.d) break;
-                float v[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = sum[32 * b + i];
-                write(at, v);
-            }
         }
     }
 };
@@ -893,7 +888,7 @@ __device__ __forceinline__ void issue_step(uint32_t to, const Operand& A, int st
 }
 
 // Maps: kLse H, -, E, -; kFactor H, Hc, E, G; kMul G, E, H, Hc.
-template <int MODE, int PLANES>
+template <int MODE, int PLANES, bool RUNS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_head_tc(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
               const __grid_constant__ CUtensorMap tm2, const __grid_constant__ CUtensorMap tm3,
@@ -939,7 +934,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const Plan<MODE> plan(a, cluster, n_clusters);
     const int pairs = a.planes == 1 ? 1 : 6;
     const int b_boxes = a.bn / 128;  // per CTA
-    const int run = MODE == kMul && PLANES == 3 ? kRun : 1 << 30;
+    const int run = RUNS ? kRun : 1 << 30;
     // A tile's products take about 0.3 us per step: the waits for a whole
     // tile are given 2 us per step on top of the usual limit.
     const uint64_t tile_ns =
@@ -1114,7 +1109,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else {
         const int ew = warp - 2, q = warp & 3, h = ew >> 2;
         constexpr int kOwn = MODE == kFactor ? kStoreBufs * kStageBuf : kTurnBuf;
-        Epilogue<MODE, PLANES> epi{a, &tm3, store_bufs + ew * kOwn, rank, q, h, lane};
+        Epilogue<MODE, PLANES, RUNS> epi{a, &tm3, store_bufs + ew * kOwn, rank, q, h, lane};
         const float alpha = MODE == kMul ? a.scale * a.counts->gmax : 0.0f;
         int t = plan.unit(0);
         Tile w = t >= 0 ? plan.at(a, t) : Tile{};
@@ -1146,14 +1141,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * 256;
                 if (epi.wanted(w, plan)) {
-                    if constexpr (MODE == kLse) {
-                        epi.lse(w, o, taddr);
-                    } else if constexpr (MODE == kFactor) {
-                        epi.factor(w, o, taddr);
+                    if (RUNS && !last) {
+                        epi.collect(taddr, c == 0);
                     } else {
-                        const bool one_run = c == 0 && last;
-                        if (PLANES == 3 && !one_run) epi.collect(w, taddr, c == 0);
-                        if (last) epi.product(w, o, taddr, alpha, one_run);
+                        epi.summed = c > 0;
+                        if constexpr (MODE == kLse)
+                            epi.lse(w, o, taddr);
+                        else if constexpr (MODE == kFactor)
+                            epi.factor(w, o, taddr);
+                        else
+                            epi.product(w, o, taddr, alpha);
                     }
                 }
                 tc::tc_fence_before();
@@ -1260,7 +1257,7 @@ bool operand_map(CUtensorMap* map, const Planes& p) {
 }
 
 // CTA pairs that can be resident at once, for the kernel of a mode.
-template <int MODE, int PLANES>
+template <int MODE, int PLANES, bool RUNS>
 int max_clusters() {
     constexpr int kMaxDev = 64;
     static int cache[kMaxDev] = {};
@@ -1269,7 +1266,7 @@ int max_clusters() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
     std::lock_guard<std::mutex> lk(mu);
     if (cache[dev] == 0) {
-        const void* k = reinterpret_cast<const void*>(k_head_tc<MODE, PLANES>);
+        const void* k = reinterpret_cast<const void*>(k_head_tc<MODE, PLANES, RUNS>);
         if (ensure_smem_limit(k, smem_of<MODE>()) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
@@ -1288,9 +1285,9 @@ int max_clusters() {
     return cache[dev];
 }
 
-template <int MODE, int PLANES>
+template <int MODE, int PLANES, bool RUNS>
 cudaError_t launch_tc(const CUtensorMap (&m)[4], TcArgs a, int64_t tiles, cudaStream_t s) {
-    const int fit = max_clusters<MODE, PLANES>();
+    const int fit = max_clusters<MODE, PLANES, RUNS>();
     if (fit <= 0) return cudaErrorUnknown;
     if (tiles <= 0) return cudaSuccess;
     if (tiles > (int64_t(1) << 30)) return cudaErrorInvalidValue;
@@ -1298,9 +1295,15 @@ cudaError_t launch_tc(const CUtensorMap (&m)[4], TcArgs a, int64_t tiles, cudaSt
     if (!a.status) return cudaErrorUnknown;
     a.stall = take_stall_injection() ? 1 : 0;
     const unsigned clusters = static_cast<unsigned>(std::min<int64_t>(tiles, fit));
-    return launch_pdl(k_head_tc<MODE, PLANES>, dim3(2 * clusters), dim3(kThreads), smem_of<MODE>(), s,
+    return launch_pdl(k_head_tc<MODE, PLANES, RUNS>, dim3(2 * clusters), dim3(kThreads), smem_of<MODE>(), s,
                       m[0], m[1], m[2], m[3], a);
 }
+
+// Whether logits over d columns are summed in runs (kRun), in narrow tiles:
+// about a sixth slower. (Normwise error of single logits, in one run and in
+// runs of 8 steps: d 1024 1.0e-6 and 4.7e-7, d 2048 2.1e-6 and 4.8e-7, d 8192
+// 9.1e-6 and 4.8e-7.) Those of a gradient in bf16 are not: its G is rounded.
+bool in_runs(int64_t d) { return d > 1024; }
 
 constexpr int kPairs = 76;  // CTA pairs of a whole GPU, for the choices below
 
@@ -1341,7 +1344,9 @@ constexpr int kGroup = 38;
 
 }  // namespace
 
-int head_columns(int64_t rows, int64_t n) { return logit_columns(rows, n); }
+int head_columns(int64_t rows, int64_t n, int64_t d) {
+    return in_runs(d) ? 128 : logit_columns(rows, n);
+}
 
 // Slices of the summed dimension of each product: 1 where whole tiles share
 // the pairs evenly (within a quarter), else the pair of cuts that ends
@@ -1427,7 +1432,9 @@ cudaError_t launch_head_lse(const HeadLogits& h, cudaStream_t s) {
     a.ld_part = h.ld_part;
     a.picked = h.picked;
     a.picks = h.picks;
-    return launch_tc<kLse, 1>(m, a, tiles_of(a.rows, kHeadTile) * tiles_of(a.n, a.bn), s);
+    const int64_t tiles = tiles_of(a.rows, kHeadTile) * tiles_of(a.n, a.bn);
+    return in_runs(a.d) ? launch_tc<kLse, 1, true>(m, a, tiles, s)
+                        : launch_tc<kLse, 1, false>(m, a, tiles, s);
 }
 
 bool make_head_maps(HeadMaps* m, const Planes& H, const Planes& Hc, const Planes& E,
@@ -1454,8 +1461,9 @@ cudaError_t launch_head_factor(const HeadLogits& h, const HeadMaps& maps, cudaSt
     a.picks = h.picks;
     a.info = h.rows;
     const int64_t tiles = tiles_of(a.rows, kHeadTile) * tiles_of(a.n, a.bn);
-    return a.planes == 1 ? launch_tc<kFactor, 1>(m, a, tiles, s)
-                         : launch_tc<kFactor, 3>(m, a, tiles, s);
+    if (a.planes == 1) return launch_tc<kFactor, 1, false>(m, a, tiles, s);
+    return in_runs(a.d) ? launch_tc<kFactor, 3, true>(m, a, tiles, s)
+                        : launch_tc<kFactor, 3, false>(m, a, tiles, s);
 }
 
 int64_t head_acc_floats(int64_t m, int64_t d, int planes, int cut) {
@@ -1503,7 +1511,8 @@ cudaError_t launch_head_products(const HeadProducts& h, const HeadMaps& maps, cu
     const int64_t t0 = h.gH ? tiles_of(a.rows, kHeadTile) * nt : 0;
     const int64_t t1 = h.gE ? tiles_of(a.n, kHeadTile) * nt : 0;
     const int64_t units = t0 * a.cut0 + t1 * a.cut1;
-    cudaError_t e = a.planes == 1 ? launch_tc<kMul, 1>(m, a, units, s) : launch_tc<kMul, 3>(m, a, units, s);
+    cudaError_t e = a.planes == 1 ? launch_tc<kMul, 1, false>(m, a, units, s)
+                                  : launch_tc<kMul, 3, true>(m, a, units, s);
     const int64_t s0 = a.cut0 > 1 && h.last ? t0 : 0, s1 = a.cut1 > 1 ? t1 : 0;
     if (e == cudaSuccess && s0 + s1 > 0) e = launch_sum(a, s0, s1, s);
     return e;
