@@ -579,8 +579,11 @@ GradSpace carve_grad(void* ws, const HeadProblem& p) {
     w.starts = c.take<uint16_t>(p.tg.many ? R * (w.bins + 1) : 0);
     // As for both gradients, whichever are asked for.
     w.cuts = head_cuts(R, std::min(w.piece, p.V), p.d, static_cast<int>(planes));
-    w.gh_acc = c.take<float>(w.piece < p.V || w.cuts.gh > 1 ? head_acc_floats(R, p.d, static_cast<int>(planes), w.cuts.gh) : 0);
-    w.ge_acc = c.take<float>(w.cuts.ge > 1 ? head_acc_floats(w.piece, p.d, static_cast<int>(planes), w.cuts.ge) : 0);
+    const int n_planes = static_cast<int>(planes);
+    w.gh_acc = c.take<float>(
+        w.piece < p.V || w.cuts.gh > 1 ? head_acc_floats(R, p.d, n_planes, w.cuts.gh) : 0);
+    w.ge_acc = c.take<float>(
+        w.cuts.ge > 1 ? head_acc_floats(w.piece, p.d, n_planes, w.cuts.ge) : 0);
     w.g = c.take<__nv_bfloat16>(planes * up(R, kHeadTile) * w.piece);
     w.h = c.take<__nv_bfloat16>(planes * R * dp);
     w.e = c.take<__nv_bfloat16>(planes * p.V * dp);

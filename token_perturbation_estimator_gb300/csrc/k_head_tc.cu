@@ -519,7 +519,7 @@ template <int MODE, int PLANES, bool RUNS>
 struct Epilogue {
     const TcArgs& a;
     const CUtensorMap* tmG;
-    unsigned char* bufs;  // this warp's shared memory: kFactor's store buffers, others' 32 x 32 values
+    unsigned char* bufs;  // this warp's: kFactor's store buffers, the others' 32 x 32 values
     uint32_t rank;
     int q, h, lane;
     uint32_t used = 0;
