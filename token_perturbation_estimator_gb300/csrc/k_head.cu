@@ -50,7 +50,9 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
+// The lanes of a warp meet first: .aligned wants them to arrive together.
 __device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

@@ -728,8 +728,11 @@ struct Epilogue {
     }
 
     // Columns [at, at + 32) of the accumulators of a run of steps: both of them
-    // for fp32 products.
+    // for fp32 products. TMEM is read by whole warps at once, and lanes come
+    // here from places where they part (a row's own entries, a lane that
+    // stores): they meet first.
     __device__ void accumulators(uint32_t taddr, int at, float (&v)[32]) const {
+        __syncwarp();
         tc::tmem_ld_32x32(taddr + at, v);
         if (MODE == kMul && PLANES == 3) {
             float big[32];

@@ -241,15 +241,15 @@ __device__ __forceinline__ float2 shared_param(const float* at, int lane, int pa
 }
 
 // The threads that share a row meet: the lanes of a warp, or (MULTI) the
-// row's own warps, so that a CTA's rows do not wait for one another.
+// row's own warps, so that a CTA's rows do not wait for one another. (bar.sync
+// wants the lanes of a warp to arrive together.)
 template <int MULTI>
 __device__ __forceinline__ void row_sync(int warps) {
+    __syncwarp();
     if constexpr (MULTI > 0)
         asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x >> 5) / warps),
                      "r"(32 * warps)
                      : "memory");
-    else
-        __syncwarp();
 }
 
 // Sums of N values over the threads that share a row, to all of them. G lanes

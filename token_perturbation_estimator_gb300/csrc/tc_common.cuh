@@ -216,7 +216,10 @@ __device__ __forceinline__ void tmem_ld_32xN(uint32_t taddr, float (&v)[N]) {
 // offsets; rank 0 issues the MMAs for both, and each CTA's TMEM gets the
 // accumulator rows of its half of A.
 
+// All threads of the cluster. The lanes of a warp meet first: .aligned wants
+// them to arrive together.
 __device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
