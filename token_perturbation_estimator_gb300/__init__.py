@@ -434,6 +434,7 @@ class _Types:
         self.i32, self.u8 = torch.int32, torch.uint8
         self.code = {torch.float32: F32, torch.bfloat16: BF16}
         self.empty, self.empty_like = torch.empty, torch.empty_like
+        self.current_device = torch.cuda.current_device
         # The current stream's handle; the public way builds an object first (5 us).
         self.stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -450,7 +451,7 @@ def _types():
 
 
 def _in_stream(fn):
-    """Gives fn a keyword `stream`: it then runs with that stream current, so
+    """Gives fn a keyword `stream`: it then runs with that stream and its device current, so
     that what it allocates (outputs not passed in, workspace) belongs to the
     stream that uses it and is not handed out again while the call runs."""
     @functools.wraps(fn)
@@ -496,15 +497,22 @@ def _rows(t, name, dtype, shape, dev):
 
 
 def _values(t, name, dims):
-    """The dtype code and CUDA device of t, an f32 or bf16 tensor with one of
-    these numbers of dimensions; raises ValueError for any other."""
-    code = _types().code.get(t.dtype)
+    """The dtype code and CUDA device of t, an f32 or bf16 tensor on the current
+    device with one of these numbers of dimensions; raises ValueError for any
+    other. (The launch goes to the current device, whatever device its stream
+    was asked for: a default stream's handle is 0 on every one.)"""
+    ty = _types()
+    code = ty.code.get(t.dtype)
     if code is None or not t.is_cuda or t.dim() not in dims:
         if not t.is_cuda:
             raise ValueError("expected a CUDA tensor")
         raise ValueError("%s must be f32 or bf16 with %s dimensions, got %s %s"
                          % (name, " or ".join(map(str, dims)), t.dtype, tuple(t.shape)))
-    return code, t.get_device()
+    dev = t.get_device()
+    if dev != ty.current_device():
+        raise ValueError("%s is on cuda:%d, but the current device (the stream's, where one is "
+                         "given) is cuda:%d" % (name, dev, ty.current_device()))
+    return code, dev
 
 
 @functools.lru_cache(maxsize=256)  # a size follows from the other sizes alone
