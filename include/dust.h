@@ -576,8 +576,9 @@ dust_status dust_layer_norm_grad(const void* gy, int64_t ld_gy, const void* x, i
  * or to 2^-133 where that is more: operands below 2^-110). All sums run in an
  * order fixed by the sizes, by which rows take part and by whether rows start
  * on 16 bytes: deterministic.
- * d >= 1, V >= 1, S >= 1; S*T, d and V up to 2^31 - 1, S*T*d and V*d up to
- * 2^40 (DUST_ERR_RANGE). T = 0 writes zeros to gE (or leaves it,
+ * d >= 1, V >= 1, S >= 1; S*T, d and V up to 2^31 - 2^16, S*T*d and V*d up
+ * to 2^40, and at most 2^30 tiles of 256 rows x 128 ids, S*T and V rounded up
+ * to whole ones (DUST_ERR_RANGE). T = 0 writes zeros to gE (or leaves it,
  * accumulating) and nothing else.
  */
 dust_status dust_head_loss_workspace(size_t* bytes, int64_t S, int64_t T, int64_t d, int64_t V,

@@ -11,6 +11,10 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
+// Of the head's rows, columns and ids: their numbers, padded to whole tiles
+// and to the row pass's thousands, fit 32 bits (the kernels' and TMA's).
+constexpr int64_t kMaxHeadDim = (int64_t(1) << 31) - (int64_t(1) << 16);
+constexpr int64_t kMaxHeadTiles = int64_t(1) << 30;  // of 256 rows x 128 ids, in a launch
 
 size_t a256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -36,8 +40,9 @@ dust_status check_norm(dust_dtype dtype, int64_t T, int64_t d) {
 
 dust_status check_head_sizes(int64_t S, int64_t T, int64_t d, int64_t V, dust_dtype dtype) {
     if (S < 1 || T < 0 || d < 1 || V < 1 || !value_dtype(dtype)) return DUST_ERR_INVALID_ARG;
-    if (T > kMaxDim / S || d > kMaxDim || V > kMaxDim) return DUST_ERR_RANGE;
+    if (T > kMaxHeadDim / S || d > kMaxHeadDim || V > kMaxHeadDim) return DUST_ERR_RANGE;
     if ((T > 0 && S * T > kMaxElems / d) || V > kMaxElems / d) return DUST_ERR_RANGE;
+    if ((S * T + 255) / 256 * ((V + 127) / 128) > kMaxHeadTiles) return DUST_ERR_RANGE;
     return DUST_OK;
 }
 
