@@ -599,9 +599,14 @@ def _head_inputs(H, E):
     code, dev = _values(H, "H", (2, 3))
     if H.dim() == 3:
         S, T, d = H.shape
-        if S > 1 and T > 0 and H.stride(0) != T * H.stride(1):
+        if S == 1:
+            rows = H[0]
+        elif T == 1:  # the stride between a slice's rows says nothing
+            rows = H[:, 0]
+        elif T > 0 and H.stride(0) != T * H.stride(1):
             raise ValueError("the slices of H must follow one another")
-        rows = H[0] if S == 1 else H.as_strided((S * T, d), (H.stride(1), H.stride(2)))
+        else:
+            rows = H.as_strided((S * T, d), (H.stride(1), H.stride(2)))
     else:
         S, (T, d), rows = 1, H.shape, H
     ld_h = _rows(rows, "H", H.dtype, (S * T, d), dev)
