@@ -552,10 +552,9 @@ struct GradSpace {
     size_t total;
 };
 
-// Columns of the tiles of G. (In bf16, G's rounding hides what the logits' sums
-// cut off, at any d.)
+// Columns of the tiles of G, whose logits are summed as the loss's are.
 int grad_columns(const HeadProblem& p, int64_t piece) {
-    return head_columns(p.S * p.T, std::min(piece, p.V), p.bf16 ? 0 : p.d);
+    return head_columns(p.S * p.T, std::min(piece, p.V), p.d);
 }
 
 GradSpace carve_grad(void* ws, const HeadProblem& p) {

@@ -1305,7 +1305,12 @@ cudaError_t launch_tc(const CUtensorMap (&m)[4], TcArgs a, int64_t tiles, cudaSt
 // Whether logits over d columns are summed in runs (kRun), in narrow tiles:
 // about a sixth slower. (Normwise error of single logits, in one run and in
 // runs of 8 steps: d 1024 1.0e-6 and 4.7e-7, d 2048 2.1e-6 and 4.8e-7, d 8192
-// 9.1e-6 and 4.8e-7.) Those of a gradient in bf16 are not: its G is rounded.
+// 9.1e-6 and 4.8e-7.) The loss and the gradient sum them alike, so that what is
+// cut off is the same in lse and in x and cancels in exp(x - lse): of a token
+// that the model is sure of, the target's entry of G is the small difference
+// p - 1, and an error of x that lse does not share is an error of it in full
+// (loss 1e-4, target's logit 30: gH was 0.8 to 1.4 off, by row, at d 2048, and
+// 10 at d 8192, when the bf16 gradient alone summed in one run).
 bool in_runs(int64_t d) { return d > 1024; }
 
 constexpr int kPairs = 76;  // CTA pairs of a whole GPU, for the choices below
@@ -1464,7 +1469,9 @@ cudaError_t launch_head_factor(const HeadLogits& h, const HeadMaps& maps, cudaSt
     a.picks = h.picks;
     a.info = h.rows;
     const int64_t tiles = tiles_of(a.rows, kHeadTile) * tiles_of(a.n, a.bn);
-    if (a.planes == 1) return launch_tc<kFactor, 1, false>(m, a, tiles, s);
+    if (a.planes == 1)
+        return in_runs(a.d) ? launch_tc<kFactor, 1, true>(m, a, tiles, s)
+                            : launch_tc<kFactor, 1, false>(m, a, tiles, s);
     return in_runs(a.d) ? launch_tc<kFactor, 3, true>(m, a, tiles, s)
                         : launch_tc<kFactor, 3, false>(m, a, tiles, s);
 }
