@@ -558,7 +558,12 @@ dust_status dust_layer_norm_grad(const void* gy, int64_t ld_gy, const void* x, i
  *            report DUST_ERR_INVALID_ARG.
  *   scale    finite.
  *   loss, lse  device f32 [S*T], written; loss may be NULL. delta device f32
- *            [S - 1][T], written, or NULL.
+ *            [S - 1][T], written, or NULL. The gradient reads lse: from a
+ *            loss over as many rows (S*T) of the same sizes, whose sums it
+ *            repeats, so that what they cut off cancels in x - lse. With
+ *            another lse (of more slices, of another program) x - lse may be
+ *            off by 2e-6 of |x|, which shows in the target's entry p - 1 of a
+ *            token whose loss is not much larger than that.
  *   gloss    device f32 [S*T]. Rows without a target and rows with gloss 0
  *            take no part in either gradient, whatever H holds there (NaN
  *            included); their gH is 0.

@@ -56,7 +56,8 @@ def _np(t):
 # CUDA cores take.
 @pytest.mark.parametrize("T,d,V", [(150, 512, 2000), (150, 1024, 1500), (150, 2048, 2000),
                                    (140, 8192, 1200), (260, 2056, 700), (1, 2048, 9000),
-                                   (2, 1024, 3000), (4, 512, 4000), (5, 2048, 3000)])
+                                   (2, 1024, 3000), (4, 512, 4000), (5, 2048, 3000),
+                                   (3, 2048, 9000), (4, 1024, 20000), (4, 4096, 2000)])
 def test_gradients_of_sure_tokens(T, d, V):
     import torch
     dev = cuda()

@@ -100,12 +100,11 @@ int head_columns(int64_t rows, int64_t n, int64_t d);
 
 cudaError_t launch_head_lse(const HeadLogits& a, cudaStream_t s);
 
-// ---- the loss of a few rows (k_head_few.cu) ----
+// ---- the loss and the gradients of a few rows (k_head_few.cu) ----
 bool head_few(const HeadProblem& p);        // whether there are few enough
 int head_few_parts(const HeadProblem& p);   // partial sums per row
 cudaError_t launch_head_few(const HeadProblem& p, HeadPart* part, int64_t ld_part, float* picked,
                             float* student, cudaStream_t s);
-bool head_few_grad(const HeadProblem& p);
 int head_few_grad_rows(const HeadProblem& p);   // rows of E a CTA takes at a time (the picks' bins)
 int head_few_grad_parts(const HeadProblem& p);  // parts of R d values
 cudaError_t launch_head_few_grad(const HeadProblem& p, const HeadPicks& picks, const int32_t* alive,

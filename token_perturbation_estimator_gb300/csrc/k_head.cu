@@ -563,7 +563,7 @@ GradSpace carve_grad(void* ws, const HeadProblem& p) {
     GradSpace w = {};
     w.alive = c.take<int32_t>(p.tg.many ? R : 0);
     w.entries = c.take<int2>(p.tg.many ? R * p.tg.K : 0);
-    if (head_few_grad(p)) {
+    if (head_few(p)) {
         w.bins = static_cast<int>((p.V + head_few_grad_rows(p) - 1) / head_few_grad_rows(p));
         w.starts = c.take<uint16_t>(p.tg.many ? R * (w.bins + 1) : 0);
         w.gh_acc = c.take<float>(head_few_grad_parts(p) * R * p.d);
@@ -714,7 +714,7 @@ cudaError_t grad_typed(const HeadProblem& p, const float* lse, const float* stud
     const GradSpace w = carve_grad(ws, p);
     unsigned int* st = status_word();
     if (!st) return cudaErrorUnknown;
-    const bool few = head_few_grad(p);
+    const bool few = head_few(p);
     HeadLogits a = {};
     if (!few) a.bn = grad_columns(p, w.piece);
     if (distill) {

@@ -28,8 +28,9 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kSums = 16;
 constexpr int kMaxRows = 8;
-constexpr int64_t kMaxH = 24 * 1024;  // floats of H in shared memory: two CTAs per SM
-constexpr int64_t kMaxGrad = 24 * 1024;  // of a gradient, which keeps as many sums
+// Floats of H in shared memory: two CTAs per SM for the loss, one for a
+// gradient, which keeps as many sums.
+constexpr int64_t kMaxH = 24 * 1024;
 constexpr int kMaxGradSmem = 208 * 1024;
 constexpr int kMaxCtas = 152 * 2;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -452,7 +453,9 @@ cudaError_t by_rows(const HeadProblem& p, const FewArgs& a, int ctas, cudaStream
         case 1: return launch_few<TX, VEC, 1>(p, a, ctas, s);
         case 2: return launch_few<TX, VEC, 2>(p, a, ctas, s);
         case 4: return launch_few<TX, VEC, 4>(p, a, ctas, s);
-        default: return launch_few<TX, VEC, 8>(p, a, ctas, s);
+        default:
+            if constexpr (sizeof(TX) == 4) return launch_few<TX, VEC, 8>(p, a, ctas, s);
+            return cudaErrorInvalidValue;
     }
 }
 
@@ -483,16 +486,27 @@ cudaError_t grad_by_rows(const HeadProblem& p, const FewGrad& a, int ctas, cudaS
 
 }  // namespace
 
-// Few enough that this is faster than the tensor cores' tiles. us here / there
-// (both with the joining launch), V 4096, d 512 and V 50257, d 2048:
-//   bf16  R 1  6 / 9,  43 / 62     R 2  6 / 9,  46 / 55
-//         R 4  7 / 9,  65 / 54     R 8  10 / 9, 96 / 54
-//   fp32  R 1  7 / 29, 75 / 477    R 8  9 / 27, 142 / 458
-// (bf16 rows of 1001 values, V 20000: R 4 33 / 38, R 8 40 / 38).
+// Few enough that this is faster than the tensor cores' tiles, loss and
+// gradients together. us here / there (with the launches that join), V 4096,
+// d 512 and V 50257, d 2048:
+//   loss       bf16  R 1  6 / 9,  43 / 62     R 2  6 / 9,  46 / 55
+//                    R 4  7 / 9,  65 / 54     R 8  10 / 9, 96 / 54
+//              fp32  R 1  7 / 29, 75 / 477    R 8  9 / 27, 142 / 458
+//   gradients  bf16  R 1  9 / 24, 105 / 236   R 2  11 / 24, 120 / 236
+//                    R 4  16 / 24, 158 / 236
+//              fp32  R 1  9 / 45, 187 / 1160  R 8  25 / 45, 527 / 1156
+// (bf16 rows of 1001 values, V 20000: loss of R 4 33 / 38, R 8 40 / 38; with d
+// 4096, V 32000, where one CTA fits an SM, gradients of bf16 R 4 346 / 287).
+// With E out of the L2, the loss of four bf16 rows takes 81 / 105 (d 2048, V
+// 50257) and 32 / 38 (d 1024, V 20000), as the binding calls it.
+// One rule for loss and gradients: the gradient takes exp(x - lse) with the x
+// that lse was formed from, and the two ways' sums of x differ by what the
+// tensor cores cut off (loss of a token 1e-4, target's logit 30: gH was 0.1 to
+// 0.2 off by row; summed alike 0.02 and less).
 bool head_few(const HeadProblem& p) {
     const int64_t R = p.S * p.T;
     if (R > kMaxRows || rows_up(R) * p.d > kMaxH) return false;
-    return !p.bf16 || R <= 2 || (R <= 4 && p.V * p.d <= (int64_t(1) << 24));
+    return !p.bf16 || R <= 2 || (R <= 4 && p.d <= kMaxH / 8);
 }
 
 int head_few_parts(const HeadProblem& p) {
@@ -526,17 +540,6 @@ cudaError_t launch_head_few(const HeadProblem& p, HeadPart* part, int64_t ld_par
         return vec ? by_rows<__nv_bfloat16, true>(p, a, ctas, s)
                    : by_rows<__nv_bfloat16, false>(p, a, ctas, s);
     return vec ? by_rows<float, true>(p, a, ctas, s) : by_rows<float, false>(p, a, ctas, s);
-}
-
-// The gradients' rule, by the same measure, us here / there:
-//   bf16  R 1  9 / 24, 105 / 236   R 2  11 / 24, 120 / 236
-//         R 4  16 / 24, 158 / 236
-//   fp32  R 1  9 / 45, 187 / 1160  R 8  25 / 45, 527 / 1156
-// and with d 4096, V 32000, where one CTA fits an SM, bf16 R 4 346 / 287.
-bool head_few_grad(const HeadProblem& p) {
-    const int64_t R = p.S * p.T;
-    if (R > kMaxRows || rows_up(R) * p.d > kMaxGrad) return false;
-    return !p.bf16 || R <= 2 || (R <= 4 && p.d <= kMaxGrad / 8);
 }
 
 int head_few_grad_rows(const HeadProblem& p) { return kWarps * grad_rows(rows_up(p.S * p.T)); }
