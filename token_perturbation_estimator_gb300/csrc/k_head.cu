@@ -457,7 +457,7 @@ __device__ void pack_rows(const PackJob<TX>& a, int64_t block) {
             }
 #pragma unroll
             for (int p = 0; p < PLANES; ++p) {
-                __nv_bfloat16 b[8];
+                alignas(16) __nv_bfloat16 b[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     b[k] = __float2bfloat16_rn(v[k]);

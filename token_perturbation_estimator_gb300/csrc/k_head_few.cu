@@ -257,7 +257,7 @@ __device__ __forceinline__ void write_values(void* out, int64_t at, const float 
                                              bool add) {
     if (bf16) {
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + at;
-        __nv_bfloat16 b[P];
+        alignas(16) __nv_bfloat16 b[P];
 #pragma unroll
         for (int k = 0; k < P; ++k) b[k] = __float2bfloat16_rn(v[k]);
         if constexpr (P == 8) *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(b);
