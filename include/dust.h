@@ -572,7 +572,19 @@ dust_status dust_layer_norm_grad(const void* gy, int64_t ld_gy, const void* x, i
  *            or NULL. Overwritten, or added to with DUST_ACCUMULATE (the only
  *            flag; needs DUST_F32).
  *   workspace  device, >= the size that the matching query gives, 256-byte
- *            aligned; contents on entry are ignored.
+ *            aligned; contents on entry are ignored. The gradients' holds G
+ *            for a piece of the vocabulary, 2 bytes for each of at most 2^28
+ *            values, or of 1024 ids of every row (rounded up to 256) where
+ *            that is more; fp32 counts each value three times; with several
+ *            pieces, fp32 sums of gH, 1 KB a row and 128 columns at most; and
+ *            up to 160 MB of slices' sums. Both calls' has room for copies of
+ *            H and E (fp32: three planes), which bf16 rows that start on 16
+ *            bytes do not touch, but for the rows of H that take part in a
+ *            gradient if others do not. 8192 rows, d 2048, V 50257: loss 291
+ *            MB, of which such rows touch 52, gradients 844; fp32 770 and
+ *            1343; 2^20 bf16 rows, d 512, V 32768: gradients 5440. A few rows
+ *            take no copies (1 row, d 2048, V 50257: 0.1 and 2.5 MB).
+ * No output overlaps an input, another output or the workspace.
  * bf16 inputs: products of the exact bf16 values summed in fp32; in the
  * gradients G is rounded to bf16 (it is a tensor-core operand), divided by
  * the largest |gloss| first so that equal weights round as 1 does (of a few

@@ -12,8 +12,9 @@
 // apart, as products of a row of H with K rows of E, they took 74 us beside
 // the logits' then 183 us, 4096 rows, d 1024, V 32768, K 64.)
 //
-// Gradient, per piece of the vocabulary (a piece's G stays below 2^28
-// values): the logits again as G = weight (exp(x - lse) - wanted) in bf16,
+// Gradient, per piece of the vocabulary (a piece's G has at most 2^28 values
+// over its planes, or 1024 ids of every row where that is more: head_piece()):
+// the logits again as G = weight (exp(x - lse) - wanted) in bf16,
 // then gH += G E and gE = G^T H in one launch. For distillation a first launch
 // puts each row's entries in order and forms exp(x - lse) - q at them, which
 // the pass over the columns puts in their places. Rows that take no part (no
