@@ -626,7 +626,8 @@ dust_status dust_head_loss_grad(const void* H, int64_t ld_h, const void* E, int6
  *            place. Ids >= V are absent too and reported as above. An id may
  *            come twice (its probabilities add). A token with no entry has
  *            loss 0 and no gradient.
- *   teacher  device f32 [T][K]; -infinity is a probability of 0. Absent
+ *   teacher  device f32 [T][K]; -infinity is a probability of 0 (with
+ *            scale > 0; otherwise it makes its token's results NaN). Absent
  *            entries' values are not used.
  *   K        1 .. DUST_MAX_TEACHER (else DUST_ERR_RANGE).
  *   student  device f32 [S*T][K]: x[r][ids[t][j]], 0 for absent entries;

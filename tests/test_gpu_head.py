@@ -23,7 +23,8 @@ pytestmark = pytest.mark.gpu
 GRAD_TOL = {"f32": 2e-5, "bf16": 5e-3}
 
 # S, T, d, V: single tokens, ragged and odd sizes, sizes about the tiles'
-# edges (64, 128, 256 rows and columns), vocabularies past one piece.
+# edges (64, 128, 256 rows and columns), vocabularies of many tiles (those of
+# several pieces: test_gpu_head_pieces.py).
 SIZES = [(1, 1, 8, 5), (1, 1, 512, 4096), (1, 3, 64, 2), (2, 5, 33, 17), (1, 127, 64, 255),
          (1, 128, 64, 256), (1, 129, 72, 257), (1, 256, 128, 512), (1, 257, 136, 1000),
          (3, 100, 96, 777), (1, 300, 301, 2049), (1, 64, 1024, 5000), (1, 2, 2056, 300),

@@ -19,8 +19,10 @@
 //
 // fp32 inputs come as three bf16 planes whose sum is the value to 24 bits
 // (each plane the bf16 rounding of what the ones before leave), and a product
-// is six products of planes, smallest first; what is left out is below 2^-24
-// of the product.
+// is six products of planes; what is left out is below 2^-24 of the product.
+// The logits take one pair of planes after another, the smallest products
+// first; the gradients' products take all planes of a step together, the
+// largest product in an accumulator of its own.
 //
 // Persistent: warp 0 loads (both CTAs), warp 1 issues the MMAs (rank 0 only),
 // eight warps drain the accumulators, two per TMEM lane quarter. All waits are
@@ -35,7 +37,9 @@
 // Bound by the tensor pipe (94 % busy at d 1024): the logits of 4096 rows, d
 // 1024, V 32768 take 139 us, 1980 TFLOP/s; in long runs the power limit
 // lowers the clock, and the gradients of 8192 rows (83 % taking part), d 2048,
-// V 50257 take 2.13 to 2.47 ms, 1970 to 1700 TFLOP/s. Below d 384 the epilogue
+// V 50257, their logits summed in runs, take 2.33 to 2.66 ms, 1800 to 1580
+// TFLOP/s. fp32 (six products counted): the loss of 4096 rows, d 1024, V 32768
+// 831 us, 1980 TFLOP/s; gradients 2760, 1790. Below d 384 the epilogue
 // binds (2.6e12 exponentials a second, half of what the special-function units
 // can do: two warps per scheduler), and fp32 gradients there HBM, by G's three
 // planes.
@@ -1327,8 +1331,10 @@ int logit_columns(int64_t rows, int64_t n) {
 }
 
 // Columns of the tiles of the products: by what is computed past d; narrow in
-// fp32, where a unit's sums have to fit the epilogue's registers (kRun), and
-// two accumulators TMEM (see launch_head_products).
+// fp32, where a thread of the epilogue holds a unit's sums over its runs (kRun:
+// 64 of them, where wide tiles would make 128; beside a block's values this
+// takes all 168 registers that ten warps leave a thread, and 236 bytes are
+// spilled), and TMEM two accumulators (see launch_head_products).
 int product_columns(int64_t d, int planes) {
     return planes == 3 || tiles_of(d, 128) * 13 < tiles_of(d, 256) * 20 ? 128 : 256;
 }
