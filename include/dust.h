@@ -715,8 +715,8 @@ int32_t dust_pipe_probe_threads(void);
  * dust_debug_inject_timeout — test hook for the device-side failure path (no
  * counterpart on the pages). With on != 0, the next tensor-core contraction
  * launched by this process (dust_contract, the unfused dust_estimate_gW path,
- * or a product of the head's losses and gradients) makes its MMA thread wait on an mbarrier that no thread ever arrives
- * at. The wait gives up after its 1 s limit, the kernel lets its issued TMA
+ * or a product of the head's losses and gradients) makes its MMA thread wait
+ * on an mbarrier that no thread ever arrives at. The wait gives up after its 1 s limit, the kernel lets its issued TMA
  * copies land, frees its tensor memory and returns without writing gW, and
  * dust_last_error then reports DUST_ERR_TIMEOUT; the CUDA context stays
  * usable. No fault, trap or hang is involved. One-shot; process-global.
