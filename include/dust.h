@@ -653,6 +653,227 @@ dust_status dust_distill_loss_grad(const void* H, int64_t ld_h, const void* E, i
                                    size_t ws_bytes, void* stream);
 
 /*
+ * The rest of a training step around the estimator: the gated feed-forward
+ * block beside the jittered linear layer, the norms and the rotation of an
+ * attention layer's queries and keys, a policy's loss on the head's per-token
+ * losses, and clipping by the norm of all gradients. All of them work on the
+ * current device in the order of `stream`, can be captured into graphs, and
+ * use no floating-point atomics: the same call gives the same bits.
+ */
+
+/*
+ * The gated feed-forward block's first half, both projections, the activation
+ * and the product in one pass, and its gradients (the block's second half is
+ * one more linear layer):
+ *   g = X Wg^T    u = X Wu^T    h = act(g) u
+ *   dG = gh u act'(g)    dU = gh act(g)
+ *   gX = dG Wg + dU Wu   gWg = dG^T X   gWu = dU^T X
+ * with act(g) one of g / (1 + exp(-g)); g / (1 + exp(-2 z)), z = sqrt(2 / pi)
+ * (g + 0.044715 g^3); and max(g, 0)^2. The backward forms g and u once more.
+ *
+ *   X        device, `dtype` (DUST_F32 or DUST_BF16), T rows of d values, row
+ *            stride ld_x >= d (elements); Wg, Wu device, `dtype`, f rows of d
+ *            values, row strides ld_wg, ld_wu >= d (the two may be the halves
+ *            of one matrix).
+ *   h        device, `dtype`, T rows of f values, row stride ld_h >= f, written.
+ *   gh       device, `dtype`, as h (row stride ld_gh).
+ *   gX       device, `dtype`, row stride ld_gx >= d, or NULL; overwritten.
+ *   gWg, gWu device [f][d], gW_dtype DUST_F32, or DUST_BF16 with bf16 inputs;
+ *            either may be NULL. Overwritten, or added to with
+ *            DUST_ACCUMULATE (the only flag; needs DUST_F32).
+ *   workspace  device, >= the size that the matching query gives, 256-byte
+ *            aligned; contents on entry are ignored.
+ * No output overlaps an input, another output or the workspace.
+ * bf16 inputs: products of the exact bf16 values summed in fp32, the
+ * activation and the product in fp32, h rounded once; the backward's dG and dU
+ * are rounded to bf16 (they are tensor-core operands). fp32 inputs: every
+ * product and sum to fp32 accuracy (operands to 24 bits, or to 2^-133 where
+ * that is more).
+ * d >= 1, f >= 1, T >= 0; T, d and f up to 2^31 - 2^16, T*d, T*f and f*d up to
+ * 2^39, and at most 2^30 tiles of 256 rows x 64 columns (DUST_ERR_RANGE).
+ * T = 0 writes zeros to gWg and gWu (or leaves them, accumulating) and nothing
+ * else.
+ */
+typedef enum {
+    DUST_ACT_SILU = 0,
+    DUST_ACT_GELU = 1,         /* the form with the hyperbolic tangent */
+    DUST_ACT_RELU2 = 2
+} dust_act;
+
+dust_status dust_gated_up_workspace(size_t* bytes, int64_t T, int64_t d, int64_t f,
+                                    dust_dtype dtype);
+dust_status dust_gated_up(const void* X, int64_t ld_x, const void* Wg, int64_t ld_wg,
+                          const void* Wu, int64_t ld_wu, dust_dtype dtype, int64_t T, int64_t d,
+                          int64_t f, dust_act act, void* h, int64_t ld_h, void* workspace,
+                          size_t ws_bytes, void* stream);
+dust_status dust_gated_up_grad_workspace(size_t* bytes, int64_t T, int64_t d, int64_t f,
+                                         dust_dtype dtype);
+dust_status dust_gated_up_grad(const void* gh, int64_t ld_gh, const void* X, int64_t ld_x,
+                               const void* Wg, int64_t ld_wg, const void* Wu, int64_t ld_wu,
+                               dust_dtype dtype, int64_t T, int64_t d, int64_t f, dust_act act,
+                               uint32_t flags, void* gX, int64_t ld_gx, void* gWg, void* gWu,
+                               dust_dtype gW_dtype, void* workspace, size_t ws_bytes,
+                               void* stream);
+
+/*
+ * The root-mean-square norm of each head's query and key, and the rotation by
+ * the token's position, in one pass, forward and backward. Per token t and
+ * head, with x its D values:
+ *   rstd = 1 / sqrt(sum x^2 / D + eps)    n = x rstd    m = n w
+ *   y = m, its first `rot` values turned: for i < rot / 2, with c =
+ *       cosine[p][i], s = sine[p][i], p = positions[t], and (a, b) the pair
+ *       (i, i + rot / 2) (DUST_ROPE_HALVES) or (2 i, 2 i + 1) (DUST_ROPE_PAIRS),
+ *       y_a = m_a c - m_b s    y_b = m_b c + m_a s
+ *   gm = gy turned back    gw = sum over tokens and heads of gm n
+ *   gx = rstd (gm w - n sum(gm w n) / D)
+ *
+ *   q, k     device, `dtype` (DUST_F32 or DUST_BF16): value j of head h of
+ *            token t at t * token stride + h * head stride + j (elements), so
+ *            that they may lie in one row of a fused projection. Strides are
+ *            positive and no two heads overlap: with H heads, the head stride
+ *            is >= D and the token stride >= (H - 1) * head stride + D, or the
+ *            two the other way round (heads outside of tokens). hk may be 0
+ *            (k and its companions are not used then).
+ *   yq, yk, gq, gk  device, `dtype`, strided alike; overwritten. Each may be
+ *            its own input (yq = q, gq = gyq; same strides); no other overlap.
+ *   wq, wk   device f32 [D], either may be NULL (1).
+ *   eps      finite, >= 0.
+ *   positions  device i32 [T]. A negative position marks a padded token: its
+ *            outputs are 0 and it adds to no gradient, whatever its inputs
+ *            hold. Positions >= n_pos are treated alike and make
+ *            dust_last_error report DUST_ERR_INVALID_ARG.
+ *   cosine, sine  device f32 [n_pos][rot / 2], of the angles. May be NULL when
+ *            rot is 0.
+ *   rot      even, 0 <= rot <= D. D from 1 to DUST_MAX_HEAD (DUST_ERR_RANGE).
+ *   gwq, gwk device f32 [D], either may be NULL; overwritten, or added to with
+ *            DUST_ACCUMULATE (the only flag). With T = 0 (or no head) they are
+ *            zeroed, or left, accumulating.
+ *   workspace  device, >= dust_qk_norm_rope_grad_workspace bytes, 256-byte
+ *            aligned (partial sums of gwq and gwk); may be NULL when both are.
+ * Statistics, sums and the rotation are fp32; outputs are rounded once.
+ * T and the numbers of heads up to 2^31 - 1, T * (hq + hk) * D up to 2^40.
+ */
+#define DUST_MAX_HEAD 512
+typedef enum {
+    DUST_ROPE_HALVES = 0,
+    DUST_ROPE_PAIRS = 1
+} dust_rope_layout;
+
+/* Where the heads of one operand lie. */
+typedef struct {
+    void* data;
+    int64_t token_stride, head_stride; /* elements */
+} dust_heads;
+
+dust_status dust_qk_norm_rope(const dust_heads* q, int64_t hq, const dust_heads* k, int64_t hk,
+                              dust_dtype dtype, int64_t T, int64_t D, const float* wq,
+                              const float* wk, float eps, const int32_t* positions,
+                              const float* cosine, const float* sine, int64_t n_pos, int64_t rot,
+                              dust_rope_layout layout, const dust_heads* yq, const dust_heads* yk,
+                              void* stream);
+dust_status dust_qk_norm_rope_grad_workspace(size_t* bytes, int64_t T, int64_t hq, int64_t hk,
+                                             int64_t D);
+dust_status dust_qk_norm_rope_grad(const dust_heads* gyq, const dust_heads* gyk,
+                                   const dust_heads* q, int64_t hq, const dust_heads* k,
+                                   int64_t hk, dust_dtype dtype, int64_t T, int64_t D,
+                                   const float* wq, const float* wk, float eps,
+                                   const int32_t* positions, const float* cosine,
+                                   const float* sine, int64_t n_pos, int64_t rot,
+                                   dust_rope_layout layout, uint32_t flags, const dust_heads* gq,
+                                   const dust_heads* gk, float* gwq, float* gwk, void* workspace,
+                                   size_t ws_bytes, void* stream);
+
+/*
+ * A policy's clipped loss with a KL term, on the per-token losses that
+ * dust_head_loss gives (nll[s][t], minus the logarithm of the sampled token's
+ * probability; slice 0 the clean pass, later ones the draws'): what the
+ * estimator's loss changes are under rewards, and the gradient that
+ * dust_head_loss_grad takes as gloss. With rho = exp(old - nll), r = nll - ref
+ * and A the token's advantage:
+ *   kl    = exp(r) - r - 1                       (0 without ref)
+ *   loss  = -min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A) + beta kl
+ *   total[s] = sum_t w[t] loss[s][t];  kl_mean, clipped likewise (clipped: the
+ *       share of tokens for which the clipped product is the smaller one)
+ *   delta[k][t] = loss[k + 1][t] - loss[0][t]
+ *   gnll[s][t] = gtotal[s] w[t] (rho A [not clipped] + beta (exp(r) - 1))
+ * and w[t] = 1 / (scored tokens) (DUST_MEAN_TOKEN), or 1 / (sequences with
+ * scored tokens * scored tokens of t's sequence) (DUST_MEAN_SEQUENCE). A token
+ * is scored if it lies in a sequence and has a target; others have loss, kl,
+ * delta and gnll 0, whatever the inputs hold there. With no scored token the
+ * means are 0.
+ *
+ *   nll      device f32 [S][T]; old, ref device f32 [T], ref may be NULL.
+ *   advantages  device f32, [T] with per_token != 0, else [n_seq].
+ *   seq_offsets device i32 [n_seq + 1], not decreasing, within 0 .. T: sequence
+ *            i holds tokens [o_i, o_i+1) (none, if they are equal). Tokens
+ *            before the first and behind the last are in no sequence. Offsets
+ *            outside 0 .. T reach nothing.
+ *   targets  device i32 [T], negative where a token has none (as for
+ *            dust_head_loss), or NULL: all have one.
+ *   clip_low in [0, 1], clip_high >= 0, beta finite (infinite clip_high: no
+ *            bound). Whether a ratio is beyond its bound is decided in 64 bits.
+ *   loss     device f32 [S][T] or NULL; total, kl_mean, clipped device f32 [S],
+ *            each may be NULL; delta device f32 [S - 1][T] or NULL.
+ *   gtotal   device f32 [S]; gnll device f32 [S][T]; may be nll itself.
+ *   workspace  device, >= dust_policy_loss_workspace bytes, 256-byte aligned;
+ *            the same for both calls.
+ * No other output overlaps an input or another output.
+ * S >= 1; S*T and n_seq up to 2^31 - 1 (DUST_ERR_RANGE). n_seq = 0: no token is
+ * scored.
+ */
+typedef enum {
+    DUST_MEAN_TOKEN = 0,
+    DUST_MEAN_SEQUENCE = 1
+} dust_mean;
+
+dust_status dust_policy_loss_workspace(size_t* bytes, int64_t S, int64_t T, int64_t n_seq);
+dust_status dust_policy_loss(const float* nll, const float* old, const float* ref,
+                             const float* advantages, int32_t per_token,
+                             const int32_t* seq_offsets, int64_t n_seq, const int32_t* targets,
+                             int64_t S, int64_t T, float clip_low, float clip_high, float beta,
+                             dust_mean mean, float* loss, float* total, float* kl_mean,
+                             float* clipped, float* delta, void* workspace, size_t ws_bytes,
+                             void* stream);
+dust_status dust_policy_loss_grad(const float* nll, const float* old, const float* ref,
+                                  const float* advantages, int32_t per_token,
+                                  const int32_t* seq_offsets, int64_t n_seq,
+                                  const int32_t* targets, int64_t S, int64_t T, float clip_low,
+                                  float clip_high, float beta, dust_mean mean,
+                                  const float* gtotal, float* gnll, void* workspace,
+                                  size_t ws_bytes, void* stream);
+
+/*
+ * dust_clip_grads — the norm over all gradients of a step (a pass of
+ * dust_estimate_gW_sites, say) and the gradients scaled so that it is at most
+ * max_norm:
+ *   norm = sqrt(sum over all values of g^2)    out = g min(1, max_norm / norm)
+ * A NaN among them makes the norm and every result NaN, an infinity the norm
+ * infinite and the factor 0 (an infinity times which is NaN).
+ *   grads    host array of n tensors: g device, n values of `dtype` (DUST_F32 or
+ *            DUST_BF16, each its own), contiguous; out device, same type, or
+ *            NULL in every one of them (the norm alone). out may be g itself;
+ *            it overlaps no other tensor's g or out (checked on the host,
+ *            DUST_ERR_INVALID_ARG).
+ *   max_norm >= 0, may be infinite (a factor of 1).
+ *   norm     device f32 [1], written.
+ *   workspace  device, >= dust_clip_grads_workspace bytes, 256-byte aligned.
+ * Squares are summed in groups of 16 values in fp32, or one by one in 64 bits
+ * where those overflow or lose bits; the groups' sums in 64 bits. norm is
+ * rounded to fp32 (infinite above its range), the factor is formed in 64 bits.
+ * At most 4096 tensors of up to 2^40 values (DUST_ERR_RANGE).
+ */
+typedef struct {
+    const void* g;
+    void* out;
+    int64_t n;
+    int32_t dtype;
+} dust_grad;
+
+dust_status dust_clip_grads_workspace(size_t* bytes, int64_t n);
+dust_status dust_clip_grads(const dust_grad* grads, int64_t n, float max_norm, float* norm,
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Per-kernel timing for benchmarks (no counterpart on the pages: this is
  * measurement plumbing). While enabled, every kernel the library launches is
  * bracketed by two CUDA events recorded on its stream; dust_profile_read

@@ -10,8 +10,10 @@ Functions keep the C names: ``dust_noise``, ``dust_jitter_apply``,
 ``dust_forward_jitter``,
 ``dust_credit_scan``, ``dust_error_estimate``, ``dust_estimate_gW``,
 ``dust_estimate_gW_host``, ``dust_last_error`` (plus the workspace queries);
-and, beside the estimator, ``dust_layer_norm``, ``dust_head_loss`` and
-``dust_distill_loss``, each with its ``_grad``.
+beside the estimator, ``dust_layer_norm``, ``dust_head_loss`` and
+``dust_distill_loss``, each with its ``_grad``; and the rest of a training step,
+``dust_gated_up``, ``dust_qk_norm_rope`` and ``dust_policy_loss``, each with its
+``_grad``, and ``dust_clip_grads``.
 """
 from __future__ import annotations
 
@@ -36,6 +38,10 @@ FORCE_UNFUSED, FORCE_FUSED, WORD_STREAM1, FORCE_SIMT = 8, 16, 32, 64
 # dust_path
 PATH_FUSED_TC, PATH_UNFUSED_TC, PATH_SIMT = 1, 2, 3
 MAX_TEACHER = 1024  # DUST_MAX_TEACHER
+# dust_act, dust_rope_layout, dust_mean
+SILU, GELU, RELU2 = 0, 1, 2
+ROPE_HALVES, ROPE_PAIRS = 0, 1
+MEAN_TOKEN, MEAN_SEQUENCE = 0, 1
 
 
 class DustError(RuntimeError):
@@ -96,6 +102,24 @@ def _signatures():
         "dust_distill_loss_grad_workspace": (i32, [PSZ, i64, i64, i64, i64, i64, i32]),
         "dust_distill_loss_grad": (i32, [P, i64, P, i64, i32, i64, i64, i64, i64, P, P, i64, f32,
                                          P, P, P, u32, P, i64, P, i32, P, SZ, P]),
+        "dust_gated_up_workspace": (i32, [PSZ, i64, i64, i64, i32]),
+        "dust_gated_up": (i32, [P, i64, P, i64, P, i64, i32, i64, i64, i64, i32, P, i64, P, SZ,
+                                P]),
+        "dust_gated_up_grad_workspace": (i32, [PSZ, i64, i64, i64, i32]),
+        "dust_gated_up_grad": (i32, [P, i64, P, i64, P, i64, P, i64, i32, i64, i64, i64, i32, u32,
+                                     P, i64, P, P, i32, P, SZ, P]),
+        "dust_qk_norm_rope": (i32, [P, i64, P, i64, i32, i64, i64, P, P, f32, P, P, P, i64, i64,
+                                    i32, P, P, P]),
+        "dust_qk_norm_rope_grad_workspace": (i32, [PSZ, i64, i64, i64, i64]),
+        "dust_qk_norm_rope_grad": (i32, [P, P, P, i64, P, i64, i32, i64, i64, P, P, f32, P, P, P,
+                                         i64, i64, i32, u32, P, P, P, P, P, SZ, P]),
+        "dust_policy_loss_workspace": (i32, [PSZ, i64, i64, i64]),
+        "dust_policy_loss": (i32, [P, P, P, P, i32, P, i64, P, i64, i64, f32, f32, f32, i32, P, P,
+                                   P, P, P, P, SZ, P]),
+        "dust_policy_loss_grad": (i32, [P, P, P, P, i32, P, i64, P, i64, i64, f32, f32, f32, i32,
+                                        P, P, P, SZ, P]),
+        "dust_clip_grads_workspace": (i32, [PSZ, i64]),
+        "dust_clip_grads": (i32, [P, i64, f32, P, P, SZ, P]),
         "dust_debug_inject_timeout": (i32, [i32]),
         "dust_pipe_probe": (i32, [i32, i64, C.POINTER(C.c_double), P, P]),
         "dust_pipe_probe_threads": (i32, []),
@@ -729,6 +753,267 @@ def dust_distill_loss_grad(H, E, ids, teacher, lse, student, gloss, scale=1.0, f
                                       ws_at, ws_bytes, ty.stream_of(dev))
     _check(st, "dust_distill_loss_grad")
     return gH, gE
+
+
+# ------------------------------------------------ the rest of a training step --
+
+def _gated_inputs(X, Wg, Wu):
+    code, dev = _values(X, "X", (2,))
+    T, d = X.shape
+    if Wg.dim() != 2 or Wg.shape[1] != d:
+        raise ValueError("Wg must be [f, d] matching X, got %s" % (tuple(Wg.shape),))
+    f = Wg.shape[0]
+    return code, dev, T, d, f, (
+        X.data_ptr(), _rows(X, "X", X.dtype, (T, d), dev), Wg.data_ptr(),
+        _rows(Wg, "Wg", X.dtype, (f, d), dev), Wu.data_ptr(), _rows(Wu, "Wu", X.dtype, (f, d), dev),
+        code, T, d, f)
+
+
+@_in_stream
+def dust_gated_up(X, Wg, Wu, act=SILU, h=None, workspace=None):
+    """X: CUDA [T, d]; Wg, Wu: [f, d] (all f32 or all bf16, rows may be strided);
+    returns h = act(X Wg^T) (X Wu^T), [T, f] of X's dtype."""
+    code, dev, T, d, f, operands = _gated_inputs(X, Wg, Wu)
+    h, h_at, ld_h = _output_rows(h, "h", X.dtype, (T, f), X, dev)
+    workspace, ws_at, ws_bytes = _space(workspace, "dust_gated_up_workspace", X, dev, T, d, f, code)
+    st = lib().dust_gated_up(*operands, act, h_at, ld_h, ws_at, ws_bytes, _types().stream_of(dev))
+    _check(st, "dust_gated_up")
+    return h
+
+
+@_in_stream
+def dust_gated_up_grad(gh, X, Wg, Wu, act=SILU, flags=0, gX=None, gWg=None, gWu=None,
+                       gW_dtype=None, workspace=None):
+    """The gradients of dust_gated_up for gh ([T, f], X's dtype): returns (gX of
+    X's shape and dtype, gWg, gWu [f, d], f32 unless gW_dtype is bf16);
+    ACCUMULATE adds to the f32 gWg and gWu that are passed in."""
+    ty = _types()
+    code, dev, T, d, f, operands = _gated_inputs(X, Wg, Wu)
+    if flags & ACCUMULATE and (gWg is None or gWu is None):
+        raise ValueError("ACCUMULATE needs the gWg and gWu to add to")
+    given = gWg if gWg is not None else gWu
+    gw_type = (gW_dtype or ty.f32) if given is None else given.dtype
+    gcode = ty.code.get(gw_type)
+    if gcode is None:
+        raise ValueError("gWg and gWu must be f32 or bf16, got %s" % gw_type)
+    gX, gx_at, ld_gx = _output_rows(gX, "gX", X.dtype, (T, d), X, dev)
+    gWg, gwg_at = _output(gWg, "gWg", gw_type, (f, d), X, dev)
+    gWu, gwu_at = _output(gWu, "gWu", gw_type, (f, d), X, dev)
+    workspace, ws_at, ws_bytes = _space(workspace, "dust_gated_up_grad_workspace", X, dev, T, d, f,
+                                        code)
+    st = lib().dust_gated_up_grad(gh.data_ptr(), _rows(gh, "gh", X.dtype, (T, f), dev), *operands,
+                                  act, flags, gx_at, ld_gx, gwg_at, gwu_at, gcode, ws_at, ws_bytes,
+                                  ty.stream_of(dev))
+    _check(st, "dust_gated_up_grad")
+    return gX, gWg, gWu
+
+
+class _Heads(C.Structure):
+    """dust_heads of include/dust.h."""
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+def _heads(t, name, dtype, shape, dev):
+    """dust_heads of t, a tensor of this dtype and shape [T, heads, D] on CUDA
+    device `dev` with unit stride inside a head; raises ValueError for any other."""
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev):
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        _expect(t, name, (dtype,), shape=shape)
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, dev, t.device))
+    token, head, step = t.stride()
+    if shape[2] > 1 and step != 1:
+        raise ValueError("%s must have unit stride inside a head" % name)
+    return _Heads(t.data_ptr(), token, head)
+
+
+def _output_heads(t, name, dtype, shape, ref, dev):
+    """The caller's output, or a new one: (tensor, dust_heads)."""
+    if t is None:
+        t = _types().empty(shape, dtype=dtype, device=ref.device)
+        return t, _Heads(t.data_ptr(), shape[1] * shape[2], shape[2])
+    return t, _heads(t, name, dtype, shape, dev)
+
+
+def _rope_inputs(q, k, wq, wk, positions, cosine, sine, eps, layout):
+    ty = _types()
+    code, dev = _values(q, "q", (3,))
+    T, hq, D = q.shape
+    hk = 0 if k is None else k.shape[1]
+    if k is not None and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != D):
+        raise ValueError("k must be [T, heads, D] matching q, got %s" % (tuple(k.shape),))
+    if cosine is None:
+        n_pos, rot = (1 << 31) - 1, 0
+    else:
+        if cosine.dim() != 2:
+            raise ValueError("cosine must be [positions, rot / 2], got %s" % (tuple(cosine.shape),))
+        n_pos, rot = cosine.shape[0], 2 * cosine.shape[1]
+    hs_q = _heads(q, "q", q.dtype, (T, hq, D), dev)
+    hs_k = None if k is None else _heads(k, "k", q.dtype, (T, hk, D), dev)
+    args = (hs_q, hq, hs_k, hk, code, T, D, _dense(wq, "wq", ty.f32, (D,), dev),
+            _dense(wk, "wk", ty.f32, (D,), dev), eps, _dense(positions, "positions", ty.i32, (T,), dev),
+            _dense(cosine, "cosine", ty.f32, (n_pos, rot // 2), dev),
+            _dense(sine, "sine", ty.f32, (n_pos, rot // 2), dev), n_pos, rot, layout)
+    return ty, dev, T, hq, hk, D, args
+
+
+@_in_stream
+def dust_qk_norm_rope(q, k, wq, wk, positions, cosine, sine, eps=1e-6, layout=ROPE_HALVES, yq=None,
+                      yk=None):
+    """q: CUDA [T, hq, D]; k: [T, hk, D] or None (f32 or bf16, tokens and heads
+    may be strided, as in a fused projection's row); wq, wk: f32 [D] or None;
+    positions: i32 [T], negative for padding; cosine, sine: f32 [positions,
+    rot / 2] (None: no rotation). Returns (yq, yk), normed and turned."""
+    ty, dev, T, hq, hk, D, args = _rope_inputs(q, k, wq, wk, positions, cosine, sine, eps, layout)
+    yq, hs_q = _output_heads(yq, "yq", q.dtype, (T, hq, D), q, dev)
+    hs_k = None
+    if k is not None:
+        yk, hs_k = _output_heads(yk, "yk", q.dtype, (T, hk, D), q, dev)
+    st = lib().dust_qk_norm_rope(*_refs(args), *_refs((hs_q, hs_k)), ty.stream_of(dev))
+    _check(st, "dust_qk_norm_rope")
+    return yq, yk
+
+
+def _refs(args):
+    return tuple(C.byref(a) if type(a) is _Heads else a for a in args)
+
+
+@_in_stream
+def dust_qk_norm_rope_grad(gyq, gyk, q, k, wq, wk, positions, cosine, sine, eps=1e-6,
+                           layout=ROPE_HALVES, flags=0, gq=None, gk=None, gwq=None, gwk=None,
+                           workspace=None):
+    """The gradients of dust_qk_norm_rope for gyq and gyk: returns (gq, gk, gwq
+    f32 [D], gwk f32 [D]); ACCUMULATE adds to the gwq and gwk that are passed
+    in. gyk, gk and gwk are not used where k is None."""
+    ty, dev, T, hq, hk, D, args = _rope_inputs(q, k, wq, wk, positions, cosine, sine, eps, layout)
+    if flags & ACCUMULATE and (gwq is None or (k is not None and gwk is None)):
+        raise ValueError("ACCUMULATE needs the gwq and gwk to add to")
+    gy_q, gy_k = _heads(gyq, "gyq", q.dtype, (T, hq, D), dev), None
+    gq, hs_q = _output_heads(gq, "gq", q.dtype, (T, hq, D), q, dev)
+    gwq, gwq_at = _output(gwq, "gwq", ty.f32, (D,), q, dev)
+    hs_k = gwk_at = None
+    if k is not None:
+        gy_k = _heads(gyk, "gyk", q.dtype, (T, hk, D), dev)
+        gk, hs_k = _output_heads(gk, "gk", q.dtype, (T, hk, D), q, dev)
+        gwk, gwk_at = _output(gwk, "gwk", ty.f32, (D,), q, dev)
+    workspace, ws_at, ws_bytes = _space(workspace, "dust_qk_norm_rope_grad_workspace", q, dev, T, hq,
+                                        hk, D)
+    st = lib().dust_qk_norm_rope_grad(*_refs((gy_q, gy_k)), *_refs(args), flags,
+                                      *_refs((hs_q, hs_k)), gwq_at, gwk_at, ws_at, ws_bytes,
+                                      ty.stream_of(dev))
+    _check(st, "dust_qk_norm_rope_grad")
+    return gq, gk, gwq, gwk
+
+
+def _policy_inputs(nll, old, advantages, seq_offsets, ref, targets, clip_low, clip_high, beta, mean,
+                   per_token):
+    ty = _types()
+    if not nll.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if nll.dtype is not ty.f32 or nll.dim() not in (1, 2):
+        raise ValueError("nll must be f32 [T] or [S, T], got %s %s" % (nll.dtype, tuple(nll.shape)))
+    _, dev = _values(nll, "nll", (1, 2))
+    S, T = (1, nll.shape[0]) if nll.dim() == 1 else nll.shape
+    n_seq = seq_offsets.numel() - 1
+    if n_seq < 0:
+        raise ValueError("seq_offsets must have at least one value")
+    if per_token is None:
+        n = advantages.numel()
+        if n == T and n == n_seq and n > 1:
+            raise ValueError("as many sequences as tokens: say whether advantages are per_token")
+        per_token = n == T
+    operands = (_dense(nll, "nll", ty.f32, nll.shape, dev), _dense(old, "old", ty.f32, (T,), dev),
+                _dense(ref, "ref", ty.f32, (T,), dev),
+                _dense(advantages, "advantages", ty.f32, (T if per_token else n_seq,), dev),
+                1 if per_token else 0,
+                _dense(seq_offsets, "seq_offsets", ty.i32, (n_seq + 1,), dev), n_seq,
+                _dense(targets, "targets", ty.i32, (T,), dev), S, T, clip_low, clip_high, beta, mean)
+    return ty, dev, S, T, n_seq, operands
+
+
+@_in_stream
+def dust_policy_loss(nll, old, advantages, seq_offsets, ref=None, targets=None, clip_low=0.2,
+                     clip_high=0.2, beta=0.0, mean=MEAN_TOKEN, per_token=None, changes=False,
+                     loss=None, total=None, kl=None, clipped=None, delta=None, workspace=None):
+    """nll: CUDA f32 [T] or [S, T], dust_head_loss's losses; old, ref: f32 [T], the
+    samples' under the policy that drew them and under the reference;
+    advantages: f32 [T] or [n_seq] (per_token tells where both fit); targets:
+    i32 [T], negative where a token is not scored. Returns (loss of nll's
+    shape, total, kl, clipped of nll's leading shape), and with changes=True
+    also delta f32 [S - 1, T], each later slice's loss minus the first one's."""
+    ty, dev, S, T, n_seq, operands = _policy_inputs(
+        nll, old, advantages, seq_offsets, ref, targets, clip_low, clip_high, beta, mean, per_token)
+    lead = nll.shape[:-1]
+    loss, loss_at = _output(loss, "loss", ty.f32, nll.shape, nll, dev)
+    total, total_at = _output(total, "total", ty.f32, lead, nll, dev)
+    kl, kl_at = _output(kl, "kl", ty.f32, lead, nll, dev)
+    clipped, clipped_at = _output(clipped, "clipped", ty.f32, lead, nll, dev)
+    delta_at = None
+    if delta is not None or changes:
+        delta, delta_at = _output(delta, "delta", ty.f32, (S - 1, T), nll, dev)
+    workspace, ws_at, ws_bytes = _space(workspace, "dust_policy_loss_workspace", nll, dev, S, T,
+                                        n_seq)
+    st = lib().dust_policy_loss(*operands, loss_at, total_at, kl_at, clipped_at, delta_at, ws_at,
+                                ws_bytes, ty.stream_of(dev))
+    _check(st, "dust_policy_loss")
+    return (loss, total, kl, clipped) if delta is None else (loss, total, kl, clipped, delta)
+
+
+@_in_stream
+def dust_policy_loss_grad(nll, old, advantages, seq_offsets, gtotal, ref=None, targets=None,
+                          clip_low=0.2, clip_high=0.2, beta=0.0, mean=MEAN_TOKEN, per_token=None,
+                          gnll=None, workspace=None):
+    """The gradient of dust_policy_loss's total for gtotal (f32, nll's leading
+    shape): gnll of nll's shape, which dust_head_loss_grad takes as gloss."""
+    ty, dev, S, T, n_seq, operands = _policy_inputs(
+        nll, old, advantages, seq_offsets, ref, targets, clip_low, clip_high, beta, mean, per_token)
+    gnll, gnll_at = _output(gnll, "gnll", ty.f32, nll.shape, nll, dev)
+    workspace, ws_at, ws_bytes = _space(workspace, "dust_policy_loss_workspace", nll, dev, S, T,
+                                        n_seq)
+    st = lib().dust_policy_loss_grad(*operands,
+                                     _dense(gtotal, "gtotal", ty.f32, nll.shape[:-1], dev),
+                                     gnll_at, ws_at, ws_bytes, ty.stream_of(dev))
+    _check(st, "dust_policy_loss_grad")
+    return gnll
+
+
+class _On:
+    """What _output and _space ask of a tensor: where it is."""
+    def __init__(self, dev):
+        self.device = "cuda:%d" % dev
+
+
+class _Grad(C.Structure):
+    """dust_grad of include/dust.h."""
+    _fields_ = [("g", C.c_void_p), ("out", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32)]
+
+
+@_in_stream
+def dust_clip_grads(grads, max_norm, out=None, norm=None, workspace=None):
+    """grads: a list of contiguous CUDA tensors (f32 or bf16 each), scaled by
+    min(1, max_norm / norm) with the norm over all of them: in place, or into
+    the tensors `out`. Returns (norm f32 [1], the scaled tensors)."""
+    ty = _types()
+    dev = ty.current_device()
+    grads = list(grads)
+    out = grads if out is None else list(out)
+    if len(out) != len(grads):
+        raise ValueError("out must have as many tensors as grads")
+    arr = (_Grad * max(1, len(grads)))()
+    for a, g, o in zip(arr, grads, out):
+        code = ty.code.get(g.dtype)
+        if code is None or not g.is_contiguous() or g.get_device() != dev:
+            _values(g, "a gradient", range(65))
+            raise ValueError("expected a contiguous tensor")
+        a.g, a.n, a.dtype = g.data_ptr(), g.numel(), code
+        a.out = a.g if o is g else _dense(o, "out", g.dtype, g.shape, dev)
+    ref = _On(dev)
+    norm, norm_at = _output(norm, "norm", ty.f32, (1,), ref, dev)
+    workspace, ws_at, ws_bytes = _space(workspace, "dust_clip_grads_workspace", ref, dev, len(grads))
+    st = lib().dust_clip_grads(C.addressof(arr), len(grads), max_norm, norm_at, ws_at, ws_bytes,
+                               ty.stream_of(dev))
+    _check(st, "dust_clip_grads")
+    return norm, out
 
 
 PIPE_XU, PIPE_ALU, PIPE_FMA, PIPE_ISSUE = 0, 1, 2, 3

@@ -31,7 +31,8 @@ cudaError_t ensure_shared_carveout(const void* kernel);
 enum Stage {
     kStageScanLocal, kStageScanCarry, kStageScanFixup, kStageWeight, kStageGemmSimt,
     kStageReduce, kStageGemmTc, kStageFused, kStageNoise, kStageJitter, kStageZero, kStageScore,
-    kStageScatter, kStageForward, kStageNorm, kStageHead, kStageCount
+    kStageScatter, kStageForward, kStageNorm, kStageHead, kStageGated, kStageRope, kStagePolicy,
+    kStageClip, kStageCount
 };
 
 // Brackets the launches issued during its lifetime with profiling events

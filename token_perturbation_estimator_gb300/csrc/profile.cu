@@ -17,7 +17,8 @@ const char* const kStageNames[kStageCount] = {"scan_local", "scan_carry", "scan_
                                               "gemm_simt",  "reduce",     "gemm_tc",    "fused",
                                               "noise",      "jitter",     "zero",
                                               "score",      "scatter",    "forward",
-                                              "norm",       "head"};
+                                              "norm",       "head",       "gated",
+                                              "rope",       "policy",     "clip"};
 constexpr int kMaxRecords = 65536;
 
 struct Rec {
