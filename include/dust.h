@@ -689,8 +689,9 @@ dust_status dust_distill_loss_grad(const void* H, int64_t ld_h, const void* E, i
  * are rounded to bf16 (they are tensor-core operands). fp32 inputs: every
  * product and sum to fp32 accuracy (operands to 24 bits, or to 2^-133 where
  * that is more).
- * d >= 1, f >= 1, T >= 0; T, d and f up to 2^31 - 2^16, T*d, T*f and f*d up to
- * 2^39, and at most 2^30 tiles of 256 rows x 64 columns (DUST_ERR_RANGE).
+ * d >= 1, f >= 1, T >= 0; T and d up to 2^31 - 2^16, f up to 2^30 - 2^16; with
+ * all of them rounded up to multiples of 256, T*d, T*f and f*d up to 2^37, and
+ * at most 2^30 tiles of 256 rows x 64 columns (DUST_ERR_RANGE).
  * T = 0 writes zeros to gWg and gWu (or leaves them, accumulating) and nothing
  * else.
  */
@@ -935,8 +936,8 @@ int32_t dust_pipe_probe_threads(void);
 /*
  * dust_debug_inject_timeout — test hook for the device-side failure path (no
  * counterpart on the pages). With on != 0, the next tensor-core contraction
- * launched by this process (dust_contract, the unfused dust_estimate_gW path,
- * or a product of the head's losses and gradients) makes its MMA thread wait
+ * launched by this process (dust_contract, the unfused dust_estimate_gW path, a
+ * product of the head's losses and gradients or of the gated block) makes its MMA thread wait
  * on an mbarrier that no thread ever arrives at. The wait gives up after its 1 s limit, the kernel lets its issued TMA
  * copies land, frees its tensor memory and returns without writing gW, and
  * dust_last_error then reports DUST_ERR_TIMEOUT; the CUDA context stays

@@ -1,147 +1,138 @@
 // The gated feed-forward block's first half, h = act(X Wg^T) (X Wu^T), and its
-// gradients (include/dust.h gives the formulas): tiles of 64 x 64 on the CUDA
-// cores, fp32 sums.
+// gradients (include/dust.h gives the formulas): what is copied first, and the
+// order of the launches. The products are k_gated_tc.cu's; a few rows go to
+// k_gated_few.cu.
+//
+// Backward: g and u once more, as D = [dG dU] in bf16, then gX = D [Wg; Wu] and
+// [gWg; gWu] = D^T X in one launch.
+//
+// fp32 operands, and bf16 ones whose rows do not start on 16 bytes, are first
+// copied into the workspace, as three bf16 planes or padded rows; gh as padded
+// rows of its own type.
 #include <algorithm>
 
-#include "step.cuh"
+#include "gated.cuh"
 
 namespace dust {
 
 namespace {
 
-constexpr int kThreads = 256, kTile = 64, kDeep = 16;
+size_t a256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+int64_t up(int64_t x, int64_t by) { return (x + by - 1) / by * by; }
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void from_f(float v, float& o) { o = v; }
-__device__ __forceinline__ void from_f(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
 
-// act(g) and its slope.
-__device__ __forceinline__ float2 act_of(int act, float g) {
-    if (act == DUST_ACT_RELU2) {
-        const float r = g > 0.0f ? g : g == g ? 0.0f : g;
-        return make_float2(r * r, 2.0f * r);
-    }
-    constexpr float kB = 0.044715f, kC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-    const float z = act == DUST_ACT_SILU ? g : kC * fmaf(kB * g * g, g, g);
-    const float p = 1.0f / (1.0f + expf(-z));
-    const float q = 1.0f / (1.0f + expf(z));  // 1 - p
-    // Where p q is 0 the slope of z may be infinite.
-    const float slope = act == DUST_ACT_SILU ? 1.0f : kC * fmaf(3.0f * kB * g, g, 1.0f);
-    const float pq = p * q;
-    return make_float2(g * p, pq == 0.0f ? p : fmaf(g * pq, slope, p));
-}
-
-// acc[a][b] += sum over k < depth of A(row0 + 4 ty + a, k) B(col0 + 4 tx + b, k).
-template <typename FA, typename FB>
-__device__ __forceinline__ void tile_product(FA A, FB B, int64_t depth, float (&acc)[4][4]) {
-    __shared__ float sa[kDeep][kTile + 4], sb[kDeep][kTile + 4];
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    for (int64_t k0 = 0; k0 < depth; k0 += kDeep) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < kTile * kDeep; i += kThreads) {
-            const int k = i % kDeep, r = i / kDeep;
-            sa[k][r] = k0 + k < depth ? A(r, k0 + k) : 0.0f;
-            sb[k][r] = k0 + k < depth ? B(r, k0 + k) : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kDeep; ++k)
-#pragma unroll
-            for (int a = 0; a < 4; ++a)
-#pragma unroll
-                for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(sa[k][4 * ty + a], sb[k][4 * tx + b], acc[a][b]);
-    }
-}
-
-struct Args {
-    GatedProblem p;
-    const void* gh;
-    int64_t ld_gh;
-    void* h;
-    int64_t ld_h;
-    void* D;              // [T][2 f]
-    void *gX, *gWg, *gWu;
-    int64_t ld_gx;
-    bool accumulate;
-    int64_t cols;         // tiles of columns
+// Rows that are copied: into bf16 planes (1 or 3), or as they are.
+struct CopyJob {
+    const void* src;
+    int64_t ld, n, d, dp;  // n rows of d values, dp apart in the copy, zero from d on
+    int vec;               // rows can be read 16 bytes at a time
+    void* dst;
+    int planes;            // 0: as they are
+    unsigned blocks;       // CTAs that work on it
+};
+struct CopyJobs {
+    CopyJob job[4];
 };
 
-template <typename TX, bool BACK>
-__global__ void __launch_bounds__(kThreads) k_gated_up(const Args a) {
-    pdl_wait();
-    pdl_trigger();
-    const GatedProblem& p = a.p;
-    const int64_t r0 = blockIdx.x / a.cols * kTile, c0 = blockIdx.x % a.cols * kTile;
-    const auto at = [&](const void* m, int64_t ld, int64_t rows, int64_t first) {
-        return [=](int r, int64_t k) {
-            return first + r < rows ? to_f(static_cast<const TX*>(m)[(first + r) * ld + k]) : 0.0f;
-        };
-    };
-    float g[4][4] = {}, u[4][4] = {};
-    tile_product(at(p.X, p.ld_x, p.T, r0), at(p.Wg, p.ld_wg, p.f, c0), p.d, g);
-    tile_product(at(p.X, p.ld_x, p.T, r0), at(p.Wu, p.ld_wu, p.f, c0), p.d, u);
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = r0 + threadIdx.x / 16 * 4 + i, c = c0 + threadIdx.x % 16 * 4 + j;
-            if (r >= p.T || c >= p.f) continue;
-            const float2 act = act_of(p.act, g[i][j]);
-            if constexpr (BACK) {
-                const float gh = to_f(static_cast<const TX*>(a.gh)[r * a.ld_gh + c]);
-                TX* D = static_cast<TX*>(a.D) + r * 2 * p.f + c;
-                from_f(gh * u[i][j] * act.y, D[0]);
-                from_f(gh * act.x, D[p.f]);
+template <typename TX>
+__device__ void copy_rows(const CopyJob& a, int64_t block) {
+    constexpr int kPer = 16 / static_cast<int>(sizeof(TX));
+    const int lane = threadIdx.x & 31;
+    for (int64_t i = block * 8 + (threadIdx.x >> 5); i < a.n; i += static_cast<int64_t>(a.blocks) * 8) {
+        const TX* s = static_cast<const TX*>(a.src) + i * a.ld;
+        for (int64_t c = lane * 8; c < a.dp; c += 256) {
+            alignas(16) TX x[8];
+            if (a.vec && c + 8 <= a.d) {
+#pragma unroll
+                for (int u = 0; u < 8 / kPer; ++u)
+                    reinterpret_cast<uint4*>(x)[u] = reinterpret_cast<const uint4*>(s + c)[u];
             } else {
-                from_f(act.x * u[i][j], static_cast<TX*>(a.h)[r * a.ld_h + c]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = c + k < a.d ? s[c + k] : TX(0.0f);
+            }
+            if (a.planes == 0) {
+                TX* o = static_cast<TX*>(a.dst) + i * a.dp + c;
+#pragma unroll
+                for (int u = 0; u < 8 / kPer; ++u)
+                    reinterpret_cast<uint4*>(o)[u] = reinterpret_cast<const uint4*>(x)[u];
+                continue;
+            }
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = to_f(x[k]);
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.dst) + i * a.dp + c;
+            for (int p = 0; p < a.planes; ++p) {
+                alignas(16) __nv_bfloat16 b[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    b[k] = __float2bfloat16_rn(v[k]);
+                    // Not up to infinity; and of an infinity nothing is left.
+                    if (__hisinf(b[k])) b[k] = __float2bfloat16_rz(v[k]);
+                    v[k] = __hisinf(b[k]) ? 0.0f : v[k] - __bfloat162float(b[k]);
+                }
+                *reinterpret_cast<uint4*>(o + p * a.n * a.dp) = *reinterpret_cast<const uint4*>(b);
             }
         }
+    }
 }
 
 template <typename TX>
-__global__ void __launch_bounds__(kThreads) k_gated_gx(const Args a) {
+__global__ void __launch_bounds__(256) k_gated_copy(const CopyJobs a) {
     pdl_wait();
     pdl_trigger();
-    const GatedProblem& p = a.p;
-    const int64_t r0 = blockIdx.x / a.cols * kTile, c0 = blockIdx.x % a.cols * kTile;
-    float acc[4][4] = {};
-    tile_product([&](int r, int64_t k) {
-        return r0 + r < p.T ? to_f(static_cast<const TX*>(a.D)[(r0 + r) * 2 * p.f + k]) : 0.0f;
-    }, [&](int c, int64_t k) {
-        if (c0 + c >= p.d) return 0.0f;
-        return k < p.f ? to_f(static_cast<const TX*>(p.Wg)[k * p.ld_wg + c0 + c])
-                       : to_f(static_cast<const TX*>(p.Wu)[(k - p.f) * p.ld_wu + c0 + c]);
-    }, 2 * p.f, acc);
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = r0 + threadIdx.x / 16 * 4 + i, c = c0 + threadIdx.x % 16 * 4 + j;
-            if (r < p.T && c < p.d) from_f(acc[i][j], static_cast<TX*>(a.gX)[r * a.ld_gx + c]);
+    unsigned block = blockIdx.x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (block < a.job[j].blocks) {
+            copy_rows<TX>(a.job[j], block);
+            return;
         }
+        block -= a.job[j].blocks;
+    }
 }
 
-template <typename TX, typename TW>
-__global__ void __launch_bounds__(kThreads) k_gated_gw(const Args a) {
-    pdl_wait();
-    pdl_trigger();
-    const GatedProblem& p = a.p;
-    const int64_t r0 = blockIdx.x / a.cols * kTile, c0 = blockIdx.x % a.cols * kTile;
-    float acc[4][4] = {};
-    tile_product([&](int r, int64_t k) {
-        return r0 + r < 2 * p.f ? to_f(static_cast<const TX*>(a.D)[k * 2 * p.f + r0 + r]) : 0.0f;
-    }, [&](int c, int64_t k) {
-        return c0 + c < p.d ? to_f(static_cast<const TX*>(p.X)[k * p.ld_x + c0 + c]) : 0.0f;
-    }, p.T, acc);
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = r0 + threadIdx.x / 16 * 4 + i, c = c0 + threadIdx.x % 16 * 4 + j;
-            if (r >= 2 * p.f || c >= p.d) continue;
-            TW* out = static_cast<TW*>(r < p.f ? a.gWg : a.gWu);
-            if (!out) continue;
-            out += (r < p.f ? r : r - p.f) * p.d + c;
-            from_f(a.accumulate ? to_f(*out) + acc[i][j] : acc[i][j], *out);
-        }
-}
+struct Carver {
+    unsigned char* base;
+    size_t at = 0;
+    template <typename T> T* take(int64_t n) {
+        T* p = base ? reinterpret_cast<T*>(base + at) : nullptr;
+        at += a256(sizeof(T) * static_cast<size_t>(n));
+        return p;
+    }
+};
 
-int64_t tiles(int64_t n) { return (n + kTile - 1) / kTile; }
+// Operands are sized as if copied, wherever they lie: the size must not
+// depend on addresses. Only what a call needs is touched.
+struct Space {
+    __nv_bfloat16 *x, *g, *u, *D;
+    unsigned char* gh;
+    float *gx_acc, *gw_acc;
+    GatedCuts cuts;
+    size_t total;
+};
+
+Space carve(void* ws, const GatedProblem& p, bool grad) {
+    const int64_t dp = up(p.d, 8), planes = p.bf16 ? 1 : 3;
+    Carver c{static_cast<unsigned char*>(ws)};
+    Space w = {};
+    if (!grad && p.T <= kGatedFew) return w;
+    w.x = c.take<__nv_bfloat16>(planes * p.T * dp);
+    w.g = c.take<__nv_bfloat16>(planes * p.f * dp);
+    w.u = c.take<__nv_bfloat16>(planes * p.f * dp);
+    if (grad) {
+        const int n = static_cast<int>(planes);
+        w.gh = c.take<unsigned char>(p.T * up(p.f, 8) * (p.bf16 ? 2 : 4));
+        w.D = c.take<__nv_bfloat16>(planes * up(p.T, kHeadTile) * 2 * gated_half(p.f));
+        // As for all gradients, whichever are asked for.
+        w.cuts = gated_cuts(p.T, p.d, p.f, n);
+        w.gx_acc = c.take<float>(w.cuts.x > 1 ? gated_acc_floats(p.T, p.d, n, w.cuts.x) : 0);
+        w.gw_acc = c.take<float>(w.cuts.w > 1 ? 2 * gated_acc_floats(p.f, p.d, n, w.cuts.w) : 0);
+    }
+    w.total = c.at;
+    return w;
+}
 
 #define DUST_TRY(x)                             \
     do {                                        \
@@ -149,56 +140,84 @@ int64_t tiles(int64_t n) { return (n + kTile - 1) / kTile; }
         if (e_ != cudaSuccess) return e_;       \
     } while (0)
 
-template <typename TX>
-cudaError_t grad_typed(Args a, bool gW_bf16, cudaStream_t s) {
-    const GatedProblem& p = a.p;
-    a.cols = tiles(p.f);
-    DUST_TRY(launch_pdl(k_gated_up<TX, true>, dim3(static_cast<unsigned>(tiles(p.T) * a.cols)),
-                        dim3(kThreads), 0, s, a));
-    a.cols = tiles(p.d);
-    if (a.gX)
-        DUST_TRY(launch_pdl(k_gated_gx<TX>, dim3(static_cast<unsigned>(tiles(p.T) * a.cols)),
-                            dim3(kThreads), 0, s, a));
-    if (!a.gWg && !a.gWu) return cudaSuccess;
-    const dim3 grid(static_cast<unsigned>(tiles(2 * p.f) * a.cols));
-    return gW_bf16 ? launch_pdl(k_gated_gw<TX, __nv_bfloat16>, grid, dim3(kThreads), 0, s, a)
-                   : launch_pdl(k_gated_gw<TX, float>, grid, dim3(kThreads), 0, s, a);
+CopyJob copy_job(const void* src, int64_t ld, int64_t n, int64_t d, bool bf16, void* dst, int planes) {
+    const int64_t size = bf16 ? 2 : 4;
+    return {src, ld, n, d, up(d, 8),
+            (ld * size) % 16 == 0 && reinterpret_cast<uintptr_t>(src) % 16 == 0, dst, planes,
+            static_cast<unsigned>(std::min<int64_t>((n + 7) / 8, 152 * 8))};
+}
+
+// Rows that start on 16 bytes, no further apart than TMA allows.
+bool direct(const void* p, int64_t ld, int64_t per) {
+    return ld % per == 0 && ld < (int64_t(1) << 36) && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+}
+
+// The matrix as an operand: where it lies, or the copy that *job is to make.
+Planes operand(const void* src, int64_t ld, int64_t n, int64_t d, bool bf16, __nv_bfloat16* copy,
+               CopyJob* job) {
+    if (bf16 && direct(src, ld, 8)) return {src, n, d, ld, 1};
+    const int planes = bf16 ? 1 : 3;
+    *job = copy_job(src, ld, n, d, bf16, copy, planes);
+    return {copy, n, up(d, 8), up(d, 8), planes};
+}
+
+cudaError_t copy(const CopyJobs& jobs, bool bf16, cudaStream_t s) {
+    unsigned blocks = 0;
+    for (const CopyJob& j : jobs.job) blocks += j.blocks;
+    if (blocks == 0) return cudaSuccess;
+    return bf16 ? launch_pdl(k_gated_copy<__nv_bfloat16>, dim3(blocks), dim3(256), 0, s, jobs)
+                : launch_pdl(k_gated_copy<float>, dim3(blocks), dim3(256), 0, s, jobs);
+}
+
+// The operands of g and u, and the copies they need.
+GatedTiles tiles_for(const GatedProblem& p, const Space& w, CopyJobs* jobs) {
+    GatedTiles t = {};
+    t.X = operand(p.X, p.ld_x, p.T, p.d, p.bf16, w.x, &jobs->job[0]);
+    t.Wg = operand(p.Wg, p.ld_wg, p.f, p.d, p.bf16, w.g, &jobs->job[1]);
+    t.Wu = operand(p.Wu, p.ld_wu, p.f, p.d, p.bf16, w.u, &jobs->job[2]);
+    t.T = p.T;
+    t.d = p.d;
+    t.f = p.f;
+    t.act = p.act;
+    return t;
 }
 
 }  // namespace
 
-size_t gated_workspace_bytes(const GatedProblem&) { return 0; }
-size_t gated_grad_workspace_bytes(const GatedProblem& p) {
-    return static_cast<size_t>(p.T * p.f) * 2 * (p.bf16 ? 2 : 4);
-}
+size_t gated_workspace_bytes(const GatedProblem& p) { return carve(nullptr, p, false).total; }
+size_t gated_grad_workspace_bytes(const GatedProblem& p) { return carve(nullptr, p, true).total; }
 
-cudaError_t launch_gated(const GatedProblem& p, void* h, int64_t ld_h, void*, cudaStream_t s) {
+cudaError_t launch_gated(const GatedProblem& p, void* h, int64_t ld_h, void* ws, cudaStream_t s) {
     ProfScope ps(kStageGated, s);
-    Args a = {};
-    a.p = p;
-    a.h = h;
-    a.ld_h = ld_h;
-    a.cols = tiles(p.f);
-    const dim3 grid(static_cast<unsigned>(tiles(p.T) * a.cols));
-    return p.bf16 ? launch_pdl(k_gated_up<__nv_bfloat16, false>, grid, dim3(kThreads), 0, s, a)
-                  : launch_pdl(k_gated_up<float, false>, grid, dim3(kThreads), 0, s, a);
+    if (p.T <= kGatedFew) return launch_gated_few(p, h, ld_h, s);
+    const Space w = carve(ws, p, false);
+    CopyJobs jobs = {};
+    GatedTiles t = tiles_for(p, w, &jobs);
+    DUST_TRY(copy(jobs, p.bf16, s));
+    t.h = h;
+    t.ld_h = ld_h;
+    return launch_gated_tiles(t, s);
 }
 
 cudaError_t launch_gated_grad(const GatedProblem& p, const void* gh, int64_t ld_gh, bool accumulate,
                               void* gX, int64_t ld_gx, void* gWg, void* gWu, bool gW_bf16, void* ws,
                               cudaStream_t s) {
     ProfScope ps(kStageGated, s);
-    Args a = {};
-    a.p = p;
-    a.gh = gh;
-    a.ld_gh = ld_gh;
-    a.D = ws;
-    a.gX = gX;
-    a.gWg = gWg;
-    a.gWu = gWu;
-    a.ld_gx = ld_gx;
-    a.accumulate = accumulate;
-    return p.bf16 ? grad_typed<__nv_bfloat16>(a, gW_bf16, s) : grad_typed<float>(a, false, s);
+    const Space w = carve(ws, p, true);
+    CopyJobs jobs = {};
+    GatedTiles t = tiles_for(p, w, &jobs);
+    t.gh = gh;
+    t.ld_gh = ld_gh;
+    if (!direct(gh, ld_gh, p.bf16 ? 8 : 4)) {
+        jobs.job[3] = copy_job(gh, ld_gh, p.T, p.f, p.bf16, w.gh, 0);
+        t.gh = w.gh;
+        t.ld_gh = up(p.f, 8);
+    }
+    t.D = {w.D, up(p.T, kHeadTile), 2 * gated_half(p.f), 2 * gated_half(p.f), p.bf16 ? 1 : 3};
+    DUST_TRY(copy(jobs, p.bf16, s));
+    DUST_TRY(launch_gated_tiles(t, s));
+    return launch_gated_products({t.X, t.Wg, t.Wu, t.D, p.T, p.d, p.f, gX, ld_gx, gWg, gWu, p.bf16,
+                                  gW_bf16, accumulate, w.cuts, w.gx_acc, w.gw_acc}, s);
 }
 
 }  // namespace dust

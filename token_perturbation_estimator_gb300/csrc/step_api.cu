@@ -12,9 +12,12 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
-// Of the block's rows, columns and units: padded to whole tiles they fit 32 bits.
+// Of the block's rows, columns and units: padded to whole tiles they fit 32
+// bits, the units twice over; a plane of a matrix, padded, stays within 2^40
+// bytes (TMA's limit).
 constexpr int64_t kMaxGatedDim = (int64_t(1) << 31) - (int64_t(1) << 16);
-constexpr int64_t kMaxGatedElems = int64_t(1) << 39;
+constexpr int64_t kMaxGatedUnits = (int64_t(1) << 30) - (int64_t(1) << 16);
+constexpr int64_t kMaxGatedElems = int64_t(1) << 37;
 constexpr int64_t kMaxGatedTiles = int64_t(1) << 30;  // of 256 rows x 64 columns, in a launch
 
 size_t a256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -37,8 +40,10 @@ bool ws_ok(const void* ws, size_t have, size_t need) {
 
 dust_status check_gated_sizes(int64_t T, int64_t d, int64_t f, dust_dtype dtype) {
     if (T < 0 || d < 1 || f < 1 || !value_dtype(dtype)) return DUST_ERR_INVALID_ARG;
-    if (T > kMaxGatedDim || d > kMaxGatedDim || f > kMaxGatedDim) return DUST_ERR_RANGE;
-    if (T > kMaxGatedElems / d || T > kMaxGatedElems / f || f > kMaxGatedElems / d) return DUST_ERR_RANGE;
+    if (T > kMaxGatedDim || d > kMaxGatedDim || f > kMaxGatedUnits) return DUST_ERR_RANGE;
+    const auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+    if (up(T) > kMaxGatedElems / up(f) || up(T) > kMaxGatedElems / up(d) || up(f) > kMaxGatedElems / up(d))
+        return DUST_ERR_RANGE;
     const auto tiles = [](int64_t rows, int64_t cols) { return (rows + 255) / 256 * ((cols + 63) / 64); };
     if (std::max({tiles(T, f), tiles(T, d), tiles(2 * f, d)}) > kMaxGatedTiles) return DUST_ERR_RANGE;
     return DUST_OK;
