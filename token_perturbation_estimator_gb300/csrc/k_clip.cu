@@ -1,9 +1,10 @@
 // The norm over all gradients of a step, and the gradients scaled to it:
 //     norm = sqrt(sum g^2),  out = g min(1, max_norm / norm)
 //
-// Two passes, each over chunks of kChunk values dealt round robin: the first
+// Two passes over chunks of kChunk values, each CTA's one after another: the first
 // leaves one sum per CTA, the second adds those up in every CTA (in one order,
-// so that all have the same factor) and scales. Squares are summed 16 at a
+// so that all have the same factor) and scales, each CTA its chunks in reverse:
+// what was read last is still in the L2. Squares are summed 16 at a
 // time in fp32, those sums in 64 bits.
 //
 // Bound by memory: g is read twice and out written once.
@@ -19,7 +20,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kGroup = 16;                  // squares summed in fp32
 constexpr int kChunk = kThreads * kGroup * 2;
-constexpr int kMaxParts = 152 * 8;          // CTAs of a launch
+constexpr int kCtas = 4;                    // per SM
+constexpr int kMaxParts = 152 * kCtas;      // CTAs of a launch
 constexpr int64_t kBatch = 512;             // tensors of a launch
 
 // The tensors of a launch (in the kernel's parameters) and their chunks,
@@ -169,25 +171,42 @@ __device__ __forceinline__ double cta_sum(double v) {
     return v;
 }
 
+// A CTA's chunks, and the tensor that one of them lies in.
 template <int N>
-__global__ void __launch_bounds__(kThreads)
+struct Walk {
+    const Batch<N>& b;
+    int64_t from, to;
+    int t;
+
+    __device__ explicit Walk(const Batch<N>& batch) : b(batch) {
+        from = b.chunks * blockIdx.x / gridDim.x;
+        to = b.chunks * (blockIdx.x + 1) / gridDim.x;
+    }
+    __device__ __forceinline__ int count(int64_t chunk) const {
+        return static_cast<int>(min(b.n[t] - (chunk - b.first[t]) * kChunk, static_cast<int64_t>(kChunk)));
+    }
+    __device__ __forceinline__ int64_t start(int64_t chunk) const { return (chunk - b.first[t]) * kChunk; }
+};
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, kCtas)
     k_clip_sum(const __grid_constant__ Batch<N> b, double* __restrict__ parts) {
     pdl_wait();
     pdl_trigger();
     double s = 0.0;
-    for (int64_t c = blockIdx.x; c < b.chunks; c += gridDim.x) {
-        const int t = b.tensor_of(c);
-        const int64_t from = (c - b.first[t]) * kChunk;
-        const int n = static_cast<int>(min(b.n[t] - from, static_cast<int64_t>(kChunk)));
-        s += b.bf16[t] ? chunk_squares<__nv_bfloat16>(b.g[t], from, n)
-                       : chunk_squares<float>(b.g[t], from, n);
+    Walk<N> w(b);
+    if (w.from < w.to) w.t = b.tensor_of(w.from);
+    for (int64_t c = w.from; c < w.to; ++c) {
+        while (c >= b.first[w.t + 1]) ++w.t;
+        s += b.bf16[w.t] ? chunk_squares<__nv_bfloat16>(b.g[w.t], w.start(c), w.count(c))
+                         : chunk_squares<float>(b.g[w.t], w.start(c), w.count(c));
     }
     s = cta_sum(s);
     if (threadIdx.x == 0) parts[blockIdx.x] = s;
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas)
     k_clip_scale(const __grid_constant__ Batch<N> b, const double* __restrict__ parts, int n_parts,
                  double max_norm, float* norm) {
     pdl_wait();
@@ -196,15 +215,14 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = threadIdx.x; i < n_parts; i += kThreads) s += parts[i];
     const double length = sqrt(cta_sum(s));
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(length);
-    const float c = length <= max_norm ? 1.0f : static_cast<float>(max_norm / length);
-    for (int64_t i = blockIdx.x; i < b.chunks; i += gridDim.x) {
-        const int64_t k = b.chunks - 1 - i;  // what was read last may still be in the L2
-        const int t = b.tensor_of(k);
-        if (!b.out[t] || (c == 1.0f && b.out[t] == b.g[t])) continue;
-        const int64_t from = (k - b.first[t]) * kChunk;
-        const int n = static_cast<int>(min(b.n[t] - from, static_cast<int64_t>(kChunk)));
-        if (b.bf16[t]) chunk_scale<__nv_bfloat16>(b.g[t], b.out[t], from, n, c);
-        else chunk_scale<float>(b.g[t], b.out[t], from, n, c);
+    const float f = length <= max_norm ? 1.0f : static_cast<float>(max_norm / length);
+    Walk<N> w(b);
+    if (w.from < w.to) w.t = b.tensor_of(w.to - 1);
+    for (int64_t c = w.to - 1; c >= w.from; --c) {
+        while (c < b.first[w.t]) --w.t;
+        if (!b.out[w.t] || (f == 1.0f && b.out[w.t] == b.g[w.t])) continue;
+        if (b.bf16[w.t]) chunk_scale<__nv_bfloat16>(b.g[w.t], b.out[w.t], w.start(c), w.count(c), f);
+        else chunk_scale<float>(b.g[w.t], b.out[w.t], w.start(c), w.count(c), f);
     }
 }
 

@@ -47,6 +47,7 @@ struct PolicyProblem {
     const int32_t *offsets, *targets;
     int64_t n_seq, S, T;
     double low, high;          // bounds of old - nll
+    float low32, high32;       // the same, rounded
     float clip_low, clip_high, beta;
     bool by_sequence;
 };

@@ -171,9 +171,11 @@ PolicyProblem policy_problem(const float* nll, const float* old, const float* re
                              const float* advantages, int32_t per_token, const int32_t* seq_offsets,
                              int64_t n_seq, const int32_t* targets, int64_t S, int64_t T,
                              float clip_low, float clip_high, float beta, dust_mean mean) {
-    return {nll, old, ref, advantages, per_token != 0, seq_offsets, targets, n_seq, S, T,
-            std::log1p(-static_cast<double>(clip_low)), std::log1p(static_cast<double>(clip_high)),
-            clip_low, clip_high, beta, mean == DUST_MEAN_SEQUENCE};
+    const double low = std::log1p(-static_cast<double>(clip_low));
+    const double high = std::log1p(static_cast<double>(clip_high));
+    return {nll, old, ref, advantages, per_token != 0, seq_offsets, targets, n_seq, S, T, low, high,
+            static_cast<float>(low), static_cast<float>(high), clip_low, clip_high, beta,
+            mean == DUST_MEAN_SEQUENCE};
 }
 
 // ------------------------------------------------------------------- clip
