@@ -192,6 +192,26 @@ def test_strides_and_alignment(room, dtype):
     assert (big[..., D:] == 9.0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hk,D", [(0, 3, 64), (0, 1, 32), (5, 0, 64), (0, 2, 30), (13, 7, 16)])
+def test_one_side_alone_and_odd_numbers_of_heads(hq, hk, D, dtype):
+    import torch
+    dev = cuda()
+    T = 70
+    q, k, wq, wk, pos, c, s, gyq, gyk = _inputs(T, max(hq, 1), max(hk, 1), D, D, dtype, dev)
+    q, gyq, k, gyk = q[:, :hq], gyq[:, :hq], k[:, :hk], gyk[:, :hk]
+    yq, yk = dust.dust_qk_norm_rope(q, k, wq, wk, pos, c, s)
+    gq, gk, gwq, gwk = dust.dust_qk_norm_rope_grad(gyq, gyk, q, k, wq, wk, pos, c, s)
+    for y, gx, gw, gy, x, w in ((yq, gq, gwq, gyq, q, wq), (yk, gk, gwk, gyk, k, wk)):
+        if x.numel() == 0:
+            assert y.numel() == 0 and (gw == 0).all()
+            continue
+        check(y, *reference(x, w, pos, c, s, D, "halves", 1e-6), D, dtype)
+        want, size, gw64, gw_size = reference(x, w, pos, c, s, D, "halves", 1e-6, gy)
+        check(gx, want, size, 2 * D, dtype)
+        assert (np.abs(_np(gw) - gw64) <= 4e-6 * gw_size + 1e-37).all()
+
+
 def test_padded_tokens_hide_what_they_hold():
     import torch
     dev = cuda()

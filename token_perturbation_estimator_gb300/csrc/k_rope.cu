@@ -8,16 +8,19 @@
 // values that are not turned), so that the rotation needs no exchange between
 // lanes. A warp keeps the same 32 / G heads, queries before keys, and goes from
 // token to token: weights and addresses then stay in registers, and the next
-// token's values are on their way meanwhile. (A warp that went from head to
-// head of a token took 280 instructions a head for the addresses, weights and
-// the queries' and keys' cases, and at 65536 tokens of 8 and 8 heads of 64
-// 80 us, a third of HBM's rate.)
+// tokens' values are on their way meanwhile.
+//
+// Heads whose vectors are 16 bytes go through k_rope_fast, with the next kRing
+// tokens' values in shared memory (cp.async, each thread's own) and two values
+// an instruction; other sizes and alignments through k_rope, value by value or
+// in smaller vectors.
 //
 // The backward keeps each lane's sums of gm n for its own columns in registers
 // over all the tokens of the warp; a CTA's warps leave one partial row, and
 // k_rope_finish adds those up in order.
 #include <algorithm>
 
+#include "f32x2.cuh"
 #include "step.cuh"
 
 namespace dust {
@@ -26,6 +29,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kRing = 3;              // tokens on their way per warp
 constexpr int kForwardCtas = 3, kBackwardCtas = 2;  // per SM
 constexpr int kMaxCtas = 152 * kBackwardCtas;       // of the backward: partial rows
 
@@ -254,11 +258,22 @@ struct Walk {
         if (t >= step) t = g.T;  // the last warps, fewer than there are chunks
         head = warp % chunks * kGroups + threadIdx.x % 32 / G;
         in = head < g.heads;
-        key = in && head >= g.hq;
+        if (!in) head = 0;  // stands at a head that there is
+        key = head >= g.hq;
         if (key) head -= g.hq;
-        if (!in) head = 0;
     }
 };
+
+// The warps' sums of gm n, [kWarps][2][D], as the CTA's partial row.
+__device__ __forceinline__ void join_rows(const Args& g, const float* rows, float* parts) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * g.D; i += kThreads) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) s += rows[k * 2 * g.D + i];
+        parts[static_cast<int64_t>(blockIdx.x) * 2 * g.D + i] = s;
+    }
+}
 
 template <typename TX, int V, int G, int PER, bool HALVES>
 __global__ void __launch_bounds__(kThreads, kForwardCtas) k_rope(const Args g) {
@@ -391,13 +406,322 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas)
         }
         __syncwarp();
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * g.D; i += kThreads) {
-        float s = 0.0f;
+    join_rows(g, rows, parts);
+}
+
+// ---- vectors of 16 bytes
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_begun() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_landed() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 16 bytes as numbers, in twos, and back.
+template <typename TX, int N>
+__device__ __forceinline__ void unpack(const uint4& q, float2 (&v)[N]) {
+    const uint32_t r[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) s += rows[k * 2 * g.D + i];
-        parts[static_cast<int64_t>(blockIdx.x) * 2 * g.D + i] = s;
+    for (int i = 0; i < N; ++i)
+        v[i] = sizeof(TX) == 2
+                   ? make_float2(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xffff0000u))
+                   : make_float2(__uint_as_float(r[(2 * i) % 4]), __uint_as_float(r[(2 * i + 1) % 4]));
+}
+template <typename TX, int N>
+__device__ __forceinline__ uint4 pack(const float2 (&v)[N]) {
+    if constexpr (sizeof(TX) == 2) {
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[i].x, v[i].y);
+            r[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(r[0], r[1], r[2], r[3]);
+    } else {
+        return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
+                          __float_as_uint(v[1].y));
     }
+}
+
+template <int N>
+__device__ __forceinline__ void load_twos(const float* p, float2 (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float4 q = reinterpret_cast<const float4*>(p)[i];
+        v[2 * i] = make_float2(q.x, q.y);
+        v[2 * i + 1] = make_float2(q.z, q.w);
+    }
+}
+
+// A lane's place in its head: a pair of vectors, wholly turned or not at all.
+// Lanes past the last pair stand at the first one and neither add nor write.
+template <typename TX, int G, bool HALVES>
+struct Place {
+    static constexpr int V = 16 / static_cast<int>(sizeof(TX));
+    int a, b, turn;   // first values of its vectors, its first angle
+    bool own, turned;
+
+    __device__ explicit Place(const Args& g) {
+        const int lane = threadIdx.x % G;
+        own = lane < g.pairs;
+        const int p = own ? lane : 0;
+        if (HALVES) {
+            turned = p < g.turned;
+            a = turned ? p * V : g.rot + 2 * (p - g.turned) * V;
+            b = turned ? a + g.rot / 2 : a + V;
+            turn = a;
+        } else {
+            a = 2 * p * V;
+            b = a + V;
+            turned = a < g.rot;
+            turn = a / 2;
+        }
+    }
+};
+
+// Turns x and y by c and s (BACK: the other way round). Pairs: x has the first
+// V / 2 turns, y the others.
+template <bool BACK, bool HALVES, int N>
+__device__ __forceinline__ void turn_twos(float2 (&x)[N], float2 (&y)[N], const float2 (&c)[N],
+                                          const float2 (&s)[N]) {
+    if constexpr (HALVES) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float2 n = make_float2(-s[i].x, -s[i].y), u = x[i], v = y[i];
+            x[i] = fma2(v, BACK ? s[i] : n, mul2(u, c[i]));
+            y[i] = fma2(u, BACK ? n : s[i], mul2(v, c[i]));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2 * N; ++k) {
+            float2& z = k < N ? x[k] : y[k - N];
+            const float ck = k & 1 ? c[k / 2].y : c[k / 2].x, sk = k & 1 ? s[k / 2].y : s[k / 2].x;
+            z = fma2(make_float2(z.y, z.x), BACK ? make_float2(sk, -sk) : make_float2(-sk, sk),
+                     mul2(z, both(ck)));
+        }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ float dot_twos(const float2 (&x)[N], const float2 (&y)[N], const float2 (&u)[N],
+                                          const float2 (&v)[N]) {
+    float2 s = mul2(x[0], u[0]), t = mul2(y[0], v[0]);
+#pragma unroll
+    for (int i = 1; i < N; ++i) {
+        s = fma2(x[i], u[i], s);
+        t = fma2(y[i], v[i], t);
+    }
+    s = add2(s, t);
+    return s.x + s.y;
+}
+
+// One warp's way through its tokens: positions, angles and values ahead.
+template <typename TX, int G, bool HALVES, bool GRAD>
+struct Stream {
+    using P = Place<TX, G, HALVES>;
+    static constexpr int N = P::V / 2, kVecs = GRAD ? 4 : 2;
+    static constexpr int kBytes = kThreads * kVecs * 16;  // of a token in the ring
+    const Args& g;
+    const Walk<G> w;
+    const P at;
+    const TX *x, *gy;        // the next token to fetch
+    TX* y;                   // the token at hand
+    int64_t x_step, gy_step, y_step, ahead;
+    const int32_t* position;
+    int32_t next;            // position of the token after the one at hand
+    uint32_t ring;
+    const unsigned char* mine;
+    int slot = 0, free = 0;
+    float2 c[N], s[N];
+
+    __device__ Stream(const Args& args, unsigned char* smem) : g(args), w(args), at(args) {
+        const Side& side = g.side[w.key];
+        x = static_cast<const TX*>(side.x) + w.head * side.x_head + w.t * side.x_token;
+        y = static_cast<TX*>(side.y) + w.head * side.y_head + w.t * side.y_token;
+        x_step = w.step * side.x_token;
+        y_step = w.step * side.y_token;
+        if (GRAD) {
+            gy = static_cast<const TX*>(side.gy) + w.head * side.gy_head + w.t * side.gy_token;
+            gy_step = w.step * side.gy_token;
+        }
+        position = g.positions + w.t;
+        mine = smem + threadIdx.x * 16;
+        ring = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+        ahead = w.t;
+        next = w.t < g.T ? *position : -1;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            c[i] = both(1.0f);
+            s[i] = both(0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < kRing; ++i) fetch();
+    }
+
+    __device__ __forceinline__ void fetch() {
+        if (ahead < g.T) {
+            const uint32_t to = ring + free * kBytes;
+            copy16(to, x + at.a);
+            copy16(to + kThreads * 16, x + at.b);
+            x += x_step;
+            if (GRAD) {
+                copy16(to + 2 * kThreads * 16, gy + at.a);
+                copy16(to + 3 * kThreads * 16, gy + at.b);
+                gy += gy_step;
+            }
+        }
+        copies_begun();
+        ahead += w.step;
+        free = free + 1 == kRing ? 0 : free + 1;
+    }
+
+    // The k-th vector of the token at hand.
+    __device__ __forceinline__ uint4 vec(int k) const {
+        return *reinterpret_cast<const uint4*>(mine + slot * kBytes + k * kThreads * 16);
+    }
+
+    // The position of token t, -1 where it is padding, and its angles.
+    __device__ __forceinline__ bool begin(int64_t t) {
+        const int64_t pos = position_of(g, next);
+        position += w.step;
+        if (t + w.step < g.T) next = *position;
+        if (at.turned && pos >= 0) {
+            const int64_t from = pos * (g.rot / 2) + at.turn;
+            load_twos(g.cosine + from, c);
+            load_twos(g.sine + from, s);
+        }
+        copies_landed<kRing - 1>();
+        return pos >= 0;
+    }
+
+    __device__ __forceinline__ void end() {
+        slot = slot + 1 == kRing ? 0 : slot + 1;
+        y += y_step;
+        fetch();
+    }
+
+    __device__ __forceinline__ void write(const float2 (&a)[N], const float2 (&b)[N]) const {
+        if (!at.own || !w.in) return;
+        *reinterpret_cast<uint4*>(y + at.a) = pack<TX>(a);
+        *reinterpret_cast<uint4*>(y + at.b) = pack<TX>(b);
+    }
+
+    // The head's weights at the lane's columns, 1 where there are none.
+    __device__ void weights(float2 (&a)[N], float2 (&b)[N]) const {
+        const float* p = g.side[w.key].w;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            a[i] = p ? make_float2(p[at.a + 2 * i], p[at.a + 2 * i + 1]) : both(1.0f);
+            b[i] = p ? make_float2(p[at.b + 2 * i], p[at.b + 2 * i + 1]) : both(1.0f);
+        }
+    }
+};
+
+template <typename TX, int G, bool HALVES>
+__global__ void __launch_bounds__(kThreads, kForwardCtas) k_rope_fast(const Args g) {
+    extern __shared__ __align__(16) unsigned char ring[];
+    pdl_wait();
+    pdl_trigger();
+    Stream<TX, G, HALVES, false> f(g, ring);
+    constexpr int N = decltype(f)::N;
+    float2 wx[N], wy[N];
+    f.weights(wx, wy);
+    for (int64_t t = f.w.t; t < g.T; t += f.w.step) {
+        const bool there = f.begin(t);
+        float2 x[N], y[N];
+        unpack<TX>(f.vec(0), x);
+        unpack<TX>(f.vec(1), y);
+        if (there) {
+            const float s = group_sum<G>(f.at.own ? dot_twos(x, y, x, y) : 0.0f);
+            const float2 r = both(rsqrtf(fmaf(s, g.inv_d, g.eps)));
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                x[i] = mul2(mul2(x[i], r), wx[i]);
+                y[i] = mul2(mul2(y[i], r), wy[i]);
+            }
+            turn_twos<false, HALVES>(x, y, f.c, f.s);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = y[i] = both(0.0f);
+        }
+        f.write(x, y);
+        f.end();
+    }
+}
+
+template <typename TX, int G, bool HALVES>
+__global__ void __launch_bounds__(kThreads, kBackwardCtas)
+    k_rope_grad_fast(const Args g, float* __restrict__ parts) {
+    extern __shared__ __align__(16) unsigned char ring[];
+    pdl_wait();
+    pdl_trigger();
+    Stream<TX, G, HALVES, true> f(g, ring);
+    constexpr int N = decltype(f)::N;
+    float2 wx[N], wy[N], sx[N], sy[N];  // weights, sums of gm n
+    f.weights(wx, wy);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sx[i] = sy[i] = both(0.0f);
+    for (int64_t t = f.w.t; t < g.T; t += f.w.step) {
+        const bool there = f.begin(t);
+        float2 x[N], y[N], u[N], v[N];
+        unpack<TX>(f.vec(0), x);
+        unpack<TX>(f.vec(1), y);
+        unpack<TX>(f.vec(2), u);
+        unpack<TX>(f.vec(3), v);
+        if (there) {
+            turn_twos<true, HALVES>(u, v, f.c, f.s);  // gm
+            float s = f.at.own ? dot_twos(x, y, x, y) : 0.0f;
+            s = group_sum<G>(s);
+            const float rstd = rsqrtf(fmaf(s, g.inv_d, g.eps));
+            const float2 r = both(rstd);
+            float2 dots = both(0.0f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                x[i] = mul2(x[i], r);  // n
+                y[i] = mul2(y[i], r);
+                sx[i] = fma2(u[i], x[i], sx[i]);
+                sy[i] = fma2(v[i], y[i], sy[i]);
+                u[i] = mul2(u[i], wx[i]);
+                v[i] = mul2(v[i], wy[i]);
+                dots = fma2(u[i], x[i], fma2(v[i], y[i], dots));
+            }
+            const float dot = group_sum<G>(f.at.own ? dots.x + dots.y : 0.0f) * g.inv_d;
+            const float2 m = both(-dot);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                u[i] = mul2(r, fma2(x[i], m, u[i]));
+                v[i] = mul2(r, fma2(y[i], m, v[i]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) u[i] = v[i] = both(0.0f);
+        }
+        f.write(u, v);
+        f.end();
+    }
+    if (!parts) return;
+    copies_landed<0>();
+    __syncthreads();  // the ring is done with: the sums take its place
+    float* rows = reinterpret_cast<float*>(ring);
+    float* mine = rows + static_cast<int>(threadIdx.x) / 32 * 2 * g.D;
+    for (int i = threadIdx.x % 32; i < 2 * g.D; i += 32) mine[i] = 0.0f;
+    __syncwarp();
+    for (int k = 0; k < 32 / G; ++k) {
+        if (static_cast<int>(threadIdx.x) % 32 / G == k && f.w.in && f.at.own) {
+            float* to = mine + (f.w.key ? g.D : 0);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                to[f.at.a + 2 * i] += sx[i].x;
+                to[f.at.a + 2 * i + 1] += sx[i].y;
+                to[f.at.b + 2 * i] += sy[i].x;
+                to[f.at.b + 2 * i + 1] += sy[i].y;
+            }
+        }
+        __syncwarp();
+    }
+    join_rows(g, rows, parts);
 }
 
 // The partial rows added up: a CTA per 32 columns, its warps every 32nd row each.
@@ -460,24 +784,39 @@ cudaError_t launch_with(const Args& g, const Launch& l) {
                       sizeof(float) * 2 * kWarps * static_cast<size_t>(g.D), l.s, g, l.parts);
 }
 
-template <typename TX, int V, int LEAST, bool HALVES>
-cudaError_t launch_groups(const Args& g, const Launch& l) {
-    if (g.pairs <= 4 && LEAST <= 4) return launch_with<TX, V, LEAST, 1, HALVES>(g, l);
-    if (g.pairs <= 8 && LEAST <= 8) return launch_with<TX, V, std::max(LEAST, 8), 1, HALVES>(g, l);
-    if (g.pairs <= 16) return launch_with<TX, V, 16, 1, HALVES>(g, l);
-    return launch_with<TX, V, 32, 1, HALVES>(g, l);
+template <typename TX, int G, bool HALVES>
+cudaError_t launch_fast(const Args& g, const Launch& l) {
+    using F = Stream<TX, G, HALVES, false>;
+    using B = Stream<TX, G, HALVES, true>;
+    if (!l.grad) {
+        const void* k = reinterpret_cast<const void*>(k_rope_fast<TX, G, HALVES>);
+        DUST_TRY(ensure_smem_limit(k, kRing * F::kBytes));
+        return launch_pdl(k_rope_fast<TX, G, HALVES>,
+                          dim3(grid_of(g.T, g.heads, 32 / G, 152 * kForwardCtas)), dim3(kThreads),
+                          kRing * F::kBytes, l.s, g);
+    }
+    *l.n_parts = grid_of(g.T, g.heads, 32 / G, kMaxCtas);
+    const size_t smem = std::max<size_t>(kRing * B::kBytes, sizeof(float) * 2 * kWarps * static_cast<size_t>(g.D));
+    const void* k = reinterpret_cast<const void*>(k_rope_grad_fast<TX, G, HALVES>);
+    DUST_TRY(ensure_smem_limit(k, kRing * B::kBytes));
+    return launch_pdl(k_rope_grad_fast<TX, G, HALVES>, dim3(*l.n_parts), dim3(kThreads), smem, l.s, g, l.parts);
 }
 
 template <typename TX, bool HALVES>
 cudaError_t launch_vectors(const Args& g, int V, const Launch& l) {
+    if (V * static_cast<int>(sizeof(TX)) == 16 && g.pairs <= 32)
+        return g.pairs <= 2    ? launch_fast<TX, 2, HALVES>(g, l)
+               : g.pairs <= 4  ? launch_fast<TX, 4, HALVES>(g, l)
+               : g.pairs <= 8  ? launch_fast<TX, 8, HALVES>(g, l)
+               : g.pairs <= 16 ? launch_fast<TX, 16, HALVES>(g, l)
+                               : launch_fast<TX, 32, HALVES>(g, l);
     const int per = (g.pairs + 31) / 32;
-    if constexpr (sizeof(TX) == 2)
-        if (V == 8) return launch_groups<TX, 8, 4, HALVES>(g, l);
-    if (V == 4) return per == 1 ? launch_groups<TX, 4, 4, HALVES>(g, l) : launch_with<TX, 4, 32, 2, HALVES>(g, l);
-    if (V == 2)
-        return per == 1   ? launch_groups<TX, 2, 16, HALVES>(g, l)
+    if (V >= 2) {
+        if (g.pairs <= 16) return launch_with<TX, 2, 16, 1, HALVES>(g, l);
+        return per == 1   ? launch_with<TX, 2, 32, 1, HALVES>(g, l)
                : per == 2 ? launch_with<TX, 2, 32, 2, HALVES>(g, l)
                           : launch_with<TX, 2, 32, 4, HALVES>(g, l);
+    }
     return per <= 2 ? launch_with<TX, 1, 32, 2, HALVES>(g, l) : launch_with<TX, 1, 32, 8, HALVES>(g, l);
 }
 
@@ -486,12 +825,7 @@ cudaError_t run(const RopeProblem& p, const Launch& l) {
     const int size = p.bf16 ? 2 : 4;
     int V = 16 / size;
     const auto fits = [&](int v) {
-        if (p.layout == DUST_ROPE_HALVES ? (p.rot / 2) % v || (p.D - p.rot) % v
-                                         : p.D % v || (v >= 4 && (p.rot / 2) % 4))
-            return false;
-        if (v >= 4 && p.rot &&
-            (reinterpret_cast<uintptr_t>(p.cosine) | reinterpret_cast<uintptr_t>(p.sine)) % 16)
-            return false;
+        if (p.layout == DUST_ROPE_HALVES ? (p.rot / 2) % v || (p.D - p.rot) % v : p.D % v) return false;
         for (const RopeSide& d : p.side) {
             if (d.heads == 0) continue;
             const auto on = [&](const dust_heads& h) {
@@ -501,9 +835,12 @@ cudaError_t run(const RopeProblem& p, const Launch& l) {
             };
             if (!on(d.x) || !on(d.y) || !on(d.gy)) return false;
         }
-        return true;
+        // 16 bytes: whole pairs of vectors, each turned or not, and the tables too.
+        return v == 2 || (p.D % (2 * v) == 0 && p.rot % (2 * v) == 0 &&
+                          (p.rot == 0 || (reinterpret_cast<uintptr_t>(p.cosine) |
+                                          reinterpret_cast<uintptr_t>(p.sine)) % 16 == 0));
     };
-    while (V > 1 && !fits(V)) V /= 2;
+    if (!fits(V) || p.D > 64 * V) V = fits(2) ? 2 : 1;
     for (int i = 0; i < 2; ++i) {
         const RopeSide& d = p.side[i];
         g.side[i] = {d.x.data, d.gy.data, d.y.data, d.x.token_stride, d.x.head_stride, d.y.token_stride,
