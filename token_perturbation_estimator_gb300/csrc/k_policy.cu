@@ -4,8 +4,8 @@
 // A first pass finds each token's sequence and counts the scored tokens (whole
 // numbers, so that the order of the additions does not show); a second one
 // forms the tokens' losses, or gradients, whose weights come from those counts,
-// and leaves each CTA's sums; a third adds the sums up in order. Few tokens
-// go through all of it in one CTA and one launch.
+// and leaves each CTA's sums, which the CTA that is done last adds up in order.
+// Few tokens go through all of it in one CTA and one launch.
 //
 // A loss takes about a hundred instructions (two exponentials, a series, the
 // sums), so that many slices are bound by issue rather than by their 12 bytes
@@ -23,13 +23,15 @@ namespace dust {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSlices = 8;   // slices that a CTA takes
+constexpr int kSlices = 5;   // slices that a CTA takes, at most
 constexpr int kPer = 4;      // tokens that a thread takes
 constexpr int kTokens = kThreads * kPer;
-constexpr int kWindow = kTokens + 1;  // sequences' starts that a CTA holds
+constexpr int kCountTokens = 512;            // of a CTA of the first pass, one a thread
+constexpr int kWindow = kCountTokens + 1;    // sequences' starts that it holds
 
 struct Counts {
     int32_t tokens, sequences;  // scored, with scored tokens
+    unsigned int done;          // CTAs of the second pass that have left their sums
 };
 
 struct Space {
@@ -89,13 +91,16 @@ __device__ __forceinline__ int64_t starts_until_alone(const int32_t* offsets, in
     return lo;
 }
 
-// The starts around a CTA's tokens, from the first one's sequence on.
+// The starts around a CTA's tokens, from the first one's sequence on, or all
+// starts where they are few.
 struct Window {
     int64_t first;  // number of the first start held, -1 where the first token precedes all
     int32_t at[kWindow];
 
     __device__ void load(const int32_t* offsets, int64_t n_seq, int64_t t0) {
-        if (threadIdx.x < 32) {
+        if (n_seq < kWindow) {  // all of them
+            if (threadIdx.x == 0) first = 0;
+        } else if (threadIdx.x < 32) {
             const int64_t k = starts_until(offsets, n_seq + 1, t0);
             if (threadIdx.x == 0) first = k - 1;
         }
@@ -107,8 +112,8 @@ struct Window {
         __syncthreads();
     }
 
-    // The sequence of token t, or -1.
-    __device__ int32_t sequence(const int32_t* offsets, int64_t n_seq, int64_t t) const {
+    // The sequence of token t, or -1; held: whether its start is.
+    __device__ int32_t sequence(const int32_t* offsets, int64_t n_seq, int64_t t, bool& held) const {
         int lo = 0, hi = kWindow;  // starts held that are at or before t
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
@@ -116,67 +121,68 @@ struct Window {
             else hi = mid;
         }
         int64_t seq = first + lo - 1;
-        if (lo == kWindow)  // more sequences than tokens: empty ones
+        held = lo < kWindow;
+        if (!held)  // more sequences than tokens: empty ones
             seq = starts_until_alone(offsets, n_seq + 1, t) - 1;
         return seq >= 0 && seq < n_seq ? static_cast<int32_t>(seq) : -1;
     }
 };
 
-// Adds a warp's scored tokens to the counts, one addition per sequence.
-__device__ __forceinline__ void count_tokens(int32_t seq, Counts* counts, int32_t* of_seq) {
-    const unsigned same = __match_any_sync(0xffffffffu, seq);
-    const int lane = threadIdx.x & 31;
-    bool opened = false;
-    if (seq >= 0 && __ffs(same) - 1 == lane) opened = atomicAdd(of_seq + seq, __popc(same)) == 0;
-    const unsigned scored = __ballot_sync(0xffffffffu, seq >= 0);
-    const unsigned open = __ballot_sync(0xffffffffu, opened);
-    if (lane == 0 && scored) {
-        atomicAdd(&counts->tokens, __popc(scored));
-        if (open) atomicAdd(&counts->sequences, __popc(open));
-    }
-}
-
 __device__ __forceinline__ bool has_target(const PolicyProblem& p, int64_t t) {
     return t < p.T && (!p.targets || p.targets[t] >= 0);
 }
 
-__global__ void __launch_bounds__(kThreads)
+// Adds 1 at each lane's place (-1: none), one addition per warp and place.
+__device__ __forceinline__ void count_places(int32_t place, int32_t* counts) {
+    const unsigned same = __match_any_sync(0xffffffffu, place);
+    if (place >= 0 && __ffs(same) - 1 == static_cast<int>(threadIdx.x & 31))
+        atomicAdd(counts + place, __popc(same));
+}
+
+// The tokens of each sequence are counted in shared memory, then added to the
+// others' once per sequence: additions that return a value take a microsecond
+// each.
+__global__ void __launch_bounds__(kCountTokens)
     k_policy_count(const PolicyProblem p, Counts* counts, int32_t* of_seq, int32_t* __restrict__ seq_of) {
     __shared__ Window window;
+    __shared__ int32_t here[kWindow];
     pdl_wait();
     pdl_trigger();
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
-    bool has[kPer];
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kCountTokens + threadIdx.x;
+    const bool has = has_target(p, t);
+    for (int i = threadIdx.x; i < kWindow; i += kCountTokens) here[i] = 0;
+    window.load(p.offsets, p.n_seq, static_cast<int64_t>(blockIdx.x) * kCountTokens);
+    bool held = true;
+    const int32_t seq = has ? window.sequence(p.offsets, p.n_seq, t, held) : -1;
+    if (t < p.T) seq_of[t] = seq;
+    count_places(seq >= 0 && held ? static_cast<int32_t>(seq - window.first) : -1, here);
+    int opened = 0;
+    if (seq >= 0 && !held) opened = atomicAdd(of_seq + seq, 1) == 0;
+    const int scored = __syncthreads_count(seq >= 0);
+    for (int i = threadIdx.x; i < kWindow; i += kCountTokens)
+        if (here[i] > 0) opened += atomicAdd(of_seq + window.first + i, here[i]) == 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) has[i] = has_target(p, t0 + i * kThreads + threadIdx.x);
-    window.load(p.offsets, p.n_seq, t0);
-#pragma unroll 1
-    for (int i = 0; i < kPer; ++i) {
-        const int64_t t = t0 + i * kThreads + threadIdx.x;
-        const int32_t seq = has[i] ? window.sequence(p.offsets, p.n_seq, t) : -1;
-        if (t < p.T) seq_of[t] = seq;
-        count_tokens(seq, counts, of_seq);
-    }
+    for (int off = 16; off > 0; off >>= 1) opened += __shfl_xor_sync(0xffffffffu, opened, off);
+    if (opened > 0 && (threadIdx.x & 31) == 0) atomicAdd(&counts->sequences, opened);
+    if (threadIdx.x == 0 && scored > 0) atomicAdd(&counts->tokens, scored);
 }
 
 // exp(r) - r - 1 without cancellation: its series where |r| < 1 (what it leaves
 // out is below 2^-27 of it).
 __device__ __forceinline__ float kl_of(float r) {
-    if (fabsf(r) < 1.0f) {
-        float s = 1.0f / 479001600.0f;  // 1 / 12!
-        s = fmaf(s, r, 1.0f / 39916800.0f);
-        s = fmaf(s, r, 1.0f / 3628800.0f);
-        s = fmaf(s, r, 1.0f / 362880.0f);
-        s = fmaf(s, r, 1.0f / 40320.0f);
-        s = fmaf(s, r, 1.0f / 5040.0f);
-        s = fmaf(s, r, 1.0f / 720.0f);
-        s = fmaf(s, r, 1.0f / 120.0f);
-        s = fmaf(s, r, 1.0f / 24.0f);
-        s = fmaf(s, r, 1.0f / 6.0f);
-        s = fmaf(s, r, 0.5f);
-        return s * r * r;
-    }
-    return expm1f(r) - r;
+    float s = 1.0f / 479001600.0f;  // 1 / 12!
+    s = fmaf(s, r, 1.0f / 39916800.0f);
+    s = fmaf(s, r, 1.0f / 3628800.0f);
+    s = fmaf(s, r, 1.0f / 362880.0f);
+    s = fmaf(s, r, 1.0f / 40320.0f);
+    s = fmaf(s, r, 1.0f / 5040.0f);
+    s = fmaf(s, r, 1.0f / 720.0f);
+    s = fmaf(s, r, 1.0f / 120.0f);
+    s = fmaf(s, r, 1.0f / 24.0f);
+    s = fmaf(s, r, 1.0f / 6.0f);
+    s = fmaf(s, r, 0.5f);
+    const float far = expf(r) - (1.0f + r);
+    return fabsf(r) < 1.0f ? s * r * r : far;
 }
 
 // What a token needs of everything but nll.
@@ -187,6 +193,7 @@ struct Token {
     __device__ __forceinline__ void load(const PolicyProblem& p, const Counts& c, const int32_t* of_seq,
                                          int32_t seq, int64_t t) {
         scored = seq >= 0;
+        old = ref = adv = weight = 0.0f;
         if (!scored) return;
         old = p.old[t];
         ref = p.ref ? p.ref[t] : 0.0f;
@@ -198,34 +205,59 @@ struct Token {
 
 // Whether the ratio is beyond the bound on its advantage's side. The fp32
 // difference is off by half a step, as the bound is: further apart than 4
-// steps, they stand as the exact ones do. (The exact ones in a call of their
-// own: in line, the compiler forms them for every value.)
-__device__ __noinline__ int compare_exactly(double old, double nll, double bound) {
-    const double step = old - nll;
-    return step > bound ? 1 : step < bound ? -1 : 0;
-}
+// steps, they stand as the exact ones do, and what is nearer is rare.
+struct Side {
+    bool beyond, near;
 
-__device__ __forceinline__ bool beyond(const PolicyProblem& p, float adv, float old, float nll) {
-    const bool up = adv > 0.0f;
-    const float bound = up ? p.high32 : p.low32, step = old - nll;
-    if (!(fabsf(step - bound) > 0x1p-22f * fabsf(bound))) {
-        const int c = compare_exactly(old, nll, up ? p.high : p.low);
-        return up ? c > 0 : adv < 0.0f && c < 0;
+    __device__ __forceinline__ Side(const PolicyProblem& p, const Token& k, float nll) {
+        const bool up = k.adv > 0.0f;
+        const float bound = up ? p.high32 : p.low32, step = k.old - nll;
+        near = !(fabsf(step - bound) > 0x1p-22f * fabsf(bound));
+        beyond = up ? step > bound : k.adv < 0.0f && step < bound;
     }
-    return up ? step > bound : adv < 0.0f && step < bound;
-}
+    // Decided in 64 bits. A call of its own: in line, the compiler would
+    // form the exact differences of every value.
+    static __device__ __noinline__ bool exactly(const PolicyProblem& p, float adv, float old, float nll) {
+        const double step = static_cast<double>(old) - static_cast<double>(nll);
+        return adv > 0.0f ? step > p.high : adv < 0.0f && step < p.low;
+    }
+};
 
-__device__ __forceinline__ float loss_of(const PolicyProblem& p, const Token& k, float nll, float& kl,
-                                         bool& clipped) {
-    clipped = beyond(p, k.adv, k.old, nll);
-    const float bound = k.adv > 0.0f ? 1.0f + p.clip_high : 1.0f - p.clip_low;
-    const float loss = -(clipped ? bound : expf(k.old - nll)) * k.adv;
-    kl = p.ref ? kl_of(nll - k.ref) : 0.0f;
-    return p.ref ? fmaf(p.beta, kl, loss) : loss;
+// N tokens' losses side by side, without branches but for the rare ones.
+template <int N>
+__device__ __forceinline__ void losses_of(const PolicyProblem& p, const Token (&k)[N], const float (&nll)[N],
+                                          float (&loss)[N], float (&kl)[N], bool (&clipped)[N]) {
+    bool near = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const Side d(p, k[i], nll[i]);
+        clipped[i] = d.beyond;
+        near |= d.near;
+    }
+    if (near)
+#pragma unroll
+        for (int i = 0; i < N; ++i) clipped[i] = Side::exactly(p, k[i].adv, k[i].old, nll[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float bound = k[i].adv > 0.0f ? 1.0f + p.clip_high : 1.0f - p.clip_low;
+        const float ratio = expf(k[i].old - nll[i]);
+        loss[i] = -(clipped[i] ? bound : ratio) * k[i].adv;
+        kl[i] = 0.0f;
+        if (p.ref) {
+            kl[i] = kl_of(nll[i] - k[i].ref);
+            loss[i] = fmaf(p.beta, kl[i], loss[i]);
+        }
+        if (!k[i].scored) {
+            loss[i] = kl[i] = 0.0f;
+            clipped[i] = false;
+        }
+    }
 }
 
 __device__ __forceinline__ float slope_of(const PolicyProblem& p, const Token& k, float nll) {
-    float g = beyond(p, k.adv, k.old, nll) ? 0.0f : expf(k.old - nll) * k.adv;
+    Side d(p, k, nll);
+    if (d.near) d.beyond = Side::exactly(p, k.adv, k.old, nll);
+    float g = d.beyond ? 0.0f : expf(k.old - nll) * k.adv;
     if (p.ref) g = fmaf(p.beta, expm1f(nll - k.ref), g);
     return g;
 }
@@ -242,87 +274,105 @@ struct Outputs {
     float *loss, *total, *kl, *clipped, *delta;
 };
 
-__global__ void __launch_bounds__(kThreads)
-    k_policy(const PolicyProblem p, const Outputs o, int64_t blocks, int64_t groups, const Counts* counts,
-             const int32_t* __restrict__ of_seq, const int32_t* __restrict__ seq_of,
-             float* __restrict__ parts) {
+// The CTAs' sums [blocks][n] added up: each column by several threads, theirs
+// in order.
+__device__ __forceinline__ void join_parts(const float* parts, int64_t blocks, int64_t n, const Outputs& o) {
+    __shared__ double sh[kThreads];
+    for (int64_t c0 = 0; c0 < n; c0 += kThreads) {
+        const int cols = static_cast<int>(min(n - c0, static_cast<int64_t>(kThreads)));
+        const int turns = kThreads / cols, c = threadIdx.x % cols, turn = threadIdx.x / cols;
+        double v = 0.0;
+        if (turn < turns)
+#pragma unroll 8
+            for (int64_t b = turn; b < blocks; b += turns) v += static_cast<double>(__ldcg(parts + b * n + c0 + c));
+        sh[threadIdx.x] = v;
+        __syncthreads();
+        if (static_cast<int>(threadIdx.x) < cols) {
+            for (int i = 1; i < turns; ++i) v += sh[i * cols + c];
+            const int64_t s = (c0 + c) / 3;
+            float* out = (c0 + c) % 3 == 0 ? o.total : (c0 + c) % 3 == 1 ? o.kl : o.clipped;
+            if (out) out[s] = static_cast<float>(v);
+        }
+        __syncthreads();
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 3)
+    k_policy(const PolicyProblem p, const Outputs o, int64_t blocks, int64_t groups, Counts* counts,
+             const int32_t* __restrict__ of_seq, const int32_t* __restrict__ seq_of, float* parts) {
     pdl_wait();
     pdl_trigger();
     __shared__ float sums[kThreads / 32][kSlices][3];
-    const Counts c = *counts;
+    __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t block = blockIdx.x % blocks, group = blockIdx.x / blocks;
     const int64_t t0 = block * kTokens + threadIdx.x;
-    const int64_t s0 = p.S * group / groups, s1 = p.S * (group + 1) / groups;
+    const int s0 = static_cast<int>(p.S * group / groups), s1 = static_cast<int>(p.S * (group + 1) / groups);
+    const int here = static_cast<int>(min(p.T - block * kTokens, static_cast<int64_t>(kTokens)));
+    // This thread's tokens that there are, the first one's place in its slice.
+    const int mine = max(0, (here - static_cast<int>(threadIdx.x) + kThreads - 1) / kThreads);
+    const float* nll = p.nll + s0 * p.T + t0;
     Token k[kPer];
     float clean[kPer], next[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int64_t t = t0 + i * kThreads;
-        next[i] = t < p.T ? p.nll[s0 * p.T + t] : 0.0f;
-        clean[i] = o.delta && t < p.T ? p.nll[t] : 0.0f;
-        k[i].load(p, c, of_seq, t < p.T ? seq_of[t] : -1, t);
+        next[i] = i < mine ? nll[i * kThreads] : 0.0f;
+        clean[i] = o.delta && i < mine ? p.nll[t0 + i * kThreads] : 0.0f;
     }
+    const Counts c = *counts;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        k[i].load(p, c, of_seq, i < mine ? seq_of[t0 + i * kThreads] : -1, t0 + i * kThreads);
+    float l[kPer], kl[kPer];
+    bool clipped[kPer];
     if (o.delta) {
+        losses_of(p, k, clean, l, kl, clipped);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            float kl;
-            bool clipped;
-            clean[i] = k[i].scored ? loss_of(p, k[i], clean[i], kl, clipped) : 0.0f;
-        }
+        for (int i = 0; i < kPer; ++i) clean[i] = l[i];
     }
+    float* loss = o.loss ? o.loss + s0 * p.T + t0 : nullptr;
+    float* delta = o.delta ? o.delta + (s0 - 1) * p.T + t0 : nullptr;
 #pragma unroll 1
-    for (int64_t s = s0; s < s1; ++s) {
+    for (int s = s0; s < s1; ++s) {
         float now[kPer];
+        nll += p.T;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int64_t t = t0 + i * kThreads;
             now[i] = next[i];
-            if (s + 1 < s1 && t < p.T) next[i] = p.nll[(s + 1) * p.T + t];
+            if (s + 1 < s1 && i < mine) next[i] = nll[i * kThreads];
         }
         float sum[3] = {0.0f, 0.0f, 0.0f};
+        losses_of(p, k, now, l, kl, clipped);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int64_t t = t0 + i * kThreads;
-            if (t >= p.T) continue;
-            float l = 0.0f, kl = 0.0f;
-            bool clipped = false;
-            if (k[i].scored) {
-                l = loss_of(p, k[i], now[i], kl, clipped);
-                sum[0] = fmaf(k[i].weight, l, sum[0]);
-                sum[1] = fmaf(k[i].weight, kl, sum[1]);
-                if (clipped) sum[2] += k[i].weight;
-            }
-            if (o.loss) o.loss[s * p.T + t] = l;
-            if (o.delta && s > 0) o.delta[(s - 1) * p.T + t] = l - clean[i];
+            sum[0] = fmaf(k[i].weight, l[i], sum[0]);
+            sum[1] = fmaf(k[i].weight, kl[i], sum[1]);
+            if (clipped[i]) sum[2] += k[i].weight;
+            if (loss && i < mine) loss[i * kThreads] = l[i];
+            if (delta && s > 0 && i < mine) delta[i * kThreads] = l[i] - clean[i];
         }
+        if (loss) loss += p.T;
+        if (delta) delta += p.T;
         warp_sums(sum);
         if (lane == 0)
 #pragma unroll
             for (int j = 0; j < 3; ++j) sums[warp][s - s0][j] = sum[j];
     }
+    if (!o.total && !o.kl && !o.clipped) return;
     __syncthreads();
     for (int i = threadIdx.x; i < (s1 - s0) * 3; i += kThreads) {
         float v = 0.0f;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) v += sums[w][i / 3][i % 3];
-        parts[(block * p.S + s0) * 3 + i] = v;
+        __stcg(parts + (block * p.S + s0) * 3 + i, v);
     }
-}
-
-// Sums over the blocks, a warp per slice and kind.
-__global__ void __launch_bounds__(96) k_policy_join(const float* __restrict__ parts, int64_t blocks,
-                                                    int64_t S, const Outputs o) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t s = blockIdx.x;
-    const int j = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    double v = 0.0;
-    for (int64_t b = lane; b < blocks; b += 32) v += static_cast<double>(parts[(b * S + s) * 3 + j]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    float* out = j == 0 ? o.total : j == 1 ? o.kl : o.clipped;
-    if (lane == 0 && out) out[s] = static_cast<float>(v);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(&counts->done, 1u) + 1 == gridDim.x;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    join_parts(parts, blocks, 3 * p.S, o);
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -358,7 +408,7 @@ __global__ void __launch_bounds__(kFewThreads)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int T = static_cast<int>(p.T), S = static_cast<int>(p.S);
     for (int i = threadIdx.x; i < p.n_seq; i += kFewThreads) of_seq[i] = 0;
-    if (threadIdx.x == 0) counts = {0, 0};
+    if (threadIdx.x == 0) counts = {0, 0, 0};
     __syncthreads();
     int32_t seq[2];
 #pragma unroll
@@ -369,8 +419,15 @@ __global__ void __launch_bounds__(kFewThreads)
             const int64_t k = starts_until_alone(p.offsets, p.n_seq + 1, t) - 1;
             if (k >= 0 && k < p.n_seq) seq[i] = static_cast<int32_t>(k);
         }
-        if (i * kFewThreads < T) count_tokens(seq[i], &counts, of_seq);
+        count_places(seq[i], of_seq);
     }
+    const int scored = __syncthreads_count(seq[0] >= 0) + __syncthreads_count(seq[1] >= 0);
+    int open = 0;
+    for (int i0 = 0; i0 < p.n_seq; i0 += kFewThreads) {
+        const int i = i0 + threadIdx.x;
+        open += __syncthreads_count(i < p.n_seq && of_seq[i] > 0);
+    }
+    if (threadIdx.x == 0) counts = {scored, open, 0};
     __syncthreads();
     float sum[kFewSlices][3] = {};
 #pragma unroll
@@ -387,17 +444,17 @@ __global__ void __launch_bounds__(kFewThreads)
             if constexpr (GRAD) {
                 gnll[s * T + t] = k.scored ? gtotal[s] * k.weight * slope_of(p, k, nll) : 0.0f;
             } else {
-                float l = 0.0f, kl = 0.0f;
-                bool clipped = false;
-                if (k.scored) {
-                    l = loss_of(p, k, nll, kl, clipped);
-                    sum[s][0] = fmaf(k.weight, l, sum[s][0]);
-                    sum[s][1] = fmaf(k.weight, kl, sum[s][1]);
-                    if (clipped) sum[s][2] += k.weight;
-                }
-                if (s == 0) clean = l;
-                if (o.loss) o.loss[s * T + t] = l;
-                if (o.delta && s > 0) o.delta[(s - 1) * T + t] = l - clean;
+                float l[1], kl[1];
+                bool clipped[1];
+                const Token one[1] = {k};
+                const float value[1] = {nll};
+                losses_of(p, one, value, l, kl, clipped);
+                sum[s][0] = fmaf(k.weight, l[0], sum[s][0]);
+                sum[s][1] = fmaf(k.weight, kl[0], sum[s][1]);
+                if (clipped[0]) sum[s][2] += k.weight;
+                if (s == 0) clean = l[0];
+                if (o.loss) o.loss[s * T + t] = l[0];
+                if (o.delta && s > 0) o.delta[(s - 1) * T + t] = l[0] - clean;
             }
         }
     }
@@ -434,8 +491,8 @@ bool few(const PolicyProblem& p) {
 
 cudaError_t count(const PolicyProblem& p, const Space& w, cudaStream_t s) {
     DUST_TRY(cudaMemsetAsync(w.counts, 0, w.clear, s));
-    return launch_pdl(k_policy_count, dim3(static_cast<unsigned>(blocks_of(p.T))), dim3(kThreads), 0, s, p,
-                      w.counts, w.of_seq, w.seq_of);
+    const unsigned grid = static_cast<unsigned>((p.T + kCountTokens - 1) / kCountTokens);
+    return launch_pdl(k_policy_count, dim3(grid), dim3(kCountTokens), 0, s, p, w.counts, w.of_seq, w.seq_of);
 }
 
 }  // namespace
@@ -453,10 +510,8 @@ cudaError_t launch_policy(const PolicyProblem& p, float* loss, float* total, flo
     const Space w = carve(ws, p.S, p.T, p.n_seq);
     DUST_TRY(count(p, w, s));
     const int64_t blocks = blocks_of(p.T), groups = groups_of(p.S);
-    DUST_TRY(launch_pdl(k_policy, dim3(static_cast<unsigned>(blocks * groups)), dim3(kThreads), 0, s, p, o,
-                        blocks, groups, w.counts, w.of_seq, w.seq_of, w.parts));
-    if (!total && !kl && !clipped) return cudaSuccess;
-    return launch_pdl(k_policy_join, dim3(static_cast<unsigned>(p.S)), dim3(96), 0, s, w.parts, blocks, p.S, o);
+    return launch_pdl(k_policy, dim3(static_cast<unsigned>(blocks * groups)), dim3(kThreads), 0, s, p, o,
+                      blocks, groups, w.counts, w.of_seq, w.seq_of, w.parts);
 }
 
 cudaError_t launch_policy_grad(const PolicyProblem& p, const float* gtotal, float* gnll, void* ws,

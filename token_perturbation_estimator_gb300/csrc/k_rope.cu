@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRing = 3;              // tokens on their way per warp
+constexpr int kRing = 2;              // tokens on their way per warp
 constexpr int kForwardCtas = 3, kBackwardCtas = 2;  // per SM
 constexpr int kMaxCtas = 152 * kBackwardCtas;       // of the backward: partial rows
 
