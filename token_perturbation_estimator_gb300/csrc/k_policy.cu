@@ -274,24 +274,27 @@ struct Outputs {
     float *loss, *total, *kl, *clipped, *delta;
 };
 
-// The CTAs' sums [blocks][n] added up: each column by several threads, theirs
-// in order.
+// The CTAs' sums [blocks][n] added up: each column by a power of two of threads,
+// then theirs by halves.
 __device__ __forceinline__ void join_parts(const float* parts, int64_t blocks, int64_t n, const Outputs& o) {
     __shared__ double sh[kThreads];
     for (int64_t c0 = 0; c0 < n; c0 += kThreads) {
         const int cols = static_cast<int>(min(n - c0, static_cast<int64_t>(kThreads)));
-        const int turns = kThreads / cols, c = threadIdx.x % cols, turn = threadIdx.x / cols;
+        const int turns = 1 << (31 - __clz(kThreads / cols)), c = threadIdx.x % cols, turn = threadIdx.x / cols;
         double v = 0.0;
         if (turn < turns)
 #pragma unroll 8
             for (int64_t b = turn; b < blocks; b += turns) v += static_cast<double>(__ldcg(parts + b * n + c0 + c));
         sh[threadIdx.x] = v;
         __syncthreads();
-        if (static_cast<int>(threadIdx.x) < cols) {
-            for (int i = 1; i < turns; ++i) v += sh[i * cols + c];
+        for (int h = turns / 2; h > 0; h /= 2) {
+            if (turn < h) sh[threadIdx.x] += sh[threadIdx.x + h * cols];
+            __syncthreads();
+        }
+        if (turn == 0) {
             const int64_t s = (c0 + c) / 3;
             float* out = (c0 + c) % 3 == 0 ? o.total : (c0 + c) % 3 == 1 ? o.kl : o.clipped;
-            if (out) out[s] = static_cast<float>(v);
+            if (out) out[s] = static_cast<float>(sh[threadIdx.x]);
         }
         __syncthreads();
     }
