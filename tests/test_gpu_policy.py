@@ -235,7 +235,7 @@ def test_missing_outputs_one_dimension_and_in_place():
     dust.dust_policy_loss_grad(mine, old, adv, off, torch.ones((), device=dev), gnll=mine, **args)
     assert torch.equal(mine, g)
     n = dust._query("dust_policy_loss_workspace", 1, 83, 2)
-    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
     kl = torch.zeros(1, device=dev)
     p = lambda t: C.c_void_p(t.data_ptr())  # noqa: E731
     st = dust.lib().dust_policy_loss(p(nll), p(old), p(ref), p(adv), 0, p(off), 2, p(tg), 1, 83, 0.2,

@@ -168,7 +168,8 @@ def test_policy(L, call):
     for kw in (dict(T=1 << 31), dict(S=1 << 16, T=1 << 16), dict(n_seq=1 << 31)):
         assert call(L, **kw) == dust.ERR_RANGE, kw
     for kw in (dict(ws=NULL), dict(wsb=8), dict(ws=C.c_void_p((1 << 20) + 16))):
-        assert call(L, **kw) == dust.ERR_WORKSPACE, kw
+        # (few tokens need none)
+        assert call(L, T=100000, **kw) == dust.ERR_WORKSPACE, kw
     if call is _policy:
         assert call(L, T=0, total=NULL, kl=NULL, clipped=NULL, nll=NULL, off=NULL) == dust.OK
     else:

@@ -550,7 +550,9 @@ def _space(workspace, name, ref, dev, *args):
     """The caller's workspace, or a new one of the size that query `name` gives:
     (tensor, address, bytes)."""
     if workspace is None:
-        n = max(_query(name, *args), 256)
+        n = _query(name, *args)
+        if n == 0:
+            return None, None, 0
         workspace = _types().empty(n, dtype=_types().u8, device=ref.device)
         return workspace, workspace.data_ptr(), n
     n = workspace.numel()
@@ -814,7 +816,7 @@ class _Heads(C.Structure):
 
 
 def _heads(t, name, dtype, shape, dev):
-    """dust_heads of t, a tensor of this dtype and shape [T, heads, D] on CUDA
+    """A reference to the dust_heads of t, a tensor of this dtype and shape [T, heads, D] on CUDA
     device `dev` with unit stride inside a head; raises ValueError for any other."""
     if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev):
         if not t.is_cuda:
@@ -824,14 +826,14 @@ def _heads(t, name, dtype, shape, dev):
     token, head, step = t.stride()
     if shape[2] > 1 and step != 1:
         raise ValueError("%s must have unit stride inside a head" % name)
-    return _Heads(t.data_ptr(), token, head)
+    return C.byref(_Heads(t.data_ptr(), token, head))
 
 
 def _output_heads(t, name, dtype, shape, ref, dev):
-    """The caller's output, or a new one: (tensor, dust_heads)."""
+    """The caller's output, or a new one: (tensor, its dust_heads)."""
     if t is None:
         t = _types().empty(shape, dtype=dtype, device=ref.device)
-        return t, _Heads(t.data_ptr(), shape[1] * shape[2], shape[2])
+        return t, C.byref(_Heads(t.data_ptr(), shape[1] * shape[2], shape[2]))
     return t, _heads(t, name, dtype, shape, dev)
 
 
@@ -869,13 +871,9 @@ def dust_qk_norm_rope(q, k, wq, wk, positions, cosine, sine, eps=1e-6, layout=RO
     hs_k = None
     if k is not None:
         yk, hs_k = _output_heads(yk, "yk", q.dtype, (T, hk, D), q, dev)
-    st = lib().dust_qk_norm_rope(*_refs(args), *_refs((hs_q, hs_k)), ty.stream_of(dev))
+    st = lib().dust_qk_norm_rope(*args, hs_q, hs_k, ty.stream_of(dev))
     _check(st, "dust_qk_norm_rope")
     return yq, yk
-
-
-def _refs(args):
-    return tuple(C.byref(a) if type(a) is _Heads else a for a in args)
 
 
 @_in_stream
@@ -898,9 +896,8 @@ def dust_qk_norm_rope_grad(gyq, gyk, q, k, wq, wk, positions, cosine, sine, eps=
         gwk, gwk_at = _output(gwk, "gwk", ty.f32, (D,), q, dev)
     workspace, ws_at, ws_bytes = _space(workspace, "dust_qk_norm_rope_grad_workspace", q, dev, T, hq,
                                         hk, D)
-    st = lib().dust_qk_norm_rope_grad(*_refs((gy_q, gy_k)), *_refs(args), flags,
-                                      *_refs((hs_q, hs_k)), gwq_at, gwk_at, ws_at, ws_bytes,
-                                      ty.stream_of(dev))
+    st = lib().dust_qk_norm_rope_grad(gy_q, gy_k, *args, flags, hs_q, hs_k, gwq_at, gwk_at, ws_at,
+                                      ws_bytes, ty.stream_of(dev))
     _check(st, "dust_qk_norm_rope_grad")
     return gq, gk, gwq, gwk
 

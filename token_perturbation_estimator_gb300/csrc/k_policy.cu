@@ -482,8 +482,8 @@ __global__ void __launch_bounds__(kFewThreads)
     }
 }
 
-bool few(const PolicyProblem& p) {
-    return p.T <= kFewTokens && p.n_seq <= kFewSequences && p.S <= kFewSlices;
+bool few(int64_t S, int64_t T, int64_t n_seq) {
+    return T <= kFewTokens && n_seq <= kFewSequences && S <= kFewSlices;
 }
 
 #define DUST_TRY(x)                             \
@@ -501,14 +501,14 @@ cudaError_t count(const PolicyProblem& p, const Space& w, cudaStream_t s) {
 }  // namespace
 
 size_t policy_workspace_bytes(int64_t S, int64_t T, int64_t n_seq) {
-    return carve(nullptr, S, T, n_seq).total;
+    return few(S, T, n_seq) ? 0 : carve(nullptr, S, T, n_seq).total;
 }
 
 cudaError_t launch_policy(const PolicyProblem& p, float* loss, float* total, float* kl,
                           float* clipped, float* delta, void* ws, cudaStream_t s) {
     ProfScope ps(kStagePolicy, s);
     const Outputs o = {loss, total, kl, clipped, delta};
-    if (few(p))
+    if (few(p.S, p.T, p.n_seq))
         return launch_pdl(k_policy_few<false>, dim3(1), dim3(kFewThreads), 0, s, p, o, nullptr, nullptr);
     const Space w = carve(ws, p.S, p.T, p.n_seq);
     DUST_TRY(count(p, w, s));
@@ -520,7 +520,7 @@ cudaError_t launch_policy(const PolicyProblem& p, float* loss, float* total, flo
 cudaError_t launch_policy_grad(const PolicyProblem& p, const float* gtotal, float* gnll, void* ws,
                                cudaStream_t s) {
     ProfScope ps(kStagePolicy, s);
-    if (few(p))
+    if (few(p.S, p.T, p.n_seq))
         return launch_pdl(k_policy_few<true>, dim3(1), dim3(kFewThreads), 0, s, p, Outputs{}, gtotal, gnll);
     const Space w = carve(ws, p.S, p.T, p.n_seq);
     DUST_TRY(count(p, w, s));
