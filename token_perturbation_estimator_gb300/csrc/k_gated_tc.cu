@@ -29,8 +29,12 @@ namespace {
 
 enum Mode { kUp, kBack, kMul };
 
+// Steps in flight; kBack's epilogue warps hold their part of gh as well.
+template <int MODE> constexpr int kDepth = MODE == kBack ? kStages - 1 : kStages;
+constexpr int kHeldBytes = 32 * 128;  // 32 rows of 64 bf16 units, or of 32 fp32 ones
 template <int MODE> constexpr int smem_of() {
-    return kStages * kStageBytes + 1024 + (MODE == kBack ? kStoreBytes : kEpiWarps * kTurnBuf);
+    return kDepth<MODE> * kStageBytes + 1024 +
+           (MODE == kBack ? kStoreBytes + kEpiWarps * kHeldBytes : kEpiWarps * kTurnBuf);
 }
 static_assert(smem_of<kBack>() + 512 <= 227 * 1024 && smem_of<kUp>() + 512 <= 227 * 1024,
               "shared memory per CTA, barriers included");
@@ -41,8 +45,6 @@ struct TcArgs {
     int group;                 // row tiles that run together (kUp, kBack)
     int act;
     OutRows h;                 // kUp
-    const unsigned char* gh;   // kBack
-    int64_t gh_pitch;
     OutRows gX, gW[2];         // kMul
     int halves, first_half;    // of gWg and gWu, those that are wanted
     float *gx_acc, *gw_acc;    // tiles of partial sums, by unit
@@ -251,67 +253,25 @@ __device__ __forceinline__ void backward_by(int act, float (&g)[32], float (&u)[
     else backward<DUST_ACT_RELU2, EXACT>(g, u, gh);
 }
 
-// 32 values of a row of gh as they lie, zeros past the first n.
-template <int PLANES>
-struct Loaded {
-    static constexpr int kVecs = PLANES == 1 ? 4 : 8;
-    static constexpr int kPer = 32 / kVecs;
-    uint4 raw[kVecs];
-
-    __device__ __forceinline__ void load(const unsigned char* p, int n) {
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            raw[i] = make_uint4(0, 0, 0, 0);
-            if ((i + 1) * kPer <= n) {
-                raw[i] = *reinterpret_cast<const uint4*>(p + 16 * i);
-            } else if (i * kPer < n) {  // the row's last values
-                uint32_t* r = &raw[i].x;
-#pragma unroll
-                for (int k = 0; k < kPer; ++k) {
-                    if (i * kPer + k >= n) continue;
-                    if (PLANES == 1)
-                        r[k / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i * kPer + k])
-                                    << (16 * (k & 1));
-                    else
-                        r[k] = reinterpret_cast<const uint32_t*>(p)[i * kPer + k];
-                }
-            }
-        }
-    }
-    __device__ __forceinline__ void values(float (&v)[32]) const {
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const uint32_t r[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (PLANES == 1) {
-                    v[8 * i + 2 * k] = __uint_as_float(r[k] << 16);
-                    v[8 * i + 2 * k + 1] = __uint_as_float(r[k] & 0xffff0000u);
-                } else {
-                    v[4 * i + k] = __uint_as_float(r[k]);
-                }
-            }
-        }
-    }
-};
-
 // Epilogue of one unit of work for one warp: rows 32 q + lane of this CTA's
 // half, and of the tile's units or columns the h-th half.
 template <int MODE, int PLANES>
 struct Epilogue {
     static constexpr bool kRuns = PLANES == 3;
     const TcArgs& a;
-    const CUtensorMap* tmD;
+    const CUtensorMap *tmD, *tmGh;
     unsigned char* bufs;  // this warp's: kBack's store buffers, the others' 32 x 32 values
+    unsigned char* held;  // kBack: this warp's part of gh
+    uint64_t* landed;     // and its barrier
     uint32_t rank;
     int q, h, lane;
     uint32_t used = 0;
+    uint32_t asked = 0, got = 0;  // kBack: parts of gh
     // A unit's sums over its runs of steps but the last, and whether there are
     // such: of kUp and kBack 32 gates and 32 ups, of kMul 64 columns.
     static constexpr int kSums = kRuns ? 64 : 1;
     float sum[kSums] = {};
     bool summed = false;
-    Loaded<PLANES> loaded;
 
     __device__ int64_t row_of(const Tile& w) const { return w.m0 + rank * kHalf + 32 * q + lane; }
 
@@ -326,10 +286,36 @@ struct Epilogue {
     // The tile's b-th 32 units of this warp.
     __device__ int unit_of(int b) const { return h * (a.bn / 4) + 32 * b; }
 
-    __device__ void fetch(const Tile& w, int b) {
-        const int64_t row = row_of(w), unit = w.n0 + unit_of(b);
-        const int left = row < a.T ? static_cast<int>(min(a.f - unit, static_cast<int64_t>(32))) : 0;
-        loaded.load(a.gh + row * a.gh_pitch + unit * (PLANES == 1 ? 2 : 4), left);
+    // Asks for this warp's rows and units of gh (zeros where there are none).
+    // All lanes have read the last ones.
+    __device__ void fetch(const Tile& w) {
+        if (lane == 0) {
+            tc::mbar_arrive_expect_tx(landed, kHeldBytes);
+            tc::tma_load_2d(held, tmGh, static_cast<int32_t>(w.n0) + unit_of(0),
+                            static_cast<int32_t>(row_of(w)), landed);
+        }
+        ++asked;
+    }
+
+    // Block b of what was asked for: a lane's row lies in 16-byte pieces that
+    // the row's number permutes.
+    __device__ void take(int b, float (&v)[32]) const {
+        constexpr int kVecs = PLANES == 1 ? 4 : 8;
+        const unsigned char* row = held + lane * 128;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4*>(row + (((b * kVecs + i) ^ (lane & 7)) << 4));
+            const uint32_t r[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (PLANES == 1) {
+                    v[(8 * i + 2 * k) % 32] = __uint_as_float(r[k] << 16);
+                    v[(8 * i + 2 * k + 1) % 32] = __uint_as_float(r[k] & 0xffff0000u);
+                } else {
+                    v[4 * i + k] = __uint_as_float(r[k]);
+                }
+            }
+        }
     }
 
     __device__ void up(const Tile& w, uint32_t taddr) {
@@ -349,16 +335,21 @@ struct Epilogue {
         }
     }
 
-    __device__ void back(const Tile& w, uint32_t taddr) {
+    // `next`: the tile to ask for once this one's part of gh has been read.
+    __device__ void back(const Tile& w, const Tile* next, uint32_t taddr) {
         const int64_t row = row_of(w);
+        const int blocks = a.bn / 128;
 #pragma unroll 1
-        for (int b = 0; b < a.bn / 128; ++b) {
+        for (int b = 0; b < blocks; ++b) {
             const int c = unit_of(b);
             const int64_t unit = w.n0 + c;
-            if (unit >= (a.f + 63) / 64 * 64) break;
             float g[32], u[32], gh[32];
-            loaded.values(gh);
-            if (b + 1 < a.bn / 128) fetch(w, b + 1);
+            take(b, gh);
+            if (b + 1 == blocks) {
+                __syncwarp();
+                if (next) fetch(*next);
+            }
+            if (unit >= (a.f + 63) / 64 * 64) continue;
             whole_sum(taddr, c, 0, g);
             whole_sum(taddr, a.bn / 2 + c, 1, u);
             backward_by<PLANES == 3>(a.act, g, u, gh);
@@ -373,6 +364,18 @@ struct Epilogue {
             store_planes(g, static_cast<int32_t>(unit), static_cast<int32_t>(row - lane));
             store_planes(u, static_cast<int32_t>(a.fp + unit), static_cast<int32_t>(row - lane));
         }
+    }
+
+    // The same, once this warp's part of gh is there; false if it did not come.
+    __device__ bool back_when_landed(const Tile& w, const Tile* next, uint32_t taddr, uint64_t limit_ns,
+                                     volatile int* abort_flag) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(landed, got & 1, limit_ns, abort_flag))) {
+            *abort_flag = 1;
+            return false;
+        }
+        ++got;
+        back(w, next, taddr);
+        return true;
     }
 
     __device__ void store_planes(float (&v)[32], int32_t col, int32_t row0) {
@@ -480,24 +483,25 @@ struct Epilogue {
     }
 };
 
-// Maps: kUp X, Wg, Wu, -; kBack X, Wg, Wu, D; kMul D, Wg, Wu, X.
+// Maps: kUp X, Wg, Wu, -, -; kBack X, Wg, Wu, D, gh; kMul D, Wg, Wu, X, -.
 template <int MODE, int PLANES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_gated_tc(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
                const __grid_constant__ CUtensorMap tm2, const __grid_constant__ CUtensorMap tm3,
-               const __grid_constant__ TcArgs a) {
+               const __grid_constant__ CUtensorMap tm4, const __grid_constant__ TcArgs a) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    unsigned char* store_bufs = smem + kStages * kStageBytes;
+    unsigned char* store_bufs = smem + kDepth<MODE> * kStageBytes;
     __shared__ Ctl ctl_s;
+    __shared__ uint64_t gh_landed[kEpiWarps];
     Ctl* ctl = &ctl_s;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = uniform(tc::cluster_rank_of_cta());
     const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kDepth<MODE>; ++i) {
             tc::mbar_init(&ctl->full[i], 1);
             tc::mbar_init(&ctl->empty[i], 1);
         }
@@ -505,6 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc::mbar_init(&ctl->tfull[i], 1);
             tc::mbar_init(&ctl->tempty[i], 2 * kEpiWarps);
         }
+        for (int i = 0; i < kEpiWarps; ++i) tc::mbar_init(&gh_landed[i], 1);
         tc::mbar_init(&ctl->drain, 1);
         tc::mbar_init(&ctl->never, 1);
         ctl->abort = 0;
@@ -580,7 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                                  b_mn ? bk : bn0 + 64, p, bar);
                     }
                     __syncwarp();
-                    if (++st == kStages) {
+                    if (++st == kDepth<MODE>) {
                         st = 0;
                         parity ^= 1;
                     }
@@ -597,7 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t parity = 0;
             const auto advance = [&] {
                 ++it;
-                if (++st == kStages) {
+                if (++st == kDepth<MODE>) {
                     st = 0;
                     parity ^= 1;
                 }
@@ -683,12 +688,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else {
         const int ew = warp - 2, q = warp & 3, h = ew >> 2;
         constexpr int kOwn = MODE == kBack ? kStoreBufs * kStageBuf : kTurnBuf;
-        Epilogue<MODE, PLANES> epi{a, &tm3, store_bufs + ew * kOwn, rank, q, h, lane};
+        Epilogue<MODE, PLANES> epi{a, &tm3, &tm4, store_bufs + kEpiWarps * kHeldBytes * (MODE == kBack) + ew * kOwn,
+                                   store_bufs + ew * kHeldBytes, &gh_landed[ew], rank, q, h, lane};
         bool ok = true;
-        for (int i = 0, j = 0, t; ok && (t = plan.unit(i)) >= 0; ++i) {
-            const Tile w = plan.at(a, t);
+        int t = plan.unit(0);
+        Tile w = t >= 0 ? plan.at(a, t) : Tile{};
+        if (MODE == kBack && t >= 0 && epi.wanted(w)) epi.fetch(w);
+        for (int i = 1, j = 0; ok && t >= 0; ++i) {
             const bool wanted = epi.wanted(w);
-            if (MODE == kBack && wanted) epi.fetch(w, 0);
+            t = plan.unit(i);
+            const Tile next = t >= 0 ? plan.at(a, t) : Tile{};
+            const bool next_wanted = t >= 0 && epi.wanted(next);
             for (int c = 0; ok && c >= 0; ++j) {  // runs of steps
                 const int acc = j & 1;
                 ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->tfull[acc], (j >> 1) & 1, tile_ns,
@@ -708,7 +718,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if constexpr (MODE == kUp)
                             epi.up(w, taddr);
                         else if constexpr (MODE == kBack)
-                            epi.back(w, taddr);
+                            ok = epi.back_when_landed(w, next_wanted ? &next : nullptr, taddr, tile_ns,
+                                                      abort_flag);
                         else
                             epi.product(w, taddr);
                     }
@@ -718,8 +729,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) tc::mbar_arrive_at(tc::at_rank(&ctl->tempty[acc], 0));
                 c = last ? -1 : c + run;
             }
+            if (MODE == kBack && ok && !wanted && next_wanted) epi.fetch(next);
+            w = next;
         }
         if (MODE == kBack) {
+            // A part of gh that was asked for and not used lands first.
+            if (epi.asked != epi.got) tc::mbar_wait(&gh_landed[ew], epi.got & 1);
             if (lane == 0) tc::bulk_wait_all();
             __syncwarp();
         }
@@ -730,7 +745,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // Let the loads already issued land (rank 0 sees both CTAs').
         if (rank == 0)
             for (int it = ctl->consumed; it < ctl->issued; ++it)
-                tc::mbar_wait(&ctl->full[it % kStages], (it / kStages) & 1);
+                tc::mbar_wait(&ctl->full[it % kDepth<MODE>], (it / kDepth<MODE>) & 1);
         atomicExch(a.status, 5u /* DUST_ERR_TIMEOUT */);
     }
     tc::tc_fence_before();
@@ -817,7 +832,7 @@ int max_clusters() {
 }
 
 template <int MODE, int PLANES>
-cudaError_t launch_tc(const CUtensorMap (&m)[4], TcArgs a, int64_t tiles, cudaStream_t s) {
+cudaError_t launch_tc(const CUtensorMap (&m)[5], TcArgs a, int64_t tiles, cudaStream_t s) {
     const int fit = max_clusters<MODE, PLANES>();
     if (fit <= 0) return cudaErrorUnknown;
     if (tiles <= 0) return cudaSuccess;
@@ -827,7 +842,7 @@ cudaError_t launch_tc(const CUtensorMap (&m)[4], TcArgs a, int64_t tiles, cudaSt
     a.stall = take_stall_injection() ? 1 : 0;
     const unsigned clusters = static_cast<unsigned>(std::min<int64_t>(tiles, fit));
     return launch_pdl(k_gated_tc<MODE, PLANES>, dim3(2 * clusters), dim3(kThreads), smem_of<MODE>(), s,
-                      m[0], m[1], m[2], m[3], a);
+                      m[0], m[1], m[2], m[3], m[4], a);
 }
 
 // Rows of `cols` values that are written.
@@ -841,16 +856,31 @@ OutRows out_rows(void* p, int64_t ld, int64_t cols, bool bf16) {
     return OutRows{static_cast<unsigned char*>(p), ld * size, bf16, align};
 }
 
+// gh as 32 rows of 128 bytes at a time.
+bool held_map(CUtensorMap* map, const GatedTiles& t) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const bool f32 = t.X.planes == 3;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(t.f), static_cast<cuuint64_t>(t.T)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(t.ld_gh) * (f32 ? 4 : 2)};
+    const cuuint32_t box[2] = {f32 ? 32u : 64u, 32u}, estr[2] = {1, 1};
+    return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+              const_cast<void*>(t.gh), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 cudaError_t launch_gated_tiles(const GatedTiles& t, cudaStream_t s) {
-    CUtensorMap m[4];
+    CUtensorMap m[5];
     if (!operand_map(&m[0], t.X) || !operand_map(&m[1], t.Wg) || !operand_map(&m[2], t.Wu))
         return cudaErrorInvalidValue;
-    m[3] = m[0];
+    m[3] = m[4] = m[0];
     const bool back = t.gh != nullptr;
     const int planes = t.X.planes;
-    if (back && !make_map(&m[3], t.D, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return cudaErrorInvalidValue;
+    if (back && (!make_map(&m[3], t.D, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) || !held_map(&m[4], t)))
+        return cudaErrorInvalidValue;
     TcArgs a = {};
     a.T = t.T;
     a.d = t.d;
@@ -859,12 +889,7 @@ cudaError_t launch_gated_tiles(const GatedTiles& t, cudaStream_t s) {
     a.bn = planes == 3 ? 128 : logit_columns(t.T, 2 * t.f);
     a.group = kGroup;
     a.act = t.act;
-    if (back) {
-        a.gh = static_cast<const unsigned char*>(t.gh);
-        a.gh_pitch = t.ld_gh * (planes == 3 ? 4 : 2);
-    } else {
-        a.h = out_rows(t.h, t.ld_h, t.f, planes == 1);
-    }
+    if (!back) a.h = out_rows(t.h, t.ld_h, t.f, planes == 1);
     const int64_t tiles = tiles_of(t.T, kHeadTile) * tiles_of(t.f, a.bn / 2);
     if (planes == 1) return back ? launch_tc<kBack, 1>(m, a, tiles, s) : launch_tc<kUp, 1>(m, a, tiles, s);
     return back ? launch_tc<kBack, 3>(m, a, tiles, s) : launch_tc<kUp, 3>(m, a, tiles, s);
@@ -882,10 +907,11 @@ int64_t gated_acc_floats(int64_t rows, int64_t d, int planes, int cut) {
 }
 
 cudaError_t launch_gated_products(const GatedProducts& g, cudaStream_t s) {
-    CUtensorMap m[4];
+    CUtensorMap m[5];
     if (!operand_map(&m[0], g.D) || !operand_map(&m[1], g.Wg) || !operand_map(&m[2], g.Wu) ||
         !operand_map(&m[3], g.X))
         return cudaErrorInvalidValue;
+    m[4] = m[3];
     const int planes = g.D.planes;
     TcArgs a = {};
     a.T = g.T;
