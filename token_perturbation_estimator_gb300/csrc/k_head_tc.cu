@@ -683,6 +683,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
         if (lane == 0) ctl->issued = it;
+        // The last stages' releases land here, too, before the CTA may leave: they
+        // come from the pair's first CTA, whenever their products are done.
+        for (int i = 0; i < kStages && !stop; ++i) {
+            if (!warp_wait(&ctl->empty[st], parity, tile_ns, abort_flag)) {
+                *abort_flag = 1;
+                stop = true;
+            }
+            if (++st == kStages) {
+                st = 0;
+                parity ^= 1;
+            }
+        }
     } else if (warp == 1) {
         if (rank == 0) {
             const bool one = elect_one();
