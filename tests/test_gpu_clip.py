@@ -4,11 +4,18 @@ Tolerances. The norm's squares are summed 16 at a time in fp32 (at most 5
 roundings of 2^-24 each, halved by the root), then in 64 bits, and the result is
 rounded once: 4 x 2^-24. A scaled value has that of the factor and one rounding
 of its own: 2^-24 x 2, bf16 2^-8 more."""
+import ctypes as C
+
 import numpy as np
 import pytest
 
 import token_perturbation_estimator_gb300 as dust
 from helpers import cuda
+
+class Grad(C.Structure):
+    """dust_grad of include/dust.h."""
+    _fields_ = [("g", C.c_void_p), ("out", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32)]
+
 
 pytestmark = pytest.mark.gpu
 
@@ -122,13 +129,12 @@ def test_nan_and_infinity():
 
 
 def test_norm_alone_and_no_tensors():
-    import ctypes as C
     import torch
     dev = cuda()
     norm, out = dust.dust_clip_grads([], 1.0)
     assert norm.item() == 0.0 and out == []
     g = torch.arange(1000, device=dev, dtype=torch.float32)
-    arr = (dust._Grad * 1)()
+    arr = (Grad * 1)()
     arr[0].g, arr[0].n, arr[0].dtype = g.data_ptr(), 1000, dust.F32
     n = dust._query("dust_clip_grads_workspace", 1)
     ws, norm = torch.empty(n, dtype=torch.uint8, device=dev), torch.zeros(1, device=dev)

@@ -231,6 +231,68 @@ def test_gradients_against_differences():
         assert abs(slope - want) <= 2e-3 * scale, act
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,f", [(40, 72, 200), (700, 96, 130)])
+def test_one_gradient_alone(T, d, f, dtype):
+    """Through the C call, which takes NULL for what is not wanted."""
+    import torch
+    dev = cuda()
+    X, Wg, Wu, gh = _inputs(T, d, f, dtype, dev)
+    want = dust.dust_gated_up_grad(gh, X, Wg, Wu)
+    code = dust.BF16 if dtype == "bf16" else dust.F32
+    n = dust._query("dust_gated_up_grad_workspace", T, d, f, code)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    for keep in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 0, 1), (0, 1, 1)):
+        outs = [torch.full_like(w, 7.0) if k else None for w, k in zip(want, keep)]
+        st = dust.lib().dust_gated_up_grad(
+            p(gh), gh.stride(0), p(X), X.stride(0), p(Wg), Wg.stride(0), p(Wu), Wu.stride(0), code, T,
+            d, f, dust.SILU, 0, p(outs[0]), d, p(outs[1]), p(outs[2]), dust.F32, p(ws), n, None)
+        assert st == dust.OK
+        for a, b in zip(outs, want):
+            # the slices of a sum go by the sizes alone: the same bits
+            assert a is None or torch.equal(a, b), keep
+
+
+def test_many_tiles_and_long_sums():
+    """Several groups of row tiles, both widths of tiles, sums over thousands of
+    rows and units, against 64 bits on the GPU."""
+    import torch
+    dev = cuda()
+    for T, d, f, dtype in ((20000, 64, 96, "bf16"), (9000, 520, 1000, "bf16"), (5000, 200, 300, "f32"),
+                           (300, 3000, 5000, "bf16"), (260, 1500, 2000, "f32")):
+        X, Wg, Wu, gh = _inputs(T, d, f, dtype, dev)
+        x, wg, wu, g64 = (t.double() for t in (X, Wg, Wu, gh))
+        g, u = x @ wg.t(), x @ wu.t()
+        p = 1.0 / (1.0 + torch.exp(-g))
+        dG, dU = g64 * u * (p + g * p * (1 - p)), g64 * g * p
+        off = 2 * BF16_TOL if dtype == "bf16" else 0
+        off += 8 * f32_tol(max(T, d, 2 * f))
+        got = (dust.dust_gated_up(X, Wg, Wu), *dust.dust_gated_up_grad(gh, X, Wg, Wu, gW_dtype=X.dtype))
+        for a, b in zip(got, (g * p * u, dG @ wg + dU @ wu, dG.t() @ x, dU.t() @ x)):
+            assert ((a.double() - b).norm() / b.norm()).item() <= off, (T, d, f)
+
+
+def test_bounded_wait_that_runs_out_is_reported():
+    """As for the head: the hook makes the issuing thread wait for nothing; the
+    kernel gives up after its limit, reports it, and the next call is right."""
+    import torch
+    dev = cuda()
+    X, Wg, Wu, gh = _inputs(300, 64, 700, "bf16", dev)
+    want, wanted = dust.dust_gated_up(X, Wg, Wu), dust.dust_gated_up_grad(gh, X, Wg, Wu)
+    assert dust.dust_last_error() == dust.OK
+    dust.lib().dust_debug_inject_timeout(1)
+    dust.dust_gated_up(X, Wg, Wu)
+    assert dust.dust_last_error() == dust.ERR_TIMEOUT
+    assert torch.equal(dust.dust_gated_up(X, Wg, Wu), want)
+    dust.lib().dust_debug_inject_timeout(1)
+    dust.dust_gated_up_grad(gh, X, Wg, Wu)
+    assert dust.dust_last_error() == dust.ERR_TIMEOUT
+    for a, b in zip(dust.dust_gated_up_grad(gh, X, Wg, Wu), wanted):
+        assert torch.equal(a, b)
+    assert dust.dust_last_error() == dust.OK
+
+
 def test_on_another_stream_and_in_a_graph():
     import torch
     dev = cuda()

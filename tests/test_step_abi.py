@@ -22,6 +22,11 @@ def _has_gpu():
         return False
 
 
+class Grad(C.Structure):
+    """dust_grad of include/dust.h."""
+    _fields_ = [("g", C.c_void_p), ("out", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32)]
+
+
 pytestmark = pytest.mark.skipif(_has_gpu(), reason="fake device addresses: CPU only")
 
 
@@ -182,7 +187,7 @@ def test_policy(L, call):
 
 
 def _clip(L, tensors, n=None, max_norm=1.0, norm=FAKE, ws=FAKE, wsb=1 << 20):
-    arr = (dust._Grad * max(1, len(tensors)))()
+    arr = (Grad * max(1, len(tensors)))()
     for a, (g, o, m, dt) in zip(arr, tensors):
         a.g, a.out, a.n, a.dtype = g, o, m, dt
     return L.dust_clip_grads(C.addressof(arr), len(tensors) if n is None else n, max_norm, norm, ws, wsb,

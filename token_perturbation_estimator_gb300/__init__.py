@@ -977,12 +977,11 @@ def dust_policy_loss_grad(nll, old, advantages, seq_offsets, gtotal, ref=None, t
 class _On:
     """What _output and _space ask of a tensor: where it is."""
     def __init__(self, dev):
-        self.device = "cuda:%d" % dev
+        import torch
+        self.device = torch.device("cuda", dev)
 
 
-class _Grad(C.Structure):
-    """dust_grad of include/dust.h."""
-    _fields_ = [("g", C.c_void_p), ("out", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32)]
+_on = functools.lru_cache(maxsize=None)(_On)
 
 
 @_in_stream
@@ -991,23 +990,29 @@ def dust_clip_grads(grads, max_norm, out=None, norm=None, workspace=None):
     min(1, max_norm / norm) with the norm over all of them: in place, or into
     the tensors `out`. Returns (norm f32 [1], the scaled tensors)."""
     ty = _types()
-    dev = ty.current_device()
+    dev, codes = ty.current_device(), ty.code
     grads = list(grads)
     out = grads if out is None else list(out)
     if len(out) != len(grads):
         raise ValueError("out must have as many tensors as grads")
-    arr = (_Grad * max(1, len(grads)))()
-    for a, g, o in zip(arr, grads, out):
-        code = ty.code.get(g.dtype)
+    flat = []  # dust_grad of include/dust.h, as 64-bit words
+    for g, o in zip(grads, out):
+        code = codes.get(g.dtype)
         if code is None or not g.is_contiguous() or g.get_device() != dev:
             _values(g, "a gradient", range(65))
             raise ValueError("expected a contiguous tensor")
-        a.g, a.n, a.dtype = g.data_ptr(), g.numel(), code
-        a.out = a.g if o is g else _dense(o, "out", g.dtype, g.shape, dev)
-    ref = _On(dev)
+        to = at = g.data_ptr()
+        if o is not g:
+            if not (o.dtype is g.dtype and o.shape == g.shape and o.is_contiguous()
+                    and o.get_device() == dev):
+                _dense(o, "out", g.dtype, g.shape, dev)  # raises
+            to = o.data_ptr()
+        flat += (at, to, g.numel(), code)
+    words = (C.c_int64 * len(flat))(*flat)
+    ref = _on(dev)
     norm, norm_at = _output(norm, "norm", ty.f32, (1,), ref, dev)
     workspace, ws_at, ws_bytes = _space(workspace, "dust_clip_grads_workspace", ref, dev, len(grads))
-    st = lib().dust_clip_grads(C.addressof(arr), len(grads), max_norm, norm_at, ws_at, ws_bytes,
+    st = lib().dust_clip_grads(C.addressof(words), len(grads), max_norm, norm_at, ws_at, ws_bytes,
                                ty.stream_of(dev))
     _check(st, "dust_clip_grads")
     return norm, out
