@@ -682,7 +682,13 @@ dust_status dust_distill_loss_grad(const void* H, int64_t ld_h, const void* E, i
  *            either may be NULL. Overwritten, or added to with
  *            DUST_ACCUMULATE (the only flag; needs DUST_F32).
  *   workspace  device, >= the size that the matching query gives, 256-byte
- *            aligned; contents on entry are ignored.
+ *            aligned; contents on entry are ignored. Both calls' has room for
+ *            copies of X, Wg and Wu (fp32: three planes of bf16), which bf16
+ *            rows that start on 16 bytes do not touch; the gradients' for dG and
+ *            dU, 4 bytes (fp32: 12) for every row and unit, rounded up to 256
+ *            each, for a copy of gh, and for slices' sums of up to 160 MB.
+ *            8192 rows, d 2048, f 8192, bf16: 101 and 504 MB. Up to 4 rows,
+ *            the forward needs none (0 bytes, and then NULL will do).
  * No output overlaps an input, another output or the workspace.
  * bf16 inputs: products of the exact bf16 values summed in fp32, the
  * activation and the product in fp32, h rounded once; the backward's dG and dU
@@ -817,7 +823,8 @@ dust_status dust_qk_norm_rope_grad(const dust_heads* gyq, const dust_heads* gyk,
  *            each may be NULL; delta device f32 [S - 1][T] or NULL.
  *   gtotal   device f32 [S]; gnll device f32 [S][T]; may be nll itself.
  *   workspace  device, >= dust_policy_loss_workspace bytes, 256-byte aligned;
- *            the same for both calls.
+ *            the same for both calls (0 bytes, and then NULL will do, for few
+ *            tokens).
  * No other output overlaps an input or another output.
  * S >= 1; S*T and n_seq up to 2^31 - 1 (DUST_ERR_RANGE). n_seq = 0: no token is
  * scored.
@@ -950,7 +957,8 @@ dust_status dust_debug_inject_timeout(int32_t on);
  * status word (DUST_OK; DUST_ERR_TIMEOUT when a kernel's bounded wait ran out
  * since the last call; DUST_ERR_INVALID_ARG when dust_scatter_gE or
  * dust_estimate_gE met a token id outside [0, V), or a head loss, a
- * distillation or one of their gradients an id >= V). DUST_ERR_CUDA if the
+ * distillation or one of their gradients an id >= V, or dust_qk_norm_rope or its
+ * gradient a position past the tables). DUST_ERR_CUDA if the
  * synchronisation failed.
  */
 dust_status dust_last_error(void* stream);

@@ -238,6 +238,19 @@ def test_padded_tokens_hide_what_they_hold():
     assert dust.dust_last_error() == dust.OK
 
 
+@pytest.mark.parametrize("D", [64, 30])
+def test_tables_without_a_position(D):
+    """No rows in the tables: every token that is no padding is past them."""
+    import torch
+    dev = cuda()
+    q, k, wq, wk, pos, c, s, gyq, gyk = _inputs(9, 2, 1, D, D, "f32", dev)
+    c, s = c[:0], s[:0]
+    yq, yk = dust.dust_qk_norm_rope(q, k, wq, wk, pos, c, s)
+    grads = dust.dust_qk_norm_rope_grad(gyq, gyk, q, k, wq, wk, pos, c, s)
+    assert (yq == 0).all() and (yk == 0).all() and all((g == 0).all() for g in grads)
+    assert dust.dust_last_error() == dust.ERR_INVALID_ARG
+
+
 def test_accumulates_and_no_tokens():
     import torch
     dev = cuda()

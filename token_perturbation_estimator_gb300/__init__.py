@@ -818,9 +818,9 @@ class _Heads(C.Structure):
 def _heads(t, name, dtype, shape, dev):
     """A reference to the dust_heads of t, a tensor of this dtype and shape [T, heads, D] on CUDA
     device `dev` with unit stride inside a head; raises ValueError for any other."""
-    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev):
-        if not t.is_cuda:
-            raise ValueError("expected a CUDA tensor")
+    if t is None or not (t.dtype is dtype and t.shape == shape and t.get_device() == dev):
+        if t is None or not t.is_cuda:
+            raise ValueError("%s: expected a CUDA tensor" % name)
         _expect(t, name, (dtype,), shape=shape)
         raise ValueError("%s must be on cuda:%d, got %s" % (name, dev, t.device))
     token, head, step = t.stride()

@@ -130,8 +130,9 @@ __device__ __forceinline__ void load_turns(const Args& g, const Columns<V, G, PE
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int from = HALVES ? col.a[i] : col.a[i] / 2;
-        // The turns that there are: all or none (halves, or a single one).
-        const int n = HALVES ? (lane + i * G < g.turned ? V : 0) : col.have[i] ? g.rot / 2 - from : 0;
+        // The turns that there are: all or none (halves, or a single one), and none
+        // without a position.
+        const int n = pos < 0 ? 0 : HALVES ? (lane + i * G < g.turned ? V : 0) : col.have[i] ? g.rot / 2 - from : 0;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             t.c[i][k] = 1.0f;
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) k_rope(const Args g) {
         next.values(col, w.in && pos >= 0, x, y);
         fetch(t + w.step);
         Turns<V, PER> turns;
-        load_turns<V, G, PER, HALVES>(g, col, lane, max(pos, static_cast<int64_t>(0)), turns);
+        load_turns<V, G, PER, HALVES>(g, col, lane, pos, turns);
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas)
         next_g.values(col, w.in && pos >= 0, u, v);
         fetch(t + w.step);
         Turns<V, PER> turns;
-        load_turns<V, G, PER, HALVES>(g, col, lane, max(pos, static_cast<int64_t>(0)), turns);
+        load_turns<V, G, PER, HALVES>(g, col, lane, pos, turns);
         turn<true, V, PER, HALVES>(u, v, turns);  // gm
         // sum x^2 and sum gm w x together; the root comes to the second later.
         float s = 0.0f, dot = 0.0f;

@@ -3,6 +3,8 @@
 // argument checks and dispatch.
 #include <algorithm>
 #include <cmath>
+#include <memory>
+#include <new>
 
 #include "step.cuh"
 
@@ -186,9 +188,8 @@ struct Span {
 };
 
 // Whether an output overlaps another tensor's input or output (or its own
-// input without being it).
-bool clip_overlaps(const dust_grad* g, int64_t n) {
-    Span spans[2 * kMaxGrads];
+// input without being it). spans: room for 2 n.
+bool clip_overlaps(const dust_grad* g, int64_t n, Span* spans) {
     int64_t m = 0;
     for (int64_t i = 0; i < n; ++i) {
         if (g[i].n == 0) continue;
@@ -382,7 +383,11 @@ dust_status dust_clip_grads(const dust_grad* grads, int64_t n, float max_norm, f
         if (!g.g || !aligned_to(g.g, g.dtype) || !aligned_to(g.out, g.dtype)) return DUST_ERR_INVALID_ARG;
         (g.out ? outs : nulls) = true;
     }
-    if (outs && (nulls || clip_overlaps(grads, n))) return DUST_ERR_INVALID_ARG;
+    if (outs) {
+        const std::unique_ptr<Span[]> spans(new (std::nothrow) Span[static_cast<size_t>(2 * n)]);
+        if (!spans) return DUST_ERR_CUDA;
+        if (nulls || clip_overlaps(grads, n, spans.get())) return DUST_ERR_INVALID_ARG;
+    }
     if (!ws_ok(workspace, ws_bytes, a256(clip_workspace_bytes()))) return DUST_ERR_WORKSPACE;
     return cuda_status(launch_clip(grads, n, max_norm, norm, workspace, static_cast<cudaStream_t>(stream)));
 }
