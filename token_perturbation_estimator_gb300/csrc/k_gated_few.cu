@@ -7,6 +7,10 @@
 // A warp takes two units, four rows of weights, over the whole width or a part
 // of it: `split` warps of a CTA share a pair of units, so that there are
 // CTAs for the whole GPU. X comes from the L1 after its first use.
+//
+// Bound by the weights' way from memory, or its latency: 1 row, d 512, f 2048
+// bf16 takes 5.0 us (9 with the weights out of the L2; 10 as tiles), 4 rows, d
+// 2048, f 8192 17 (28; 21 as tiles for 16 rows), 67 MB at 3.9 TB/s.
 #include <algorithm>
 
 #include "gated.cuh"

@@ -12,7 +12,8 @@
 // a value, and single ones by the launches' latency. Whether a ratio is beyond
 // its bound is decided in fp32 where that is certain, else in 64 bits, of which
 // the GPU does a 64th as many a second: in 64 bits throughout, 33 slices of
-// 65536 tokens took 48 us.
+// 65536 tokens took 48 us. Now 25, where one slice takes 14.7; a gradient of one
+// slice 9.2; 1531 tokens 7.
 #include <algorithm>
 #include <cmath>
 
