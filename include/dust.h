@@ -818,7 +818,8 @@ dust_status dust_qk_norm_rope_grad(const dust_heads* gyq, const dust_heads* gyk,
  *   targets  device i32 [T], negative where a token has none (as for
  *            dust_head_loss), or NULL: all have one.
  *   clip_low in [0, 1], clip_high >= 0, beta finite (infinite clip_high: no
- *            bound). Whether a ratio is beyond its bound is decided in 64 bits.
+ *            bound). Whether a ratio is beyond its bound is decided in 64 bits
+ *            (the bounds as given, the difference of nll and old exactly).
  *   loss     device f32 [S][T] or NULL; total, kl_mean, clipped device f32 [S],
  *            each may be NULL; delta device f32 [S - 1][T] or NULL.
  *   gtotal   device f32 [S]; gnll device f32 [S][T]; may be nll itself.
@@ -838,15 +839,15 @@ dust_status dust_policy_loss_workspace(size_t* bytes, int64_t S, int64_t T, int6
 dust_status dust_policy_loss(const float* nll, const float* old, const float* ref,
                              const float* advantages, int32_t per_token,
                              const int32_t* seq_offsets, int64_t n_seq, const int32_t* targets,
-                             int64_t S, int64_t T, float clip_low, float clip_high, float beta,
+                             int64_t S, int64_t T, double clip_low, double clip_high, float beta,
                              dust_mean mean, float* loss, float* total, float* kl_mean,
                              float* clipped, float* delta, void* workspace, size_t ws_bytes,
                              void* stream);
 dust_status dust_policy_loss_grad(const float* nll, const float* old, const float* ref,
                                   const float* advantages, int32_t per_token,
                                   const int32_t* seq_offsets, int64_t n_seq,
-                                  const int32_t* targets, int64_t S, int64_t T, float clip_low,
-                                  float clip_high, float beta, dust_mean mean,
+                                  const int32_t* targets, int64_t S, int64_t T, double clip_low,
+                                  double clip_high, float beta, dust_mean mean,
                                   const float* gtotal, float* gnll, void* workspace,
                                   size_t ws_bytes, void* stream);
 

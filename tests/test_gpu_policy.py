@@ -50,9 +50,9 @@ def reference(nll, old, ref, adv, off, tg, beta, by_sequence, per_token, gtotal=
     seq = np.where(inside, seq, 0)
     A = adv if per_token else (adv[seq] if len(adv) else np.zeros(T))
     step = old - nll
-    clipped = np.where(A > 0, step > np.log1p(np.float64(np.float32(HIGH))),
-                       (A < 0) & (step < np.log1p(-np.float64(np.float32(LOW)))))
-    bound = np.where(A > 0, 1 + np.float64(np.float32(HIGH)), 1 - np.float64(np.float32(LOW)))
+    clipped = np.where(A > 0, step > np.log1p(HIGH),
+                       (A < 0) & (step < np.log1p(-LOW)))
+    bound = np.where(A > 0, 1 + HIGH, 1 - LOW)
     ratio = np.exp(step)
     first = -np.where(clipped, bound, ratio) * A
     r = nll - _np(ref) if ref is not None else np.zeros_like(nll)
@@ -157,7 +157,7 @@ def test_borders_are_decided_exactly():
     import torch
     dev = cuda()
     f = np.float32
-    hi, lo = np.log1p(np.float64(f(HIGH))), np.log1p(-np.float64(f(LOW)))
+    hi, lo = np.log1p(HIGH), np.log1p(-LOW)
     steps = []
     for b in (hi, lo):
         x = f(b)

@@ -55,6 +55,7 @@ _lib = None
 
 def _signatures():
     i32, i64, u32, u64, f32 = C.c_int32, C.c_int64, C.c_uint32, C.c_uint64, C.c_float
+    f64 = C.c_double
     P, SZ, PSZ = C.c_void_p, C.c_size_t, C.POINTER(C.c_size_t)
     return {
         "dust_status_string": (C.c_char_p, [i32]),
@@ -114,9 +115,9 @@ def _signatures():
         "dust_qk_norm_rope_grad": (i32, [P, P, P, i64, P, i64, i32, i64, i64, P, P, f32, P, P, P,
                                          i64, i64, i32, u32, P, P, P, P, P, SZ, P]),
         "dust_policy_loss_workspace": (i32, [PSZ, i64, i64, i64]),
-        "dust_policy_loss": (i32, [P, P, P, P, i32, P, i64, P, i64, i64, f32, f32, f32, i32, P, P,
+        "dust_policy_loss": (i32, [P, P, P, P, i32, P, i64, P, i64, i64, f64, f64, f32, i32, P, P,
                                    P, P, P, P, SZ, P]),
-        "dust_policy_loss_grad": (i32, [P, P, P, P, i32, P, i64, P, i64, i64, f32, f32, f32, i32,
+        "dust_policy_loss_grad": (i32, [P, P, P, P, i32, P, i64, P, i64, i64, f64, f64, f32, i32,
                                         P, P, P, SZ, P]),
         "dust_clip_grads_workspace": (i32, [PSZ, i64]),
         "dust_clip_grads": (i32, [P, i64, f32, P, P, SZ, P]),

@@ -240,7 +240,7 @@ __device__ __forceinline__ void losses_of(const PolicyProblem& p, const Token (&
         for (int i = 0; i < N; ++i) clipped[i] = Side::exactly(p, k[i].adv, k[i].old, nll[i]);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float bound = k[i].adv > 0.0f ? 1.0f + p.clip_high : 1.0f - p.clip_low;
+        const float bound = k[i].adv > 0.0f ? p.most : p.least;
         const float ratio = expf(k[i].old - nll[i]);
         loss[i] = -(clipped[i] ? bound : ratio) * k[i].adv;
         kl[i] = 0.0f;

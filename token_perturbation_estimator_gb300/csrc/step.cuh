@@ -48,7 +48,8 @@ struct PolicyProblem {
     int64_t n_seq, S, T;
     double low, high;          // bounds of old - nll
     float low32, high32;       // the same, rounded
-    float clip_low, clip_high, beta;
+    float least, most;         // the ratio's bounds
+    float beta;
     bool by_sequence;
 };
 size_t policy_workspace_bytes(int64_t S, int64_t T, int64_t n_seq);

@@ -156,11 +156,11 @@ dust_status check_policy_sizes(int64_t S, int64_t T, int64_t n_seq) {
     return DUST_OK;
 }
 
-dust_status check_policy(const PolicyProblem& p, float clip_low, float clip_high, dust_mean mean,
+dust_status check_policy(const PolicyProblem& p, double clip_low, double clip_high, dust_mean mean,
                          const void* ws, size_t ws_bytes) {
     const dust_status st = check_policy_sizes(p.S, p.T, p.n_seq);
     if (st != DUST_OK) return st;
-    if (!(clip_low >= 0.0f && clip_low <= 1.0f) || !(clip_high >= 0.0f) || !std::isfinite(p.beta))
+    if (!(clip_low >= 0.0 && clip_low <= 1.0) || !(clip_high >= 0.0) || !std::isfinite(p.beta))
         return DUST_ERR_INVALID_ARG;
     if (mean != DUST_MEAN_TOKEN && mean != DUST_MEAN_SEQUENCE) return DUST_ERR_INVALID_ARG;
     if (p.T > 0 && (!p.nll || !p.old || !p.offsets)) return DUST_ERR_INVALID_ARG;
@@ -172,11 +172,11 @@ dust_status check_policy(const PolicyProblem& p, float clip_low, float clip_high
 PolicyProblem policy_problem(const float* nll, const float* old, const float* ref,
                              const float* advantages, int32_t per_token, const int32_t* seq_offsets,
                              int64_t n_seq, const int32_t* targets, int64_t S, int64_t T,
-                             float clip_low, float clip_high, float beta, dust_mean mean) {
-    const double low = std::log1p(-static_cast<double>(clip_low));
-    const double high = std::log1p(static_cast<double>(clip_high));
+                             double clip_low, double clip_high, float beta, dust_mean mean) {
+    const double low = std::log1p(-clip_low), high = std::log1p(clip_high);
     return {nll, old, ref, advantages, per_token != 0, seq_offsets, targets, n_seq, S, T, low, high,
-            static_cast<float>(low), static_cast<float>(high), clip_low, clip_high, beta,
+            static_cast<float>(low), static_cast<float>(high), static_cast<float>(1.0 - clip_low),
+            static_cast<float>(1.0 + clip_high), beta,
             mean == DUST_MEAN_SEQUENCE};
 }
 
@@ -332,7 +332,7 @@ dust_status dust_policy_loss_workspace(size_t* bytes, int64_t S, int64_t T, int6
 dust_status dust_policy_loss(const float* nll, const float* old, const float* ref,
                              const float* advantages, int32_t per_token, const int32_t* seq_offsets,
                              int64_t n_seq, const int32_t* targets, int64_t S, int64_t T,
-                             float clip_low, float clip_high, float beta, dust_mean mean, float* loss,
+                             double clip_low, double clip_high, float beta, dust_mean mean, float* loss,
                              float* total, float* kl_mean, float* clipped, float* delta,
                              void* workspace, size_t ws_bytes, void* stream) {
     const PolicyProblem p = policy_problem(nll, old, ref, advantages, per_token, seq_offsets, n_seq, targets,
@@ -352,7 +352,7 @@ dust_status dust_policy_loss(const float* nll, const float* old, const float* re
 dust_status dust_policy_loss_grad(const float* nll, const float* old, const float* ref,
                                   const float* advantages, int32_t per_token, const int32_t* seq_offsets,
                                   int64_t n_seq, const int32_t* targets, int64_t S, int64_t T,
-                                  float clip_low, float clip_high, float beta, dust_mean mean,
+                                  double clip_low, double clip_high, float beta, dust_mean mean,
                                   const float* gtotal, float* gnll, void* workspace, size_t ws_bytes,
                                   void* stream) {
     const PolicyProblem p = policy_problem(nll, old, ref, advantages, per_token, seq_offsets, n_seq, targets,
