@@ -695,6 +695,8 @@ dust_status dust_distill_loss_grad(const void* H, int64_t ld_h, const void* E, i
  * are rounded to bf16 (they are tensor-core operands). fp32 inputs: every
  * product and sum to fp32 accuracy (operands to 24 bits, or to 2^-133 where
  * that is more).
+ * An infinity or NaN in a row reaches what the row enters, in fp32 as a NaN
+ * where fp32 arithmetic might have kept an infinity.
  * d >= 1, f >= 1, T >= 0; T and d up to 2^31 - 2^16, f up to 2^30 - 2^16; with
  * all of them rounded up to multiples of 256, T*d, T*f and f*d up to 2^37, and
  * at most 2^30 tiles of 256 rows x 64 columns (DUST_ERR_RANGE).
