@@ -201,6 +201,63 @@ def test_bounds_at_their_ends():
     assert near(one, -torch.minimum(torch.exp(step) * adv.double(), adv.double()))
 
 
+@pytest.mark.parametrize("by_sequence", [False, True])
+@pytest.mark.parametrize("S", [1, 2, 7])
+@pytest.mark.parametrize("lengths", [[43], [7, 29, 7], [1531], [300, 25], [3, 4000, 900], [70001]],
+                         ids=lambda v: "%dx%d" % (len(v), sum(v)))
+def test_total_of_losses_that_cancel(lengths, S, by_sequence):
+    """A ratio of 1 makes a token's loss the advantage, exactly, so that only the
+    weights and sums can be off. Up to 2048 tokens of 4 slices those carry what
+    their roundings lose along: below 2^7 roundings of 2^-48 of the magnitudes, and
+    the result's own half step. Beyond, in either, a thread adds 4 tokens' terms in
+    fp32: each of the 4 additions rounds by at most half a step of its running sum,
+    that is of the thread's magnitudes, so that together they are off by at most
+    4 * 2^-24 of all magnitudes; all else is in 64 bits or carried along."""
+    import torch
+    dev = cuda()
+    rng = np.random.default_rng(5)
+    T, f = sum(lengths), np.float32
+    adv = rng.standard_normal(T).astype(f)
+    adv[1::2] = -adv[:T - 1:2][:len(adv[1::2])] * f(1 + 1e-4)  # pairs of nearly opposite sign
+    old = rng.uniform(0.1, 9.0, T).astype(f)
+    off = offsets_from_lengths(lengths).astype(np.int32)
+    loss, total = dust.dust_policy_loss(
+        _dev(np.tile(old, (S, 1)), dev), _dev(old, dev), _dev(adv, dev), _dev(off, dev),
+        clip_low=LOW, clip_high=HIGH, per_token=True,
+        mean=dust.MEAN_SEQUENCE if by_sequence else dust.MEAN_TOKEN)[:2]
+    assert torch.equal(loss, _dev(np.tile(-adv, (S, 1)), dev))
+    n = np.repeat(lengths, lengths) * len(lengths) if by_sequence else np.full(T, T)
+    terms = -adv.astype(np.float64) / n
+    m, mag = terms.sum(), np.abs(terms).sum()
+    tol = 2.0 ** -24 * abs(m) + (2.0 ** -41 if T <= 2048 and S <= 4 else 4 * 2.0 ** -24) * mag
+    assert (np.abs(_np(total) - m) <= tol).all()
+
+
+@pytest.mark.parametrize("T", [1, 4, 64, 1000, 2048, 2049, 4096])
+def test_infinite_losses_make_an_infinite_total(T):
+    """One token whose ratio is above fp32's range: its loss is infinite, and the
+    mean with it, in this slice alone; a NaN makes the mean a NaN."""
+    import torch
+    dev = cuda()
+    for S, bad in ((1, 0), (3, 1), (33, 32)):
+        nll = torch.ones(S, T, device=dev)
+        old = torch.ones(T, device=dev)
+        adv = torch.full((T,), -1.0, device=dev)
+        off = torch.tensor([0, T], dtype=torch.int32, device=dev)
+        t = T // 2
+        nll[bad, t] = -100.0  # e^101 > 2^128
+        for mean in (dust.MEAN_TOKEN, dust.MEAN_SEQUENCE):
+            total = dust.dust_policy_loss(nll, old, adv, off, per_token=True, mean=mean)[1]
+            want = torch.ones(S, device=dev)
+            want[bad] = float("inf")
+            assert torch.equal(total[want == 1], want[want == 1].double().to(total.dtype))
+            assert total[bad] == float("inf")
+            two = adv.clone()
+            two[t] = float("nan")
+            total = dust.dust_policy_loss(nll, old, two, off, per_token=True, mean=mean)[1]
+            assert torch.isnan(total).all()
+
+
 def test_gradient_against_differences():
     """Central differences of the total, where no ratio is near a bound."""
     import torch

@@ -9,11 +9,13 @@
 //
 // A loss takes about a hundred instructions (two exponentials, a series, the
 // sums), so that many slices are bound by issue rather than by their 12 bytes
-// a value, and single ones by the launches' latency. Whether a ratio is beyond
-// its bound is decided in fp32 where that is certain, else in 64 bits, of which
-// the GPU does a 64th as many a second: in 64 bits throughout, 33 slices of
-// 65536 tokens took 48 us. Now 25, where one slice takes 14.7; a gradient of one
-// slice 9.2; 1531 tokens 7.
+// a value, and single ones by the launches' latency. The losses' signs cancel in
+// their mean, so that it is added up in 64 bits beyond a thread's 4 tokens, or
+// with what roundings lose, and the weights' own rounding is made good. Whether
+// a ratio is beyond its bound is decided in fp32 where that is certain, else in
+// 64 bits, of which the GPU does a 64th as many a second: in 64 bits throughout,
+// 33 slices of 65536 tokens took 48 us. Now 25, where one slice takes 14.9; a
+// gradient of one slice 9.2; 1531 tokens 7.
 #include <algorithm>
 #include <cmath>
 
@@ -39,7 +41,7 @@ struct Space {
     Counts* counts;
     int32_t* of_seq;   // [n_seq] scored tokens
     int32_t* seq_of;   // [T] sequence of a scored token, or -1
-    float* parts;      // [blocks][S][3]
+    double* parts;     // [blocks][S][3]
     size_t clear;      // bytes that start at 0, from counts on
     size_t total;
 };
@@ -60,7 +62,7 @@ Space carve(void* ws, int64_t S, int64_t T, int64_t n_seq) {
     w.of_seq = reinterpret_cast<int32_t*>(take(4 * n_seq));
     w.clear = at;
     w.seq_of = reinterpret_cast<int32_t*>(take(4 * T));
-    w.parts = reinterpret_cast<float*>(take(12 * blocks_of(T) * S));
+    w.parts = reinterpret_cast<double*>(take(24 * blocks_of(T) * S));
     w.total = at;
     return w;
 }
@@ -189,18 +191,21 @@ __device__ __forceinline__ float kl_of(float r) {
 // What a token needs of everything but nll.
 struct Token {
     bool scored;
-    float old, ref, adv, weight;
+    float old, ref, adv;
+    float weight, rest;  // and what its rounding leaves, the same for a whole sequence
 
     __device__ __forceinline__ void load(const PolicyProblem& p, const Counts& c, const int32_t* of_seq,
                                          int32_t seq, int64_t t) {
         scored = seq >= 0;
-        old = ref = adv = weight = 0.0f;
+        old = ref = adv = weight = rest = 0.0f;
         if (!scored) return;
         old = p.old[t];
         ref = p.ref ? p.ref[t] : 0.0f;
         adv = p.advantages[p.per_token ? t : seq];
-        weight = 1.0f / (p.by_sequence ? static_cast<float>(c.sequences) * static_cast<float>(of_seq[seq])
-                                       : static_cast<float>(c.tokens));
+        const float n = p.by_sequence ? static_cast<float>(c.sequences) * static_cast<float>(of_seq[seq])
+                                      : static_cast<float>(c.tokens);
+        weight = 1.0f / n;
+        rest = fmaf(-weight, n, 1.0f) * weight;
     }
 };
 
@@ -263,12 +268,30 @@ __device__ __forceinline__ float slope_of(const PolicyProblem& p, const Token& k
     return g;
 }
 
-// A slice's sums over the lanes, to lane 0.
-__device__ __forceinline__ void warp_sums(float (&sum)[3]) {
+// A sum over the lanes: of terms of one sign (the KL term, clipped tokens) ...
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-    for (int j = 0; j < 3; ++j)
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// ... and of the losses, whose signs cancel: what the roundings lose (and have
+// lost) is added up as well (Knuth), and counts unless the sum has overflowed,
+// where it is no number. In fp32, the sum of 12 sequences' 325 tokens was 1.2e-6
+// off where its losses' own roundings make 0.8e-6.
+__device__ __forceinline__ double with_rest(double v, double lost) { return isfinite(v) ? v + lost : v; }
+__device__ __forceinline__ void add_exactly(float& v, float& lost, float u) {
+    const float s = v + u, t = s - v;
+    lost += (v - (s - t)) + (u - t);
+    v = s;
+}
+__device__ __forceinline__ double warp_sum_exact(float v, float lost) {
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], off);
+    for (int off = 16; off > 0; off >>= 1) {
+        lost += __shfl_xor_sync(0xffffffffu, lost, off);
+        add_exactly(v, lost, __shfl_xor_sync(0xffffffffu, v, off));
+    }
+    return with_rest(v, lost);
 }
 
 struct Outputs {
@@ -277,7 +300,7 @@ struct Outputs {
 
 // The CTAs' sums [blocks][n] added up: each column by a power of two of threads,
 // then theirs by halves.
-__device__ __forceinline__ void join_parts(const float* parts, int64_t blocks, int64_t n, const Outputs& o) {
+__device__ __forceinline__ void join_parts(const double* parts, int64_t blocks, int64_t n, const Outputs& o) {
     __shared__ double sh[kThreads];
     for (int64_t c0 = 0; c0 < n; c0 += kThreads) {
         const int cols = static_cast<int>(min(n - c0, static_cast<int64_t>(kThreads)));
@@ -285,7 +308,7 @@ __device__ __forceinline__ void join_parts(const float* parts, int64_t blocks, i
         double v = 0.0;
         if (turn < turns)
 #pragma unroll 8
-            for (int64_t b = turn; b < blocks; b += turns) v += static_cast<double>(__ldcg(parts + b * n + c0 + c));
+            for (int64_t b = turn; b < blocks; b += turns) v += __ldcg(parts + b * n + c0 + c);
         sh[threadIdx.x] = v;
         __syncthreads();
         for (int h = turns / 2; h > 0; h /= 2) {
@@ -303,9 +326,10 @@ __device__ __forceinline__ void join_parts(const float* parts, int64_t blocks, i
 
 __global__ void __launch_bounds__(kThreads, 3)
     k_policy(const PolicyProblem p, const Outputs o, int64_t blocks, int64_t groups, Counts* counts,
-             const int32_t* __restrict__ of_seq, const int32_t* __restrict__ seq_of, float* parts) {
+             const int32_t* __restrict__ of_seq, const int32_t* __restrict__ seq_of, double* parts) {
     pdl_wait();
     pdl_trigger();
+    __shared__ float losses[kSlices][kThreads];  // each thread's
     __shared__ float sums[kThreads / 32][kSlices][3];
     __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -345,11 +369,12 @@ __global__ void __launch_bounds__(kThreads, 3)
             now[i] = next[i];
             if (s + 1 < s1 && i < mine) next[i] = nll[i * kThreads];
         }
-        float sum[3] = {0.0f, 0.0f, 0.0f};
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         losses_of(p, k, now, l, kl, clipped);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             sum[0] = fmaf(k[i].weight, l[i], sum[0]);
+            sum[3] = fmaf(k[i].rest, l[i], sum[3]);
             sum[1] = fmaf(k[i].weight, kl[i], sum[1]);
             if (clipped[i]) sum[2] += k[i].weight;
             if (loss && i < mine) loss[i * kThreads] = l[i];
@@ -357,18 +382,30 @@ __global__ void __launch_bounds__(kThreads, 3)
         }
         if (loss) loss += p.T;
         if (delta) delta += p.T;
-        warp_sums(sum);
-        if (lane == 0)
+        losses[s - s0][threadIdx.x] = sum[0];
 #pragma unroll
-            for (int j = 0; j < 3; ++j) sums[warp][s - s0][j] = sum[j];
+        for (int j = 0; j < 3; ++j) {
+            sum[j + 1] = warp_sum(sum[j + 1]);
+            if (lane == 0) sums[warp][s - s0][j] = sum[j + 1];
+        }
     }
     if (!o.total && !o.kl && !o.clipped) return;
     __syncthreads();
-    for (int i = threadIdx.x; i < (s1 - s0) * 3; i += kThreads) {
-        float v = 0.0f;
+    // The losses' signs cancel: their sums in 64 bits, a warp per slice.
+    for (int s = warp; s < s1 - s0; s += kThreads / 32) {
+        double v = 0.0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) v += sums[w][i / 3][i % 3];
-        __stcg(parts + (block * p.S + s0) * 3 + i, v);
+        for (int i = 0; i < kThreads / 32; ++i) v += static_cast<double>(losses[s][32 * i + lane]);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+        float own = 0.0f;
+        if (lane < 3)
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) own += sums[w][s][lane];
+        const double rest = static_cast<double>(__shfl_sync(0xffffffffu, own, 2));
+        double* to = parts + (block * p.S + s0 + s) * 3;
+        if (lane < 2) __stcg(to + 1 + lane, static_cast<double>(own));
+        if (lane == 0) __stcg(to, with_rest(v, rest));
     }
     __threadfence();
     __syncthreads();
@@ -406,7 +443,7 @@ __global__ void __launch_bounds__(kFewThreads)
     k_policy_few(const PolicyProblem p, const Outputs o, const float* __restrict__ gtotal, float* gnll) {
     __shared__ Counts counts;
     __shared__ int32_t of_seq[kFewSequences];
-    __shared__ float sums[kFewThreads / 32][kFewSlices][3];
+    __shared__ double sums[kFewThreads / 32][kFewSlices][3];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -433,7 +470,7 @@ __global__ void __launch_bounds__(kFewThreads)
     }
     if (threadIdx.x == 0) counts = {scored, open, 0};
     __syncthreads();
-    float sum[kFewSlices][3] = {};
+    float sum[kFewSlices][4] = {};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = i * kFewThreads + threadIdx.x;
@@ -453,7 +490,9 @@ __global__ void __launch_bounds__(kFewThreads)
                 const Token one[1] = {k};
                 const float value[1] = {nll};
                 losses_of(p, one, value, l, kl, clipped);
-                sum[s][0] = fmaf(k.weight, l[0], sum[s][0]);
+                const float term = k.weight * l[0];
+                sum[s][3] += fmaf(k.rest, l[0], fmaf(k.weight, l[0], -term));
+                add_exactly(sum[s][0], sum[s][3], term);
                 sum[s][1] = fmaf(k.weight, kl[0], sum[s][1]);
                 if (clipped[0]) sum[s][2] += k.weight;
                 if (s == 0) clean = l[0];
@@ -466,15 +505,19 @@ __global__ void __launch_bounds__(kFewThreads)
 #pragma unroll
         for (int s = 0; s < kFewSlices; ++s) {
             if (s >= S) continue;
-            warp_sums(sum[s]);
-            if (lane == 0)
-#pragma unroll
-                for (int j = 0; j < 3; ++j) sums[warp][s][j] = sum[s][j];
+            const double total = warp_sum_exact(sum[s][0], sum[s][3]);
+            sum[s][1] = warp_sum(sum[s][1]);
+            sum[s][2] = warp_sum(sum[s][2]);
+            if (lane == 0) {
+                sums[warp][s][0] = total;
+                sums[warp][s][1] = sum[s][1];
+                sums[warp][s][2] = sum[s][2];
+            }
         }
         __syncthreads();
         if (warp < 3 * S) {
             const int s = warp / 3, j = warp % 3;
-            double v = static_cast<double>(sums[lane][s][j]);
+            double v = sums[lane][s][j];
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
             float* out = j == 0 ? o.total : j == 1 ? o.kl : o.clipped;
