@@ -799,7 +799,7 @@ dust_status dust_qk_norm_rope_grad(const dust_heads* gyq, const dust_heads* gyk,
  * estimator's loss changes are under rewards, and the gradient that
  * dust_head_loss_grad takes as gloss. With rho = exp(old - nll), r = nll - ref
  * and A the token's advantage:
- *   kl    = exp(r) - r - 1                       (0 without ref)
+ *   kl    = exp(r) - r - 1                       (0 without ref; beta 0: kl_mean only)
  *   loss  = -min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A) + beta kl
  *   total[s] = sum_t w[t] loss[s][t];  kl_mean, clipped likewise (clipped: the
  *       share of tokens for which the clipped product is the smaller one)

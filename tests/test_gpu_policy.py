@@ -258,6 +258,30 @@ def test_infinite_losses_make_an_infinite_total(T):
             assert torch.isnan(total).all()
 
 
+@pytest.mark.parametrize("T", [5, 3000])
+def test_terms_of_no_weight_do_not_overflow(T):
+    """Without advantage a ratio above fp32's range adds nothing to the loss, and
+    without beta neither does such a KL term."""
+    import torch
+    dev = cuda()
+    old = torch.full((T,), 200.0, device=dev)  # e^200 > 2^128
+    nll = torch.zeros(2, T, device=dev)
+    adv = torch.zeros(T, device=dev)
+    ref = torch.full((T,), -100.0, device=dev)
+    off = torch.tensor([0, T], dtype=torch.int32, device=dev)
+    gt = torch.ones(2, device=dev)
+    for kw in ({}, dict(ref=ref, beta=0.0)):
+        loss, total, kl, clipped = dust.dust_policy_loss(nll, old, adv, off, per_token=True, **kw)
+        assert (loss == 0).all() and (total == 0).all() and (clipped == 0).all()
+        assert (kl == (float("inf") if kw else 0)).all()
+        g = dust.dust_policy_loss_grad(nll, old, adv, off, gt, per_token=True, **kw)
+        assert (g == 0).all()
+    adv[T - 1] = float("nan")  # but no NaN is hidden
+    assert torch.isnan(dust.dust_policy_loss(nll, old, adv, off, per_token=True)[0][:, -1]).all()
+    adv[T - 1], old[T - 1] = 0, float("nan")
+    assert torch.isnan(dust.dust_policy_loss(nll, old, adv, off, per_token=True)[0][:, -1]).all()
+
+
 def test_gradient_against_differences():
     """Central differences of the total, where no ratio is near a bound."""
     import torch

@@ -229,6 +229,12 @@ struct Side {
     }
 };
 
+// The ratio that the advantage is multiplied by: exp(step), but finite where the
+// product is 0 whatever it is.
+__device__ __forceinline__ float ratio_of(float step, float adv) {
+    return expf(adv == 0.0f && step > 0.0f ? 0.0f : step);
+}
+
 // N tokens' losses side by side, without branches but for the rare ones.
 template <int N>
 __device__ __forceinline__ void losses_of(const PolicyProblem& p, const Token (&k)[N], const float (&nll)[N],
@@ -246,12 +252,12 @@ __device__ __forceinline__ void losses_of(const PolicyProblem& p, const Token (&
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const float bound = k[i].adv > 0.0f ? p.most : p.least;
-        const float ratio = expf(k[i].old - nll[i]);
+        const float ratio = ratio_of(k[i].old - nll[i], k[i].adv);
         loss[i] = -(clipped[i] ? bound : ratio) * k[i].adv;
         kl[i] = 0.0f;
         if (p.ref) {
             kl[i] = kl_of(nll[i] - k[i].ref);
-            loss[i] = fmaf(p.beta, kl[i], loss[i]);
+            if (p.beta != 0.0f) loss[i] = fmaf(p.beta, kl[i], loss[i]);
         }
         if (!k[i].scored) {
             loss[i] = kl[i] = 0.0f;
@@ -263,8 +269,8 @@ __device__ __forceinline__ void losses_of(const PolicyProblem& p, const Token (&
 __device__ __forceinline__ float slope_of(const PolicyProblem& p, const Token& k, float nll) {
     Side d(p, k, nll);
     if (d.near) d.beyond = Side::exactly(p, k.adv, k.old, nll);
-    float g = d.beyond ? 0.0f : expf(k.old - nll) * k.adv;
-    if (p.ref) g = fmaf(p.beta, expm1f(nll - k.ref), g);
+    float g = d.beyond ? 0.0f : ratio_of(k.old - nll, k.adv) * k.adv;
+    if (p.ref && p.beta != 0.0f) g = fmaf(p.beta, expm1f(nll - k.ref), g);
     return g;
 }
 
