@@ -100,9 +100,19 @@ SIZES = [(1, 8, 8, 64, 64), (1, 1, 0, 1, 0), (3, 2, 1, 2, 2), (5, 3, 1, 7, 6), (
          (11, 7, 3, 100, 0), (1000, 4, 4, 64, 64), (2, 40, 40, 12, 12), (50, 9, 3, 36, 20)]
 
 
+# Sizes of every width of vectors and lanes, and so many tokens that warps take
+# several, the last time fewer than they can. A warp's sums over its tokens (up to
+# 16), a CTA's over 8 warps and the rows' (10 and 5 halvings) are below 40
+# roundings: 40 * 2^-24 < 4e-6.
+LONG = [(9001, 1, 1, 9, 4), (9001, 2, 2, 13, 12), (12000, 1, 1, 45, 44), (7000, 2, 1, 90, 90),
+        (5000, 2, 1, 201, 200), (2500, 2, 1, 301, 300), (9001, 2, 1, 26, 26), (8000, 1, 1, 58, 20),
+        (7000, 2, 1, 110, 110), (4000, 2, 2, 202, 200), (2500, 2, 1, 330, 64), (9001, 3, 1, 24, 8),
+        (8000, 1, 1, 56, 24), (7000, 2, 1, 120, 120), (2500, 1, 1, 328, 200), (6000, 2, 1, 104, 40)]
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("layout", ["halves", "pairs"])
-@pytest.mark.parametrize("T,hq,hk,D,rot", SIZES)
+@pytest.mark.parametrize("T,hq,hk,D,rot", SIZES + LONG)
 def test_forward_and_gradients(T, hq, hk, D, rot, layout, dtype):
     dev = cuda()
     for fused in (False, True):

@@ -13,7 +13,9 @@
 // Heads whose vectors are 16 bytes go through k_rope_fast, with the next kRing
 // tokens' values in shared memory (cp.async, each thread's own) and two values
 // an instruction; other sizes and alignments through k_rope, value by value or
-// in smaller vectors.
+// in smaller vectors, the next tokens' values in registers. Those lanes move
+// fewer bytes each, so that latency bounds them: 1.2 to 3.4 TB/s, by single
+// bf16 values the least (head sizes of 13 to 201).
 //
 // Measured, bf16: 65536 tokens of 8 and 8 heads of 64 in rows of 24, 45 to 48 us
 // = 5.9 to 6.4 TB/s; backward of 16384 tokens of 32 and 8 heads of 128, 91 to 94
@@ -76,8 +78,14 @@ struct alignas(sizeof(TX) * V) Raw {
 template <typename TX, int V>
 __device__ __forceinline__ void store(TX* p, const float (&v)[V]) {
     Raw<TX, V> q;
+    if constexpr (sizeof(TX) == 2 && V % 2 == 0) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) from_f(v[i], q.x[i]);
+        for (int i = 0; i < V; i += 2)
+            *reinterpret_cast<__nv_bfloat162*>(q.x + i) = __floats2bfloat162_rn(v[i], v[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) from_f(v[i], q.x[i]);
+    }
     *reinterpret_cast<Raw<TX, V>*>(p) = q;
 }
 
@@ -104,6 +112,7 @@ __device__ __forceinline__ void load_floats(const float* p, float (&v)[V]) {
 template <int V, int G, int PER, bool HALVES>
 struct Columns {
     int a[PER], b[PER], have[PER];
+    int turns[PER];  // angles: all V or none (halves), or what is left of the tables (pairs)
 
     __device__ Columns(const Args& g, int lane) {
 #pragma unroll
@@ -118,47 +127,50 @@ struct Columns {
                 b[i] = a[i] + V;
             }
             have[i] = p >= g.pairs ? 0 : b[i] + V <= g.D ? 2 : 1;
+            turns[i] = HALVES ? (p < g.turned ? V : 0) : have[i] ? g.rot / 2 - a[i] / 2 : 0;
         }
     }
 };
 
-// The angles' cosines and sines of a lane's vector pairs. Halves: those of a
-// pair's V turns. Pairs: V / 2 turns of either vector, one after another in the
-// tables too.
+// The angles' cosines and sines of a lane's vector pairs, 1 and 0 where nothing
+// turns. Halves: those of a pair's V turns. Pairs: V / 2 turns of either vector,
+// one after another in the tables too.
 template <int V, int PER>
 struct Turns {
     float c[PER][V], s[PER][V];
-};
 
-template <int V, int G, int PER, bool HALVES>
-__device__ __forceinline__ void load_turns(const Args& g, const Columns<V, G, PER, HALVES>& col, int lane,
-                                           int64_t pos, Turns<V, PER>& t) {
-    const float* cs = g.cosine + pos * (g.rot / 2);
-    const float* sn = g.sine + pos * (g.rot / 2);
+    __device__ Turns() {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int from = HALVES ? col.a[i] : col.a[i] / 2;
-        // The turns that there are: all or none (halves, or a single one), and none
-        // without a position.
-        const int n = pos < 0 ? 0 : HALVES ? (lane + i * G < g.turned ? V : 0) : col.have[i] ? g.rot / 2 - from : 0;
+        for (int i = 0; i < PER; ++i)
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            t.c[i][k] = 1.0f;
-            t.s[i][k] = 0.0f;
-        }
-        if (n >= V) {
-            load_floats<V>(cs + from, t.c[i]);
-            load_floats<V>(sn + from, t.s[i]);
-        } else if (!HALVES && n > 0) {
+            for (int k = 0; k < V; ++k) {
+                c[i][k] = 1.0f;
+                s[i][k] = 0.0f;
+            }
+    }
+
+    // Of a position. How many there are is the same for all of them.
+    template <int G, bool HALVES>
+    __device__ __forceinline__ void load(const Args& g, const Columns<V, G, PER, HALVES>& col, int64_t pos) {
+        const float* cs = g.cosine + pos * (g.rot / 2);
+        const float* sn = g.sine + pos * (g.rot / 2);
 #pragma unroll
-            for (int k = 0; k < V; ++k)
-                if (k < n) {
-                    t.c[i][k] = cs[from + k];
-                    t.s[i][k] = sn[from + k];
-                }
+        for (int i = 0; i < PER; ++i) {
+            const int from = HALVES ? col.a[i] : col.a[i] / 2;
+            if (col.turns[i] >= V) {
+                load_floats<V>(cs + from, c[i]);
+                load_floats<V>(sn + from, s[i]);
+            } else if (!HALVES && col.turns[i] > 0) {
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if (k < col.turns[i]) {
+                        c[i][k] = cs[from + k];
+                        s[i][k] = sn[from + k];
+                    }
+            }
         }
     }
-}
+};
 
 // Turns a lane's values: x its first vectors, y its second ones; BACK: the other
 // way round.
@@ -185,11 +197,18 @@ __device__ __forceinline__ void turn(float (&x)[PER][V], float (&y)[PER][V], con
     }
 }
 
-// A head's values of a lane as they lie, and as numbers, zeros where there are
-// none.
+// A head's values of a lane as they lie, and as numbers; zeros where there are
+// none, which no load touches.
 template <typename TX, int V, int PER>
 struct Head {
     Raw<TX, V> a[PER], b[PER];
+
+    __device__ Head() {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+#pragma unroll
+            for (int k = 0; k < V; ++k) a[i].x[k] = b[i].x[k] = TX(0.0f);
+    }
 
     template <int G, bool HALVES>
     __device__ __forceinline__ void fetch(const Columns<V, G, PER, HALVES>& col, const TX* p) {
@@ -199,15 +218,13 @@ struct Head {
             if (col.have[i] > 1) b[i] = *reinterpret_cast<const Raw<TX, V>*>(p + col.b[i]);
         }
     }
-    template <int G, bool HALVES>
-    __device__ __forceinline__ void values(const Columns<V, G, PER, HALVES>& col, bool there,
-                                           float (&x)[PER][V], float (&y)[PER][V]) const {
+    __device__ __forceinline__ void values(float (&x)[PER][V], float (&y)[PER][V]) const {
 #pragma unroll
         for (int i = 0; i < PER; ++i)
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                x[i][k] = there && col.have[i] > 0 ? to_f(a[i].x[k]) : 0.0f;
-                y[i][k] = there && col.have[i] > 1 ? to_f(b[i].x[k]) : 0.0f;
+                x[i][k] = to_f(a[i].x[k]);
+                y[i][k] = to_f(b[i].x[k]);
             }
     }
 };
@@ -284,10 +301,31 @@ __device__ __forceinline__ void join_rows(const Args& g, const float* rows, floa
     }
 }
 
+template <int V, int PER>
+__device__ __forceinline__ void clear(float (&x)[PER][V], float (&y)[PER][V]) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) x[i][k] = y[i][k] = 0.0f;
+}
+
+// Tokens that a warp of k_rope and k_rope_grad takes at once, and has on their
+// way, and CTAs per SM, for lanes of PER vector pairs, `values` in all: as far
+// as registers go. Measured at 20000 tokens of 20 heads of 80 (turned by 40,
+// bf16: vectors of 4) and of 16 heads of 201 (4 pairs of single values): forward
+// one token at once 58 and 102 us, two 78 and 113; backward 106 and 183, two 158
+// and 334. Of 25751 x 20 heads of 45: forward 62 us with two or 64 with four,
+// backward 114.
+constexpr int at_once(int values, bool grad) {
+    return grad ? (values <= 1 ? 4 : values <= 2 ? 2 : 1) : values <= 1 ? 2 : 1;
+}
+constexpr int forward_ctas(int values, int per) { return values <= 2 || per == 1 ? 4 : 3; }
+
 template <typename TX, int V, int G, int PER, bool HALVES>
-__global__ void __launch_bounds__(kThreads, kForwardCtas) k_rope(const Args g) {
+__global__ void __launch_bounds__(kThreads, forward_ctas(V * PER, PER)) k_rope(const Args g) {
     pdl_wait();
     pdl_trigger();
+    constexpr int N = at_once(V * PER, false);
     const int lane = threadIdx.x % G;
     const Columns<V, G, PER, HALVES> col(g, lane);
     const Walk<G> w(g);
@@ -296,40 +334,64 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) k_rope(const Args g) {
     TX* y_at = static_cast<TX*>(side.y) + w.head * side.y_head;
     float wx[PER][V], wy[PER][V];
     load_weight(col, side.w, wx, wy);
-    Head<TX, V, PER> next;
-    int32_t next_pos = -1;
-    const auto fetch = [&](int64_t t) {
-        if (t >= g.T) return;
-        next_pos = g.positions[t];
-        if (w.in) next.fetch(col, x_at + t * side.x_token);
+    Head<TX, V, PER> next[N];
+    Turns<V, PER> turns[N];
+    int32_t next_pos[N];
+    const int64_t x_step = w.step * side.x_token, y_step = w.step * side.y_token;
+    const TX* x_next = x_at + w.t * side.x_token;
+    const int32_t* pos_next = g.positions + w.t;
+    int64_t t_next = w.t;
+    const auto fetch = [&] {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            next_pos[j] = -1;
+            if (t_next < g.T) {
+                next_pos[j] = *pos_next;
+                if (w.in) next[j].fetch(col, x_next);
+            }
+            t_next += w.step;
+            pos_next += w.step;
+            x_next += x_step;
+        }
     };
-    fetch(w.t);
-    for (int64_t t = w.t; t < g.T; t += w.step) {
-        const int64_t pos = position_of(g, next_pos);
-        float x[PER][V], y[PER][V];
-        next.values(col, w.in && pos >= 0, x, y);
-        fetch(t + w.step);
-        Turns<V, PER> turns;
-        load_turns<V, G, PER, HALVES>(g, col, lane, pos, turns);
-        float s = 0.0f;
+    fetch();
+    y_at += w.t * side.y_token;
+    for (int64_t t0 = w.t; t0 < g.T; t0 += N * w.step) {
+        bool there[N];
+        float x[N][PER][V], y[N][PER][V];
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
+        for (int j = 0; j < N; ++j) {
+            const int64_t pos = position_of(g, next_pos[j]);
+            there[j] = pos >= 0;
+            next[j].values(x[j], y[j]);
+            if (there[j]) turns[j].load(g, col, pos);
+        }
+        fetch();
 #pragma unroll
-            for (int k = 0; k < V; ++k) s = fmaf(x[i][k], x[i][k], fmaf(y[i][k], y[i][k], s));
-        s = group_sum<G>(s);
-        if (!w.in) continue;
-        if (pos >= 0) {
-            const float rstd = rsqrtf(fmaf(s, g.inv_d, g.eps));
+        for (int j = 0; j < N; ++j, y_at += y_step) {
+            const int64_t t = t0 + j * w.step;
+            float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    x[i][k] *= rstd * wx[i][k];
-                    y[i][k] *= rstd * wy[i][k];
-                }
-            turn<false, V, PER, HALVES>(x, y, turns);
+                for (int k = 0; k < V; ++k) s = fmaf(x[j][i][k], x[j][i][k], fmaf(y[j][i][k], y[j][i][k], s));
+            s = group_sum<G>(s);
+            if (!w.in || t >= g.T) continue;
+            if (there[j]) {
+                const float rstd = rsqrtf(fmaf(s, g.inv_d, g.eps));
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        x[j][i][k] *= rstd * wx[i][k];
+                        y[j][i][k] *= rstd * wy[i][k];
+                    }
+                turn<false, V, PER, HALVES>(x[j], y[j], turns[j]);
+            } else {
+                clear(x[j], y[j]);
+            }
+            store_head<V, G, PER, HALVES>(col, y_at, x[j], y[j]);
         }
-        store_head<V, G, PER, HALVES>(col, y_at + t * side.y_token, x, y);
     }
 }
 
@@ -339,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas)
     extern __shared__ float rows[];  // [kWarps][2][D]
     pdl_wait();
     pdl_trigger();
+    constexpr int N = at_once(V * PER, true);
     const int lane = threadIdx.x % G, group = threadIdx.x % 32 / G;
     const Columns<V, G, PER, HALVES> col(g, lane);
     const Walk<G> w(g);
@@ -349,53 +412,80 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas)
     float wx[PER][V], wy[PER][V];
     load_weight(col, side.w, wx, wy);
     float sx[PER][V] = {}, sy[PER][V] = {};  // of gm n
-    Head<TX, V, PER> next_x, next_g;
-    int32_t next_pos = -1;
-    const auto fetch = [&](int64_t t) {
-        if (t >= g.T) return;
-        next_pos = g.positions[t];
-        if (!w.in) return;
-        next_x.fetch(col, x_at + t * side.x_token);
-        next_g.fetch(col, g_at + t * side.gy_token);
-    };
-    fetch(w.t);
-    for (int64_t t = w.t; t < g.T; t += w.step) {
-        const int64_t pos = position_of(g, next_pos);
-        float x[PER][V], y[PER][V], u[PER][V], v[PER][V];
-        next_x.values(col, w.in && pos >= 0, x, y);
-        next_g.values(col, w.in && pos >= 0, u, v);
-        fetch(t + w.step);
-        Turns<V, PER> turns;
-        load_turns<V, G, PER, HALVES>(g, col, lane, pos, turns);
-        turn<true, V, PER, HALVES>(u, v, turns);  // gm
-        // sum x^2 and sum gm w x together; the root comes to the second later.
-        float s = 0.0f, dot = 0.0f;
+    Head<TX, V, PER> next_x[N], next_g[N];
+    Turns<V, PER> turns[N];
+    int32_t next_pos[N];
+    const int64_t x_step = w.step * side.x_token, y_step = w.step * side.y_token;
+    const int64_t g_step = w.step * side.gy_token;
+    const TX *x_next = x_at + w.t * side.x_token, *g_next = g_at + w.t * side.gy_token;
+    const int32_t* pos_next = g.positions + w.t;
+    int64_t t_next = w.t;
+    const auto fetch = [&] {
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                s = fmaf(x[i][k], x[i][k], fmaf(y[i][k], y[i][k], s));
-                dot = fmaf(u[i][k] * wx[i][k], x[i][k], fmaf(v[i][k] * wy[i][k], y[i][k], dot));
+        for (int j = 0; j < N; ++j) {
+            next_pos[j] = -1;
+            if (t_next < g.T) {
+                next_pos[j] = *pos_next;
+                if (w.in) {
+                    next_x[j].fetch(col, x_next);
+                    next_g[j].fetch(col, g_next);
+                }
             }
-        s = group_sum<G>(s);
-        dot = group_sum<G>(dot);
-        if (!w.in) continue;
-        if (pos >= 0) {
-            const float rstd = rsqrtf(fmaf(s, g.inv_d, g.eps));
-            dot *= rstd * g.inv_d;
+            t_next += w.step;
+            pos_next += w.step;
+            x_next += x_step;
+            g_next += g_step;
+        }
+    };
+    fetch();
+    y_at += w.t * side.y_token;
+    for (int64_t t0 = w.t; t0 < g.T; t0 += N * w.step) {
+        bool there[N];
+        float x[N][PER][V], y[N][PER][V], u[N][PER][V], v[N][PER][V];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int64_t pos = position_of(g, next_pos[j]);
+            there[j] = pos >= 0;
+            next_x[j].values(x[j], y[j]);
+            next_g[j].values(u[j], v[j]);
+            if (there[j]) turns[j].load(g, col, pos);
+        }
+        fetch();
+#pragma unroll
+        for (int j = 0; j < N; ++j, y_at += y_step) {
+            const int64_t t = t0 + j * w.step;
+            turn<true, V, PER, HALVES>(u[j], v[j], turns[j]);  // gm
+            // sum x^2 and sum gm w x together; the root comes to the second later.
+            float s = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
 #pragma unroll
                 for (int k = 0; k < V; ++k) {
-                    x[i][k] *= rstd;  // n
-                    y[i][k] *= rstd;
-                    sx[i][k] = fmaf(u[i][k], x[i][k], sx[i][k]);
-                    sy[i][k] = fmaf(v[i][k], y[i][k], sy[i][k]);
-                    u[i][k] = rstd * fmaf(-x[i][k], dot, u[i][k] * wx[i][k]);
-                    v[i][k] = rstd * fmaf(-y[i][k], dot, v[i][k] * wy[i][k]);
+                    s = fmaf(x[j][i][k], x[j][i][k], fmaf(y[j][i][k], y[j][i][k], s));
+                    dot = fmaf(u[j][i][k] * wx[i][k], x[j][i][k], fmaf(v[j][i][k] * wy[i][k], y[j][i][k], dot));
                 }
+            s = group_sum<G>(s);
+            dot = group_sum<G>(dot);
+            if (!w.in || t >= g.T) continue;
+            if (there[j]) {
+                const float rstd = rsqrtf(fmaf(s, g.inv_d, g.eps));
+                dot *= rstd * g.inv_d;
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        x[j][i][k] *= rstd;  // n
+                        y[j][i][k] *= rstd;
+                        sx[i][k] = fmaf(u[j][i][k], x[j][i][k], sx[i][k]);
+                        sy[i][k] = fmaf(v[j][i][k], y[j][i][k], sy[i][k]);
+                        u[j][i][k] = rstd * fmaf(-x[j][i][k], dot, u[j][i][k] * wx[i][k]);
+                        v[j][i][k] = rstd * fmaf(-y[j][i][k], dot, v[j][i][k] * wy[i][k]);
+                    }
+            } else {
+                clear(u[j], v[j]);
+            }
+            store_head<V, G, PER, HALVES>(col, y_at, u[j], v[j]);
         }
-        store_head<V, G, PER, HALVES>(col, y_at + t * side.y_token, u, v);
     }
     if (!parts) return;
     // The groups of a warp one after another, then the warps.
@@ -787,7 +877,7 @@ template <typename TX, int V, int G, int PER, bool HALVES>
 cudaError_t launch_with(const Args& g, const Launch& l) {
     if (!l.grad)
         return launch_pdl(k_rope<TX, V, G, PER, HALVES>,
-                          dim3(grid_of(g.T, g.heads, 32 / G, 152 * kForwardCtas)), dim3(kThreads), 0, l.s, g);
+                          dim3(grid_of(g.T, g.heads, 32 / G, 152 * forward_ctas(V * PER, PER))), dim3(kThreads), 0, l.s, g);
     *l.n_parts = grid_of(g.T, g.heads, 32 / G, kMaxCtas);
     return launch_pdl(k_rope_grad<TX, V, G, PER, HALVES>, dim3(*l.n_parts), dim3(kThreads),
                       sizeof(float) * 2 * kWarps * static_cast<size_t>(g.D), l.s, g, l.parts);
@@ -819,14 +909,24 @@ cudaError_t launch_vectors(const Args& g, int V, const Launch& l) {
                : g.pairs <= 8  ? launch_fast<TX, 8, HALVES>(g, l)
                : g.pairs <= 16 ? launch_fast<TX, 16, HALVES>(g, l)
                                : launch_fast<TX, 32, HALVES>(g, l);
-    const int per = (g.pairs + 31) / 32;
-    if (V >= 2) {
-        if (g.pairs <= 16) return launch_with<TX, 2, 16, 1, HALVES>(g, l);
-        return per == 1   ? launch_with<TX, 2, 32, 1, HALVES>(g, l)
-               : per == 2 ? launch_with<TX, 2, 32, 2, HALVES>(g, l)
-                          : launch_with<TX, 2, 32, 4, HALVES>(g, l);
-    }
-    return per <= 2 ? launch_with<TX, 1, 32, 2, HALVES>(g, l) : launch_with<TX, 1, 32, 8, HALVES>(g, l);
+    if constexpr (sizeof(TX) == 2)
+        if (V == 4)
+            return g.pairs <= 8    ? launch_with<TX, 4, 8, 1, HALVES>(g, l)
+                   : g.pairs <= 16 ? launch_with<TX, 4, 16, 1, HALVES>(g, l)
+                   : g.pairs <= 32 ? launch_with<TX, 4, 32, 1, HALVES>(g, l)
+                                   : launch_with<TX, 4, 32, 2, HALVES>(g, l);
+    if (V >= 2)
+        return g.pairs <= 8    ? launch_with<TX, 2, 8, 1, HALVES>(g, l)
+               : g.pairs <= 16 ? launch_with<TX, 2, 16, 1, HALVES>(g, l)
+               : g.pairs <= 32 ? launch_with<TX, 2, 32, 1, HALVES>(g, l)
+               : g.pairs <= 64 ? launch_with<TX, 2, 32, 2, HALVES>(g, l)
+                               : launch_with<TX, 2, 32, 4, HALVES>(g, l);
+    return g.pairs <= 8     ? launch_with<TX, 1, 8, 1, HALVES>(g, l)
+           : g.pairs <= 16  ? launch_with<TX, 1, 16, 1, HALVES>(g, l)
+           : g.pairs <= 32  ? launch_with<TX, 1, 32, 1, HALVES>(g, l)
+           : g.pairs <= 64  ? launch_with<TX, 1, 32, 2, HALVES>(g, l)
+           : g.pairs <= 128 ? launch_with<TX, 1, 32, 4, HALVES>(g, l)
+                            : launch_with<TX, 1, 32, 8, HALVES>(g, l);
 }
 
 cudaError_t run(const RopeProblem& p, const Launch& l) {
@@ -844,12 +944,13 @@ cudaError_t run(const RopeProblem& p, const Launch& l) {
             };
             if (!on(d.x) || !on(d.y) || !on(d.gy)) return false;
         }
-        // 16 bytes: whole pairs of vectors, each turned or not, and the tables too.
-        return v == 2 || (p.D % (2 * v) == 0 && p.rot % (2 * v) == 0 &&
+        // From 4 values on the tables' vectors are 16 bytes too; and of 16 bytes,
+        // whole pairs of vectors, each turned or not.
+        return v == 2 || (p.rot % (2 * v) == 0 && (v * size < 16 || p.D % (2 * v) == 0) &&
                           (p.rot == 0 || (reinterpret_cast<uintptr_t>(p.cosine) |
                                           reinterpret_cast<uintptr_t>(p.sine)) % 16 == 0));
     };
-    if (!fits(V) || p.D > 64 * V) V = fits(2) ? 2 : 1;
+    if (!fits(V) || p.D > 64 * V) V = p.bf16 && fits(4) ? 4 : fits(2) ? 2 : 1;
     for (int i = 0; i < 2; ++i) {
         const RopeSide& d = p.side[i];
         g.side[i] = {d.x.data, d.gy.data, d.y.data, d.x.token_stride, d.x.head_stride, d.y.token_stride,
