@@ -191,6 +191,48 @@ def test_far_values(act, T, dtype):
         assert (np.abs(_np(got) - want) <= 2 * tol * np.abs(want) + T * 1e-12).all()
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T", [2, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_of_gates_as_far_as_their_type_goes(act, T, dtype):
+    """Gates up to 1e37 on both sides, whose slope is exactly 0 or 1: every gradient
+    is finite and right. A slope, or an activation relative to its gate, is a
+    handful of fp32 roundings of terms of at most 2, where the exponentials'
+    argument is at most 2 and else saturates: 32 * 2^-24 = 2^-19 covers them. bf16
+    rounds dG and dU (2^-8), and gX once more; n products' sum cuts off at most
+    n 2^-23 of their magnitudes."""
+    import torch
+    dev = cuda()
+    d, f = 16, 64
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    X = torch.zeros((T, d), dtype=dt, device=dev)
+    X[:, 0] = 1.0
+    X[:, 1] = 0.5
+    Wg = torch.zeros((f, d), dtype=dt, device=dev)
+    for i, v in enumerate([1.0, 1e3, 1e15, 1e30, 2e31, 1e32, 1e35, 1e37]):
+        Wg[2 * i, 0], Wg[2 * i + 1, 0] = v, -v
+    Wu = torch.zeros_like(Wg)
+    Wu[:, 1] = 2.0
+    gh = torch.full((T, f), 2.0 ** -9, dtype=dt, device=dev)
+    h64, gX64, gWg64, gWu64 = reference(gh, X, Wg, Wu, act)
+    gate = _np(X) @ _np(Wg).T
+    a, slope = act64(gate, act)
+    rounding = 2.0 ** -8 if dtype == "bf16" else 0.0
+    off = np.abs(_np(dust.dust_gated_up(X, Wg, Wu, ACTS[act])) - h64)
+    assert (off <= (rounding + 2.0 ** -19) * np.abs(h64) + 1e-37).all()
+    dG, dU = _np(gh) * slope, _np(gh) * a  # u is 1
+    eG = 2.0 ** -19 * _np(gh) + rounding * np.abs(dG) + 1e-37
+    eU = (2.0 ** -19 + rounding) * np.abs(dU) + 1e-37
+    gX, gWg, gWu = (_np(t) for t in dust.dust_gated_up_grad(gh, X, Wg, Wu, ACTS[act]))
+    aX, aG, aU = (np.abs(_np(t)) for t in (X, Wg, Wu))
+    cut = 2 * f * 2.0 ** -23
+    e = (eG + cut * np.abs(dG)) @ aG + (eU + cut * np.abs(dU)) @ aU
+    assert (np.abs(gX - gX64) <= e + rounding * (np.abs(gX64) + e)).all()
+    cut = T * 2.0 ** -23
+    assert (np.abs(gWg - gWg64) <= (eG + cut * np.abs(dG)).T @ aX).all()
+    assert (np.abs(gWu - gWu64) <= (eU + cut * np.abs(dU)).T @ aX).all()
+
+
 @pytest.mark.parametrize("T", [1, 300])
 def test_infinities_and_nan_stay_in_their_rows(T):
     import torch

@@ -241,9 +241,10 @@ __device__ __forceinline__ void backward(float (&g)[32], float (&u)[32], const f
             float e, dz = x;
             const float p = sigmoid<EXACT>(ACT == DUST_ACT_GELU ? gelu_z(x) : x, e);
             if (ACT == DUST_ACT_GELU) {
-                // Far out p (1 - p) is 0, and the slope of z stays finite.
+                // Far out p (1 - p) is 0, and its factor has to stay finite there: all
+                // of it at the nearer of x and 1e4.
                 const float y = fminf(fmaxf(x, -1e4f), 1e4f);
-                dz = x * (1.5957691216057308f * fmaf(3.0f * 0.044715f * y, y, 1.0f));
+                dz = y * (1.5957691216057308f * fmaf(3.0f * 0.044715f * y, y, 1.0f));
             }
             act = x * p;
             slope = fmaf(dz, p * (p * e), p);
