@@ -233,6 +233,38 @@ def test_total_of_losses_that_cancel(lengths, S, by_sequence):
     assert (np.abs(_np(total) - m) <= tol).all()
 
 
+@pytest.mark.parametrize("S", [1, 7])
+def test_weights_of_more_tokens_than_fp32_counts(S):
+    """4097 sequences, one of them with 4099 scored tokens: their product is above
+    2^24 and odd. All of its losses are 1 and all those of one with fewer tokens -1,
+    so that the means cancel and the weights alone show; all others are 0.
+    Each thread has one of these tokens, so that its term is exact; the terms are
+    added in 64 bits. What a weight leaves is at most 3 * 2^-24 for the rounding of
+    the counts and their product and 2^-24 for its own, 2^-22 of it in all: what is
+    of second order below 2^-44, its computing and adding up (3 and 14 roundings)
+    below 2^-41 with that. (A weight of the rounded product is 6e-8 off.)"""
+    dev = cuda()
+    f, ones, singles = np.float32, (16 * 1024 + 3, 15 * 1024 + 700), 4095
+    lengths = list(ones) + [1] * singles
+    off = offsets_from_lengths(lengths).astype(np.int32)
+    T = int(off[-1])
+    seq = np.repeat(np.arange(len(lengths)), lengths)
+    scored = (np.arange(T) % 1024 < 256) | (seq > 1)
+    count = np.bincount(seq[scored])
+    assert count[0] == 4099 and len(count) * int(count[0]) > 2 ** 24 and (count > 0).all()
+    w = f(1) / (f(len(count)) * count.astype(f))  # weights of the rounded products
+    assert abs(w[0] * np.float64(count[0]) - w[1] * np.float64(count[1])) > 2.0 ** -26 / len(count)
+    adv = np.zeros(len(lengths), f)
+    adv[:2] = -1.0, 1.0
+    old = np.random.default_rng(5).uniform(0.1, 9.0, T).astype(f)
+    loss, total = dust.dust_policy_loss(
+        _dev(np.tile(old, (S, 1)), dev), _dev(old, dev), _dev(adv, dev), _dev(off, dev),
+        targets=_dev(np.where(scored, 1, -1).astype(np.int32), dev), clip_low=LOW, clip_high=HIGH,
+        per_token=False, mean=dust.MEAN_SEQUENCE)[:2]
+    assert (np.abs(_np(loss)).sum(1) == count[0] + count[1]).all()
+    assert (np.abs(_np(total)) <= 2.0 ** -41 * 2.0 / len(count)).all()
+
+
 @pytest.mark.parametrize("T", [1, 4, 64, 1000, 2048, 2049, 4096])
 def test_infinite_losses_make_an_infinite_total(T):
     """One token whose ratio is above fp32's range: its loss is infinite, and the

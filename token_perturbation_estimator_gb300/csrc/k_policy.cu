@@ -188,6 +188,12 @@ __device__ __forceinline__ float kl_of(float r) {
     return fabsf(r) < 1.0f ? s * r * r : far;
 }
 
+// What the rounding of a count v >= 0 to f leaves (2^31, which it may round to,
+// fits 32 bits without a sign).
+__device__ __forceinline__ float beyond_fp32(int32_t v, float f) {
+    return static_cast<float>(static_cast<int32_t>(static_cast<uint32_t>(v) - static_cast<uint32_t>(f)));
+}
+
 // What a token needs of everything but nll.
 struct Token {
     bool scored;
@@ -202,10 +208,13 @@ struct Token {
         old = p.old[t];
         ref = p.ref ? p.ref[t] : 0.0f;
         adv = p.advantages[p.per_token ? t : seq];
-        const float n = p.by_sequence ? static_cast<float>(c.sequences) * static_cast<float>(of_seq[seq])
-                                      : static_cast<float>(c.tokens);
+        // The tokens that share the mean: a product that has up to 62 bits, as n and
+        // what is beyond it.
+        const int32_t a = p.by_sequence ? c.sequences : 1, b = p.by_sequence ? of_seq[seq] : c.tokens;
+        const float fa = static_cast<float>(a), fb = static_cast<float>(b), n = fa * fb;
+        const float beyond = fmaf(beyond_fp32(a, fa), fb, fmaf(fa, beyond_fp32(b, fb), fmaf(fa, fb, -n)));
         weight = 1.0f / n;
-        rest = fmaf(-weight, n, 1.0f) * weight;
+        rest = fmaf(-weight, beyond, fmaf(-weight, n, 1.0f)) * weight;
     }
 };
 
