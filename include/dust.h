@@ -869,8 +869,10 @@ dust_status dust_policy_loss_grad(const float* nll, const float* old, const floa
  *   norm     device f32 [1], written.
  *   workspace  device, >= dust_clip_grads_workspace bytes, 256-byte aligned.
  * Squares are summed in groups of 16 values in fp32, or one by one in 64 bits
- * where those overflow or lose bits; the groups' sums in 64 bits. norm is
- * rounded to fp32 (infinite above its range), the factor is formed in 64 bits.
+ * where those overflow or lose bits; the groups' sums as pairs of fp32 numbers
+ * (the sum and what its roundings lose) within a warp, from there on in 64 bits.
+ * norm is rounded to fp32 (infinite above its range), the factor is formed in 64
+ * bits and kept to 24 of them, also below fp32's normal numbers.
  * At most 4096 tensors of up to 2^40 values (DUST_ERR_RANGE).
  */
 typedef struct {

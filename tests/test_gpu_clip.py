@@ -97,6 +97,38 @@ def test_squares_past_the_range(scale):
     check(_tensors([(3000,), (17,)], ["bf16"], dev, scale), scale * 1e3)
 
 
+@pytest.mark.parametrize("max_norm", [1e3, 1.0, 1e-3, 1e-6, 1e-12, 1e-37, 1e-44])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("big", [500, 1 << 21])
+def test_factors_below_fp32s_range(big, dtype, max_norm):
+    """Gradients of 1e38 and of every size below it, scaled to a norm that is far from
+    theirs: the factor is below fp32's normal numbers or all of its numbers, the
+    scaled values are not. As in check(): the factor's rounding, two products'
+    and bf16's; below 2^-126 of the result each of these is at most half of 2^-149
+    (bf16 2^-133) instead, of which four fit into 2^-147 (2^-131)."""
+    import torch
+    dev = cuda()
+    g = torch.Generator().manual_seed(big)
+    a = torch.randn(big, generator=g).clamp(-3, 3) * 1e38
+    a[1::2] *= 10.0 ** (-40 * torch.rand(big // 2, generator=g))
+    a = a.to(torch.bfloat16 if dtype == "bf16" else torch.float32).to(dev)
+    grads = [a, torch.ones(7, device=dev)]
+    want = [_np(t) for t in grads]
+    norm64 = np.sqrt(sum((t * t).sum() for t in want))
+    c = float(np.float32(max_norm)) / norm64
+    assert c < 2.0 ** -115 and norm64 > 3.4e38
+    norm, got = dust.dust_clip_grads(grads, max_norm, out=[torch.empty_like(t) for t in grads])
+    assert norm.item() == float("inf")
+    for x, w in zip(got, want):
+        e = 2.0 ** -22 * np.abs(w * c) + 2.0 ** -147
+        if x.dtype == torch.bfloat16:
+            e = e + 2.0 ** -8 * np.abs(w * c) + 2.0 ** -131
+        assert (np.abs(_np(x) - w * c) <= e).all()
+    assert max_norm < 1e-40 or (got[0] != 0).any()
+    same, again = dust.dust_clip_grads(grads, max_norm)
+    assert torch.equal(same, norm) and all(torch.equal(x, y) for x, y in zip(again, got))
+
+
 def test_one_large_value_among_small_ones():
     import torch
     dev = cuda()

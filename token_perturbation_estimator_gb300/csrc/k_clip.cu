@@ -95,6 +95,16 @@ struct Squares {
     }
 };
 
+// What values are multiplied by, one after the other: a factor below fp32's
+// normal numbers, which would have few bits as one of them or none, is a number
+// below 1 times a power of two; else that is 1. (Values whose squares overflow are
+// scaled so: 1e38 to a norm of 1. A product of them and `normal` does not overflow
+// and loses bits only where the result has none left; `normal` has all of its own
+// where that is above 2^-147.)
+struct Factor {
+    float normal, power;
+};
+
 // A thread's group of a chunk: 16 bytes at a time (VEC), or value by value,
 // neighbouring lanes on neighbouring ones.
 template <typename TX, bool VEC>
@@ -121,12 +131,12 @@ struct Group {
         }
     }
     template <bool FULL>
-    static __device__ __forceinline__ void store(TX* p, int n, const float (&v)[kGroup], float c) {
+    static __device__ __forceinline__ void store(TX* p, int n, const float (&v)[kGroup], Factor c) {
 #pragma unroll
         for (int j = 0; j < kGroup / kPer; ++j) {
             Raw q;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) from_f(v[j * kPer + i] * c, q.x[i]);
+            for (int i = 0; i < kPer; ++i) from_f(v[j * kPer + i] * c.normal * c.power, q.x[i]);
             if (FULL || at(j) + kPer <= n) {
                 *reinterpret_cast<Raw*>(p + at(j)) = q;
             } else {
@@ -158,7 +168,7 @@ __device__ void add_squares(Squares& s, const TX* p, int64_t n) {
 
 // n values from p to out, times c, the last ones first.
 template <typename TX, bool VEC>
-__device__ void scale_to(const TX* p, TX* out, int64_t n, float c) {
+__device__ void scale_to(const TX* p, TX* out, int64_t n, Factor c) {
     using G = Group<TX, VEC>;
     const int64_t full = n / kChunk * kChunk;
     if (n > full) {
@@ -192,7 +202,7 @@ __device__ __forceinline__ void squares_by(Squares& s, const void* g, int64_t fr
 }
 
 template <typename TX>
-__device__ __forceinline__ void scale_by(const void* g, void* out, int64_t from, int64_t n, float c) {
+__device__ __forceinline__ void scale_by(const void* g, void* out, int64_t from, int64_t n, Factor c) {
     const TX* p = static_cast<const TX*>(g) + from;
     TX* o = static_cast<TX*>(out) + from;
     if (on_16(g, out)) scale_to<TX, true>(p, o, n, c);
@@ -222,10 +232,10 @@ struct Walk {
         return s;
     }
 
-    __device__ void scale(float c) const {
+    __device__ void scale(Factor c) const {
         if (from >= to) return;
         for (int t = b.tensor_of(to - 1); t >= 0 && b.first[t + 1] > from; --t) {
-            if (!b.out[t] || (c == 1.0f && b.out[t] == b.g[t])) continue;
+            if (!b.out[t] || (c.normal == 1.0f && b.out[t] == b.g[t])) continue;
             const int64_t at = (max(from, b.first[t]) - b.first[t]) * kChunk;
             const int64_t n = min(b.n[t], (to - b.first[t]) * kChunk) - at;
             if (b.bf16[t]) scale_by<__nv_bfloat16>(b.g[t], b.out[t], at, n, c);
@@ -257,8 +267,13 @@ __device__ __forceinline__ double cta_sum(Squares s) {
     return v;
 }
 
-__device__ __forceinline__ float factor(double length, double max_norm) {
-    return length <= max_norm ? 1.0f : static_cast<float>(max_norm / length);
+// min(1, max_norm / length).
+__device__ __forceinline__ Factor factor(double length, double max_norm) {
+    if (length <= max_norm) return {1.0f, 1.0f};
+    const double c = max_norm / length;
+    if (!(c > 0.0 && c < 0x1p-126)) return {static_cast<float>(c), 1.0f};
+    const int up = min(-1 - ilogb(c), 149);  // 2^-149 is the least power that there is
+    return {static_cast<float>(scalbn(c, up)), scalbnf(1.0f, -up)};
 }
 
 template <int N>
@@ -274,7 +289,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, kCtas)
     k_clip_scale(const __grid_constant__ Batch<N> b, const double* __restrict__ parts, int n_parts,
                  double max_norm, float* norm) {
-    __shared__ float shared_factor;
+    __shared__ Factor shared_factor;
     pdl_wait();
     pdl_trigger();
     if (threadIdx.x < 32) {
@@ -315,7 +330,7 @@ __device__ __forceinline__ void cluster_barrier() {
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kTeams * kThreads)
     k_clip_few(const __grid_constant__ Batch<kFewTensors> b, double max_norm, float* norm) {
     __shared__ double mine;
-    __shared__ float shared_factor;
+    __shared__ Factor shared_factor;
     pdl_wait();
     pdl_trigger();
     const Walk<kFewTensors> w(b, blockIdx.x * kTeams + threadIdx.x / kThreads, kCluster * kTeams);
