@@ -694,7 +694,8 @@ dust_status dust_distill_loss_grad(const void* H, int64_t ld_h, const void* E, i
  * activation and the product in fp32, h rounded once; the backward's dG and dU
  * are rounded to bf16 (they are tensor-core operands). fp32 inputs: every
  * product and sum to fp32 accuracy (operands to 24 bits, or to 2^-133 where
- * that is more).
+ * that is more; an operand's leading bits are rounded up to 2^-8 away first, so
+ * that a product within 2^-7 of the range's end may be infinite).
  * An infinity or NaN in a row reaches what the row enters, in fp32 as a NaN
  * where fp32 arithmetic might have kept an infinity.
  * d >= 1, f >= 1, T >= 0; T and d up to 2^31 - 2^16, f up to 2^30 - 2^16; with

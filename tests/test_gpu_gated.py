@@ -233,6 +233,32 @@ def test_gradients_of_gates_as_far_as_their_type_goes(act, T, dtype):
     assert (np.abs(gWu - gWu64) <= (eU + cut * np.abs(dU)).T @ aX).all()
 
 
+def test_fp32_gradients_beyond_bf16s_range():
+    """dG and dU of both signs between bf16's largest number and fp32's, which are
+    operands of their own products: those are finite, and right to fp32's
+    accuracy. Each row has one unit, so that every value is one term: a handful of
+    roundings in dG and dU, and what three planes leave, 2^-24.
+    An operand's first plane is its value rounded to bf16, up to (1 + 2^-8) times as
+    large, and the product of two such up to (1 + 2^-8)^2 times: from 2^128 by that
+    on a value may be infinite (1.7e38, 2^127 as bf16, times 2), of its sign."""
+    import torch
+    dev = cuda()
+    T, d, f = 8, 2, 8
+    X, Wg, Wu, gh = (torch.zeros(n, device=dev) for n in ((T, d), (f, d), (f, d), (T, f)))
+    X[:, 0], X[:, 1] = 0.5, 1.0
+    Wg[:, 1] = 1.0  # the gate is 1: squared ReLU has 1 there and a slope of 2
+    for i, v in enumerate((3.4e38, -3.4e38, 3.398e38, -3.392e38)):
+        gh[2 * i, 2 * i], gh[2 * i + 1, 2 * i + 1] = v, v / 2  # dU
+        Wu[2 * i, 0], Wu[2 * i + 1, 0] = 2.0 ** -4, 2.0        # dG: v / 16, v
+    want = reference(gh, X, Wg, Wu, "relu2")[1:]
+    assert all(3.39e38 < np.abs(w).max() < 3.4028e38 for w in want)
+    for a, b in zip(dust.dust_gated_up_grad(gh, X, Wg, Wu, dust.RELU2), want):
+        a = _np(a)
+        past = np.isinf(a) & (np.abs(b) >= 2.0 ** 128 / (1 + 2.0 ** -8) ** 2) & (np.sign(a) == np.sign(b))
+        assert past.sum() < b.size / 2
+        assert (np.abs(a - b)[~past] <= 8 * 2.0 ** -24 * np.abs(b)[~past]).all()
+
+
 @pytest.mark.parametrize("T", [1, 300])
 def test_infinities_and_nan_stay_in_their_rows(T):
     import torch

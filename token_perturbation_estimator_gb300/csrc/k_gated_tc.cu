@@ -188,6 +188,13 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
+// As pack2, but the largest bf16 numbers where these round to infinity.
+__device__ __forceinline__ uint32_t pack2_finite(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
 __device__ __forceinline__ float max_nan(float a, float b) {
     float d;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
@@ -409,7 +416,9 @@ struct Epilogue {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float x0 = v[8 * i + 2 * j], x1 = v[8 * i + 2 * j + 1];
-                    pk[j] = pack2(x0, x1);
+                    // The largest of several planes: not up to infinity, of which the
+                    // others could not take anything back.
+                    pk[j] = PLANES > 1 && p == 0 ? pack2_finite(x0, x1) : pack2(x0, x1);
                     if (p + 1 < PLANES) {  // what this plane leaves
                         v[8 * i + 2 * j] = x0 - __uint_as_float(pk[j] << 16);
                         v[8 * i + 2 * j + 1] = x1 - __uint_as_float(pk[j] & 0xffff0000u);
