@@ -340,3 +340,21 @@ def test_offsets_past_32_bits():
     assert (got == want).all()
     dust.dust_qk_norm_rope(src, None, None, None, pos, c, s, yq=q)
     assert (q == want).all()
+
+
+def test_any_position_without_tables():
+    """Where nothing turns, the largest position is one like any other."""
+    import torch
+    dev = cuda()
+    for dtype in ("bf16", "f32"):
+        q, k, wq, wk, pos, c, s, gyq, gyk = _inputs(5, 3, 2, 32, 0, dtype, dev, pad=0.0)
+        want = dust.dust_qk_norm_rope(q, k, wq, wk, pos, None, None)
+        wanted = dust.dust_qk_norm_rope_grad(gyq, gyk, q, k, wq, wk, pos, None, None)
+        far = torch.full_like(pos, 2 ** 31 - 1)
+        for a, b in zip(dust.dust_qk_norm_rope(q, k, wq, wk, far, None, None), want):
+            assert torch.equal(a, b)
+        for a, b in zip(dust.dust_qk_norm_rope_grad(gyq, gyk, q, k, wq, wk, far, None, None), wanted):
+            assert torch.equal(a, b)
+        far[1] = -1
+        assert (dust.dust_qk_norm_rope(q, k, wq, wk, far, None, None)[0][1] == 0).all()
+    assert dust.dust_last_error() == dust.OK

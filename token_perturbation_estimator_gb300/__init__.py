@@ -846,7 +846,7 @@ def _rope_inputs(q, k, wq, wk, positions, cosine, sine, eps, layout):
     if k is not None and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != D):
         raise ValueError("k must be [T, heads, D] matching q, got %s" % (tuple(k.shape),))
     if cosine is None:
-        n_pos, rot = (1 << 31) - 1, 0
+        n_pos, rot = 1 << 31, 0  # no table: any position will do
     else:
         if cosine.dim() != 2:
             raise ValueError("cosine must be [positions, rot / 2], got %s" % (tuple(cosine.shape),))
