@@ -201,6 +201,38 @@ def test_bounds_at_their_ends():
     assert near(one, -torch.minimum(torch.exp(step) * adv.double(), adv.double()))
 
 
+def test_no_bound_takes_no_longer():
+    """The documented calls without a bound on one side or both: few tokens may take
+    the slow way, in 64 bits (which made them 1.9 times as long)."""
+    import torch
+    dev = cuda()
+    S, T = 33, 65536
+    g = torch.Generator().manual_seed(3)
+    nll = torch.rand((S, T), generator=g).to(dev)
+    old = nll[0] + 0.3 * torch.randn(T, generator=g).to(dev)
+    adv = torch.randn(T, generator=g).to(dev)
+    off = torch.tensor([0, T], dtype=torch.int32, device=dev)
+    graphs = []
+    for low, high in ((0.2, 0.28), (0.2, float("inf")), (1.0, 0.28), (1.0, float("inf"))):
+        args = dict(ref=old, beta=BETA, per_token=True, clip_low=low, clip_high=high, changes=True)
+        dust.dust_policy_loss(nll, old, adv, off, **args)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(10):
+                dust.dust_policy_loss(nll, old, adv, off, **args)
+        graphs.append(graph)
+    best = [float("inf")] * len(graphs)
+    for _ in range(12):  # in turn, the shortest of each
+        for i, graph in enumerate(graphs):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            graph.replay()
+            b.record()
+            torch.cuda.synchronize()
+            best[i] = min(best[i], a.elapsed_time(b))
+    assert max(best[1:]) < 1.4 * best[0], best
+
+
 @pytest.mark.parametrize("by_sequence", [False, True])
 @pytest.mark.parametrize("S", [1, 2, 7])
 @pytest.mark.parametrize("lengths", [[43], [7, 29, 7], [1531], [300, 25], [3, 4000, 900], [70001]],

@@ -220,16 +220,22 @@ struct Token {
 
 // Whether the ratio is beyond the bound on its advantage's side. The fp32
 // difference is off by half a step, as the bound is: further apart than 4
-// steps, they stand as the exact ones do, and what is nearer is rare.
+// steps, they stand as the exact ones do, and what is nearer is rare. An infinite
+// bound is the exception: everything seems near it and is decided all the same,
+// which is asked last, as it would cost the common way 2 per cent. (With all
+// tokens in 64 bits there, 33 slices of 65536 tokens took 46 us without a bound.)
 struct Side {
     bool beyond, near;
+    float bound;
 
     __device__ __forceinline__ Side(const PolicyProblem& p, const Token& k, float nll) {
         const bool up = k.adv > 0.0f;
-        const float bound = up ? p.high32 : p.low32, step = k.old - nll;
+        bound = up ? p.high32 : p.low32;
+        const float step = k.old - nll;
         near = !(fabsf(step - bound) > 0x1p-22f * fabsf(bound));
         beyond = up ? step > bound : k.adv < 0.0f && step < bound;
     }
+    __device__ __forceinline__ bool open() const { return near && !isinf(bound); }
     // Decided in 64 bits. A call of its own: in line, the compiler would
     // form the exact differences of every value.
     static __device__ __noinline__ bool exactly(const PolicyProblem& p, float adv, float old, float nll) {
@@ -257,7 +263,8 @@ __device__ __forceinline__ void losses_of(const PolicyProblem& p, const Token (&
     }
     if (near)
 #pragma unroll
-        for (int i = 0; i < N; ++i) clipped[i] = Side::exactly(p, k[i].adv, k[i].old, nll[i]);
+        for (int i = 0; i < N; ++i)
+            if (Side(p, k[i], nll[i]).open()) clipped[i] = Side::exactly(p, k[i].adv, k[i].old, nll[i]);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const float bound = k[i].adv > 0.0f ? p.most : p.least;
@@ -277,7 +284,7 @@ __device__ __forceinline__ void losses_of(const PolicyProblem& p, const Token (&
 
 __device__ __forceinline__ float slope_of(const PolicyProblem& p, const Token& k, float nll) {
     Side d(p, k, nll);
-    if (d.near) d.beyond = Side::exactly(p, k.adv, k.old, nll);
+    if (d.open()) d.beyond = Side::exactly(p, k.adv, k.old, nll);
     float g = d.beyond ? 0.0f : ratio_of(k.old - nll, k.adv) * k.adv;
     if (p.ref && p.beta != 0.0f) g = fmaf(p.beta, expm1f(nll - k.ref), g);
     return g;
