@@ -274,6 +274,101 @@ def test_infinities_and_nan_stay_in_their_rows(T):
     assert h[T].isnan().all() and not h[T + 1].isfinite().all()
 
 
+def test_copies_of_rows_off_16_bytes_keep_every_bit():
+    """Rows that are copied before their products give what rows that start on 16
+    bytes do: the same products of the same values, in one order."""
+    import torch
+    dev = cuda()
+    for dtype in ("bf16", "f32"):
+        for T, d, f in ((70, 72, 90), (300, 200, 136)):
+            ops = _inputs(T, d, f, dtype, dev)
+            want = dust.dust_gated_up(*ops[:3]), *dust.dust_gated_up_grad(ops[3], *ops[:3])
+            for which in (0, 1, 2, 3):
+                moved = list(ops)
+                flat = torch.empty(ops[which].numel() + 1, dtype=ops[0].dtype, device=dev)
+                moved[which] = flat[1:].view(ops[which].shape)
+                moved[which].copy_(ops[which])
+                got = (dust.dust_gated_up(*moved[:3]), *dust.dust_gated_up_grad(moved[3], *moved[:3]))
+                for a, b in zip(got, want):
+                    assert torch.equal(a, b), (dtype, T, which)
+
+
+def test_no_plane_of_fp32_rows_off_16_bytes_is_lost():
+    """The same in fp32 against 64 bits, to fp32's accuracy (the planes behind the first
+    are worth 2e-3 together)."""
+    import torch
+    dev = cuda()
+    T, d, f = 70, 72, 90
+    X, Wg, Wu, gh = (
+        torch.cat([t.flatten(), t.new_zeros(3)]).roll(1)[1:-2].view(t.shape)
+        for t in _inputs(T, d, f, "f32", dev))
+    assert all(t.data_ptr() % 16 for t in (X, Wg, Wu, gh))
+    got = dust.dust_gated_up(X, Wg, Wu), *dust.dust_gated_up_grad(gh, X, Wg, Wu)
+    for a, b in zip(got, reference(gh, X, Wg, Wu, "silu")):
+        assert rel_fro(_np(a), b) <= 5 * f32_tol(max(d, 2 * f, T))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 300])
+def test_infinities_and_nan_reach_their_rows_gradient_alone(T, dtype):
+    """A NaN and an infinity in rows of X, and in rows of gh: h and gX of all other
+    rows keep their bits, these rows' are no numbers, nor are gWg and gWu, which
+    all rows enter."""
+    import torch
+    dev = cuda()
+    d, f = 64, 128
+    X, Wg, Wu, gh = _inputs(T + 4, d, f, dtype, dev)
+    want = dust.dust_gated_up(X, Wg, Wu)
+    gX0 = dust.dust_gated_up_grad(gh, X, Wg, Wu)[0]
+    bad_X, bad_gh = X.clone(), gh.clone()
+    bad_X[T, 3], bad_X[T + 1, 5] = float("nan"), float("inf")
+    bad_gh[T + 2, 7], bad_gh[T + 3, 9] = float("nan"), -float("inf")
+    h = dust.dust_gated_up(bad_X, Wg, Wu)
+    assert torch.equal(h[:T], want[:T]) and torch.equal(h[T + 2:], want[T + 2:])
+    assert h[T].isnan().all() and not h[T + 1].isfinite().any()
+    gX, gWg, gWu = dust.dust_gated_up_grad(bad_gh, bad_X, Wg, Wu)
+    assert torch.equal(gX[:T], gX0[:T])
+    assert gX[T].isnan().all() and gX[T + 2].isnan().all()
+    assert not gX[T + 1].isfinite().any() and not gX[T + 3].isfinite().any()
+    assert not gWg.isfinite().any() and not gWu.isfinite().any()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu2"])
+@pytest.mark.parametrize("T", [2, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_gradient_of_far_values(act, T, dtype):
+    """gX where gates are far out, each row with a unit of its own, so that no large
+    term hides a small one: dG and dU are a handful of fp32 roundings (2^-19), the
+    exponential's argument (100 at most until it saturates: 2^-24 * 100 < 2^-17) and
+    bf16's, the product two terms, and gX is rounded once. (A slope that is far below
+    the two terms it is made of is held to 1e-3 instead.)"""
+    import torch
+    dev = cuda()
+    d, f = 16, 64
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    X = torch.zeros((T, d), dtype=dt, device=dev)
+    X[:, 0], X[:, 1] = 1.0, 0.5
+    Wg = torch.zeros((f, d), dtype=dt, device=dev)
+    Wu = torch.zeros_like(Wg)
+    Wu[:, 1] = 2.0
+    gates = [0.0, 1.0, -1.0, 3.0, -3.0, 100.0, -100.0, 1e4, -1e4, 1e8, -1e8, 1e15, -1e15]
+    for i, v in enumerate(gates):
+        Wg[i, 0] = v
+        Wg[i, 2] = 1.0
+    gh = torch.zeros((T, f), dtype=dt, device=dev)
+    gh[torch.arange(T), torch.arange(T) % len(gates)] = 1.0
+    want = reference(gh, X, Wg, Wu, act)[1]
+    gX = _np(dust.dust_gated_up_grad(gh, X, Wg, Wu, ACTS[act])[0])
+    gate = _np(X) @ _np(Wg).T
+    a, slope = act64(gate, act)
+    size = (_np(gh) * np.maximum(np.abs(slope), 1e-3)) @ np.abs(_np(Wg)) + \
+        (_np(gh) * np.abs(a)) @ np.abs(_np(Wu))
+    e = (2.0 ** -19 + 2.0 ** -17) * size
+    if dtype == "bf16":
+        e = e + 2.0 ** -8 * size + 2.0 ** -8 * (np.abs(want) + e)
+    assert np.isfinite(gX).all() and (np.abs(gX - want) <= e + 1e-37).all()
+
+
 def test_gradients_against_differences():
     """Central differences of <gh, h> along random directions, fp32: at step
     e, their error is e^2 of the third derivative (1e-4 here) and the values'
