@@ -698,6 +698,10 @@ dust_status dust_distill_loss_grad(const void* H, int64_t ld_h, const void* E, i
  * that a product within 2^-7 of the range's end may be infinite).
  * An infinity or NaN in a row reaches what the row enters, in fp32 as a NaN
  * where fp32 arithmetic might have kept an infinity.
+ * Every fp32 call but a forward of up to 4 rows first copies the weights into
+ * planes, and all gradients work on tiles of 256 rows: few rows under wide weights
+ * are far from what their bytes take, in fp32 slower than two library products (9
+ * rows, d 2632, f 4968: gradients 416 us, 367 so).
  * d >= 1, f >= 1, T >= 0; T and d up to 2^31 - 2^16, f up to 2^30 - 2^16; with
  * all of them rounded up to multiples of 256, T*d, T*f and f*d up to 2^37, and
  * at most 2^30 tiles of 256 rows x 64 columns (DUST_ERR_RANGE).
@@ -760,7 +764,8 @@ dust_status dust_gated_up_grad(const void* gh, int64_t ld_gh, const void* X, int
  *            zeroed, or left, accumulating.
  *   workspace  device, >= dust_qk_norm_rope_grad_workspace bytes, 256-byte
  *            aligned (partial sums of gwq and gwk); may be NULL when both are.
- * Statistics, sums and the rotation are fp32; outputs are rounded once.
+ * Statistics, sums and the rotation are fp32; outputs are rounded once. A head
+ * whose sum of squares leaves fp32's range (values of 1e19) becomes 0.
  * T and the numbers of heads up to 2^31 - 1, T * (hq + hk) * D up to 2^40.
  */
 #define DUST_MAX_HEAD 512
@@ -823,6 +828,8 @@ dust_status dust_qk_norm_rope_grad(const dust_heads* gyq, const dust_heads* gyk,
  *   clip_low in [0, 1], clip_high >= 0, beta finite (infinite clip_high: no
  *            bound). Whether a ratio is beyond its bound is decided in 64 bits
  *            (the bounds as given, the difference of nll and old exactly).
+ *            A ratio above fp32's range (a difference above 88.7) that is not
+ *            beyond a bound counts as infinite, whatever A but 0.
  *   loss     device f32 [S][T] or NULL; total, kl_mean, clipped device f32 [S],
  *            each may be NULL; delta device f32 [S - 1][T] or NULL.
  *   gtotal   device f32 [S]; gnll device f32 [S][T]; may be nll itself.

@@ -8,9 +8,12 @@
 // of it: `split` warps of a CTA share a pair of units, so that there are
 // CTAs for the whole GPU. X comes from the L1 after its first use.
 //
-// Bound by the weights' way from memory, or its latency: 1 row, d 512, f 2048
-// bf16 takes 5.0 us (9 with the weights out of the L2; 10 as tiles), 4 rows, d
-// 2048, f 8192 17 (28; 21 as tiles for 16 rows), 67 MB at 3.9 TB/s.
+// 1 row, d 512, f 2048 bf16 is a round trip to memory: 5.0 us alone (10 as tiles),
+// 2.2 in a row of captured calls, 2.7 with weights that are not in the L2. 1 row, d
+// 2048, f 8192, 67 MB of weights: 13.2 us from memory, 5.1 TB/s, 7.1 from the L2; 4
+// rows 18.0 and 14.0, where their products and X's loads, four times as many, show
+// beside the weights (16 rows as tiles 20.2 and 18.8). HBM's rate makes 9.9 of
+// either: a warp has few loads on their way while it waits for those it has begun.
 #include <algorithm>
 
 #include "gated.cuh"

@@ -7,15 +7,20 @@
 // and leaves each CTA's sums, which the CTA that is done last adds up in order.
 // Few tokens go through all of it in one CTA and one launch.
 //
-// A loss takes about a hundred instructions (two exponentials, a series, the
-// sums), so that many slices are bound by issue rather than by their 12 bytes
-// a value, and single ones by the launches' latency. The losses' signs cancel in
-// their mean, so that it is added up in 64 bits beyond a thread's 4 tokens, or
-// with what roundings lose, and the weights' own rounding is made good. Whether
-// a ratio is beyond its bound is decided in fp32 where that is certain, else in
-// 64 bits, of which the GPU does a 64th as many a second: in 64 bits throughout,
-// 33 slices of 65536 tokens took 48 us. Now 25, where one slice takes 14.9; a
-// gradient of one slice 9.2; 1531 tokens 7.
+// Bound by latency: clearing, counting, one wave of CTAs that start, wait for
+// their first values and join, one after another. One slice of 65536 tokens takes
+// 14.5 us, 33 of them 24.7. A loss takes about 115 instructions (two exponentials,
+// a series, the sums), which are a third of the second pass (36 % of its cycles
+// issue one, 58 % of those in which an SM has work), and its 12 bytes a value less;
+// each group of slices forms the clean one's losses again. A gradient of one slice
+// takes 9.2 us, 1531 tokens 4.7 (7 alone).
+//
+// The losses' signs cancel in their mean, so that it is added up in 64 bits beyond
+// a thread's 4 tokens, or with what roundings lose, and what the weights'
+// roundings leave (of the counts, their product and its inverse) is added as
+// well. Whether a ratio is beyond its bound is decided in fp32 where that is
+// certain, else in 64 bits, of which the GPU does a 64th as many a second: in 64
+// bits throughout, 33 slices took 48 us.
 #include <algorithm>
 #include <cmath>
 
